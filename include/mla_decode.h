@@ -318,6 +318,186 @@ int32_t mla_extend(const mla_extend_params* p, const void* q_nope, const void* q
                    float scale, void* out, float* lse, void* workspace, void* stream);
 
 /*
+ * Attention of ragged chunks of new tokens over the paged cache, in the absorbed form ("MLA
+ * inference: two computation paths and FlashMLA", section "Two equivalent paths", path two, and
+ * section "Which is faster: count new tokens and cached tokens": new tokens only see what
+ * precedes them).  Where mla_decode takes the same 1..8 new tokens for every sequence, here
+ * sequence b brings its own number n_b >= 0: prompt pieces, speculative tokens and single tokens
+ * in one call.  With H <= 64 heads, 128 / H tokens of a sequence share every key tile.
+ */
+typedef struct mla_chunk_params {
+  int32_t batch;             /* B >= 1 sequences */
+  int32_t max_tokens;        /* T >= 1: rows of the token buffers; cu_seqlens[B] <= T */
+  int32_t num_heads;         /* H, 1..128 query heads */
+  int32_t num_pages;         /* physical pages in the pool (>= 1) */
+  int32_t page_size;         /* tokens per page; must be 64 */
+  int32_t max_pages_per_seq; /* row length of block_table (>= 1) */
+  int32_t causal;            /* nonzero: token i of b sees keys 0 .. L_b - n_b + i; zero: all L_b */
+  int32_t kv_dtype;          /* mla_kv_dtype */
+  int32_t num_units;         /* work units (one CTA pair each); 0 = as many as fit at once */
+  int32_t timeout_us;        /* limit of every bounded wait inside the kernels; 0 = 2,000,000 us */
+  int64_t max_kv_tokens;     /* FP8 cache: room for the expanded rows in the workspace, in tokens: at
+                                least the sum of 64 * ceil(L_b / 64) over the sequences with n_b > 0
+                                (a plan that needs more is refused).  bf16 cache: not used */
+  int32_t reserved[4];       /* must be zero */
+} mla_chunk_params;
+
+/*
+ * Sizes of the two caller-provided device buffers: *sched_bytes for the plan, *workspace_bytes for
+ * the split partials (float32) and, with an FP8 cache, the expanded rows (1152 bytes a token).
+ * They depend on p alone, never on the lengths.  Needs a CUDA device only when p->num_units == 0.
+ */
+int32_t mla_chunk_workspace_size(const mla_chunk_params* p, size_t* sched_bytes, size_t* workspace_bytes);
+
+/*
+ * The work plan of one step, from the lengths, on the device; reused by every layer that shares
+ * them.
+ *   cu_seqlens     device int32 [B + 1]: tokens cu[b] .. cu[b + 1] - 1 of the token buffers are
+ *                  sequence b's new ones; cu[0] = 0, not decreasing
+ *   cache_seqlens  device int32 [B]: L_b with the n_b new tokens, 0 .. 64 * max_pages_per_seq; a
+ *                  length below n_b leaves the first n_b - L_b tokens without keys
+ *   sched          device, sched_bytes
+ * Lengths outside these rules, or FP8 sequences past max_kv_tokens, set MLA_ERR_INVALID_ARG in the
+ * device error word; the plan is then marked refused, mla_chunk_attend writes nothing and sets
+ * MLA_ERR_WORKSPACE unless an error is set already.
+ */
+int32_t mla_chunk_schedule(const mla_chunk_params* p, const int32_t* cu_seqlens, const int32_t* cache_seqlens, void* sched,
+                           void* stream);
+
+/*
+ * The attention.
+ *   q_nope_absorbed  device bf16 [T][H][512]; q_rope device bf16 [T][H][64]
+ *   kv_pages         device, the pool of mla_decode (bf16 or FP8 pages).  FP8 rows stand for
+ *                    bf16(code * scale): they are expanded once per call into the workspace
+ *   block_table      device int32 [B][max_pages_per_seq]; entries past ceil(L_b / 64) are never read.
+ *                    An entry outside [0, num_pages) sets MLA_ERR_INVALID_ARG in the device error
+ *                    word and leaves that sequence's result undefined
+ *   cache_seqlens    device int32 [B], those of the plan
+ *   scale            softmax scale, finite and > 0 (1/sqrt(192) for DeepSeek-V3 shapes)
+ *   out              device bf16 [T][H][512], latent outputs (W_UV is not applied)
+ *   lse              device float32 [T][H], natural log; a token that sees no key gets out = 0,
+ *                    lse = -inf.  Rows of tokens at or past cu_seqlens[B] are left as they were
+ *   sched            device, from mla_chunk_schedule with the same p
+ *   workspace        device, workspace_bytes, 256-byte aligned; not shared by calls that overlap
+ * Scores, softmax statistics and sums are float32; P is bf16 for the P.V product.  A row of the
+ * cache that is not finite makes NaN of the tokens that see it and of no others.  Cache rows past
+ * L_b may hold any bits.  The kernels run on stream, each a programmatic dependent of the one
+ * before, and can be captured into a graph.
+ */
+int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed, const void* q_rope, const void* kv_pages,
+                         const int32_t* block_table, const int32_t* cache_seqlens, float scale, void* out, float* lse,
+                         const void* sched, void* workspace, void* stream);
+
+/*
+ * Host-side twin of mla_chunk_schedule for tests and capacity planning (host pointers, sched as
+ * large as mla_chunk_workspace_size says for that unit count).  Layout of sched (int32): [0] =
+ * 0x4D4C4143, [1] = units, [2] = block capacity, [3] = blocks, [4] = partial slots, [5] = budget of
+ * cost positions per unit, [6] = tokens per block, [7] = split blocks, [8] = pages of the sequences
+ * with new tokens, [9..15] = 0; then per unit 8 ints {first block, first tile, last block, end tile,
+ * split index of the first piece, 0, 0, 0} (first block -1: no work); then per block 8 ints {first
+ * token, tokens, sequence, keys the first token sees before clipping, L, tiles of 256 keys, splits,
+ * first slot}; then the split blocks, and the first page of each sequence.
+ * MLA_ERR_INVALID_ARG where the scheduler kernel refuses.
+ */
+int32_t mla_chunk_plan_host(const mla_chunk_params* p, int32_t num_units, const int32_t* cu_seqlens,
+                            const int32_t* cache_seqlens, void* sched);
+
+/*
+ * The paged cache's own upkeep.  One block table serves the pools of all layers: layer l's pages
+ * start layer_stride bytes after those of layer l - 1.  ref_counts[page] is the number of
+ * block-table entries that hold the page (0 = free); the caller starts with zeros, an empty table
+ * and zero lengths, and every call keeps the three consistent on the device, with no host
+ * synchronisation.  Free pages are taken lowest first, in the order of the caller's list, so the
+ * results are determined by the inputs.
+ */
+typedef struct mla_pool_params {
+  int32_t batch;             /* rows of the block table (>= 1) */
+  int32_t num_pages;         /* physical pages in each pool (>= 1) */
+  int32_t page_size;         /* must be 64 */
+  int32_t max_pages_per_seq; /* row length of block_table (>= 1) */
+  int32_t kv_dtype;          /* mla_kv_dtype: pages of 64 rows of 1152 or 656 bytes */
+  int32_t num_layers;        /* pools that share the table (1..16383) */
+  int64_t layer_stride;      /* bytes, a multiple of 16, at least a pool's size; 0 = pools are packed */
+  int32_t reserved[4];       /* must be zero */
+} mla_pool_params;
+
+/*
+ * Appends the rows of ragged new tokens to the cache of one layer (num_layers and layer_stride are
+ * not used): token cu[b] + i goes to row L_b - n_b + i of sequence b, through the block table.
+ *   max_tokens     rows of latent and k_rope; tokens at or past cu_seqlens[B] are not read
+ *   latent         device bf16, row t at latent + t * latent_stride elements: 512 latent values
+ *   k_rope         device bf16, row t at k_rope + t * rope_stride elements: 64 RoPE key values
+ *                  (strides: multiples of 8 elements, so the two parts of one [T][576] array will do)
+ *   cu_seqlens, cache_seqlens, block_table   as for mla_chunk_schedule / mla_chunk_attend
+ *   kv_pages       device, the layer's pool.  FP8: quantised by the rule of mla_quantize_kv_fp8 (the
+ *                  same bytes for finite rows); a tile that holds a value that is not finite reads
+ *                  back as NaN there (as NaN throughout, where the value is infinite)
+ * A token whose row lies outside the block table, or whose page is not in [0, num_pages), is not
+ * written and sets MLA_ERR_INVALID_ARG in the device error word.
+ */
+int32_t mla_append_kv(const mla_pool_params* p, int64_t max_tokens, const void* latent, int64_t latent_stride,
+                      const void* k_rope, int64_t rope_stride, const int32_t* cu_seqlens, const int32_t* cache_seqlens,
+                      const int32_t* block_table, void* kv_pages, void* stream);
+
+/* Bytes of the device workspace of fork (of at most max_forks), reserve and compact.  Host only. */
+int32_t mla_pool_workspace_size(const mla_pool_params* p, int32_t max_forks, size_t* workspace_bytes);
+
+/*
+ * Page dst_pages[i] := page src_pages[i] in every layer (device int32 [num_copies]).  No page may be
+ * named as a destination twice, or both as a source and as another's destination (its content is
+ * undefined then); src == dst does nothing.  Reference counts are not touched.  A page outside
+ * [0, num_pages) sets MLA_ERR_INVALID_ARG in the device error word and its pair is skipped.
+ */
+int32_t mla_copy_pages(const mla_pool_params* p, void* kv_pages, const int32_t* src_pages, const int32_t* dst_pages,
+                       int32_t num_copies, void* stream);
+
+/*
+ * Forks sequences: the empty row children[i] becomes a copy of row parents[i].  Full pages are
+ * shared (their reference count grows); the rows of a partly filled last page are copied, in every
+ * layer, to a page of the child's own, so that either can be appended to.  The forks of a call see
+ * the tables as they were before it.
+ *   parents, children  device int32 [num_forks], rows of the block table
+ *   new_pages          device int32 [num_forks]: the child's own page; -1: done, none was needed; -2:
+ *                      refused (a row out of range, a child that is not empty or that an earlier fork
+ *                      of the list names, a parent's length out of range; also sets
+ *                      MLA_ERR_INVALID_ARG in the device error word); -3: no free page was left.  A
+ *                      child that was not forked stays empty
+ *   workspace          device, mla_pool_workspace_size(p, num_forks) bytes; not shared by calls that overlap
+ * The rest of a child's table row is set to -1.
+ */
+int32_t mla_fork_sequences(const mla_pool_params* p, void* kv_pages, const int32_t* parents, const int32_t* children,
+                           int32_t num_forks, int32_t* block_table, int32_t* cache_seqlens, int32_t* ref_counts,
+                           int32_t* new_pages, void* workspace, void* stream);
+
+/*
+ * Makes room for num_new[b] >= 0 more rows of every sequence (device int32 [batch]): the pages its
+ * table row lacks are taken, and its length grows by num_new[b].
+ *   served  device int32 [batch]: 1: done; 0: not enough free pages (sequences are served in order, up to
+ *           the first whose pages are not there; later ones that need no page are served); -2: refused (a
+ *           negative count, or a length past the block table; sets MLA_ERR_INVALID_ARG in the device error word)
+ * A sequence that is not served keeps its length and pages.  A last page that others share must not be
+ * grown into: mla_fork_sequences leaves none.
+ */
+int32_t mla_reserve_pages(const mla_pool_params* p, const int32_t* num_new, int32_t* block_table, int32_t* cache_seqlens,
+                          int32_t* ref_counts, int32_t* served, void* workspace, void* stream);
+
+/*
+ * Ends sequences (device int32 [num_sequences], rows of the block table; a row named twice is ended
+ * once): each of its pages loses one reference, its table entries become -1 and its length 0.  A row
+ * out of range, or a page without a reference, sets MLA_ERR_INVALID_ARG in the device error word.
+ */
+int32_t mla_free_sequences(const mla_pool_params* p, const int32_t* sequences, int32_t num_sequences, int32_t* block_table,
+                           int32_t* cache_seqlens, int32_t* ref_counts, void* stream);
+
+/*
+ * Draws the used pages together: they become pages 0 .. n - 1, n their number (written to num_used,
+ * device int32).  The used pages at or above n move, in order and in every layer, into the free ones
+ * below n, and the block table follows.  Pages below n that are in use stay where they are.
+ */
+int32_t mla_compact_pages(const mla_pool_params* p, void* kv_pages, int32_t* block_table, const int32_t* cache_seqlens,
+                          int32_t* ref_counts, int32_t* num_used, void* workspace, void* stream);
+
+/*
  * Device error word of the current device: synchronises the device, writes the
  * word to *word (MLA_OK if none; MLA_ERR_TIMEOUT + 16 * site for a bounded wait that ran
  * out; MLA_ERR_INVALID_ARG for a length beyond the block table; MLA_ERR_WORKSPACE for

@@ -61,6 +61,29 @@ class MlaExtendParams(ctypes.Structure):
                    chunk_tokens, timeout_us)
 
 
+class MlaChunkParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("kv_dtype", ctypes.c_int32), ("num_units", ctypes.c_int32),
+                ("timeout_us", ctypes.c_int32), ("max_kv_tokens", ctypes.c_int64), ("reserved", ctypes.c_int32 * 4)]
+
+    @classmethod
+    def make(cls, batch, max_tokens, num_heads, num_pages, max_pages_per_seq, causal=True, kv_dtype=MLA_KV_BF16,
+             max_kv_tokens=0, num_units=0, timeout_us=0, page_size=64):
+        return cls(batch, max_tokens, num_heads, num_pages, page_size, max_pages_per_seq, int(bool(causal)), kv_dtype,
+                   num_units, timeout_us, max_kv_tokens)
+
+
+class MlaPoolParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages_per_seq", ctypes.c_int32), ("kv_dtype", ctypes.c_int32), ("num_layers", ctypes.c_int32),
+                ("layer_stride", ctypes.c_int64), ("reserved", ctypes.c_int32 * 4)]
+
+    @classmethod
+    def make(cls, batch, num_pages, max_pages_per_seq, kv_dtype=MLA_KV_BF16, num_layers=1, layer_stride=0, page_size=64):
+        return cls(batch, num_pages, page_size, max_pages_per_seq, kv_dtype, num_layers, layer_stride)
+
+
 def load_library():
     """Load the built library (raises if it has not been built)."""
     global _lib
@@ -73,7 +96,9 @@ def load_library():
         lib = ctypes.CDLL(path)
         P = ctypes.POINTER(MlaDecodeParams)
         X = ctypes.POINTER(MlaExtendParams)
-        vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        C = ctypes.POINTER(MlaChunkParams)
+        K = ctypes.POINTER(MlaPoolParams)
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         sig = {
             "mla_get_workspace_size": ([P, ctypes.POINTER(sz), ctypes.POINTER(sz)], i32),
             "mla_get_scheduler_metadata": ([P, vp, vp, vp], i32),
@@ -92,6 +117,17 @@ def load_library():
             "mla_extend_workspace_size": ([X, ctypes.POINTER(sz)], i32),
             "mla_expand_kv": ([X, vp, vp, vp, vp, vp, i32, vp, vp, vp], i32),
             "mla_extend": ([X, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp], i32),
+            "mla_chunk_workspace_size": ([C, ctypes.POINTER(sz), ctypes.POINTER(sz)], i32),
+            "mla_chunk_plan_host": ([C, i32, vp, vp, vp], i32),
+            "mla_chunk_schedule": ([C, vp, vp, vp, vp], i32),
+            "mla_chunk_attend": ([C, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp], i32),
+            "mla_append_kv": ([K, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp], i32),
+            "mla_pool_workspace_size": ([K, i32, ctypes.POINTER(sz)], i32),
+            "mla_copy_pages": ([K, vp, vp, vp, i32, vp], i32),
+            "mla_fork_sequences": ([K, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp], i32),
+            "mla_reserve_pages": ([K, vp, vp, vp, vp, vp, vp, vp], i32),
+            "mla_free_sequences": ([K, vp, i32, vp, vp, vp, vp], i32),
+            "mla_compact_pages": ([K, vp, vp, vp, vp, vp, vp, vp], i32),
             "mla_status_string": ([i32], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -241,6 +277,171 @@ def mla_extend(p: MlaExtendParams, q_nope, q_rope, kv_pages, block_table, cache_
                                      _ptr(workspace), _stream(stream)), "mla_extend")
 
 
+def _expect(what: str, t, dtype: str, size=None, shape=None):
+    """A contiguous tensor of the named type with at least `size` elements, or of `shape` (None: any)."""
+    ok = t is not None and str(t.dtype) == "torch." + dtype and t.is_contiguous()
+    ok = ok and (size is None or t.numel() >= size)
+    ok = ok and (shape is None or (t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape))))
+    if not ok:
+        raise MlaError(MLA_ERR_INVALID_ARG, what)
+
+
+def _expect_pool(what: str, t, p, num_layers: int = 1):
+    """The pools' pages: large enough for the last layer's last page, rows not strided."""
+    row = 1152 if p.kv_dtype == MLA_KV_BF16 else 656
+    pool = p.num_pages * 64 * row
+    need = (num_layers - 1) * (getattr(p, "layer_stride", 0) or pool) + pool
+    if t is None or not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise MlaError(MLA_ERR_INVALID_ARG, what)
+
+
+def mla_chunk_workspace_size(p: MlaChunkParams):
+    sb, wb = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load_library().mla_chunk_workspace_size(ctypes.byref(p), ctypes.byref(sb), ctypes.byref(wb)),
+           "mla_chunk_workspace_size")
+    return sb.value, wb.value
+
+
+def mla_chunk_plan_host(p: MlaChunkParams, num_units: int, cu_seqlens, cache_seqlens) -> np.ndarray:
+    """Host twin of mla_chunk_schedule; returns the int32 metadata array."""
+    cu = np.ascontiguousarray(cu_seqlens, dtype=np.int32)
+    seq = np.ascontiguousarray(cache_seqlens, dtype=np.int32)
+    if cu.shape != (p.batch + 1,) or seq.shape != (p.batch,):
+        raise MlaError(MLA_ERR_INVALID_ARG, "mla_chunk_plan_host")
+    q = MlaChunkParams.from_buffer_copy(p)
+    q.num_units = num_units
+    out = np.zeros(mla_chunk_workspace_size(q)[0] // 4, np.int32)
+    _check(load_library().mla_chunk_plan_host(ctypes.byref(p), num_units, cu.ctypes.data, seq.ctypes.data,
+                                              out.ctypes.data), "mla_chunk_plan_host")
+    return out
+
+
+def mla_chunk_schedule(p: MlaChunkParams, cu_seqlens, cache_seqlens, sched, stream=None):
+    """Work plan of ragged chunks: cu_seqlens int32 [B + 1], cache_seqlens int32 [B] (new tokens included)."""
+    _expect("mla_chunk_schedule: cu_seqlens", cu_seqlens, "int32", shape=(p.batch + 1,))
+    _expect("mla_chunk_schedule: cache_seqlens", cache_seqlens, "int32", shape=(p.batch,))
+    _check(load_library().mla_chunk_schedule(ctypes.byref(p), _ptr(cu_seqlens), _ptr(cache_seqlens), _ptr(sched),
+                                             _stream(stream)), "mla_chunk_schedule")
+
+
+def mla_chunk_attend(p: MlaChunkParams, q_nope_absorbed, q_rope, kv_pages, block_table, cache_seqlens, scale: float,
+                     out, lse, sched, workspace, stream=None):
+    """Attention of ragged chunks over the paged cache: q bf16 [T, H, 512] and [T, H, 64], out bf16 [T, H, 512],
+    lse float32 [T, H]."""
+    T, H = p.max_tokens, p.num_heads
+    _expect("mla_chunk_attend: q_nope_absorbed", q_nope_absorbed, "bfloat16", shape=(T, H, 512))
+    _expect("mla_chunk_attend: q_rope", q_rope, "bfloat16", shape=(T, H, 64))
+    _expect("mla_chunk_attend: block_table", block_table, "int32", shape=(p.batch, p.max_pages_per_seq))
+    _expect("mla_chunk_attend: cache_seqlens", cache_seqlens, "int32", shape=(p.batch,))
+    _expect("mla_chunk_attend: out", out, "bfloat16", shape=(T, H, 512))
+    _expect("mla_chunk_attend: lse", lse, "float32", shape=(T, H))
+    _expect_pool("mla_chunk_attend: kv_pages", kv_pages, p)
+    _check(load_library().mla_chunk_attend(ctypes.byref(p), _ptr(q_nope_absorbed), _ptr(q_rope), _ptr(kv_pages),
+                                           _ptr(block_table), _ptr(cache_seqlens), float(scale), _ptr(out), _ptr(lse),
+                                           _ptr(sched), _ptr(workspace), _stream(stream)), "mla_chunk_attend")
+
+
+def mla_append_kv(p: MlaPoolParams, latent, k_rope, cu_seqlens, cache_seqlens, block_table, kv_pages, stream=None):
+    """Rows of ragged new tokens into the pages: latent bf16 [T, 512] and k_rope bf16 [T, 64], rows of either may be
+    strided (the two parts of one [T, 576] array)."""
+    for what, t, n in (("latent", latent, 512), ("k_rope", k_rope, 64)):
+        if (t is None or str(t.dtype) != "torch.bfloat16" or t.dim() != 2 or t.shape[1] != n or t.stride(1) != 1
+                or t.shape[0] != latent.shape[0]):
+            raise MlaError(MLA_ERR_INVALID_ARG, "mla_append_kv: " + what)
+    _expect("mla_append_kv: cu_seqlens", cu_seqlens, "int32", shape=(p.batch + 1,))
+    _expect("mla_append_kv: cache_seqlens", cache_seqlens, "int32", shape=(p.batch,))
+    _expect("mla_append_kv: block_table", block_table, "int32", shape=(p.batch, p.max_pages_per_seq))
+    _expect_pool("mla_append_kv: kv_pages", kv_pages, p)
+    if latent.shape[0] == 0:
+        return
+    # (one row: its stride says nothing)
+    ls, rs = (int(t.stride(0)) if t.shape[0] > 1 else n for t, n in ((latent, 512), (k_rope, 64)))
+    _check(load_library().mla_append_kv(ctypes.byref(p), int(latent.shape[0]), _ptr(latent), ls, _ptr(k_rope), rs,
+                                        _ptr(cu_seqlens), _ptr(cache_seqlens), _ptr(block_table), _ptr(kv_pages),
+                                        _stream(stream)), "mla_append_kv")
+
+
+def mla_pool_workspace_size(p: MlaPoolParams, max_forks: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().mla_pool_workspace_size(ctypes.byref(p), int(max_forks), ctypes.byref(n)),
+           "mla_pool_workspace_size")
+    return n.value
+
+
+def _expect_tables(what: str, p: MlaPoolParams, block_table, cache_seqlens, ref_counts):
+    _expect(what + ": block_table", block_table, "int32", shape=(p.batch, p.max_pages_per_seq))
+    _expect(what + ": cache_seqlens", cache_seqlens, "int32", shape=(p.batch,))
+    _expect(what + ": ref_counts", ref_counts, "int32", shape=(p.num_pages,))
+
+
+def _expect_workspace(what: str, p: MlaPoolParams, workspace, forks: int = 0):
+    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if n < mla_pool_workspace_size(p, forks):
+        raise MlaError(MLA_ERR_WORKSPACE, what + ": workspace")
+
+
+def mla_copy_pages(p: MlaPoolParams, kv_pages, src_pages, dst_pages, stream=None):
+    """Page dst_pages[i] := page src_pages[i] in every layer (int32 [n])."""
+    _expect("mla_copy_pages: src_pages", src_pages, "int32", shape=(None,))
+    _expect("mla_copy_pages: dst_pages", dst_pages, "int32", shape=tuple(src_pages.shape))
+    _expect_pool("mla_copy_pages: kv_pages", kv_pages, p, p.num_layers)
+    if src_pages.numel() == 0:
+        return
+    _check(load_library().mla_copy_pages(ctypes.byref(p), _ptr(kv_pages), _ptr(src_pages), _ptr(dst_pages),
+                                         int(src_pages.numel()), _stream(stream)), "mla_copy_pages")
+
+
+def mla_fork_sequences(p: MlaPoolParams, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages,
+                       workspace, stream=None):
+    """Row children[i] of the table becomes a copy of row parents[i]; new_pages int32 [n] takes the outcomes."""
+    _expect("mla_fork_sequences: parents", parents, "int32", shape=(None,))
+    _expect("mla_fork_sequences: children", children, "int32", shape=tuple(parents.shape))
+    _expect("mla_fork_sequences: new_pages", new_pages, "int32", shape=tuple(parents.shape))
+    _expect_tables("mla_fork_sequences", p, block_table, cache_seqlens, ref_counts)
+    _expect_pool("mla_fork_sequences: kv_pages", kv_pages, p, p.num_layers)
+    _expect_workspace("mla_fork_sequences", p, workspace, int(parents.numel()))
+    if parents.numel() == 0:
+        return
+    _check(load_library().mla_fork_sequences(ctypes.byref(p), _ptr(kv_pages), _ptr(parents), _ptr(children),
+                                             int(parents.numel()), _ptr(block_table), _ptr(cache_seqlens),
+                                             _ptr(ref_counts), _ptr(new_pages), _ptr(workspace), _stream(stream)),
+           "mla_fork_sequences")
+
+
+def mla_reserve_pages(p: MlaPoolParams, num_new, block_table, cache_seqlens, ref_counts, served, workspace, stream=None):
+    """Room for num_new[b] more rows of every sequence; served int32 [batch] takes the outcomes."""
+    _expect("mla_reserve_pages: num_new", num_new, "int32", shape=(p.batch,))
+    _expect("mla_reserve_pages: served", served, "int32", shape=(p.batch,))
+    _expect_tables("mla_reserve_pages", p, block_table, cache_seqlens, ref_counts)
+    _expect_workspace("mla_reserve_pages", p, workspace)
+    _check(load_library().mla_reserve_pages(ctypes.byref(p), _ptr(num_new), _ptr(block_table), _ptr(cache_seqlens),
+                                            _ptr(ref_counts), _ptr(served), _ptr(workspace), _stream(stream)),
+           "mla_reserve_pages")
+
+
+def mla_free_sequences(p: MlaPoolParams, sequences, block_table, cache_seqlens, ref_counts, stream=None):
+    """Ends the sequences (int32 [n], rows of the block table) and gives their pages back."""
+    _expect("mla_free_sequences: sequences", sequences, "int32", shape=(None,))
+    _expect_tables("mla_free_sequences", p, block_table, cache_seqlens, ref_counts)
+    if sequences.numel() == 0:
+        return
+    _check(load_library().mla_free_sequences(ctypes.byref(p), _ptr(sequences), int(sequences.numel()),
+                                             _ptr(block_table), _ptr(cache_seqlens), _ptr(ref_counts),
+                                             _stream(stream)), "mla_free_sequences")
+
+
+def mla_compact_pages(p: MlaPoolParams, kv_pages, block_table, cache_seqlens, ref_counts, num_used, workspace,
+                      stream=None):
+    """Draws the used pages together at the start of the pools; num_used int32 [1] takes their number."""
+    _expect("mla_compact_pages: num_used", num_used, "int32", size=1)
+    _expect_tables("mla_compact_pages", p, block_table, cache_seqlens, ref_counts)
+    _expect_pool("mla_compact_pages: kv_pages", kv_pages, p, p.num_layers)
+    _expect_workspace("mla_compact_pages", p, workspace)
+    _check(load_library().mla_compact_pages(ctypes.byref(p), _ptr(kv_pages), _ptr(block_table), _ptr(cache_seqlens),
+                                            _ptr(ref_counts), _ptr(num_used), _ptr(workspace), _stream(stream)),
+           "mla_compact_pages")
+
+
 def mla_device_error(clear: bool = True) -> int:
     w = ctypes.c_int32()
     _check(load_library().mla_device_error(ctypes.byref(w), int(clear)), "mla_device_error")
@@ -282,3 +483,83 @@ class Decoder:
         mla_decode(self.p, q_nope_absorbed, q_rope, kv_pages, block_table, cache_seqlens, scale, out, lse,
                    self.sched, self.workspace, stream)
         return out, lse
+
+
+class ChunkAttention:
+    """Convenience wrapper of the chunk attention: owns the plan and the workspace of one problem shape."""
+
+    def __init__(self, p: MlaChunkParams, device=None):
+        import torch
+        self.p = p
+        self.device = torch.device("cuda" if device is None else device)
+        sb, wb = mla_chunk_workspace_size(p)
+        self.sched = torch.zeros(sb // 4, dtype=torch.int32, device=self.device)
+        self.workspace = torch.empty(wb, dtype=torch.uint8, device=self.device)
+        self.seqlens = None
+
+    def plan(self, cu_seqlens, cache_seqlens, stream=None):
+        """The plan of a step's lengths; the tensors are read again by attend()."""
+        mla_chunk_schedule(self.p, cu_seqlens, cache_seqlens, self.sched, stream)
+        self.seqlens = cache_seqlens
+
+    def attend(self, q_nope_absorbed, q_rope, kv_pages, block_table, scale, out=None, lse=None, stream=None):
+        import torch
+        if self.seqlens is None:
+            raise MlaError(MLA_ERR_WORKSPACE, "ChunkAttention.attend before plan")
+        if out is None:
+            out = torch.empty_like(q_nope_absorbed)
+        if lse is None:
+            lse = torch.empty(q_nope_absorbed.shape[:2], dtype=torch.float32, device=q_nope_absorbed.device)
+        mla_chunk_attend(self.p, q_nope_absorbed, q_rope, kv_pages, block_table, self.seqlens, scale, out, lse,
+                         self.sched, self.workspace, stream)
+        return out, lse
+
+
+class PagePool:
+    """Convenience wrapper of the page upkeep: owns the workspace of one pool shape, for calls that fork at most
+    max_forks sequences.  The tables belong to the caller."""
+
+    def __init__(self, p: MlaPoolParams, max_forks: int = 1024, device=None):
+        import torch
+        self.p = p
+        self.device = torch.device("cuda" if device is None else device)
+        self.max_forks = int(max_forks)
+        self.workspace = torch.empty(mla_pool_workspace_size(p, self.max_forks), dtype=torch.uint8, device=self.device)
+
+    def new_tables(self):
+        """An empty pool's (block_table, cache_seqlens, ref_counts)."""
+        import torch
+        p, kw = self.p, dict(dtype=torch.int32, device=self.device)
+        return (torch.full((p.batch, p.max_pages_per_seq), -1, **kw), torch.zeros(p.batch, **kw),
+                torch.zeros(p.num_pages, **kw))
+
+    def _outcome(self, n: int):
+        import torch
+        return torch.empty(n, dtype=torch.int32, device=self.device)
+
+    def copy(self, kv_pages, src_pages, dst_pages, stream=None):
+        mla_copy_pages(self.p, kv_pages, src_pages, dst_pages, stream)
+
+    def fork(self, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, stream=None):
+        """Returns new_pages int32 [n]: the child's own page, -1 (none needed), -2 (refused), -3 (no page left)."""
+        if parents.numel() > self.max_forks:
+            raise MlaError(MLA_ERR_WORKSPACE, "PagePool.fork: more forks than max_forks")
+        new_pages = self._outcome(parents.numel())
+        mla_fork_sequences(self.p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages,
+                           self.workspace, stream)
+        return new_pages
+
+    def reserve(self, num_new, block_table, cache_seqlens, ref_counts, stream=None):
+        """Returns served int32 [batch]: 1 (done), 0 (not enough pages), -2 (refused)."""
+        served = self._outcome(self.p.batch)
+        mla_reserve_pages(self.p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
+        return served
+
+    def free(self, sequences, block_table, cache_seqlens, ref_counts, stream=None):
+        mla_free_sequences(self.p, sequences, block_table, cache_seqlens, ref_counts, stream)
+
+    def compact(self, kv_pages, block_table, cache_seqlens, ref_counts, stream=None):
+        """Returns the number of used pages, int32 [1] on the device."""
+        used = self._outcome(1)
+        mla_compact_pages(self.p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
+        return used

@@ -1,0 +1,837 @@
+// Attention of ragged chunks of new tokens over the paged cache, in the absorbed form: for every
+// new token and head, s_j = scale (q~ . c_j + q^R . k^R_j) over the keys the token may see,
+// out = sum_j softmax(s)_j c_j (512 dims), lse = ln sum_j exp(s_j)  ("MLA inference: two
+// computation paths and FlashMLA", section "Two equivalent paths", path two; the causal rule of
+// "Which is faster: count new tokens and cached tokens": new tokens only see what precedes them).
+//
+// What bounds it: 2176 FLOP per (row, key) against 1152 bytes per key shared by all rows of a
+// sequence's chunk -- from two tokens at 128 heads on it is the tensor cores, not HBM.
+//
+// Work split.  A block is 128 rows (128 / H tokens of one sequence).  Its fp32 output, 128 x 512,
+// is one SM's whole tensor memory, so a CTA pair takes a block with tcgen05 cta_group::2, M = 128:
+// each CTA holds 64 rows, as 128 lanes x half the columns (lanes 64..127 hold the upper half of an
+// MMA's N columns for the same 64 rows): O takes 256 columns, two score buffers of a 256-key tile
+// 128 each.  Measured issue rate of M = 128, N = 256: 64 cycles, the same FLOP/s as M = 256; with
+// N = 128 it drops to 68%, which is why a tile is 256 keys.  Scores are complete in fp32 -- no
+// exchange of partial scores between the CTAs, unlike the decode kernel's split by latent dims.
+//
+// The MMAs take half of each B operand from either CTA: QK wants 128 keys x 576 dims per CTA (two
+// of the tile's four pages), PV all 256 keys x 128 dims of every 256.  Both stream through one
+// ring of seven 16 KB slots (K: 128 keys x 64 dims; V: 64 keys x 128 dims), 17 slots a tile.  One
+// thread issues a TMA copy every ~0.3 us whatever its size, so six warps share the copies.
+//
+// Roles (512 threads a CTA): warps 0..5 copy pages, warp 6 issues the MMAs of the pair (first CTA
+// only), warp 7 copies queries, warps 8..15 (two warpgroups, half of a tile's score columns each)
+// run the softmax.  A row's 256 scores lie in four threads, which agree on its maximum through
+// shared memory; O is rescaled only when the maximum grows by more than 2^8.
+//
+// Rows of a block see different numbers of keys where it holds several tokens.  P is zero past a
+// row's limit, but 0 x NaN is NaN, so in the pages that some row does not see in full the copying
+// warp zeroes what no row sees and whatever is not finite; a row that does see such a key gets NaN
+// through its score.
+#pragma once
+#include <type_traits>
+
+#include "chunk_plan.h"
+#include "common.cuh"
+#include "decode_kernel.cuh"  // packed float pairs, bf16 packing
+
+namespace mla {
+
+constexpr int kCkThreads = 512;
+constexpr int kCkCopyWarps = 6;
+constexpr int kCkSlots = 7;
+constexpr uint32_t kCkBlk = 8192;                            // [64 rows][64 bf16], 128-byte swizzle
+constexpr uint32_t kCkSlot = 2 * kCkBlk;
+constexpr uint32_t CK_Q = 0;                                 // 9 blocks: 64 rows x 576 dims
+constexpr uint32_t CK_P = 9 * kCkBlk;                        // 4 blocks: 64 rows x 256 keys
+constexpr uint32_t CK_RING = CK_P + 4 * kCkBlk;
+constexpr uint32_t CK_RED = CK_RING + kCkSlots * kCkSlot;    // row maxima [tile parity][4][64]
+constexpr uint32_t CK_SUM = CK_RED + 2 * 4 * 64 * 4;         // row sums [4][64]
+constexpr uint32_t CK_BAR = CK_SUM + 4 * 64 * 4;
+constexpr uint32_t kCkSmem = CK_BAR + 512 + 1024;            // + alignment slack
+static_assert(kCkSmem <= 232448, "shared memory");
+
+// Barriers.  "leader": used in the first CTA only, arrived on by both.
+enum : uint32_t {
+  CB_FULL = 0,                        // + slot, leader: one arrival and the bytes of each CTA
+  CB_EMPTY = CB_FULL + kCkSlots,      // + slot: the MMAs that read it are done
+  CB_RAW = CB_EMPTY + kCkSlots,       // + copying warp: a page it looks through has landed
+  CB_Q_FULL = CB_RAW + kCkCopyWarps,  // leader
+  CB_Q_EMPTY,
+  CB_S_FULL,                          // + tile parity
+  CB_S_EMPTY = CB_S_FULL + 2,         // + tile parity, leader: one arrival per softmax warp
+  CB_P_FULL = CB_S_EMPTY + 2,         // leader: one arrival per softmax warp
+  CB_P_FREE,                          // PV done
+  CB_RED,                             // + tile parity: row maxima in shared memory, one arrival per softmax warp
+  CB_SUM = CB_RED + 2,                // row sums in shared memory
+  CB_DRAIN,
+  kCkBars
+};
+constexpr uint32_t kCkTmemSlot = 8 * kCkBars, kCkAbort = kCkTmemSlot + 4;
+static_assert(kCkAbort + 4 <= 512, "barrier area");
+
+// tensor memory columns
+constexpr uint32_t CT_S = 0, CT_O = 256;  // S buffers at 0 and 128
+
+enum ChunkSite : int { kSiteCkRing = 32, kSiteCkRaw, kSiteCkQ, kSiteCkScores, kSiteCkP, kSiteCkPv, kSiteCkRed, kSiteCkDrain };
+
+struct ChunkArgs {
+  CUtensorMap map_q;    // q~ rows: bf16 {512, T * H}, box {64, 64}, 128-byte swizzle
+  CUtensorMap map_qr;   // q^R rows: bf16 {64, T * H}, box {64, 64}
+  CUtensorMap map_k;    // cache rows: bf16 {576, pages * 64}, box {64, 64}
+  CUtensorMap map_v;    // the same rows as {64, pages * 64, 9 blocks 128 bytes apart}, box {64, 64, 2}
+  const int32_t* block_table;
+  const int32_t* sched;
+  __nv_bfloat16* out;   // [T][H][512]
+  float* lse;           // [T][H]
+  float* o_acc;         // split partials [slots][128][512], normalised
+  float* lse_acc;       // [slots][128]
+  float scale_log2;
+  int32_t H, causal, max_pages, num_pages, num_units, capacity, batch;
+  int32_t expanded;     // the cache rows are the expanded ones: page = page_off[seq] + logical page
+  uint64_t timeout_ns;
+};
+
+// ----------------------------------------------------------------- CTA-pair instructions
+// (mbar: a barrier of either CTA of the pair, shared::cluster address)
+__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t mbar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(mbar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t mbar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(mbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_remote(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void mma2_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive (once) on the barrier at this offset in both CTAs when this thread's MMAs so far are done.
+__device__ __forceinline__ void mma2_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// One tile of a unit's work.
+struct ChunkTileRef {
+  ChunkBlock b;
+  int blk, tile, vis;  // vis: keys the block's last token sees
+  int split;           // this unit's share of the block
+  bool first, last;
+  __device__ int pages() const { return min(max((vis - kChunkTile * tile + 63) >> 6, 0), 4); }
+};
+
+// Walks the unit's tiles in order, across blocks.
+struct ChunkCursor {
+  const ChunkBlock* blocks;
+  int causal, blk, blk0, blk1, tile0, tile1, split0, t, end;
+  bool open;
+  ChunkBlock b;
+  int vis;
+  __device__ void init(const ChunkBlock* blk_records, const int32_t* rec, int causal_) {
+    blocks = blk_records;
+    causal = causal_;
+    blk = blk0 = rec[0];
+    tile0 = rec[1];
+    blk1 = rec[2];
+    tile1 = rec[3];
+    split0 = rec[4];
+    open = false;
+  }
+  __device__ bool next(ChunkTileRef& r) {
+    if (!open || t >= end) {
+      if (open) ++blk;
+      if (blk > blk1) return false;
+      const int4* src = reinterpret_cast<const int4*>(blocks + blk);
+      const int4 lo = src[0], hi = src[1];
+      b.tok0 = lo.x; b.ntok = lo.y; b.seq = lo.z; b.base = lo.w;
+      b.len = hi.x; b.nt = hi.y; b.splits = hi.z; b.offset = hi.w;
+      vis = chunk_visible(b, b.ntok - 1, causal);
+      t = blk == blk0 ? tile0 : 0;
+      end = blk == blk1 ? tile1 : b.nt;
+      open = true;
+      r.first = true;
+    } else {
+      r.first = false;
+    }
+    r.b = b;
+    r.blk = blk;
+    r.vis = vis;
+    r.split = blk == blk0 ? split0 : 0;
+    r.tile = t++;
+    r.last = t >= end;
+    return true;
+  }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
+    mla_chunk_kernel(const __grid_constant__ ChunkArgs args) {
+  extern __shared__ uint8_t ck_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ck_smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  auto bar = [&](uint32_t i) { return base + CK_BAR + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + CK_BAR + kCkAbort);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + CK_BAR + kCkTmemSlot);
+
+  if (tid == 0) {
+    for (uint32_t i = 0; i < kCkBars; ++i) {
+      uint32_t count = 1;
+      if (i < CB_EMPTY || i == CB_Q_FULL) count = 2;                                    // one per CTA
+      if (i == CB_S_EMPTY || i == CB_S_EMPTY + 1 || i == CB_P_FULL) count = 16;         // 8 softmax warps per CTA
+      if (i >= CB_RED && i <= CB_SUM) count = 8;
+      mbar_init(bar(i), count);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 6) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (tid == 0) {
+    prefetch_tensormap(&args.map_q);
+    prefetch_tensormap(&args.map_qr);
+    prefetch_tensormap(&args.map_k);
+    prefetch_tensormap(&args.map_v);
+  }
+  pdl_wait_prerequisites();
+  const int32_t* sched = args.sched;
+  const ChunkLayout lay = chunk_layout(args.num_units, args.capacity, args.batch);
+  const int32_t* rec = sched + lay.units + kUnitInts * (blockIdx.x >> 1);
+  const bool bad_meta = sched[kChMagic] != kChunkMagic || sched[kChUnits] != args.num_units ||
+                        sched[kChCapacity] != args.capacity || sched[kChTokens] != chunk_tokens_per_block(args.H);
+  const bool idle = bad_meta || rec[0] < 0;  // the same in both CTAs
+  if (bad_meta && tid == 0) atomicCAS(&g_mla_error, 0, 5);
+  pdl_launch_dependents();
+
+  WaitCtx wc;
+  wc.abort_local = abort_flag;
+  wc.abort_peer = map_to_rank(smem_addr((const void*)abort_flag), rank ^ 1);
+  wc.timeout_ns = args.timeout_ns;
+  const uint32_t lead0 = map_to_rank(bar(0), 0);  // the leader's barrier i is at lead0 + 8 i
+  ChunkCursor cur;
+  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), rec, args.causal);
+
+  if (idle) {
+  } else if (warp < kCkCopyWarps) {
+    // ================================================================ page copies
+    const int32_t* page_off = sched + lay.page_off;
+    uint32_t seq = 0, n_raw = 0;
+    bool ok = true;
+    // lane j < 4: physical page of the tile's page j
+    auto page_of = [&](const ChunkTileRef& r) -> int {
+      const int lp = 4 * r.tile + lane;
+      if (lane >= 4 || lane >= r.pages()) return 0;
+      if (args.expanded) return page_off[r.b.seq] + lp;
+      int page = args.block_table[(int64_t)r.b.seq * args.max_pages + lp];
+      if (page < 0 || page >= args.num_pages) {  // outside the contract: reported, and another page read
+        atomicCAS(&g_mla_error, 0, 1);
+        page = 0;
+      }
+      return page;
+    };
+    auto claim = [&](uint32_t s) -> bool {  // slot s is free again
+      return s < kCkSlots || wait_warp<true>(bar(CB_EMPTY + s % kCkSlots), (s / kCkSlots - 1) & 1, wc, kSiteCkRing);
+    };
+    auto copy_k = [&](const ChunkTileRef& r, int page) -> bool {
+      const int np = min(max(r.pages() - 2 * (int)rank, 0), 2);
+      const int p0 = __shfl_sync(0xffffffffu, page, 2 * rank), p1 = __shfl_sync(0xffffffffu, page, 2 * rank + 1);
+#pragma unroll 1
+      for (int d = 0; d < 9; ++d, ++seq) {
+        if (seq % kCkCopyWarps != (uint32_t)warp) continue;
+        if (!claim(seq)) return false;
+        if (lane == 0) {
+          const uint32_t full = lead0 + 8 * (CB_FULL + seq % kCkSlots), dst = base + CK_RING + (seq % kCkSlots) * kCkSlot;
+          if (np == 0) {
+            mbar_arrive_remote(full);
+          } else {
+            mbar_arrive_expect_tx_remote(full, np * kCkBlk);
+            tma2_load_2d(dst, &args.map_k, full, 64 * d, p0 * 64);
+            if (np == 2) tma2_load_2d(dst + kCkBlk, &args.map_k, full, 64 * d, p1 * 64);
+          }
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    auto copy_v = [&](const ChunkTileRef& r, int page) -> bool {
+      const int np = r.pages(), some = chunk_visible(r.b, 0, args.causal);  // keys every row of the block sees
+#pragma unroll 1
+      for (int kb = 0; kb < np; ++kb) {
+        const int pg = __shfl_sync(0xffffffffu, page, kb), key0 = kChunkTile * r.tile + 64 * kb;
+#pragma unroll 1
+        for (int n = 0; n < 2; ++n, ++seq) {
+          if (seq % kCkCopyWarps != (uint32_t)warp) continue;
+          if (!claim(seq)) return false;
+          const uint32_t full = lead0 + 8 * (CB_FULL + seq % kCkSlots), dst = base + CK_RING + (seq % kCkSlots) * kCkSlot;
+          const int z = 4 * n + 2 * (int)rank;  // dims 256 n + 128 rank, in blocks of 64
+          if (key0 + 64 <= some) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx_remote(full, kCkSlot);
+              tma2_load_3d(dst, &args.map_v, full, 0, pg * 64, z);
+            }
+            __syncwarp();
+            continue;
+          }
+          // some row does not see all of this page: rows [from, to) of it are looked through
+          const uint32_t raw = bar(CB_RAW + warp);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(raw, kCkSlot);
+            tma2_load_3d(dst, &args.map_v, map_to_rank(raw, rank), 0, pg * 64, z);
+          }
+          if (!wait_warp(raw, n_raw & 1, wc, kSiteCkRaw)) return false;
+          ++n_raw;
+          const int from = max(some - key0, 0), seen = min(r.vis - key0, 64), to = (seen + 15) & ~15;
+          for (int i = from * 16 + lane; i < to * 16; i += 32) {  // 16-byte chunks: two blocks of 8 a row
+            const int row = i >> 4;
+            const uint32_t a = dst + ((i >> 3) & 1) * kCkBlk + row * 128 + (i & 7) * 16;
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
+            bool bad = row >= seen;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              bad |= (v[q] & 0x7F80u) == 0x7F80u || (v[q] & 0x7F800000u) == 0x7F800000u;
+            if (bad) asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0u) : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(full);
+          __syncwarp();
+        }
+      }
+      return true;
+    };
+    // the order of the MMA warp: K of the next tile, then V of the current one; a tile's page
+    // numbers are read one tile ahead of their use
+    ChunkTileRef a, b, c;
+    bool has_b, has_c;
+    cur.next(a);
+    int pa = page_of(a), pb = 0, pc = 0;
+    has_b = cur.next(b);
+    if (has_b) pb = page_of(b);
+    ok = copy_k(a, pa);
+    while (ok) {
+      has_c = has_b && cur.next(c);
+      if (has_c) pc = page_of(c);
+      if (has_b && !(ok = copy_k(b, pb))) break;
+      if (!(ok = copy_v(a, pa)) || !has_b) break;
+      a = b;
+      pa = pb;
+      b = c;
+      pb = pc;
+      has_b = has_c;
+    }
+  } else if (warp == 6) {
+    // ================================================================ MMAs
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t id_qk = idesc_bf16_f32(128, 256, 0, 0), id_pv = idesc_bf16_f32(128, 256, 0, 1);
+      uint32_t seq = 0, g = 0, piece = 0;
+      auto qk = [&](const ChunkTileRef& r, uint32_t t) -> bool {
+        if (r.first) {
+          if (!wait_one<true>(bar(CB_Q_FULL), piece & 1, wc, kSiteCkQ)) return false;
+          ++piece;
+        }
+        if (t >= 2 && !wait_one<true>(bar(CB_S_EMPTY + (t & 1)), ((t >> 1) - 1) & 1, wc, kSiteCkScores)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int d = 0; d < 9; ++d, ++seq) {
+          const uint32_t s = seq % kCkSlots, src = base + CK_RING + s * kCkSlot;
+          if (!wait_one<true>(bar(CB_FULL + s), (seq / kCkSlots) & 1, wc, kSiteCkRing)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma2_bf16_ss(tmem + CT_S + 128 * (t & 1), smem_desc(base + CK_Q + d * kCkBlk + 32 * k, 16, 1024, kSwizzle128B),
+                         smem_desc(src + 32 * k, 16, 1024, kSwizzle128B), id_qk, (d | k) ? 1u : 0u);
+          mma2_commit_both(bar(CB_EMPTY + s));
+        }
+        mma2_commit_both(bar(CB_S_FULL + (t & 1)));
+        if (r.last) mma2_commit_both(bar(CB_Q_EMPTY));
+        return true;
+      };
+      auto pv = [&](const ChunkTileRef& r, uint32_t t) -> bool {
+        if (!wait_one<true>(bar(CB_P_FULL), t & 1, wc, kSiteCkP)) return false;
+        tc_fence_after();
+        const int np = r.pages();
+#pragma unroll 1
+        for (int kb = 0; kb < np; ++kb) {
+          const int steps = (min(r.vis - kChunkTile * r.tile - 64 * kb, 64) + 15) >> 4;
+#pragma unroll 1
+          for (int n = 0; n < 2; ++n, ++seq) {
+            const uint32_t s = seq % kCkSlots, src = base + CK_RING + s * kCkSlot;
+            if (!wait_one<true>(bar(CB_FULL + s), (seq / kCkSlots) & 1, wc, kSiteCkRing)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < steps)
+                mma2_bf16_ss(tmem + CT_O + 128 * n, smem_desc(base + CK_P + kb * kCkBlk + 32 * k, 16, 1024, kSwizzle128B),
+                             smem_desc(src + k * 2048, kCkBlk, 1024, kSwizzle128B), id_pv,
+                             (!r.first || kb > 0 || k > 0) ? 1u : 0u);
+            mma2_commit_both(bar(CB_EMPTY + s));
+          }
+        }
+        mma2_commit_both(bar(CB_P_FREE));
+        return true;
+      };
+      ChunkTileRef a, b;
+      cur.next(a);
+      bool ok = qk(a, 0);
+      while (ok) {
+        const bool more = cur.next(b);
+        if (more && !(ok = qk(b, g + 1))) break;
+        if (!(ok = pv(a, g)) || !more) break;
+        a = b;
+        ++g;
+      }
+      // no MMA may still run, and no copy may still land, when the pair leaves
+      mma2_commit_both(bar(CB_DRAIN));
+      WaitCtx wd = wc;
+      wd.timeout_ns = 100000000ull;
+      volatile int no_abort = 0;
+      wd.abort_local = &no_abort;
+      wd.abort_peer = 0;
+      wait_one<true>(bar(CB_DRAIN), 0, wd, kSiteCkDrain);
+    }
+  } else if (warp == 7) {
+    // ================================================================ query copies
+    if (lane == 0) {
+      ChunkTileRef r;
+      uint32_t piece = 0;
+      const uint32_t full = lead0 + 8 * CB_Q_FULL;
+      while (cur.next(r)) {
+        if (!r.first) continue;
+        if (piece > 0 && !wait_one<true>(bar(CB_Q_EMPTY), (piece - 1) & 1, wc, kSiteCkQ)) break;
+        const int row = r.b.tok0 * args.H + 64 * (int)rank;
+        mbar_arrive_expect_tx_remote(full, 9 * kCkBlk);
+        for (int d = 0; d < 8; ++d) tma2_load_2d(base + CK_Q + d * kCkBlk, &args.map_q, full, 64 * d, row);
+        tma2_load_2d(base + CK_Q + 8 * kCkBlk, &args.map_qr, full, 0, row);
+        ++piece;
+      }
+    }
+  } else {
+    // ================================================================ softmax
+    const int w = (warp - 8) >> 2, quarter = warp & 3;
+    const int L = 32 * quarter + lane, row = L & 63, hi = L >> 6;
+    const int part = 2 * hi + w;                     // this thread's keys of a tile: [64 part, 64 part + 64)
+    const int r = 64 * (int)rank + row;              // row of the block
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+    const uint32_t prow = base + CK_P + part * kCkBlk + row * 128;
+    float* red = reinterpret_cast<float*>(smem + CK_RED);
+    float* sums = reinterpret_cast<float*>(smem + CK_SUM);
+    const float sl2 = args.scale_log2;
+    const int col0 = 256 * w + 128 * hi;             // output dims [col0, col0 + 128)
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+
+    // O / l of a finished piece -> its rows of out, or a split partial
+    uint32_t pieces = 0;
+    auto epilogue = [&](const ChunkTileRef& e) -> bool {
+      sums[part * 64 + row] = l_run;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(CB_SUM));
+      if (!wait_warp(bar(CB_SUM), pieces & 1, wc, kSiteCkRed)) return false;
+      ++pieces;
+      const float l = sums[row] + sums[64 + row] + sums[128 + row] + sums[192 + row];
+      const bool store = r < e.b.ntok * args.H, split = e.b.splits > 1;
+      const float inv = 1.f / l;
+      const int64_t slot_row = (int64_t)(e.b.offset + e.split) * kChunkRows + r;
+      const int64_t q_row = (int64_t)e.b.tok0 * args.H + r;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tmem + lane_off + CT_O + 128 * w + 32 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)  // (a row that saw no key: zeros, whatever the accumulator holds)
+          v[j] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(v[j]) * inv);
+        if (!store) continue;
+        if (split) {
+          float4* dst = reinterpret_cast<float4*>(args.o_acc + slot_row * 512 + col0 + 32 * c);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
+                                 __uint_as_float(v[4 * q + 3]));
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(args.out + q_row * 512 + col0 + 32 * c);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* u = v + 8 * q;
+            dst[q] = make_uint4(pack_bf16(__uint_as_float(u[0]), __uint_as_float(u[1])),
+                                pack_bf16(__uint_as_float(u[2]), __uint_as_float(u[3])),
+                                pack_bf16(__uint_as_float(u[4]), __uint_as_float(u[5])),
+                                pack_bf16(__uint_as_float(u[6]), __uint_as_float(u[7])));
+          }
+        }
+      }
+      if (store && part == 0) {
+        const float lse = l == 0.f ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994530942f;
+        if (split) args.lse_acc[slot_row] = lse; else args.lse[q_row] = lse;
+      }
+      return true;
+    };
+
+    ChunkTileRef a, prev;
+    int lim = 0, some = 0;
+    bool pend = false;
+    uint32_t g = 0;
+    for (; ok && cur.next(a); ++g) {
+      if (a.first) {
+        const int j = r / args.H;  // this row's token of the block
+        lim = j < a.b.ntok ? chunk_visible(a.b, j, args.causal) : 0;
+        some = chunk_visible(a.b, 0, args.causal);
+      }
+      const uint32_t sb = g & 1;
+      if (!(ok = wait_warp<true>(bar(CB_S_FULL + sb), (g >> 1) & 1, wc, kSiteCkScores))) break;
+      tc_fence_after();
+      uint32_t sv[64];
+      tmem_ld32(tmem + lane_off + CT_S + 128 * sb + 64 * w, *reinterpret_cast<uint32_t(*)[32]>(sv));
+      tmem_ld32(tmem + lane_off + CT_S + 128 * sb + 64 * w + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(lead0 + 8 * (CB_S_EMPTY + sb));
+      if (kChunkTile * (a.tile + 1) > some || r >= a.b.ntok * args.H) {
+        // keys this row sees of the thread's 64; a seen score of -inf comes of a key that is not
+        // finite (and whose value row was zeroed): the row becomes NaN
+        const int nv = lim - (kChunkTile * a.tile + 64 * part);
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          sv[j] = j < nv ? (sv[j] == 0xFF800000u ? 0x7FC00000u : sv[j]) : 0xFF800000u;
+      }
+      float mt;
+      {
+        float c[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[q] = fmaxf(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1]));
+#pragma unroll
+        for (int j = 8; j < 64; j += 2)
+          c[(j >> 1) & 3] = fmax3(c[(j >> 1) & 3], __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
+        mt = fmax3(c[0], c[1], fmaxf(c[2], c[3]));
+      }
+      red[(sb * 4 + part) * 64 + row] = mt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(CB_RED + sb));
+      if (!(ok = wait_warp(bar(CB_RED + sb), (g >> 1) & 1, wc, kSiteCkRed))) break;
+      const float* rr = red + sb * 256 + row;
+      const float cm = fmax3(rr[0], rr[64], fmaxf(rr[128], rr[192])) * sl2;  // log2 units (sl2 > 0)
+      const float m_old = a.first ? -INFINITY : m_run;
+      const bool grow = cm > m_old + 8.f;  // also the first keys that the row sees
+      const float m_new = grow ? cm : m_old;
+      const float alpha = grow ? exp2f(m_old - cm) : 1.f;
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      uint32_t pp[32];
+      float ls;
+      {
+        const uint64_t s2 = splat_f32x2(sl2), nm = splat_f32x2(-m_use);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float x0, x1;
+          unpack_f32x2(ffma_f32x2(pack_b32x2(sv[2 * j], sv[2 * j + 1]), s2, nm), x0, x1);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          pp[j] = pack_bf16(p0, p1);
+          acc[j & 3] = fadd_f32x2(acc[j & 3], pack_f32x2(p0, p1));
+        }
+        float z0, z1;
+        unpack_f32x2(fadd_f32x2(fadd_f32x2(acc[0], acc[1]), fadd_f32x2(acc[2], acc[3])), z0, z1);
+        ls = z0 + z1;
+      }
+      // PV of the tile before is done: P may be overwritten, O read and rescaled
+      if (g > 0 && !(ok = wait_warp<true>(bar(CB_P_FREE), (g - 1) & 1, wc, kSiteCkPv))) break;
+      tc_fence_after();
+      if (pend && !(ok = epilogue(prev))) break;  // (m_run, l_run still those of the finished piece)
+      pend = false;
+      if (!a.first && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_off + CT_O + 128 * w + 32 * c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+          tmem_st32(tmem + lane_off + CT_O + 128 * w + 32 * c, v);
+        }
+        tmem_wait_st();
+      }
+      l_run = (a.first ? 0.f : l_run * alpha) + ls;
+      m_run = m_new;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(prow + ((uint32_t)(c ^ (row & 7)) << 4)), "r"(pp[4 * c]),
+                     "r"(pp[4 * c + 1]), "r"(pp[4 * c + 2]), "r"(pp[4 * c + 3])
+                     : "memory");
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(lead0 + 8 * CB_P_FULL);
+      if (a.last) {
+        pend = true;
+        prev = a;
+      }
+    }
+    if (ok && pend && (ok = wait_warp<true>(bar(CB_P_FREE), (g - 1) & 1, wc, kSiteCkPv))) {
+      tc_fence_after();
+      epilogue(prev);
+    }
+    tc_fence_before();
+  }
+
+  // ---------------------------------------------------------------- teardown
+  __syncwarp();
+  __syncthreads();
+  if (*abort_flag) drain_delay(200000);  // in-flight copies and MMAs land before release
+  cluster_sync();
+  if (warp == 6) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// ----------------------------------------------------------------- merge of split blocks
+// out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  grid (U, 8 groups of 16
+// rows, 4 slices of 128 dims): 16 threads a row, 8 dims each, four splits in flight.
+__global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, int U, int capacity, int batch, int H,
+                                                                const float* o_acc, const float* lse_acc,
+                                                                __nv_bfloat16* out, float* lse) {
+  pdl_wait_prerequisites();
+  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity ||
+      (int)blockIdx.x >= sched[kChNumSplit])
+    return;
+  const ChunkLayout lay = chunk_layout(U, capacity, batch);
+  const ChunkBlock b = reinterpret_cast<const ChunkBlock*>(sched + lay.blocks)[sched[lay.split_list + blockIdx.x]];
+  const int row = blockIdx.y * 16 + (threadIdx.x >> 4), sub = threadIdx.x & 15;
+  if (row >= b.ntok * H) return;  // (whole groups of 16 lanes)
+  const float* lsrc = lse_acc + (int64_t)b.offset * kChunkRows + row;
+  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
+  float M = -INFINITY, S = 0.f;
+  bool nan = false;  // a partial of NaN keys: the maximum would not show it
+  for (int i = sub; i < b.splits; i += 16) {
+    const float x = lsrc[(int64_t)i * kChunkRows];
+    nan |= isnan(x);
+    M = fmaxf(M, x);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(mask, M, o));
+  if (M > -INFINITY)
+    for (int i = sub; i < b.splits; i += 16) S += expf(lsrc[(int64_t)i * kChunkRows] - M);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) S += __shfl_xor_sync(mask, S, o);
+  nan = __any_sync(mask, nan);
+  const float Lt = nan ? NAN : M > -INFINITY ? M + logf(S) : -INFINITY;
+  const int c0 = 32 * blockIdx.z + sub;  // float4 columns c0 and c0 + 16
+  const float4* src = reinterpret_cast<const float4*>(o_acc) + ((int64_t)b.offset * kChunkRows + row) * 128 + c0;
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i0 = 0; i0 < b.splits; i0 += 4) {
+    float4 v[4][2];
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool in = i0 + k < b.splits;
+      x[k] = in ? lsrc[(int64_t)(i0 + k) * kChunkRows] : -INFINITY;
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+        v[k][f] = in ? __ldcs(src + (int64_t)(i0 + k) * kChunkRows * 128 + 16 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float wk = Lt == -INFINITY ? 0.f : expf(x[k] - Lt);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        acc[f].x += wk * v[k][f].x;
+        acc[f].y += wk * v[k][f].y;
+        acc[f].z += wk * v[k][f].z;
+        acc[f].w += wk * v[k][f].w;
+      }
+    }
+  }
+  const int64_t q_row = (int64_t)b.tok0 * H + row;
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+    *reinterpret_cast<uint2*>(out + q_row * 512 + 4 * (c0 + 16 * f)) =
+        make_uint2(pack_bf16(acc[f].x, acc[f].y), pack_bf16(acc[f].z, acc[f].w));
+  if (sub == 0 && blockIdx.z == 0) lse[q_row] = Lt;
+}
+
+// ----------------------------------------------------------------- FP8 rows -> bf16 rows
+// The pages of the sequences that have new tokens, expanded once per call into consecutive bf16
+// pages (sequence b's from page_off[b]): value = bf16(code x scale), RoPE copied.  A chunk's rows
+// read every cached row many times over, so 1808 bytes of traffic a cached token stand against
+// 278,528 FLOP per new token at 128 heads.  A warp takes a row: lane l the codes [16 l, 16 l + 16).
+__global__ void __launch_bounds__(256) mla_chunk_expand_kernel(const int32_t* sched, int U, int capacity, int batch,
+                                                               const uint8_t* pages, const int32_t* block_table,
+                                                               int max_pages, int num_pages, const int32_t* lens,
+                                                               __nv_bfloat16* rows) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity) return;
+  const ChunkLayout lay = chunk_layout(U, capacity, batch);
+  const int32_t* page_off = sched + lay.page_off;
+  const int total = sched[kChPages], warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int pg = blockIdx.x; pg < total; pg += gridDim.x) {
+    const int b = chunk_find(page_off, batch, pg), lp = pg - page_off[b];
+    int page = block_table[(int64_t)b * max_pages + lp];
+    if (page < 0 || page >= num_pages) {
+      if (threadIdx.x == 0) atomicCAS(&g_mla_error, 0, 1);
+      page = 0;
+    }
+    const int n = min(lens[b] - 64 * lp, 64);  // rows past the sequence's end are not expanded
+#pragma unroll 4
+    for (int r = warp; r < n; r += 8) {
+      const uint8_t* src = pages + ((int64_t)page * 64 + r) * 656;
+      __nv_bfloat16* dst = rows + ((int64_t)pg * 64 + r) * 576;
+      const uint4 c = *reinterpret_cast<const uint4*>(src + 16 * lane);
+      const float s = *reinterpret_cast<const float*>(src + 512 + 4 * (lane >> 3));
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[q >> 1] >> (16 * (q & 1)));
+        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3));  // exact
+        const float2 f = __half22float2(h);
+        o[q] = pack_bf16(f.x * s, f.y * s);
+      }
+      uint4* d = reinterpret_cast<uint4*>(dst + 16 * lane);
+      d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      if (lane < 8) *reinterpret_cast<uint4*>(dst + 512 + 8 * lane) = *reinterpret_cast<const uint4*>(src + 528 + 16 * lane);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- scheduler
+// Exclusive prefix sum over the 1024 threads of a CTA; total of all threads in *sum.
+__device__ __forceinline__ int64_t block_scan_1024(int64_t v, int64_t* sh, int64_t* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // (sh may still be read from the scan before)
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t s = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    sh[lane] = s;
+  }
+  __syncthreads();
+  *sum = sh[31];
+  return x - v + (warp > 0 ? sh[warp - 1] : 0);
+}
+
+// One CTA of 1024 threads; the phases of chunk_plan_host with the sums in parallel.
+__global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu, const int32_t* lens, int B,
+                                                               int64_t max_tokens, int H, int causal, int max_pages,
+                                                               int64_t max_kv_pages, int U, int64_t cap, int32_t* sched) {
+  __shared__ int64_t sh[32];
+  __shared__ int bad;
+  const int tid = threadIdx.x, tb = chunk_tokens_per_block(H);
+  const ChunkLayout l = chunk_layout(U, cap, B);
+  ChunkBlock* blocks = reinterpret_cast<ChunkBlock*>(sched + l.blocks);
+  int32_t *page_off = sched + l.page_off, *blk_off = sched + l.blk_off, *pos = sched + l.pos;
+  if (tid == 0) bad = cu[0] != 0;
+  if (tid < kChunkHeader) sched[tid] = 0;
+  __syncthreads();
+  for (int b = tid; b < B; b += 1024)
+    if (!chunk_sequence_ok(cu[b], cu[b + 1], lens[b], max_tokens, max_pages)) bad = 1;
+  __syncthreads();
+  auto refuse = [&]() {  // (the header without the magic word stands)
+    if (tid == 0) atomicCAS(&g_mla_error, 0, 1);
+  };
+  if (bad) return refuse();
+  int64_t pages = 0, nb = 0, sum;
+  for (int b0 = 0; b0 < B; b0 += 1024) {
+    const int b = b0 + tid;
+    const int32_t n = b < B ? cu[b + 1] - cu[b] : 0;
+    const int64_t pe = block_scan_1024(n > 0 ? num_tiles(lens[b]) : 0, sh, &sum);
+    if (b < B) page_off[b] = (int32_t)(pages + pe);
+    pages += sum;
+    const int64_t be = block_scan_1024(chunk_seq_blocks(n, tb), sh, &sum);
+    if (b < B) blk_off[b] = (int32_t)(nb + be);
+    nb += sum;
+  }
+  if (pages > max_kv_pages) return refuse();
+  if (tid == 0) {
+    page_off[B] = (int32_t)pages;
+    blk_off[B] = (int32_t)nb;
+  }
+  __syncthreads();
+  int64_t total = 0;
+  for (int64_t k0 = 0; k0 < nb; k0 += 1024) {
+    const int64_t k = k0 + tid;
+    int32_t cost = 0;
+    if (k < nb) {
+      const int b = chunk_find(blk_off, B, (int32_t)k);
+      blocks[k] = chunk_make_block(cu, lens, b, (int)k, blk_off[b], tb, causal);
+      cost = blocks[k].nt + kChunkPieceCost;
+    }
+    const int64_t e = block_scan_1024(cost, sh, &sum);
+    if (k < nb) pos[k] = (int32_t)(total + e);
+    total += sum;
+  }
+  if (total > kMaxPlanPositions) return refuse();
+  __syncthreads();
+  const int64_t budget = plan_budget(total, U);
+  for (int u = tid; u < U; u += 1024) chunk_unit(blocks, pos, (int)nb, total, budget, u, sched + l.units + kUnitInts * u);
+  int64_t slots = 0, ns = 0;
+  __syncthreads();  // (the units read the records that the next phase completes)
+  for (int64_t k0 = 0; k0 < nb; k0 += 1024) {
+    const int64_t k = k0 + tid;
+    const int32_t s = k < nb ? chunk_splits(pos[k], blocks[k].nt, budget) : 0;
+    const int64_t oe = block_scan_1024(s > 1 ? s : 0, sh, &sum);
+    const int64_t o = slots + oe;
+    slots += sum;
+    const int64_t le = block_scan_1024(s > 1 ? 1 : 0, sh, &sum);
+    if (k < nb) {
+      blocks[k].splits = s;
+      blocks[k].offset = (int32_t)o;
+      if (s > 1) sched[l.split_list + ns + le] = (int32_t)k;
+    }
+    ns += sum;
+  }
+  if (tid == 0) {
+    sched[kChUnits] = U;
+    sched[kChCapacity] = (int32_t)cap;
+    sched[kChBlocks] = (int32_t)nb;
+    sched[kChSlots] = (int32_t)slots;
+    sched[kChBudget] = (int32_t)budget;
+    sched[kChTokens] = tb;
+    sched[kChNumSplit] = (int32_t)ns;
+    sched[kChPages] = (int32_t)pages;
+    sched[kChMagic] = kChunkMagic;
+  }
+}
+
+}  // namespace mla

@@ -1,0 +1,204 @@
+// Planner of the chunk attention: ragged new tokens -> blocks of rows -> stretches of work for
+// the units (CTA pairs).
+//
+// A block is up to 128 rows of the flattened [token][head] order of one sequence: 128 / H whole
+// tokens, so with few heads several tokens share every key tile.  A block's tiles are 256 keys
+// each, up to what its last token sees; a block that sees nothing keeps one (fully masked) tile,
+// which writes its zero rows.  Blocks lie one after another on a line of cost positions
+// (kChunkPieceCost, then one per tile) and unit u owns the tiles in [u * budget, (u + 1) * budget):
+// long sequences are split over units ("MLA inference: two computation paths and FlashMLA",
+// section "Decode attention becomes a compute problem") and merged by their LSE.
+//
+// The per-item functions are shared by the scheduler kernel (which runs the prefix sums in
+// parallel) and the host twin.
+#pragma once
+#include <cstdint>
+
+#include "plan.h"
+
+namespace mla {
+
+constexpr int32_t kChunkMagic = 0x4D4C4143;  // "MLAC"
+constexpr int kChunkHeader = 16;              // int32 header words
+constexpr int kChunkBlockInts = 8;            // int32 words per block record
+constexpr int kChunkRows = 128;               // rows of a block (MMA M of a CTA pair)
+constexpr int kChunkTile = 256;               // keys of a tile (four pages)
+// Cost of a piece beyond its tiles, in tiles: the query load, the epilogue, the pipeline's refill.
+#ifndef MLA_CHUNK_PIECE_COST
+#define MLA_CHUNK_PIECE_COST 1
+#endif
+constexpr int kChunkPieceCost = MLA_CHUNK_PIECE_COST;
+
+// header words
+enum { kChMagic = 0, kChUnits, kChCapacity, kChBlocks, kChSlots, kChBudget, kChTokens, kChNumSplit, kChPages };
+
+// Block record.
+struct ChunkBlock {
+  int32_t tok0;    // first token (row of q / H)
+  int32_t ntok;    // tokens of this block
+  int32_t seq;
+  int32_t base;    // keys the first token sees under the causal rule, before clipping to [0, L]
+  int32_t len;     // L of the sequence
+  int32_t nt;      // tiles
+  int32_t splits;  // units its tiles span
+  int32_t offset;  // first partial slot (splits > 1)
+};
+
+struct ChunkLayout {
+  int64_t units, blocks, split_list, page_off, blk_off, pos, total;  // int32 offsets into sched
+};
+
+MLA_HD inline int chunk_tokens_per_block(int H) { return H >= kChunkRows ? 1 : kChunkRows / H; }
+
+// Blocks that max_tokens tokens in at most `batch` sequences can make.
+MLA_HD inline int64_t chunk_block_capacity(int64_t max_tokens, int batch, int H) {
+  const int tb = chunk_tokens_per_block(H);
+  const int64_t partial = tb == 1 ? 0 : (batch < max_tokens ? batch : max_tokens);
+  const int64_t cap = max_tokens / tb + partial;
+  return cap < 1 ? 1 : cap;
+}
+
+MLA_HD inline ChunkLayout chunk_layout(int U, int64_t cap, int batch) {
+  ChunkLayout l;
+  l.units = kChunkHeader;
+  l.blocks = l.units + (int64_t)kUnitInts * U;
+  l.split_list = l.blocks + kChunkBlockInts * cap;
+  l.page_off = l.split_list + U;
+  l.blk_off = l.page_off + batch + 1;
+  l.pos = l.blk_off + batch + 1;
+  l.total = l.pos + cap;
+  return l;
+}
+
+// Keys token j of a block sees.
+MLA_HD inline int32_t chunk_visible(const ChunkBlock& b, int j, int causal) {
+  int32_t v = causal ? b.base + j : b.len;
+  if (v > b.len) v = b.len;
+  return v < 0 ? 0 : v;
+}
+
+// Lengths a plan accepts: new tokens in order within the buffer, rows within the block table.
+MLA_HD inline bool chunk_sequence_ok(int32_t lo, int32_t hi, int32_t L, int64_t max_tokens, int max_pages) {
+  return lo >= 0 && hi >= lo && hi <= max_tokens && L >= 0 && (int64_t)L <= (int64_t)max_pages * 64;
+}
+
+MLA_HD inline int32_t chunk_seq_blocks(int32_t n, int tb) { return (n + tb - 1) / tb; }
+
+// Block `blk` of sequence `b`, whose blocks start at first_blk.
+MLA_HD inline ChunkBlock chunk_make_block(const int32_t* cu, const int32_t* lens, int b, int blk, int first_blk, int tb,
+                                          int causal) {
+  ChunkBlock k;
+  const int32_t n = cu[b + 1] - cu[b], i0 = (blk - first_blk) * tb;
+  k.tok0 = cu[b] + i0;
+  k.ntok = n - i0 < tb ? n - i0 : tb;
+  k.seq = b;
+  k.len = lens[b];
+  k.base = k.len - n + i0 + 1;  // token i of n sees keys 0 .. L - n + i
+  const int32_t nt = (chunk_visible(k, k.ntok - 1, causal) + kChunkTile - 1) / kChunkTile;
+  k.nt = nt > 0 ? nt : 1;
+  k.splits = k.offset = 0;
+  return k;
+}
+
+// The sequence that holds block blk: the last b with blk_off[b] <= blk (sequences without new
+// tokens hold none).
+MLA_HD inline int chunk_find(const int32_t* off, int n, int32_t v) {
+  int a = 0, b = n;
+  while (b - a > 1) {
+    const int m = (a + b) / 2;
+    if (off[m] <= v) a = m; else b = m;
+  }
+  return a;
+}
+
+// Unit u's record {first block, first tile, last block, end tile, split index of the first piece}.
+MLA_HD inline void chunk_unit(const ChunkBlock* blocks, const int32_t* pos, int NB, int64_t total, int64_t budget, int u,
+                              int32_t* rec) {
+  rec[0] = -1;
+  for (int i = 1; i < kUnitInts; ++i) rec[i] = 0;
+  const int64_t lo = (int64_t)u * budget, hi = lo + budget;
+  if (lo >= total || NB == 0) return;
+  int a = 0, b = NB;  // first block whose last tile lies at or past lo
+  while (a < b) {
+    const int m = (a + b) / 2;
+    if ((int64_t)pos[m] + kChunkPieceCost + blocks[m].nt - 1 >= lo) b = m; else a = m + 1;
+  }
+  if (a >= NB) return;
+  const int64_t first0 = (int64_t)pos[a] + kChunkPieceCost;
+  if (first0 >= hi) return;  // the stretch holds overhead positions only
+  int c = a, d = NB;  // last block whose first tile lies before hi
+  while (d - c > 1) {
+    const int m = (c + d) / 2;
+    if ((int64_t)pos[m] + kChunkPieceCost < hi) c = m; else d = m;
+  }
+  int64_t end = hi - ((int64_t)pos[c] + kChunkPieceCost);
+  if (end > blocks[c].nt) end = blocks[c].nt;
+  rec[0] = a;
+  rec[1] = (int32_t)(lo > first0 ? lo - first0 : 0);
+  rec[2] = c;
+  rec[3] = (int32_t)end;
+  rec[4] = (int32_t)(u - first0 / budget);
+}
+
+MLA_HD inline int32_t chunk_splits(int32_t pos, int32_t nt, int64_t budget) {
+  const int64_t first = (int64_t)pos + kChunkPieceCost;
+  return (int32_t)((first + nt - 1) / budget - first / budget + 1);
+}
+
+// Host twin: writes sched as the scheduler kernel does; false (and a header without the magic
+// word) where the lengths are refused.
+inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64_t max_tokens, int H, int causal,
+                            int max_pages, int64_t max_kv_pages, int U, int32_t* sched) {
+  const int tb = chunk_tokens_per_block(H);
+  const int64_t cap = chunk_block_capacity(max_tokens, B, H);
+  const ChunkLayout l = chunk_layout(U, cap, B);
+  for (int i = 0; i < kChunkHeader; ++i) sched[i] = 0;
+  ChunkBlock* blocks = reinterpret_cast<ChunkBlock*>(sched + l.blocks);
+  int32_t *page_off = sched + l.page_off, *blk_off = sched + l.blk_off, *pos = sched + l.pos;
+  int64_t pages = 0, nb = 0;
+  bool ok = cu[0] == 0;
+  for (int b = 0; b < B && ok; ++b) {
+    ok = chunk_sequence_ok(cu[b], cu[b + 1], lens[b], max_tokens, max_pages);
+    page_off[b] = (int32_t)pages;
+    blk_off[b] = (int32_t)nb;
+    if (!ok) break;
+    const int32_t n = cu[b + 1] - cu[b];
+    nb += chunk_seq_blocks(n, tb);
+    if (n > 0) pages += num_tiles(lens[b]);
+    ok = pages <= max_kv_pages;
+  }
+  if (!ok) return false;
+  page_off[B] = (int32_t)pages;
+  blk_off[B] = (int32_t)nb;
+  int64_t total = 0;
+  for (int k = 0; k < nb; ++k) {
+    const int b = chunk_find(blk_off, B, k);
+    blocks[k] = chunk_make_block(cu, lens, b, k, blk_off[b], tb, causal);
+    pos[k] = (int32_t)total;
+    total += blocks[k].nt + kChunkPieceCost;
+  }
+  if (total > kMaxPlanPositions) return false;
+  const int64_t budget = plan_budget(total, U);
+  for (int u = 0; u < U; ++u) chunk_unit(blocks, pos, (int)nb, total, budget, u, sched + l.units + kUnitInts * u);
+  int32_t slots = 0, ns = 0;
+  for (int k = 0; k < nb; ++k) {
+    blocks[k].splits = chunk_splits(pos[k], blocks[k].nt, budget);
+    blocks[k].offset = slots;
+    if (blocks[k].splits > 1) {
+      slots += blocks[k].splits;
+      sched[l.split_list + ns++] = k;
+    }
+  }
+  sched[kChMagic] = kChunkMagic;
+  sched[kChUnits] = U;
+  sched[kChCapacity] = (int32_t)cap;
+  sched[kChBlocks] = (int32_t)nb;
+  sched[kChSlots] = slots;
+  sched[kChBudget] = (int32_t)budget;
+  sched[kChTokens] = tb;
+  sched[kChNumSplit] = ns;
+  sched[kChPages] = (int32_t)pages;
+  return true;
+}
+
+}  // namespace mla

@@ -15,6 +15,8 @@
 #include "decode_kernel.cuh"
 #include "head_gemm.cuh"
 #include "extend_kernel.cuh"
+#include "chunk_kernel.cuh"
+#include "pages.cuh"
 
 namespace mla {
 
@@ -171,30 +173,10 @@ __global__ void __launch_bounds__(256) mla_quantize_fp8_kernel(const __nv_bfloat
   const __nv_bfloat16* src = lat + tok * lat_stride;
   const __nv_bfloat16* src_r = rope + tok * rope_stride;
   uint8_t* dst = out + tok * 656;
-  float x[16];
-  {
-    const uint4 a = *reinterpret_cast<const uint4*>(src + 16 * lane);
-    const uint4 b = *reinterpret_cast<const uint4*>(src + 16 * lane + 8);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float scale = amax > 0.f ? amax / 448.f : 1.f;
-  uint32_t codes[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float y = fminf(fmaxf(x[i] / scale, -448.f), 448.f);
-    const uint32_t c = (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-    codes[i >> 2] |= c << (8 * (i & 3));
-  }
+  float x[16], scale;
+  uint32_t codes[4];
+  widen16(*reinterpret_cast<const uint4*>(src + 16 * lane), *reinterpret_cast<const uint4*>(src + 16 * lane + 8), x);
+  quantize_tile16<false>(x, codes, scale);
   *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
   if ((lane & 7) == 0) *reinterpret_cast<float*>(dst + 512 + 4 * (lane >> 3)) = scale;
   if (lane < 8) *reinterpret_cast<uint4*>(dst + 528 + 16 * lane) = *reinterpret_cast<const uint4*>(src_r + 8 * lane);
@@ -998,3 +980,5 @@ extern "C" int32_t mla_decode_noalloc(const mla_decode_params* p, const void* q_
   return mla_decode(p, q_nope_absorbed, q_rope, kv_pages, block_table, cache_seqlens, scale, out, lse, sched,
                     workspace, stream);
 }
+
+#include "cache_api.cuh"
