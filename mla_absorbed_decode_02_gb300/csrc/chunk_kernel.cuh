@@ -130,6 +130,20 @@ __device__ __forceinline__ void mma2_commit_both(uint32_t bar) {
       : "memory");
 }
 
+// One lane of a converged warp.  The issuing roles below run converged, with one lane's predicate on
+// the instruction alone: descriptors and addresses then stay in uniform registers.  (One lane in a
+// branch of its own instead: 12,100 cycles a tile for the MMAs' issue alone, against 4352 of MMA time.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+// Bounded wait by a converged warp.
+__device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
+  return wait_warp<true>(bar, parity, w, site);
+}
+
 // One tile of a unit's work.
 struct ChunkTileRef {
   ChunkBlock b;
@@ -350,53 +364,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     }
   } else if (warp == 6) {
     // ================================================================ MMAs
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t id_qk = idesc_bf16_f32(128, 256, 0, 0), id_pv = idesc_bf16_f32(128, 256, 0, 1);
-      uint32_t seq = 0, g = 0, piece = 0;
+      // descriptors: an address 16 n bytes further is n more in the low word
+      const uint64_t desc_q = smem_desc(base + CK_Q, 16, 1024, kSwizzle128B), desc_p = smem_desc(base + CK_P, 16, 1024, kSwizzle128B);
+      const uint64_t desc_k = smem_desc(base + CK_RING, 16, 1024, kSwizzle128B);
+      const uint64_t desc_v = smem_desc(base + CK_RING, kCkBlk, 1024, kSwizzle128B);
+      const bool el = elect_one();
+      uint32_t slot = 0, phase = 0, g = 0, piece = 0;
+      auto advance = [&]() {
+        if (++slot == kCkSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
       auto qk = [&](const ChunkTileRef& r, uint32_t t) -> bool {
         if (r.first) {
-          if (!wait_one<true>(bar(CB_Q_FULL), piece & 1, wc, kSiteCkQ)) return false;
+          if (!wait_uniform(bar(CB_Q_FULL), piece & 1, wc, kSiteCkQ)) return false;
           ++piece;
         }
-        if (t >= 2 && !wait_one<true>(bar(CB_S_EMPTY + (t & 1)), ((t >> 1) - 1) & 1, wc, kSiteCkScores)) return false;
-        tc_fence_after();
+        if (t >= 2 && !wait_uniform(bar(CB_S_EMPTY + (t & 1)), ((t >> 1) - 1) & 1, wc, kSiteCkScores)) return false;
+        const uint32_t d_tmem = tmem + CT_S + 128 * (t & 1);
 #pragma unroll 1
-        for (int d = 0; d < 9; ++d, ++seq) {
-          const uint32_t s = seq % kCkSlots, src = base + CK_RING + s * kCkSlot;
-          if (!wait_one<true>(bar(CB_FULL + s), (seq / kCkSlots) & 1, wc, kSiteCkRing)) return false;
+        for (int d = 0; d < 9; ++d) {
+          if (!wait_uniform(bar(CB_FULL + slot), phase, wc, kSiteCkRing)) return false;
           tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma2_bf16_ss(tmem + CT_S + 128 * (t & 1), smem_desc(base + CK_Q + d * kCkBlk + 32 * k, 16, 1024, kSwizzle128B),
-                         smem_desc(src + 32 * k, 16, 1024, kSwizzle128B), id_qk, (d | k) ? 1u : 0u);
-          mma2_commit_both(bar(CB_EMPTY + s));
+          const uint64_t da = desc_q + d * (kCkBlk >> 4), db = desc_k + slot * (kCkSlot >> 4);
+          if (el) {
+            mma2_bf16_ss(d_tmem, da, db, id_qk, d ? 1u : 0u);
+            mma2_bf16_ss(d_tmem, da + 2, db + 2, id_qk, 1u);
+            mma2_bf16_ss(d_tmem, da + 4, db + 4, id_qk, 1u);
+            mma2_bf16_ss(d_tmem, da + 6, db + 6, id_qk, 1u);
+            mma2_commit_both(bar(CB_EMPTY + slot));
+          }
+          __syncwarp();
+          advance();
         }
-        mma2_commit_both(bar(CB_S_FULL + (t & 1)));
-        if (r.last) mma2_commit_both(bar(CB_Q_EMPTY));
+        if (el) {
+          mma2_commit_both(bar(CB_S_FULL + (t & 1)));
+          if (r.last) mma2_commit_both(bar(CB_Q_EMPTY));
+        }
+        __syncwarp();
         return true;
       };
       auto pv = [&](const ChunkTileRef& r, uint32_t t) -> bool {
-        if (!wait_one<true>(bar(CB_P_FULL), t & 1, wc, kSiteCkP)) return false;
-        tc_fence_after();
+        if (!wait_uniform(bar(CB_P_FULL), t & 1, wc, kSiteCkP)) return false;
         const int np = r.pages();
 #pragma unroll 1
         for (int kb = 0; kb < np; ++kb) {
           const int steps = (min(r.vis - kChunkTile * r.tile - 64 * kb, 64) + 15) >> 4;
+          const uint32_t acc = !r.first || kb > 0 ? 1u : 0u;
+          const uint64_t da = desc_p + kb * (kCkBlk >> 4);
 #pragma unroll 1
-          for (int n = 0; n < 2; ++n, ++seq) {
-            const uint32_t s = seq % kCkSlots, src = base + CK_RING + s * kCkSlot;
-            if (!wait_one<true>(bar(CB_FULL + s), (seq / kCkSlots) & 1, wc, kSiteCkRing)) return false;
+          for (int n = 0; n < 2; ++n) {
+            if (!wait_uniform(bar(CB_FULL + slot), phase, wc, kSiteCkRing)) return false;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < steps)
-                mma2_bf16_ss(tmem + CT_O + 128 * n, smem_desc(base + CK_P + kb * kCkBlk + 32 * k, 16, 1024, kSwizzle128B),
-                             smem_desc(src + k * 2048, kCkBlk, 1024, kSwizzle128B), id_pv,
-                             (!r.first || kb > 0 || k > 0) ? 1u : 0u);
-            mma2_commit_both(bar(CB_EMPTY + s));
+            const uint32_t d_tmem = tmem + CT_O + 128 * n;
+            const uint64_t db = desc_v + slot * (kCkSlot >> 4);
+            if (el) {
+              mma2_bf16_ss(d_tmem, da, db, id_pv, acc);
+              if (steps > 1) mma2_bf16_ss(d_tmem, da + 2, db + 128, id_pv, 1u);
+              if (steps > 2) mma2_bf16_ss(d_tmem, da + 4, db + 256, id_pv, 1u);
+              if (steps > 3) mma2_bf16_ss(d_tmem, da + 6, db + 384, id_pv, 1u);
+              mma2_commit_both(bar(CB_EMPTY + slot));
+            }
+            __syncwarp();
+            advance();
           }
         }
-        mma2_commit_both(bar(CB_P_FREE));
+        if (el) mma2_commit_both(bar(CB_P_FREE));
+        __syncwarp();
         return true;
       };
       ChunkTileRef a, b;
@@ -410,13 +447,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
         ++g;
       }
       // no MMA may still run, and no copy may still land, when the pair leaves
-      mma2_commit_both(bar(CB_DRAIN));
+      if (el) mma2_commit_both(bar(CB_DRAIN));
+      __syncwarp();
       WaitCtx wd = wc;
       wd.timeout_ns = 100000000ull;
       volatile int no_abort = 0;
       wd.abort_local = &no_abort;
       wd.abort_peer = 0;
-      wait_one<true>(bar(CB_DRAIN), 0, wd, kSiteCkDrain);
+      wait_warp<true>(bar(CB_DRAIN), 0, wd, kSiteCkDrain);
     }
   } else if (warp == 7) {
     // ================================================================ query copies
