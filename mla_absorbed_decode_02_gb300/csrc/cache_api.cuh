@@ -187,12 +187,12 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
   const uint64_t q_rows = (uint64_t)p->max_tokens * p->num_heads;
   const uint64_t kv_rows = fp8 ? (uint64_t)(p->max_kv_tokens / 64) * 64 : (uint64_t)p->num_pages * 64;
   const void* kv = fp8 ? rows : kv_pages;
-  const uint32_t box2[2] = {64, 64}, box3[3] = {64, 64, 2};
+  const uint32_t box2[2] = {64, 64}, box3[3] = {64, 64, 2}, boxq[3] = {64, 64, 8};
   {
-    const uint64_t dq[2] = {512, q_rows}, sq[1] = {1024}, dr[2] = {64, q_rows}, sr[1] = {128};
+    const uint64_t dq[3] = {64, q_rows, 8}, sq[2] = {1024, 128}, dr[2] = {64, q_rows}, sr[1] = {128};
     const uint64_t dk[2] = {576, kv_rows}, sk[1] = {1152}, dv[3] = {64, kv_rows, 9}, sv[2] = {1152, 128};
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if ((st = encode_map(&a.map_q, bf, 2, q_nope_absorbed, dq, sq, box2, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+    if ((st = encode_map(&a.map_q, bf, 3, q_nope_absorbed, dq, sq, boxq, CU_TENSOR_MAP_SWIZZLE_128B)) ||
         (st = encode_map(&a.map_qr, bf, 2, q_rope, dr, sr, box2, CU_TENSOR_MAP_SWIZZLE_128B)) ||
         (st = encode_map(&a.map_k, bf, 2, kv, dk, sk, box2, CU_TENSOR_MAP_SWIZZLE_128B)) ||
         (st = encode_map(&a.map_v, bf, 3, kv, dv, sv, box3, CU_TENSOR_MAP_SWIZZLE_128B)))

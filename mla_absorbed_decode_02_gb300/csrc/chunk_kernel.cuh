@@ -17,8 +17,8 @@
 //
 // The MMAs take half of each B operand from either CTA: QK wants 128 keys x 576 dims per CTA (two
 // of the tile's four pages), PV all 256 keys x 128 dims of every 256.  Both stream through one
-// ring of seven 16 KB slots (K: 128 keys x 64 dims; V: 64 keys x 128 dims), 17 slots a tile.  One
-// thread issues a TMA copy every ~0.3 us whatever its size, so six warps share the copies.
+// ring of seven 16 KB slots (K: 128 keys x 64 dims; V: 64 keys x 128 dims), 17 slots a tile.  A
+// warp issues a TMA copy every ~0.18 us whatever its size, so six warps share the copies.
 //
 // Roles (512 threads a CTA): warps 0..5 copy pages, warp 6 issues the MMAs of the pair (first CTA
 // only), warp 7 copies queries, warps 8..15 (two warpgroups, half of a tile's score columns each)
@@ -77,7 +77,7 @@ constexpr uint32_t CT_S = 0, CT_O = 256;  // S buffers at 0 and 128
 enum ChunkSite : int { kSiteCkRing = 32, kSiteCkRaw, kSiteCkQ, kSiteCkScores, kSiteCkP, kSiteCkPv, kSiteCkRed, kSiteCkDrain };
 
 struct ChunkArgs {
-  CUtensorMap map_q;    // q~ rows: bf16 {512, T * H}, box {64, 64}, 128-byte swizzle
+  CUtensorMap map_q;    // q~ rows: bf16 {64, T * H, 8 blocks 128 bytes apart}, box {64, 64, 8}, 128-byte swizzle
   CUtensorMap map_qr;   // q^R rows: bf16 {64, T * H}, box {64, 64}
   CUtensorMap map_k;    // cache rows: bf16 {576, pages * 64}, box {64, 64}
   CUtensorMap map_v;    // the same rows as {64, pages * 64, 9 blocks 128 bytes apart}, box {64, 64, 2}
@@ -109,8 +109,10 @@ __device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* ma
       "l"(map), "r"(mbar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// (relaxed: the copies themselves order their bytes; a release arrive on the other CTA's barrier waits
+// for this thread's earlier writes, ~1400 cycles measured)
 __device__ __forceinline__ void mbar_arrive_expect_tx_remote(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void mma2_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -257,8 +259,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   } else if (warp < kCkCopyWarps) {
     // ================================================================ page copies
     const int32_t* page_off = sched + lay.page_off;
-    uint32_t seq = 0, n_raw = 0;
+    const bool el = elect_one();
+    // ring position (the waits of the first round pass: "the phase before" of a fresh barrier) and
+    // whose turn it is
+    uint32_t slot = 0, phase = 1, n_raw = 0;
+    int turn = 0;
     bool ok = true;
+    auto advance = [&]() {
+      if (++slot == kCkSlots) {
+        slot = 0;
+        phase ^= 1;
+      }
+      turn = turn == kCkCopyWarps - 1 ? 0 : turn + 1;
+    };
     // lane j < 4: physical page of the tile's page j
     auto page_of = [&](const ChunkTileRef& r) -> int {
       const int lp = 4 * r.tile + lane;
@@ -271,24 +284,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       }
       return page;
     };
-    auto claim = [&](uint32_t s) -> bool {  // slot s is free again
-      return s < kCkSlots || wait_warp<true>(bar(CB_EMPTY + s % kCkSlots), (s / kCkSlots - 1) & 1, wc, kSiteCkRing);
-    };
     auto copy_k = [&](const ChunkTileRef& r, int page) -> bool {
       const int np = min(max(r.pages() - 2 * (int)rank, 0), 2);
-      const int p0 = __shfl_sync(0xffffffffu, page, 2 * rank), p1 = __shfl_sync(0xffffffffu, page, 2 * rank + 1);
+      const int y0 = 64 * __shfl_sync(0xffffffffu, page, 2 * rank), y1 = 64 * __shfl_sync(0xffffffffu, page, 2 * rank + 1);
 #pragma unroll 1
-      for (int d = 0; d < 9; ++d, ++seq) {
-        if (seq % kCkCopyWarps != (uint32_t)warp) continue;
-        if (!claim(seq)) return false;
-        if (lane == 0) {
-          const uint32_t full = lead0 + 8 * (CB_FULL + seq % kCkSlots), dst = base + CK_RING + (seq % kCkSlots) * kCkSlot;
+      for (int d = 0; d < 9; ++d, advance()) {
+        if (turn != warp) continue;
+        if (!wait_uniform(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
+        const uint32_t full = lead0 + 8 * (CB_FULL + slot), dst = base + CK_RING + slot * kCkSlot;
+        if (el) {
           if (np == 0) {
             mbar_arrive_remote(full);
           } else {
             mbar_arrive_expect_tx_remote(full, np * kCkBlk);
-            tma2_load_2d(dst, &args.map_k, full, 64 * d, p0 * 64);
-            if (np == 2) tma2_load_2d(dst + kCkBlk, &args.map_k, full, 64 * d, p1 * 64);
+            tma2_load_2d(dst, &args.map_k, full, 64 * d, y0);
+            if (np == 2) tma2_load_2d(dst + kCkBlk, &args.map_k, full, 64 * d, y1);
           }
         }
         __syncwarp();
@@ -299,27 +309,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       const int np = r.pages(), some = chunk_visible(r.b, 0, args.causal);  // keys every row of the block sees
 #pragma unroll 1
       for (int kb = 0; kb < np; ++kb) {
-        const int pg = __shfl_sync(0xffffffffu, page, kb), key0 = kChunkTile * r.tile + 64 * kb;
+        const int y = 64 * __shfl_sync(0xffffffffu, page, kb), key0 = kChunkTile * r.tile + 64 * kb;
 #pragma unroll 1
-        for (int n = 0; n < 2; ++n, ++seq) {
-          if (seq % kCkCopyWarps != (uint32_t)warp) continue;
-          if (!claim(seq)) return false;
-          const uint32_t full = lead0 + 8 * (CB_FULL + seq % kCkSlots), dst = base + CK_RING + (seq % kCkSlots) * kCkSlot;
+        for (int n = 0; n < 2; ++n, advance()) {
+          if (turn != warp) continue;
+          if (!wait_uniform(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
+          const uint32_t full = lead0 + 8 * (CB_FULL + slot), dst = base + CK_RING + slot * kCkSlot;
           const int z = 4 * n + 2 * (int)rank;  // dims 256 n + 128 rank, in blocks of 64
           if (key0 + 64 <= some) {
-            if (lane == 0) {
+            if (el) {
               mbar_arrive_expect_tx_remote(full, kCkSlot);
-              tma2_load_3d(dst, &args.map_v, full, 0, pg * 64, z);
+              tma2_load_3d(dst, &args.map_v, full, 0, y, z);
             }
             __syncwarp();
             continue;
           }
           // some row does not see all of this page: rows [from, to) of it are looked through
           const uint32_t raw = bar(CB_RAW + warp);
-          if (lane == 0) {
+          if (el) {
             mbar_arrive_expect_tx(raw, kCkSlot);
-            tma2_load_3d(dst, &args.map_v, map_to_rank(raw, rank), 0, pg * 64, z);
+            tma2_load_3d(dst, &args.map_v, map_to_rank(raw, rank), 0, y, z);
           }
+          __syncwarp();
           if (!wait_warp(raw, n_raw & 1, wc, kSiteCkRaw)) return false;
           ++n_raw;
           const int from = max(some - key0, 0), seen = min(r.vis - key0, 64), to = (seen + 15) & ~15;
@@ -458,19 +469,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     }
   } else if (warp == 7) {
     // ================================================================ query copies
-    if (lane == 0) {
-      ChunkTileRef r;
-      uint32_t piece = 0;
-      const uint32_t full = lead0 + 8 * CB_Q_FULL;
-      while (cur.next(r)) {
-        if (!r.first) continue;
-        if (piece > 0 && !wait_one<true>(bar(CB_Q_EMPTY), (piece - 1) & 1, wc, kSiteCkQ)) break;
-        const int row = r.b.tok0 * args.H + 64 * (int)rank;
+    ChunkTileRef r;
+    uint32_t piece = 0;
+    const uint32_t full = lead0 + 8 * CB_Q_FULL;
+    const bool el = elect_one();
+    while (cur.next(r)) {
+      if (!r.first) continue;
+      if (piece > 0 && !wait_uniform(bar(CB_Q_EMPTY), (piece - 1) & 1, wc, kSiteCkQ)) break;
+      const int row = r.b.tok0 * args.H + 64 * (int)rank;
+      if (el) {
         mbar_arrive_expect_tx_remote(full, 9 * kCkBlk);
-        for (int d = 0; d < 8; ++d) tma2_load_2d(base + CK_Q + d * kCkBlk, &args.map_q, full, 64 * d, row);
+        tma2_load_3d(base + CK_Q, &args.map_q, full, 0, row, 0);
         tma2_load_2d(base + CK_Q + 8 * kCkBlk, &args.map_qr, full, 0, row);
-        ++piece;
       }
+      __syncwarp();
+      ++piece;
     }
   } else {
     // ================================================================ softmax
@@ -553,7 +566,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(lead0 + 8 * (CB_S_EMPTY + sb));
+      // (relaxed: the scores are in registers; nothing was written that the MMA warp reads)
+      if (lane == 0) mbar_arrive_remote_relaxed(lead0 + 8 * (CB_S_EMPTY + sb), sv[0] ^ sv[63]);
       if (kChunkTile * (a.tile + 1) > some || r >= a.b.ntok * args.H) {
         // keys this row sees of the thread's 64; a seen score of -inf comes of a key that is not
         // finite (and whose value row was zeroed): the row becomes NaN
