@@ -109,6 +109,13 @@ __device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* ma
       "l"(map), "r"(mbar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 // (relaxed: the copies themselves order their bytes; a release arrive on the other CTA's barrier waits
 // for this thread's earlier writes, ~1400 cycles measured)
 __device__ __forceinline__ void mbar_arrive_expect_tx_remote(uint32_t cluster_bar, uint32_t bytes) {
@@ -140,10 +147,10 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
   return ok != 0;
 }
-// Bounded wait by a converged warp.
+// Bounded wait by a converged warp (the lanes agree but for a wait that runs out, and then all leave).
 __device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
-  if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
-  return wait_warp<true>(bar, parity, w, site);
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  return wait_one<true>(bar, parity, w, site);
 }
 
 // One tile of a unit's work.
@@ -196,6 +203,7 @@ struct ChunkCursor {
     r.last = t >= end;
     return true;
   }
+  __device__ void skip_block() { t = end; }
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
@@ -353,8 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       }
       return true;
     };
-    // the order of the MMA warp: K of the next tile, then V of the current one; a tile's page
-    // numbers are read one tile ahead of their use
+    // the order of the MMA warp: K of the next tile, then V of the current one (the other way at a block's
+    // end); a tile's page numbers are read one tile ahead of their use
     ChunkTileRef a, b, c;
     bool has_b, has_c;
     cur.next(a);
@@ -365,8 +373,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     while (ok) {
       has_c = has_b && cur.next(c);
       if (has_c) pc = page_of(c);
-      if (has_b && !(ok = copy_k(b, pb))) break;
+      if (has_b && !b.first && !(ok = copy_k(b, pb))) break;
       if (!(ok = copy_v(a, pa)) || !has_b) break;
+      if (b.first && !(ok = copy_k(b, pb))) break;
       a = b;
       pa = pb;
       b = c;
@@ -396,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
         }
         if (t >= 2 && !wait_uniform(bar(CB_S_EMPTY + (t & 1)), ((t >> 1) - 1) & 1, wc, kSiteCkScores)) return false;
         const uint32_t d_tmem = tmem + CT_S + 128 * (t & 1);
-#pragma unroll 1
+#pragma unroll
         for (int d = 0; d < 9; ++d) {
           if (!wait_uniform(bar(CB_FULL + slot), phase, wc, kSiteCkRing)) return false;
           tc_fence_after();
@@ -426,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
           const int steps = (min(r.vis - kChunkTile * r.tile - 64 * kb, 64) + 15) >> 4;
           const uint32_t acc = !r.first || kb > 0 ? 1u : 0u;
           const uint64_t da = desc_p + kb * (kCkBlk >> 4);
-#pragma unroll 1
+#pragma unroll
           for (int n = 0; n < 2; ++n) {
             if (!wait_uniform(bar(CB_FULL + slot), phase, wc, kSiteCkRing)) return false;
             tc_fence_after();
@@ -451,9 +460,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       cur.next(a);
       bool ok = qk(a, 0);
       while (ok) {
+        // scores of the next tile first, so that the softmax always has one; but a block's last PV before
+        // the next block's first QK, whose query is loaded meanwhile
         const bool more = cur.next(b);
-        if (more && !(ok = qk(b, g + 1))) break;
+        if (more && !b.first && !(ok = qk(b, g + 1))) break;
         if (!(ok = pv(a, g)) || !more) break;
+        if (b.first && !(ok = qk(b, g + 1))) break;
         a = b;
         ++g;
       }
@@ -469,14 +481,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     }
   } else if (warp == 7) {
     // ================================================================ query copies
+    // (the next block's rows are brought into L2 while this block runs)
     ChunkTileRef r;
     uint32_t piece = 0;
     const uint32_t full = lead0 + 8 * CB_Q_FULL;
     const bool el = elect_one();
     while (cur.next(r)) {
-      if (!r.first) continue;
-      if (piece > 0 && !wait_uniform(bar(CB_Q_EMPTY), (piece - 1) & 1, wc, kSiteCkQ)) break;
       const int row = r.b.tok0 * args.H + 64 * (int)rank;
+      if (piece > 0) {
+        if (el) {
+          tma_prefetch_3d(&args.map_q, 0, row, 0);
+          tma_prefetch_2d(&args.map_qr, 0, row);
+        }
+        __syncwarp();
+        if (!wait_uniform(bar(CB_Q_EMPTY), (piece - 1) & 1, wc, kSiteCkQ)) break;
+      }
       if (el) {
         mbar_arrive_expect_tx_remote(full, 9 * kCkBlk);
         tma2_load_3d(base + CK_Q, &args.map_q, full, 0, row, 0);
@@ -484,6 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       }
       __syncwarp();
       ++piece;
+      cur.skip_block();
     }
   } else {
     // ================================================================ softmax
@@ -509,47 +529,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       if (!wait_warp(bar(CB_SUM), pieces & 1, wc, kSiteCkRed)) return false;
       ++pieces;
       const float l = sums[row] + sums[64 + row] + sums[128 + row] + sums[192 + row];
-      const bool store = r < e.b.ntok * args.H, split = e.b.splits > 1;
+      const int rows = e.b.ntok * args.H - (r - lane);  // rows of this warp's 32 that the block has
+      const bool split = e.b.splits > 1;
       const float inv = 1.f / l;
       const int64_t slot_row = (int64_t)(e.b.offset + e.split) * kChunkRows + r;
       const int64_t q_row = (int64_t)e.b.tok0 * args.H + r;
+      // Through the warp's own 4 KB of the P buffer (its rows' chunks, free once PV is done), so that
+      // eight lanes write 128 bytes of a row: 16-byte chunks, XOR-swizzled by row both ways.
+      const int sub = lane >> 3, chk = lane & 7;
+      auto stg = [&](int rw, int c) -> uint32_t { return prow - row * 128 + (row - lane + rw) * 128 + ((uint32_t)(c ^ (rw & 7)) << 4); };
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 4; ++c) {  // 32 columns a round: 128 bytes of a float32 partial, 64 of a bf16 row
         uint32_t v[32];
         tmem_ld32(tmem + lane_off + CT_O + 128 * w + 32 * c, v);
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 32; ++j)  // (a row that saw no key: zeros, whatever the accumulator holds)
           v[j] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(v[j]) * inv);
-        if (!store) continue;
         if (split) {
-          float4* dst = reinterpret_cast<float4*>(args.o_acc + slot_row * 512 + col0 + 32 * c);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
-                                 __uint_as_float(v[4 * q + 3]));
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg(lane, q)), "r"(v[4 * q]), "r"(v[4 * q + 1]),
+                         "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                         : "memory");
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(args.out + q_row * 512 + col0 + 32 * c);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t* u = v + 8 * q;
-            dst[q] = make_uint4(pack_bf16(__uint_as_float(u[0]), __uint_as_float(u[1])),
-                                pack_bf16(__uint_as_float(u[2]), __uint_as_float(u[3])),
-                                pack_bf16(__uint_as_float(u[4]), __uint_as_float(u[5])),
-                                pack_bf16(__uint_as_float(u[6]), __uint_as_float(u[7])));
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg(lane, 4 * (c & 1) + q)),
+                         "r"(pack_bf16(__uint_as_float(u[0]), __uint_as_float(u[1]))),
+                         "r"(pack_bf16(__uint_as_float(u[2]), __uint_as_float(u[3]))),
+                         "r"(pack_bf16(__uint_as_float(u[4]), __uint_as_float(u[5]))),
+                         "r"(pack_bf16(__uint_as_float(u[6]), __uint_as_float(u[7])))
+                         : "memory");
           }
+          if ((c & 1) == 0) continue;
         }
+        __syncwarp();
+        uint8_t* dst = split ? reinterpret_cast<uint8_t*>(args.o_acc + (slot_row - lane) * 512 + col0 + 32 * c)
+                             : reinterpret_cast<uint8_t*>(args.out + (q_row - lane) * 512 + col0 + 32 * (c - 1));
+        const int64_t stride = split ? 2048 : 1024;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rw = 4 * i + sub;
+          uint4 o;
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "r"(stg(rw, chk)) : "memory");
+          if (rw < rows) *reinterpret_cast<uint4*>(dst + rw * stride + 16 * chk) = o;
+        }
+        __syncwarp();
       }
-      if (store && part == 0) {
+      if (lane < rows && part == 0) {
         const float lse = l == 0.f ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994530942f;
         if (split) args.lse_acc[slot_row] = lse; else args.lse[q_row] = lse;
       }
       return true;
     };
 
-    ChunkTileRef a, prev;
+    ChunkTileRef a;
     int lim = 0, some = 0;
-    bool pend = false;
     uint32_t g = 0;
     for (; ok && cur.next(a); ++g) {
       if (a.first) {
@@ -617,8 +654,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       // PV of the tile before is done: P may be overwritten, O read and rescaled
       if (g > 0 && !(ok = wait_warp<true>(bar(CB_P_FREE), (g - 1) & 1, wc, kSiteCkPv))) break;
       tc_fence_after();
-      if (pend && !(ok = epilogue(prev))) break;  // (m_run, l_run still those of the finished piece)
-      pend = false;
       if (!a.first && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -642,14 +677,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(lead0 + 8 * CB_P_FULL);
-      if (a.last) {
-        pend = true;
-        prev = a;
+      if (a.last) {  // (the next block's scores are computed meanwhile)
+        if (!(ok = wait_warp<true>(bar(CB_P_FREE), g & 1, wc, kSiteCkPv))) break;
+        tc_fence_after();
+        if (!(ok = epilogue(a))) break;
       }
-    }
-    if (ok && pend && (ok = wait_warp<true>(bar(CB_P_FREE), (g - 1) & 1, wc, kSiteCkPv))) {
-      tc_fence_after();
-      epilogue(prev);
     }
     tc_fence_before();
   }
