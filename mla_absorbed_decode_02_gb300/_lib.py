@@ -87,6 +87,8 @@ class MlaPoolParams(ctypes.Structure):
 def load_library():
     """Load the built library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -160,6 +162,18 @@ def _stream(stream) -> int:
         import torch
         return int(torch.cuda.current_stream().cuda_stream)
     return int(getattr(stream, "cuda_stream", stream))
+
+
+_types = None
+
+
+def _dtypes():
+    """(int32, float32, bfloat16) of torch, looked up once."""
+    global _types
+    if _types is None:
+        import torch
+        _types = (torch.int32, torch.float32, torch.bfloat16)
+    return _types
 
 
 def mla_status_string(status: int) -> str:
@@ -277,22 +291,20 @@ def mla_extend(p: MlaExtendParams, q_nope, q_rope, kv_pages, block_table, cache_
                                      _ptr(workspace), _stream(stream)), "mla_extend")
 
 
-def _expect(what: str, t, dtype: str, size=None, shape=None):
-    """A contiguous tensor of the named type with at least `size` elements, or of `shape` (None: any)."""
-    ok = t is not None and str(t.dtype) == "torch." + dtype and t.is_contiguous()
-    ok = ok and (size is None or t.numel() >= size)
-    ok = ok and (shape is None or (t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape))))
-    if not ok:
-        raise MlaError(MLA_ERR_INVALID_ARG, what)
+def _expect(call: str, *wanted):
+    """Each of (name, tensor, dtype, shape): a contiguous tensor of that type and shape.  The library itself sees
+    pointers alone, so what it cannot check is checked here."""
+    for name, t, dtype, shape in wanted:
+        if t is None or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise MlaError(MLA_ERR_INVALID_ARG, f"{call}: {name}")
 
 
-def _expect_pool(what: str, t, p, num_layers: int = 1):
+def _expect_pool(call: str, t, p, num_layers: int = 1, layer_stride: int = 0):
     """The pools' pages: large enough for the last layer's last page, rows not strided."""
-    row = 1152 if p.kv_dtype == MLA_KV_BF16 else 656
-    pool = p.num_pages * 64 * row
-    need = (num_layers - 1) * (getattr(p, "layer_stride", 0) or pool) + pool
-    if t is None or not t.is_contiguous() or t.numel() * t.element_size() < need:
-        raise MlaError(MLA_ERR_INVALID_ARG, what)
+    pool = p.num_pages * (64 * 1152 if p.kv_dtype == MLA_KV_BF16 else 64 * 656)
+    if (t is None or not t.is_contiguous()
+            or t.numel() * t.element_size() < (num_layers - 1) * (layer_stride or pool) + pool):
+        raise MlaError(MLA_ERR_INVALID_ARG, call + ": kv_pages")
 
 
 def mla_chunk_workspace_size(p: MlaChunkParams):
@@ -318,8 +330,9 @@ def mla_chunk_plan_host(p: MlaChunkParams, num_units: int, cu_seqlens, cache_seq
 
 def mla_chunk_schedule(p: MlaChunkParams, cu_seqlens, cache_seqlens, sched, stream=None):
     """Work plan of ragged chunks: cu_seqlens int32 [B + 1], cache_seqlens int32 [B] (new tokens included)."""
-    _expect("mla_chunk_schedule: cu_seqlens", cu_seqlens, "int32", shape=(p.batch + 1,))
-    _expect("mla_chunk_schedule: cache_seqlens", cache_seqlens, "int32", shape=(p.batch,))
+    i32 = _dtypes()[0]
+    _expect("mla_chunk_schedule", ("cu_seqlens", cu_seqlens, i32, (p.batch + 1,)),
+            ("cache_seqlens", cache_seqlens, i32, (p.batch,)))
     _check(load_library().mla_chunk_schedule(ctypes.byref(p), _ptr(cu_seqlens), _ptr(cache_seqlens), _ptr(sched),
                                              _stream(stream)), "mla_chunk_schedule")
 
@@ -328,14 +341,12 @@ def mla_chunk_attend(p: MlaChunkParams, q_nope_absorbed, q_rope, kv_pages, block
                      out, lse, sched, workspace, stream=None):
     """Attention of ragged chunks over the paged cache: q bf16 [T, H, 512] and [T, H, 64], out bf16 [T, H, 512],
     lse float32 [T, H]."""
-    T, H = p.max_tokens, p.num_heads
-    _expect("mla_chunk_attend: q_nope_absorbed", q_nope_absorbed, "bfloat16", shape=(T, H, 512))
-    _expect("mla_chunk_attend: q_rope", q_rope, "bfloat16", shape=(T, H, 64))
-    _expect("mla_chunk_attend: block_table", block_table, "int32", shape=(p.batch, p.max_pages_per_seq))
-    _expect("mla_chunk_attend: cache_seqlens", cache_seqlens, "int32", shape=(p.batch,))
-    _expect("mla_chunk_attend: out", out, "bfloat16", shape=(T, H, 512))
-    _expect("mla_chunk_attend: lse", lse, "float32", shape=(T, H))
-    _expect_pool("mla_chunk_attend: kv_pages", kv_pages, p)
+    T, H, B = p.max_tokens, p.num_heads, p.batch
+    i32, f32, bf16 = _dtypes()
+    _expect("mla_chunk_attend", ("q_nope_absorbed", q_nope_absorbed, bf16, (T, H, 512)), ("q_rope", q_rope, bf16, (T, H, 64)),
+            ("block_table", block_table, i32, (B, p.max_pages_per_seq)), ("cache_seqlens", cache_seqlens, i32, (B,)),
+            ("out", out, bf16, (T, H, 512)), ("lse", lse, f32, (T, H)))
+    _expect_pool("mla_chunk_attend", kv_pages, p)
     _check(load_library().mla_chunk_attend(ctypes.byref(p), _ptr(q_nope_absorbed), _ptr(q_rope), _ptr(kv_pages),
                                            _ptr(block_table), _ptr(cache_seqlens), float(scale), _ptr(out), _ptr(lse),
                                            _ptr(sched), _ptr(workspace), _stream(stream)), "mla_chunk_attend")
@@ -344,14 +355,16 @@ def mla_chunk_attend(p: MlaChunkParams, q_nope_absorbed, q_rope, kv_pages, block
 def mla_append_kv(p: MlaPoolParams, latent, k_rope, cu_seqlens, cache_seqlens, block_table, kv_pages, stream=None):
     """Rows of ragged new tokens into the pages: latent bf16 [T, 512] and k_rope bf16 [T, 64], rows of either may be
     strided (the two parts of one [T, 576] array)."""
-    for what, t, n in (("latent", latent, 512), ("k_rope", k_rope, 64)):
-        if (t is None or str(t.dtype) != "torch.bfloat16" or t.dim() != 2 or t.shape[1] != n or t.stride(1) != 1
-                or t.shape[0] != latent.shape[0]):
-            raise MlaError(MLA_ERR_INVALID_ARG, "mla_append_kv: " + what)
-    _expect("mla_append_kv: cu_seqlens", cu_seqlens, "int32", shape=(p.batch + 1,))
-    _expect("mla_append_kv: cache_seqlens", cache_seqlens, "int32", shape=(p.batch,))
-    _expect("mla_append_kv: block_table", block_table, "int32", shape=(p.batch, p.max_pages_per_seq))
-    _expect_pool("mla_append_kv: kv_pages", kv_pages, p)
+    i32, _, bf16 = _dtypes()
+    B = p.batch
+    for name, t, n in (("latent", latent, 512), ("k_rope", k_rope, 64)):
+        if t is None or t.dtype != bf16 or t.dim() != 2 or t.shape[1] != n or t.stride(1) != 1:
+            raise MlaError(MLA_ERR_INVALID_ARG, "mla_append_kv: " + name)
+    if k_rope.shape[0] != latent.shape[0]:
+        raise MlaError(MLA_ERR_INVALID_ARG, "mla_append_kv: k_rope")
+    _expect("mla_append_kv", ("cu_seqlens", cu_seqlens, i32, (B + 1,)), ("cache_seqlens", cache_seqlens, i32, (B,)),
+            ("block_table", block_table, i32, (B, p.max_pages_per_seq)))
+    _expect_pool("mla_append_kv", kv_pages, p)
     if latent.shape[0] == 0:
         return
     # (one row: its stride says nothing)
@@ -368,52 +381,67 @@ def mla_pool_workspace_size(p: MlaPoolParams, max_forks: int) -> int:
     return n.value
 
 
-def _expect_tables(what: str, p: MlaPoolParams, block_table, cache_seqlens, ref_counts):
-    _expect(what + ": block_table", block_table, "int32", shape=(p.batch, p.max_pages_per_seq))
-    _expect(what + ": cache_seqlens", cache_seqlens, "int32", shape=(p.batch,))
-    _expect(what + ": ref_counts", ref_counts, "int32", shape=(p.num_pages,))
+def _tables(p: MlaPoolParams, block_table, cache_seqlens, ref_counts):
+    i32 = _dtypes()[0]
+    return (("block_table", block_table, i32, (p.batch, p.max_pages_per_seq)),
+            ("cache_seqlens", cache_seqlens, i32, (p.batch,)), ("ref_counts", ref_counts, i32, (p.num_pages,)))
 
 
-def _expect_workspace(what: str, p: MlaPoolParams, workspace, forks: int = 0):
-    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if n < mla_pool_workspace_size(p, forks):
-        raise MlaError(MLA_ERR_WORKSPACE, what + ": workspace")
+def _expect_workspace(call: str, p: MlaPoolParams, workspace, forks: int = 0):
+    if workspace is None or workspace.numel() * workspace.element_size() < mla_pool_workspace_size(p, forks):
+        raise MlaError(MLA_ERR_WORKSPACE, call + ": workspace")
+
+
+def _list_of(call: str, name: str, t) -> int:
+    """Length of a one-dimensional int32 list."""
+    if t is None or t.dim() != 1:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{call}: {name}")
+    _expect(call, (name, t, _dtypes()[0], t.shape))
+    return int(t.shape[0])
 
 
 def mla_copy_pages(p: MlaPoolParams, kv_pages, src_pages, dst_pages, stream=None):
     """Page dst_pages[i] := page src_pages[i] in every layer (int32 [n])."""
-    _expect("mla_copy_pages: src_pages", src_pages, "int32", shape=(None,))
-    _expect("mla_copy_pages: dst_pages", dst_pages, "int32", shape=tuple(src_pages.shape))
-    _expect_pool("mla_copy_pages: kv_pages", kv_pages, p, p.num_layers)
-    if src_pages.numel() == 0:
+    n = _list_of("mla_copy_pages", "src_pages", src_pages)
+    _expect("mla_copy_pages", ("dst_pages", dst_pages, _dtypes()[0], (n,)))
+    _expect_pool("mla_copy_pages", kv_pages, p, p.num_layers, p.layer_stride)
+    if n == 0:
         return
-    _check(load_library().mla_copy_pages(ctypes.byref(p), _ptr(kv_pages), _ptr(src_pages), _ptr(dst_pages),
-                                         int(src_pages.numel()), _stream(stream)), "mla_copy_pages")
+    _check(load_library().mla_copy_pages(ctypes.byref(p), _ptr(kv_pages), _ptr(src_pages), _ptr(dst_pages), n,
+                                         _stream(stream)), "mla_copy_pages")
 
 
 def mla_fork_sequences(p: MlaPoolParams, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages,
                        workspace, stream=None):
     """Row children[i] of the table becomes a copy of row parents[i]; new_pages int32 [n] takes the outcomes."""
-    _expect("mla_fork_sequences: parents", parents, "int32", shape=(None,))
-    _expect("mla_fork_sequences: children", children, "int32", shape=tuple(parents.shape))
-    _expect("mla_fork_sequences: new_pages", new_pages, "int32", shape=tuple(parents.shape))
-    _expect_tables("mla_fork_sequences", p, block_table, cache_seqlens, ref_counts)
-    _expect_pool("mla_fork_sequences: kv_pages", kv_pages, p, p.num_layers)
-    _expect_workspace("mla_fork_sequences", p, workspace, int(parents.numel()))
-    if parents.numel() == 0:
+    _expect_workspace("mla_fork_sequences", p, workspace, 0 if parents is None else parents.numel())
+    _fork(p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, workspace, stream)
+
+
+def _fork(p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, workspace, stream):
+    n = _list_of("mla_fork_sequences", "parents", parents)
+    i32 = _dtypes()[0]
+    _expect("mla_fork_sequences", ("children", children, i32, (n,)), ("new_pages", new_pages, i32, (n,)),
+            *_tables(p, block_table, cache_seqlens, ref_counts))
+    _expect_pool("mla_fork_sequences", kv_pages, p, p.num_layers, p.layer_stride)
+    if n == 0:
         return
-    _check(load_library().mla_fork_sequences(ctypes.byref(p), _ptr(kv_pages), _ptr(parents), _ptr(children),
-                                             int(parents.numel()), _ptr(block_table), _ptr(cache_seqlens),
-                                             _ptr(ref_counts), _ptr(new_pages), _ptr(workspace), _stream(stream)),
+    _check(load_library().mla_fork_sequences(ctypes.byref(p), _ptr(kv_pages), _ptr(parents), _ptr(children), n,
+                                             _ptr(block_table), _ptr(cache_seqlens), _ptr(ref_counts),
+                                             _ptr(new_pages), _ptr(workspace), _stream(stream)),
            "mla_fork_sequences")
 
 
 def mla_reserve_pages(p: MlaPoolParams, num_new, block_table, cache_seqlens, ref_counts, served, workspace, stream=None):
     """Room for num_new[b] more rows of every sequence; served int32 [batch] takes the outcomes."""
-    _expect("mla_reserve_pages: num_new", num_new, "int32", shape=(p.batch,))
-    _expect("mla_reserve_pages: served", served, "int32", shape=(p.batch,))
-    _expect_tables("mla_reserve_pages", p, block_table, cache_seqlens, ref_counts)
     _expect_workspace("mla_reserve_pages", p, workspace)
+    _reserve(p, num_new, block_table, cache_seqlens, ref_counts, served, workspace, stream)
+
+
+def _reserve(p, num_new, block_table, cache_seqlens, ref_counts, served, workspace, stream):
+    i32 = _dtypes()[0]
+    _expect("mla_reserve_pages", ("num_new", num_new, i32, (p.batch,)), ("served", served, i32, (p.batch,)),
+            *_tables(p, block_table, cache_seqlens, ref_counts))
     _check(load_library().mla_reserve_pages(ctypes.byref(p), _ptr(num_new), _ptr(block_table), _ptr(cache_seqlens),
                                             _ptr(ref_counts), _ptr(served), _ptr(workspace), _stream(stream)),
            "mla_reserve_pages")
@@ -421,22 +449,26 @@ def mla_reserve_pages(p: MlaPoolParams, num_new, block_table, cache_seqlens, ref
 
 def mla_free_sequences(p: MlaPoolParams, sequences, block_table, cache_seqlens, ref_counts, stream=None):
     """Ends the sequences (int32 [n], rows of the block table) and gives their pages back."""
-    _expect("mla_free_sequences: sequences", sequences, "int32", shape=(None,))
-    _expect_tables("mla_free_sequences", p, block_table, cache_seqlens, ref_counts)
-    if sequences.numel() == 0:
+    n = _list_of("mla_free_sequences", "sequences", sequences)
+    _expect("mla_free_sequences", *_tables(p, block_table, cache_seqlens, ref_counts))
+    if n == 0:
         return
-    _check(load_library().mla_free_sequences(ctypes.byref(p), _ptr(sequences), int(sequences.numel()),
-                                             _ptr(block_table), _ptr(cache_seqlens), _ptr(ref_counts),
-                                             _stream(stream)), "mla_free_sequences")
+    _check(load_library().mla_free_sequences(ctypes.byref(p), _ptr(sequences), n, _ptr(block_table),
+                                             _ptr(cache_seqlens), _ptr(ref_counts), _stream(stream)),
+           "mla_free_sequences")
 
 
 def mla_compact_pages(p: MlaPoolParams, kv_pages, block_table, cache_seqlens, ref_counts, num_used, workspace,
                       stream=None):
     """Draws the used pages together at the start of the pools; num_used int32 [1] takes their number."""
-    _expect("mla_compact_pages: num_used", num_used, "int32", size=1)
-    _expect_tables("mla_compact_pages", p, block_table, cache_seqlens, ref_counts)
-    _expect_pool("mla_compact_pages: kv_pages", kv_pages, p, p.num_layers)
     _expect_workspace("mla_compact_pages", p, workspace)
+    _compact(p, kv_pages, block_table, cache_seqlens, ref_counts, num_used, workspace, stream)
+
+
+def _compact(p, kv_pages, block_table, cache_seqlens, ref_counts, num_used, workspace, stream):
+    _expect("mla_compact_pages", ("num_used", num_used, _dtypes()[0], (1,)),
+            *_tables(p, block_table, cache_seqlens, ref_counts))
+    _expect_pool("mla_compact_pages", kv_pages, p, p.num_layers, p.layer_stride)
     _check(load_library().mla_compact_pages(ctypes.byref(p), _ptr(kv_pages), _ptr(block_table), _ptr(cache_seqlens),
                                             _ptr(ref_counts), _ptr(num_used), _ptr(workspace), _stream(stream)),
            "mla_compact_pages")
@@ -545,14 +577,14 @@ class PagePool:
         if parents.numel() > self.max_forks:
             raise MlaError(MLA_ERR_WORKSPACE, "PagePool.fork: more forks than max_forks")
         new_pages = self._outcome(parents.numel())
-        mla_fork_sequences(self.p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages,
-                           self.workspace, stream)
+        _fork(self.p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, self.workspace,
+              stream)
         return new_pages
 
     def reserve(self, num_new, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns served int32 [batch]: 1 (done), 0 (not enough pages), -2 (refused)."""
         served = self._outcome(self.p.batch)
-        mla_reserve_pages(self.p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
+        _reserve(self.p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
         return served
 
     def free(self, sequences, block_table, cache_seqlens, ref_counts, stream=None):
@@ -561,5 +593,5 @@ class PagePool:
     def compact(self, kv_pages, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns the number of used pages, int32 [1] on the device."""
         used = self._outcome(1)
-        mla_compact_pages(self.p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
+        _compact(self.p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
         return used

@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
                                                                int64_t max_tokens, int H, int causal, int max_pages,
                                                                int64_t max_kv_pages, int U, int64_t cap, int32_t* sched) {
   __shared__ int64_t sh[32];
-  __shared__ int bad;
+  __shared__ int bad, sh_share;
   const int tid = threadIdx.x, tb = chunk_tokens_per_block(H);
   const ChunkLayout l = chunk_layout(U, cap, B);
   ChunkBlock* blocks = reinterpret_cast<ChunkBlock*>(sched + l.blocks);
@@ -887,13 +887,31 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
   }
   if (total > kMaxPlanPositions) return refuse();
   __syncthreads();
-  const int64_t budget = plan_budget(total, U);
-  for (int u = tid; u < U; u += 1024) chunk_unit(blocks, pos, (int)nb, total, budget, u, sched + l.units + kUnitInts * u);
-  int64_t slots = 0, ns = 0;
-  __syncthreads();  // (the units read the records that the next phase completes)
+  const bool shares = nb <= U;
+  int64_t budget = plan_budget(total, U);
+  if (shares) {
+    if (tid < 32) {  // the least share that U units suffice for
+      int32_t longest = 1;
+      for (int k = tid; k < nb; k += 32) longest = max(longest, blocks[k].nt);
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      int32_t lo = 1, hi = longest;
+      while (lo < hi) {
+        const int32_t m = (lo + hi) / 2;
+        int32_t need = 0;  // (at most U + NB < 2^18 until it no longer matters)
+        for (int k = tid; k < nb; k += 32) need = min(need + chunk_shares(blocks[k].nt, m), 1 << 24);
+        if (__reduce_add_sync(0xffffffffu, need) <= U) hi = m; else lo = m + 1;
+      }
+      if (tid == 0) sh_share = longest <= lo + kChunkMergeCost ? longest : lo;
+    }
+    __syncthreads();
+    budget = sh_share;
+  }
+  int64_t slots = 0, ns = 0, at = 0;
   for (int64_t k0 = 0; k0 < nb; k0 += 1024) {
     const int64_t k = k0 + tid;
-    const int32_t s = k < nb ? chunk_splits(pos[k], blocks[k].nt, budget) : 0;
+    const int32_t s = k >= nb ? 0
+                      : shares ? chunk_shares(blocks[k].nt, (int32_t)budget)
+                               : chunk_splits(pos[k], blocks[k].nt, budget);
     const int64_t oe = block_scan_1024(s > 1 ? s : 0, sh, &sum);
     const int64_t o = slots + oe;
     slots += sum;
@@ -904,6 +922,19 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
       if (s > 1) sched[l.split_list + ns + le] = (int32_t)k;
     }
     ns += sum;
+    if (shares) {
+      const int64_t ae = block_scan_1024(s, sh, &sum);
+      if (k < nb) pos[k] = (int32_t)(at + ae);
+      at += sum;
+    }
+  }
+  __syncthreads();
+  for (int u = tid; u < U; u += 1024) {
+    int32_t* rec = sched + l.units + kUnitInts * u;
+    if (shares)
+      chunk_share_unit(blocks, pos, (int)nb, at, u, rec);
+    else
+      chunk_unit(blocks, pos, (int)nb, total, budget, u, rec);
   }
   if (tid == 0) {
     sched[kChUnits] = U;
@@ -914,6 +945,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     sched[kChTokens] = tb;
     sched[kChNumSplit] = (int32_t)ns;
     sched[kChPages] = (int32_t)pages;
+    sched[kChShares] = shares;
     sched[kChMagic] = kChunkMagic;
   }
 }

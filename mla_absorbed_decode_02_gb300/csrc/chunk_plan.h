@@ -7,7 +7,10 @@
 // which writes its zero rows.  Blocks lie one after another on a line of cost positions
 // (kChunkPieceCost, then one per tile) and unit u owns the tiles in [u * budget, (u + 1) * budget):
 // long sequences are split over units ("MLA inference: two computation paths and FlashMLA",
-// section "Decode attention becomes a compute problem") and merged by their LSE.
+// section "Decode attention becomes a compute problem") and merged by their LSE.  Where there are
+// no more blocks than units, each unit takes one share of one block instead: shares of at most m
+// tiles, m the least that the units suffice for -- or whole blocks, where the longest is at most
+// kChunkMergeCost tiles longer than that, since then nothing has to be merged.
 //
 // The per-item functions are shared by the scheduler kernel (which runs the prefix sums in
 // parallel) and the host twin.
@@ -28,9 +31,14 @@ constexpr int kChunkTile = 256;               // keys of a tile (four pages)
 #define MLA_CHUNK_PIECE_COST 1
 #endif
 constexpr int kChunkPieceCost = MLA_CHUNK_PIECE_COST;
+// What writing and merging the partial results of split blocks costs, in tiles.
+#ifndef MLA_CHUNK_MERGE_COST
+#define MLA_CHUNK_MERGE_COST 2
+#endif
+constexpr int kChunkMergeCost = MLA_CHUNK_MERGE_COST;
 
 // header words
-enum { kChMagic = 0, kChUnits, kChCapacity, kChBlocks, kChSlots, kChBudget, kChTokens, kChNumSplit, kChPages };
+enum { kChMagic = 0, kChUnits, kChCapacity, kChBlocks, kChSlots, kChBudget, kChTokens, kChNumSplit, kChPages, kChShares };
 
 // Block record.
 struct ChunkBlock {
@@ -145,6 +153,26 @@ MLA_HD inline int32_t chunk_splits(int32_t pos, int32_t nt, int64_t budget) {
   return (int32_t)((first + nt - 1) / budget - first / budget + 1);
 }
 
+// Shares of a block of nt tiles in shares of at most m tiles, made equal.
+MLA_HD inline int32_t chunk_shares(int32_t nt, int32_t m) {
+  const int32_t s = (nt + m - 1) / m, even = (nt + s - 1) / s;
+  return (nt + even - 1) / even;
+}
+
+// Unit u's share: pos[k] = the shares before block k.
+MLA_HD inline void chunk_share_unit(const ChunkBlock* blocks, const int32_t* pos, int NB, int64_t total, int u,
+                                    int32_t* rec) {
+  rec[0] = -1;
+  for (int i = 1; i < kUnitInts; ++i) rec[i] = 0;
+  if (u >= total) return;
+  const int k = chunk_find(pos, NB, u), i = u - pos[k];
+  const int32_t nt = blocks[k].nt, s = blocks[k].splits, even = (nt + s - 1) / s;
+  rec[0] = rec[2] = k;
+  rec[1] = i * even;
+  rec[3] = nt < (i + 1) * even ? nt : (i + 1) * even;
+  rec[4] = i;
+}
+
 // Host twin: writes sched as the scheduler kernel does; false (and a header without the magic
 // word) where the lengths are refused.
 inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64_t max_tokens, int H, int causal,
@@ -171,23 +199,45 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
   page_off[B] = (int32_t)pages;
   blk_off[B] = (int32_t)nb;
   int64_t total = 0;
+  int32_t longest = 1;
   for (int k = 0; k < nb; ++k) {
     const int b = chunk_find(blk_off, B, k);
     blocks[k] = chunk_make_block(cu, lens, b, k, blk_off[b], tb, causal);
+    if (blocks[k].nt > longest) longest = blocks[k].nt;
     pos[k] = (int32_t)total;
     total += blocks[k].nt + kChunkPieceCost;
   }
   if (total > kMaxPlanPositions) return false;
-  const int64_t budget = plan_budget(total, U);
-  for (int u = 0; u < U; ++u) chunk_unit(blocks, pos, (int)nb, total, budget, u, sched + l.units + kUnitInts * u);
+  const bool shares = nb <= U;
+  int64_t budget = plan_budget(total, U);
+  if (shares) {
+    int32_t lo = 1, hi = longest;  // the least m that U units suffice for
+    while (lo < hi) {
+      const int32_t m = (lo + hi) / 2;
+      int64_t need = 0;
+      for (int k = 0; k < nb; ++k) need += chunk_shares(blocks[k].nt, m);
+      if (need <= U) hi = m; else lo = m + 1;
+    }
+    budget = longest <= lo + kChunkMergeCost ? longest : lo;
+  }
+  int64_t at = 0;
   int32_t slots = 0, ns = 0;
   for (int k = 0; k < nb; ++k) {
-    blocks[k].splits = chunk_splits(pos[k], blocks[k].nt, budget);
+    blocks[k].splits = shares ? chunk_shares(blocks[k].nt, (int32_t)budget) : chunk_splits(pos[k], blocks[k].nt, budget);
     blocks[k].offset = slots;
+    if (shares) pos[k] = (int32_t)at;
+    at += blocks[k].splits;
     if (blocks[k].splits > 1) {
       slots += blocks[k].splits;
       sched[l.split_list + ns++] = k;
     }
+  }
+  for (int u = 0; u < U; ++u) {
+    int32_t* rec = sched + l.units + kUnitInts * u;
+    if (shares)
+      chunk_share_unit(blocks, pos, (int)nb, at, u, rec);
+    else
+      chunk_unit(blocks, pos, (int)nb, total, budget, u, rec);
   }
   sched[kChMagic] = kChunkMagic;
   sched[kChUnits] = U;
@@ -198,6 +248,7 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
   sched[kChTokens] = tb;
   sched[kChNumSplit] = ns;
   sched[kChPages] = (int32_t)pages;
+  sched[kChShares] = shares;
   return true;
 }
 
