@@ -160,6 +160,8 @@ def _ptr(t) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
+        if torch.cuda.is_initialized() and hasattr(torch._C, "_cuda_getCurrentRawStream"):
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())  # 0.2 us; the Stream object costs 3
         return int(torch.cuda.current_stream().cuda_stream)
     return int(getattr(stream, "cuda_stream", stream))
 

@@ -85,7 +85,7 @@ struct ChunkArgs {
   const int32_t* sched;
   __nv_bfloat16* out;   // [T][H][512]
   float* lse;           // [T][H]
-  float* o_acc;         // split partials [slots][128][512], normalised
+  float* o_acc;         // split partials, normalised, 128 x 512 each in the accumulators' order
   float* lse_acc;       // [slots][128]
   float scale_log2;
   int32_t H, causal, max_pages, num_pages, num_units, capacity, batch;
@@ -139,6 +139,11 @@ __device__ __forceinline__ void mma2_commit_both(uint32_t bar) {
       : "memory");
 }
 
+__device__ __forceinline__ uint64_t fmul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // One lane of a converged warp.  The issuing roles below run converged, with one lane's predicate on
 // the instruction alone: descriptors and addresses then stay in uniform registers.  (One lane in a
 // branch of its own instead: 12,100 cycles a tile for the MMAs' issue alone, against 4352 of MMA time.)
@@ -531,56 +536,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       const float l = sums[row] + sums[64 + row] + sums[128 + row] + sums[192 + row];
       const int rows = e.b.ntok * args.H - (r - lane);  // rows of this warp's 32 that the block has
       const bool split = e.b.splits > 1;
-      const float inv = 1.f / l;
-      const int64_t slot_row = (int64_t)(e.b.offset + e.split) * kChunkRows + r;
-      const int64_t q_row = (int64_t)e.b.tok0 * args.H + r;
-      // Through the warp's own 4 KB of the P buffer (its rows' chunks, free once PV is done), so that
-      // eight lanes write 128 bytes of a row: 16-byte chunks, XOR-swizzled by row both ways.
-      const int sub = lane >> 3, chk = lane & 7;
-      auto stg = [&](int rw, int c) -> uint32_t { return prow - row * 128 + (row - lane + rw) * 128 + ((uint32_t)(c ^ (rw & 7)) << 4); };
+      const bool none = e.vis == 0;  // no tile had keys: the accumulator was never written
+      const uint64_t inv = splat_f32x2(l == 0.f ? 0.f : 1.f / l);
+      const int64_t q_row = (int64_t)e.b.tok0 * args.H + r, slot = e.b.offset + e.split;
+      const uint32_t acc = tmem + lane_off + CT_O + 128 * w;
+      if (split) {
+        // partials stay in the accumulator's order, [slot][CTA][warp][4 columns][lane]: whole 512-byte
+        // stores straight from the registers
+        float4* dst = reinterpret_cast<float4*>(args.o_acc) + (((slot * 2 + rank) * 8 + (warp - 8)) * 32) * 32 + lane;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {  // 32 columns a round: 128 bytes of a float32 partial, 64 of a bf16 row
-        uint32_t v[32];
-        tmem_ld32(tmem + lane_off + CT_O + 128 * w + 32 * c, v);
-        tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(acc + 32 * c, v);
+          tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j)  // (a row that saw no key: zeros, whatever the accumulator holds)
-          v[j] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(v[j]) * inv);
-        if (split) {
+          for (int q = 0; q < 8; ++q) {
+            float x[4];
+            unpack_f32x2(fmul_f32x2(pack_b32x2(v[4 * q], v[4 * q + 1]), inv), x[0], x[1]);
+            unpack_f32x2(fmul_f32x2(pack_b32x2(v[4 * q + 2], v[4 * q + 3]), inv), x[2], x[3]);
+            if (lane < rows) dst[(8 * c + q) * 32] = make_float4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      } else {
+        // rows through the warp's own 4 KB of the P buffer (its rows' chunks, free once PV is done), so
+        // that eight lanes write 128 bytes of a row: 16-byte chunks, XOR-swizzled by row both ways
+        const int sub = lane >> 3, chk = lane & 7;
+        const uint32_t mine = prow + ((uint32_t)(row & 7) << 4), region = prow - lane * 128;
+        uint8_t* dst = reinterpret_cast<uint8_t*>(args.out + (q_row - lane + sub) * 512 + col0) + 16 * chk;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {  // 64 columns a round: 128 bytes of a row
+          uint32_t v[64];
+          tmem_ld32(acc + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_ld32(acc + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg(lane, q)), "r"(v[4 * q]), "r"(v[4 * q + 1]),
-                         "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
-                         : "memory");
-        } else {
+          for (int q = 0; q < 8; ++q) {
+            uint32_t o[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t* u = v + 8 * q;
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg(lane, 4 * (c & 1) + q)),
-                         "r"(pack_bf16(__uint_as_float(u[0]), __uint_as_float(u[1]))),
-                         "r"(pack_bf16(__uint_as_float(u[2]), __uint_as_float(u[3]))),
-                         "r"(pack_bf16(__uint_as_float(u[4]), __uint_as_float(u[5]))),
-                         "r"(pack_bf16(__uint_as_float(u[6]), __uint_as_float(u[7])))
+            for (int k = 0; k < 4; ++k) {
+              float x0, x1;
+              unpack_f32x2(fmul_f32x2(pack_b32x2(v[8 * q + 2 * k], v[8 * q + 2 * k + 1]), inv), x0, x1);
+              o[k] = none ? 0u : pack_bf16(x0, x1);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(mine ^ (uint32_t)(q << 4)), "r"(o[0]), "r"(o[1]),
+                         "r"(o[2]), "r"(o[3])
                          : "memory");
           }
-          if ((c & 1) == 0) continue;
-        }
-        __syncwarp();
-        uint8_t* dst = split ? reinterpret_cast<uint8_t*>(args.o_acc + (slot_row - lane) * 512 + col0 + 32 * c)
-                             : reinterpret_cast<uint8_t*>(args.out + (q_row - lane) * 512 + col0 + 32 * (c - 1));
-        const int64_t stride = split ? 2048 : 1024;
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rw = 4 * i + sub;
-          uint4 o;
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "r"(stg(rw, chk)) : "memory");
-          if (rw < rows) *reinterpret_cast<uint4*>(dst + rw * stride + 16 * chk) = o;
+          for (int i = 0; i < 8; ++i) {
+            const int rw = 4 * i + sub;
+            uint4 o;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                         : "r"(region + rw * 128 + ((uint32_t)(chk ^ (rw & 7)) << 4))
+                         : "memory");
+            if (rw < rows) *reinterpret_cast<uint4*>(dst + 4096 * i + 128 * c) = o;
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (lane < rows && part == 0) {
         const float lse = l == 0.f ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994530942f;
-        if (split) args.lse_acc[slot_row] = lse; else args.lse[q_row] = lse;
+        if (split) args.lse_acc[slot * kChunkRows + r] = lse; else args.lse[q_row] = lse;
       }
       return true;
     };
@@ -698,8 +716,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 }
 
 // ----------------------------------------------------------------- merge of split blocks
-// out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  grid (U, 8 groups of 16
-// rows, 4 slices of 128 dims): 16 threads a row, 8 dims each, four splits in flight.
+// out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  grid (U, 2 CTAs x 8 warps of
+// the attention): a block of eight warps merges the 32 rows x 128 dims that one of its warps wrote, each
+// warp 16 of the dims (32 bytes of a bf16 row), four splits in flight.
 __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, int U, int capacity, int batch, int H,
                                                                 const float* o_acc, const float* lse_acc,
                                                                 __nv_bfloat16* out, float* lse) {
@@ -709,44 +728,40 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
     return;
   const ChunkLayout lay = chunk_layout(U, capacity, batch);
   const ChunkBlock b = reinterpret_cast<const ChunkBlock*>(sched + lay.blocks)[sched[lay.split_list + blockIdx.x]];
-  const int row = blockIdx.y * 16 + (threadIdx.x >> 4), sub = threadIdx.x & 15;
-  if (row >= b.ntok * H) return;  // (whole groups of 16 lanes)
+  const int rank = blockIdx.y >> 3, wi = blockIdx.y & 7, lane = threadIdx.x & 31, j = threadIdx.x >> 5;
+  const int L = 32 * (wi & 3) + lane, row = 64 * rank + (L & 63);
+  if (row >= b.ntok * H) return;
   const float* lsrc = lse_acc + (int64_t)b.offset * kChunkRows + row;
-  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
-  float M = -INFINITY, S = 0.f;
+  const float4* src = reinterpret_cast<const float4*>(o_acc) + (((int64_t)b.offset * 16 + blockIdx.y) * 32 + 4 * j) * 32 + lane;
+  constexpr int64_t kStep = 16 * 32 * 32;  // float4 per split
+  float M = -INFINITY;
   bool nan = false;  // a partial of NaN keys: the maximum would not show it
-  for (int i = sub; i < b.splits; i += 16) {
+  for (int i = 0; i < b.splits; ++i) {
     const float x = lsrc[(int64_t)i * kChunkRows];
     nan |= isnan(x);
     M = fmaxf(M, x);
   }
+  float S = 0.f;
+  float4 acc[4];
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(mask, M, o));
-  if (M > -INFINITY)
-    for (int i = sub; i < b.splits; i += 16) S += expf(lsrc[(int64_t)i * kChunkRows] - M);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) S += __shfl_xor_sync(mask, S, o);
-  nan = __any_sync(mask, nan);
-  const float Lt = nan ? NAN : M > -INFINITY ? M + logf(S) : -INFINITY;
-  const int c0 = 32 * blockIdx.z + sub;  // float4 columns c0 and c0 + 16
-  const float4* src = reinterpret_cast<const float4*>(o_acc) + ((int64_t)b.offset * kChunkRows + row) * 128 + c0;
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < b.splits; i0 += 4) {
-    float4 v[4][2];
+    float4 v[4][4];
     float x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool in = i0 + k < b.splits;
       x[k] = in ? lsrc[(int64_t)(i0 + k) * kChunkRows] : -INFINITY;
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
-        v[k][f] = in ? __ldcs(src + (int64_t)(i0 + k) * kChunkRows * 128 + 16 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int f = 0; f < 4; ++f)
+        v[k][f] = in ? __ldcs(src + (i0 + k) * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float wk = Lt == -INFINITY ? 0.f : expf(x[k] - Lt);
+      const float wk = M == -INFINITY ? 0.f : expf(x[k] - M);
+      S += wk;
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
+      for (int f = 0; f < 4; ++f) {
         acc[f].x += wk * v[k][f].x;
         acc[f].y += wk * v[k][f].y;
         acc[f].z += wk * v[k][f].z;
@@ -754,12 +769,15 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
       }
     }
   }
+  const float inv = nan ? NAN : M == -INFINITY ? 0.f : 1.f / S;
   const int64_t q_row = (int64_t)b.tok0 * H + row;
+  uint4* dst = reinterpret_cast<uint4*>(out + q_row * 512 + 256 * (wi >> 2) + 128 * (L >> 6) + 16 * j);
 #pragma unroll
   for (int f = 0; f < 2; ++f)
-    *reinterpret_cast<uint2*>(out + q_row * 512 + 4 * (c0 + 16 * f)) =
-        make_uint2(pack_bf16(acc[f].x, acc[f].y), pack_bf16(acc[f].z, acc[f].w));
-  if (sub == 0 && blockIdx.z == 0) lse[q_row] = Lt;
+    dst[f] = make_uint4(pack_bf16(acc[2 * f].x * inv, acc[2 * f].y * inv), pack_bf16(acc[2 * f].z * inv, acc[2 * f].w * inv),
+                        pack_bf16(acc[2 * f + 1].x * inv, acc[2 * f + 1].y * inv),
+                        pack_bf16(acc[2 * f + 1].z * inv, acc[2 * f + 1].w * inv));
+  if (j == 0 && (wi >> 2) == 0 && L < 64) lse[q_row] = nan ? NAN : M == -INFINITY ? -INFINITY : M + logf(S);
 }
 
 // ----------------------------------------------------------------- FP8 rows -> bf16 rows
