@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     if (k < nb) {
       const int b = chunk_find(blk_off, B, (int32_t)k);
       blocks[k] = chunk_make_block(cu, lens, b, (int)k, blk_off[b], tb, causal);
-      cost = blocks[k].nt + kChunkPieceCost;
+      cost = chunk_cost(blocks[k].nt);
     }
     const int64_t e = block_scan_1024(cost, sh, &sum);
     if (k < nb) pos[k] = (int32_t)(total + e);
@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
   }
   if (total > kMaxPlanPositions) return refuse();
   __syncthreads();
-  const bool shares = nb <= U;
+  bool shares = nb <= U;
   int64_t budget = plan_budget(total, U);
   if (shares) {
     if (tid < 32) {  // the least share that U units suffice for
@@ -919,10 +919,11 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
         for (int k = tid; k < nb; k += 32) need = min(need + chunk_shares(blocks[k].nt, m), 1 << 24);
         if (__reduce_add_sync(0xffffffffu, need) <= U) hi = m; else lo = m + 1;
       }
-      if (tid == 0) sh_share = longest <= lo + kChunkMergeCost ? longest : lo;
+      if (tid == 0) sh_share = chunk_share_tiles(longest, lo, budget);
     }
     __syncthreads();
-    budget = sh_share;
+    shares = sh_share > 0;
+    if (shares) budget = sh_share;
   }
   int64_t slots = 0, ns = 0, at = 0;
   for (int64_t k0 = 0; k0 < nb; k0 += 1024) {

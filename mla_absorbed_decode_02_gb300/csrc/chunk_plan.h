@@ -5,12 +5,12 @@
 // tokens, so with few heads several tokens share every key tile.  A block's tiles are 256 keys
 // each, up to what its last token sees; a block that sees nothing keeps one (fully masked) tile,
 // which writes its zero rows.  Blocks lie one after another on a line of cost positions
-// (kChunkPieceCost, then one per tile) and unit u owns the tiles in [u * budget, (u + 1) * budget):
+// (kChunkPieceCost, then kChunkTileCost per tile) and unit u owns the tiles in [u * budget, (u + 1) * budget):
 // long sequences are split over units ("MLA inference: two computation paths and FlashMLA",
 // section "Decode attention becomes a compute problem") and merged by their LSE.  Where there are
-// no more blocks than units, each unit takes one share of one block instead: shares of at most m
-// tiles, m the least that the units suffice for -- or whole blocks, where the longest is at most
-// kChunkMergeCost tiles longer than that, since then nothing has to be merged.
+// no more blocks than units, a unit can take one share of one block instead -- a whole block, which
+// needs no merging, or at most m tiles of one, m the least that the units suffice for -- and the
+// plan is the one of the three whose longest unit costs least.
 //
 // The per-item functions are shared by the scheduler kernel (which runs the prefix sums in
 // parallel) and the host twin.
@@ -26,16 +26,30 @@ constexpr int kChunkHeader = 16;              // int32 header words
 constexpr int kChunkBlockInts = 8;            // int32 words per block record
 constexpr int kChunkRows = 128;               // rows of a block (MMA M of a CTA pair)
 constexpr int kChunkTile = 256;               // keys of a tile (four pages)
-// Cost of a piece beyond its tiles, in tiles: the query load, the epilogue, the pipeline's refill.
-#ifndef MLA_CHUNK_PIECE_COST
-#define MLA_CHUNK_PIECE_COST 1
+// Cost positions of a tile, and of a piece beyond its tiles (the query load, the epilogue, the
+// pipeline's refill).
+#ifndef MLA_CHUNK_TILE_COST
+#define MLA_CHUNK_TILE_COST 4
 #endif
-constexpr int kChunkPieceCost = MLA_CHUNK_PIECE_COST;
+#ifndef MLA_CHUNK_PIECE_COST
+#define MLA_CHUNK_PIECE_COST 3
+#endif
+constexpr int kChunkTileCost = MLA_CHUNK_TILE_COST, kChunkPieceCost = MLA_CHUNK_PIECE_COST;
+MLA_HD inline int32_t chunk_cost(int32_t nt) { return kChunkPieceCost + kChunkTileCost * nt; }
 // What writing and merging the partial results of split blocks costs, in tiles.
 #ifndef MLA_CHUNK_MERGE_COST
 #define MLA_CHUNK_MERGE_COST 2
 #endif
 constexpr int kChunkMergeCost = MLA_CHUNK_MERGE_COST;
+// Tiles of a share (of whole blocks: `longest`), or 0 for stretches of `budget` positions.  The walk
+// over stretches needs a budget of at least a tile's cost.
+MLA_HD inline int32_t chunk_share_tiles(int32_t longest, int32_t least, int64_t budget) {
+  const int64_t merge = (int64_t)kChunkTileCost * kChunkMergeCost;
+  const int64_t whole = chunk_cost(longest), share = chunk_cost(least) + merge;
+  const int64_t stretch = budget >= kChunkTileCost ? budget + kChunkPieceCost + merge : INT64_MAX;
+  if (whole <= share && whole <= stretch) return longest;
+  return share <= stretch ? least : 0;
+}
 
 // header words
 enum { kChMagic = 0, kChUnits, kChCapacity, kChBlocks, kChSlots, kChBudget, kChTokens, kChNumSplit, kChPages, kChShares };
@@ -129,7 +143,7 @@ MLA_HD inline void chunk_unit(const ChunkBlock* blocks, const int32_t* pos, int 
   int a = 0, b = NB;  // first block whose last tile lies at or past lo
   while (a < b) {
     const int m = (a + b) / 2;
-    if ((int64_t)pos[m] + kChunkPieceCost + blocks[m].nt - 1 >= lo) b = m; else a = m + 1;
+    if ((int64_t)pos[m] + chunk_cost(blocks[m].nt - 1) >= lo) b = m; else a = m + 1;
   }
   if (a >= NB) return;
   const int64_t first0 = (int64_t)pos[a] + kChunkPieceCost;
@@ -139,18 +153,20 @@ MLA_HD inline void chunk_unit(const ChunkBlock* blocks, const int32_t* pos, int 
     const int m = (c + d) / 2;
     if ((int64_t)pos[m] + kChunkPieceCost < hi) c = m; else d = m;
   }
-  int64_t end = hi - ((int64_t)pos[c] + kChunkPieceCost);
+  int64_t end = (hi - ((int64_t)pos[c] + kChunkPieceCost) + kChunkTileCost - 1) / kChunkTileCost;
   if (end > blocks[c].nt) end = blocks[c].nt;
   rec[0] = a;
-  rec[1] = (int32_t)(lo > first0 ? lo - first0 : 0);
+  rec[1] = (int32_t)(lo > first0 ? (lo - first0 + kChunkTileCost - 1) / kChunkTileCost : 0);
   rec[2] = c;
   rec[3] = (int32_t)end;
   rec[4] = (int32_t)(u - first0 / budget);
 }
 
+// (The budget is at least a tile's cost -- with more blocks than units it always is -- so every unit between
+// a block's first and its last holds some of its tiles.)
 MLA_HD inline int32_t chunk_splits(int32_t pos, int32_t nt, int64_t budget) {
   const int64_t first = (int64_t)pos + kChunkPieceCost;
-  return (int32_t)((first + nt - 1) / budget - first / budget + 1);
+  return (int32_t)((first + kChunkTileCost * (int64_t)(nt - 1)) / budget - first / budget + 1);
 }
 
 // Shares of a block of nt tiles in shares of at most m tiles, made equal.
@@ -205,10 +221,10 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
     blocks[k] = chunk_make_block(cu, lens, b, k, blk_off[b], tb, causal);
     if (blocks[k].nt > longest) longest = blocks[k].nt;
     pos[k] = (int32_t)total;
-    total += blocks[k].nt + kChunkPieceCost;
+    total += chunk_cost(blocks[k].nt);
   }
   if (total > kMaxPlanPositions) return false;
-  const bool shares = nb <= U;
+  bool shares = nb <= U;
   int64_t budget = plan_budget(total, U);
   if (shares) {
     int32_t lo = 1, hi = longest;  // the least m that U units suffice for
@@ -218,7 +234,9 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
       for (int k = 0; k < nb; ++k) need += chunk_shares(blocks[k].nt, m);
       if (need <= U) hi = m; else lo = m + 1;
     }
-    budget = longest <= lo + kChunkMergeCost ? longest : lo;
+    const int32_t m = chunk_share_tiles(longest, lo, budget);
+    shares = m > 0;
+    if (shares) budget = m;
   }
   int64_t at = 0;
   int32_t slots = 0, ns = 0;

@@ -56,7 +56,8 @@ __device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&
 // ----------------------------------------------------------------- append
 // Token t of the ragged buffer belongs to the sequence b with cu[b] <= t < cu[b + 1] and goes to
 // row L_b - n_b + (t - cu[b]) of that sequence.  A warp takes a token: its row is loaded first,
-// then the sequence is found by a 32-way search (two rounds for up to 1024 sequences).
+// then the sequence is found by a 32-way search (one round for up to 31 sequences, two for up to
+// ~1000).
 template <bool kFp8>
 __global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max_tokens, const __nv_bfloat16* latent,
                                                          int64_t latent_stride, const __nv_bfloat16* rope,
@@ -66,22 +67,29 @@ __global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max
   const int lane = threadIdx.x & 31;
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  const int32_t end = cu[p.batch];
-  if (t >= max_tokens || t >= end) return;  // rows behind the last sequence
+  if (t >= max_tokens) return;
   const uint4* src = reinterpret_cast<const uint4*>(latent + t * latent_stride);
   const uint4 a = src[kFp8 ? 2 * lane : lane], b = src[kFp8 ? 2 * lane + 1 : lane + 32];
   uint4 kr = make_uint4(0, 0, 0, 0);
   if (lane < 8) kr = *reinterpret_cast<const uint4*>(rope + t * rope_stride + 8 * lane);
+  const int32_t end = cu[p.batch];
   int lo = 0, hi = p.batch;  // cu[lo] <= t < cu[hi]
-  while (hi - lo > 1) {
+  while (hi - lo > 31) {
     const int step = (hi - lo + 31) >> 5, at = lo + step * lane;
     const uint32_t le = __ballot_sync(0xffffffffu, at < hi && cu[at] <= t);
     const int k = le ? 31 - __clz(le) : 0;
     hi = min(hi, lo + step * (k + 1));
     lo = lo + step * k;
   }
-  const int n = cu[lo + 1] - cu[lo];
-  const int64_t pos = (int64_t)lens[lo] - n + (t - cu[lo]);
+  // the last round: lane j holds cu[lo + j] and the length of sequence lo + j
+  const int32_t start = lo + lane <= p.batch ? cu[lo + lane] : INT32_MAX;
+  const int32_t len = lo + lane < p.batch ? lens[lo + lane] : 0;
+  if (t >= end) return;  // rows behind the last sequence
+  const uint32_t le = __ballot_sync(0xffffffffu, lo + lane < hi && start <= t);
+  const int k = le ? 31 - __clz(le) : 0;  // (at most 30: the next sequence's start is a lane's too)
+  lo += k;
+  const int first = __shfl_sync(0xffffffffu, start, k), n = __shfl_sync(0xffffffffu, start, k + 1) - first;
+  const int64_t pos = (int64_t)__shfl_sync(0xffffffffu, len, k) - n + (t - first);
   if (n < 0 || pos < 0 || pos >= (int64_t)p.max_pages * kPageRows) {
     if (lane == 0) pool_error(1);
     return;
