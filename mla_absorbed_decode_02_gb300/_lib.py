@@ -293,12 +293,14 @@ def mla_extend(p: MlaExtendParams, q_nope, q_rope, kv_pages, block_table, cache_
                                      _ptr(workspace), _stream(stream)), "mla_extend")
 
 
-def _expect(call: str, *wanted):
-    """Each of (name, tensor, dtype, shape): a contiguous tensor of that type and shape.  The library itself sees
-    pointers alone, so what it cannot check is checked here."""
-    for name, t, dtype, shape in wanted:
-        if t is None or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-            raise MlaError(MLA_ERR_INVALID_ARG, f"{call}: {name}")
+def _bad(t, dtype, shape) -> bool:
+    """Not a contiguous tensor of this type and shape.  The library sees pointers alone, so what it cannot check is
+    checked here (inline in each call: a step's small operations are bound by the host)."""
+    return t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+
+
+def _refuse(what: str, status: int = MLA_ERR_INVALID_ARG):
+    raise MlaError(status, what)
 
 
 def _expect_pool(call: str, t, p, num_layers: int = 1, layer_stride: int = 0):
@@ -306,7 +308,7 @@ def _expect_pool(call: str, t, p, num_layers: int = 1, layer_stride: int = 0):
     pool = p.num_pages * (64 * 1152 if p.kv_dtype == MLA_KV_BF16 else 64 * 656)
     if (t is None or not t.is_contiguous()
             or t.numel() * t.element_size() < (num_layers - 1) * (layer_stride or pool) + pool):
-        raise MlaError(MLA_ERR_INVALID_ARG, call + ": kv_pages")
+        _refuse(call + ": kv_pages")
 
 
 def mla_chunk_workspace_size(p: MlaChunkParams):
@@ -333,9 +335,11 @@ def mla_chunk_plan_host(p: MlaChunkParams, num_units: int, cu_seqlens, cache_seq
 def mla_chunk_schedule(p: MlaChunkParams, cu_seqlens, cache_seqlens, sched, stream=None):
     """Work plan of ragged chunks: cu_seqlens int32 [B + 1], cache_seqlens int32 [B] (new tokens included)."""
     i32 = _dtypes()[0]
-    _expect("mla_chunk_schedule", ("cu_seqlens", cu_seqlens, i32, (p.batch + 1,)),
-            ("cache_seqlens", cache_seqlens, i32, (p.batch,)))
-    _check(load_library().mla_chunk_schedule(ctypes.byref(p), _ptr(cu_seqlens), _ptr(cache_seqlens), _ptr(sched),
+    if _bad(cu_seqlens, i32, (p.batch + 1,)):
+        _refuse("mla_chunk_schedule: cu_seqlens")
+    if _bad(cache_seqlens, i32, (p.batch,)):
+        _refuse("mla_chunk_schedule: cache_seqlens")
+    _check(load_library().mla_chunk_schedule(ctypes.byref(p), cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), _ptr(sched),
                                              _stream(stream)), "mla_chunk_schedule")
 
 
@@ -345,9 +349,18 @@ def mla_chunk_attend(p: MlaChunkParams, q_nope_absorbed, q_rope, kv_pages, block
     lse float32 [T, H]."""
     T, H, B = p.max_tokens, p.num_heads, p.batch
     i32, f32, bf16 = _dtypes()
-    _expect("mla_chunk_attend", ("q_nope_absorbed", q_nope_absorbed, bf16, (T, H, 512)), ("q_rope", q_rope, bf16, (T, H, 64)),
-            ("block_table", block_table, i32, (B, p.max_pages_per_seq)), ("cache_seqlens", cache_seqlens, i32, (B,)),
-            ("out", out, bf16, (T, H, 512)), ("lse", lse, f32, (T, H)))
+    if _bad(q_nope_absorbed, bf16, (T, H, 512)):
+        _refuse("mla_chunk_attend: q_nope_absorbed")
+    if _bad(q_rope, bf16, (T, H, 64)):
+        _refuse("mla_chunk_attend: q_rope")
+    if _bad(block_table, i32, (B, p.max_pages_per_seq)):
+        _refuse("mla_chunk_attend: block_table")
+    if _bad(cache_seqlens, i32, (B,)):
+        _refuse("mla_chunk_attend: cache_seqlens")
+    if _bad(out, bf16, (T, H, 512)):
+        _refuse("mla_chunk_attend: out")
+    if _bad(lse, f32, (T, H)):
+        _refuse("mla_chunk_attend: lse")
     _expect_pool("mla_chunk_attend", kv_pages, p)
     _check(load_library().mla_chunk_attend(ctypes.byref(p), _ptr(q_nope_absorbed), _ptr(q_rope), _ptr(kv_pages),
                                            _ptr(block_table), _ptr(cache_seqlens), float(scale), _ptr(out), _ptr(lse),
@@ -361,18 +374,22 @@ def mla_append_kv(p: MlaPoolParams, latent, k_rope, cu_seqlens, cache_seqlens, b
     B = p.batch
     for name, t, n in (("latent", latent, 512), ("k_rope", k_rope, 64)):
         if t is None or t.dtype != bf16 or t.dim() != 2 or t.shape[1] != n or t.stride(1) != 1:
-            raise MlaError(MLA_ERR_INVALID_ARG, "mla_append_kv: " + name)
+            _refuse("mla_append_kv: " + name)
     if k_rope.shape[0] != latent.shape[0]:
-        raise MlaError(MLA_ERR_INVALID_ARG, "mla_append_kv: k_rope")
-    _expect("mla_append_kv", ("cu_seqlens", cu_seqlens, i32, (B + 1,)), ("cache_seqlens", cache_seqlens, i32, (B,)),
-            ("block_table", block_table, i32, (B, p.max_pages_per_seq)))
+        _refuse("mla_append_kv: k_rope")
+    if _bad(cu_seqlens, i32, (B + 1,)):
+        _refuse("mla_append_kv: cu_seqlens")
+    if _bad(cache_seqlens, i32, (B,)):
+        _refuse("mla_append_kv: cache_seqlens")
+    if _bad(block_table, i32, (B, p.max_pages_per_seq)):
+        _refuse("mla_append_kv: block_table")
     _expect_pool("mla_append_kv", kv_pages, p)
     if latent.shape[0] == 0:
         return
     # (one row: its stride says nothing)
     ls, rs = (int(t.stride(0)) if t.shape[0] > 1 else n for t, n in ((latent, 512), (k_rope, 64)))
-    _check(load_library().mla_append_kv(ctypes.byref(p), int(latent.shape[0]), _ptr(latent), ls, _ptr(k_rope), rs,
-                                        _ptr(cu_seqlens), _ptr(cache_seqlens), _ptr(block_table), _ptr(kv_pages),
+    _check(load_library().mla_append_kv(ctypes.byref(p), int(latent.shape[0]), latent.data_ptr(), ls, k_rope.data_ptr(), rs,
+                                        cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(), kv_pages.data_ptr(),
                                         _stream(stream)), "mla_append_kv")
 
 
@@ -383,33 +400,37 @@ def mla_pool_workspace_size(p: MlaPoolParams, max_forks: int) -> int:
     return n.value
 
 
-def _tables(p: MlaPoolParams, block_table, cache_seqlens, ref_counts):
+def _expect_tables(call: str, p: MlaPoolParams, block_table, cache_seqlens, ref_counts):
     i32 = _dtypes()[0]
-    return (("block_table", block_table, i32, (p.batch, p.max_pages_per_seq)),
-            ("cache_seqlens", cache_seqlens, i32, (p.batch,)), ("ref_counts", ref_counts, i32, (p.num_pages,)))
+    if _bad(block_table, i32, (p.batch, p.max_pages_per_seq)):
+        _refuse(call + ": block_table")
+    if _bad(cache_seqlens, i32, (p.batch,)):
+        _refuse(call + ": cache_seqlens")
+    if _bad(ref_counts, i32, (p.num_pages,)):
+        _refuse(call + ": ref_counts")
 
 
 def _expect_workspace(call: str, p: MlaPoolParams, workspace, forks: int = 0):
     if workspace is None or workspace.numel() * workspace.element_size() < mla_pool_workspace_size(p, forks):
-        raise MlaError(MLA_ERR_WORKSPACE, call + ": workspace")
+        _refuse(call + ": workspace", MLA_ERR_WORKSPACE)
 
 
 def _list_of(call: str, name: str, t) -> int:
     """Length of a one-dimensional int32 list."""
-    if t is None or t.dim() != 1:
-        raise MlaError(MLA_ERR_INVALID_ARG, f"{call}: {name}")
-    _expect(call, (name, t, _dtypes()[0], t.shape))
-    return int(t.shape[0])
+    if t is None or t.dim() != 1 or _bad(t, _dtypes()[0], t.shape):
+        _refuse(f"{call}: {name}")
+    return t.numel()
 
 
 def mla_copy_pages(p: MlaPoolParams, kv_pages, src_pages, dst_pages, stream=None):
     """Page dst_pages[i] := page src_pages[i] in every layer (int32 [n])."""
     n = _list_of("mla_copy_pages", "src_pages", src_pages)
-    _expect("mla_copy_pages", ("dst_pages", dst_pages, _dtypes()[0], (n,)))
+    if _bad(dst_pages, _dtypes()[0], (n,)):
+        _refuse("mla_copy_pages: dst_pages")
     _expect_pool("mla_copy_pages", kv_pages, p, p.num_layers, p.layer_stride)
     if n == 0:
         return
-    _check(load_library().mla_copy_pages(ctypes.byref(p), _ptr(kv_pages), _ptr(src_pages), _ptr(dst_pages), n,
+    _check(load_library().mla_copy_pages(ctypes.byref(p), kv_pages.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(), n,
                                          _stream(stream)), "mla_copy_pages")
 
 
@@ -423,14 +444,17 @@ def mla_fork_sequences(p: MlaPoolParams, kv_pages, parents, children, block_tabl
 def _fork(p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, workspace, stream):
     n = _list_of("mla_fork_sequences", "parents", parents)
     i32 = _dtypes()[0]
-    _expect("mla_fork_sequences", ("children", children, i32, (n,)), ("new_pages", new_pages, i32, (n,)),
-            *_tables(p, block_table, cache_seqlens, ref_counts))
+    if _bad(children, i32, (n,)):
+        _refuse("mla_fork_sequences: children")
+    if _bad(new_pages, i32, (n,)):
+        _refuse("mla_fork_sequences: new_pages")
+    _expect_tables("mla_fork_sequences", p, block_table, cache_seqlens, ref_counts)
     _expect_pool("mla_fork_sequences", kv_pages, p, p.num_layers, p.layer_stride)
     if n == 0:
         return
-    _check(load_library().mla_fork_sequences(ctypes.byref(p), _ptr(kv_pages), _ptr(parents), _ptr(children), n,
-                                             _ptr(block_table), _ptr(cache_seqlens), _ptr(ref_counts),
-                                             _ptr(new_pages), _ptr(workspace), _stream(stream)),
+    _check(load_library().mla_fork_sequences(ctypes.byref(p), kv_pages.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
+                                             block_table.data_ptr(), cache_seqlens.data_ptr(), ref_counts.data_ptr(),
+                                             new_pages.data_ptr(), _ptr(workspace), _stream(stream)),
            "mla_fork_sequences")
 
 
@@ -442,21 +466,24 @@ def mla_reserve_pages(p: MlaPoolParams, num_new, block_table, cache_seqlens, ref
 
 def _reserve(p, num_new, block_table, cache_seqlens, ref_counts, served, workspace, stream):
     i32 = _dtypes()[0]
-    _expect("mla_reserve_pages", ("num_new", num_new, i32, (p.batch,)), ("served", served, i32, (p.batch,)),
-            *_tables(p, block_table, cache_seqlens, ref_counts))
-    _check(load_library().mla_reserve_pages(ctypes.byref(p), _ptr(num_new), _ptr(block_table), _ptr(cache_seqlens),
-                                            _ptr(ref_counts), _ptr(served), _ptr(workspace), _stream(stream)),
+    if _bad(num_new, i32, (p.batch,)):
+        _refuse("mla_reserve_pages: num_new")
+    if _bad(served, i32, (p.batch,)):
+        _refuse("mla_reserve_pages: served")
+    _expect_tables("mla_reserve_pages", p, block_table, cache_seqlens, ref_counts)
+    _check(load_library().mla_reserve_pages(ctypes.byref(p), num_new.data_ptr(), block_table.data_ptr(), cache_seqlens.data_ptr(),
+                                            ref_counts.data_ptr(), served.data_ptr(), _ptr(workspace), _stream(stream)),
            "mla_reserve_pages")
 
 
 def mla_free_sequences(p: MlaPoolParams, sequences, block_table, cache_seqlens, ref_counts, stream=None):
     """Ends the sequences (int32 [n], rows of the block table) and gives their pages back."""
     n = _list_of("mla_free_sequences", "sequences", sequences)
-    _expect("mla_free_sequences", *_tables(p, block_table, cache_seqlens, ref_counts))
+    _expect_tables("mla_free_sequences", p, block_table, cache_seqlens, ref_counts)
     if n == 0:
         return
-    _check(load_library().mla_free_sequences(ctypes.byref(p), _ptr(sequences), n, _ptr(block_table),
-                                             _ptr(cache_seqlens), _ptr(ref_counts), _stream(stream)),
+    _check(load_library().mla_free_sequences(ctypes.byref(p), sequences.data_ptr(), n, block_table.data_ptr(),
+                                             cache_seqlens.data_ptr(), ref_counts.data_ptr(), _stream(stream)),
            "mla_free_sequences")
 
 
@@ -468,11 +495,12 @@ def mla_compact_pages(p: MlaPoolParams, kv_pages, block_table, cache_seqlens, re
 
 
 def _compact(p, kv_pages, block_table, cache_seqlens, ref_counts, num_used, workspace, stream):
-    _expect("mla_compact_pages", ("num_used", num_used, _dtypes()[0], (1,)),
-            *_tables(p, block_table, cache_seqlens, ref_counts))
+    if _bad(num_used, _dtypes()[0], (1,)):
+        _refuse("mla_compact_pages: num_used")
+    _expect_tables("mla_compact_pages", p, block_table, cache_seqlens, ref_counts)
     _expect_pool("mla_compact_pages", kv_pages, p, p.num_layers, p.layer_stride)
-    _check(load_library().mla_compact_pages(ctypes.byref(p), _ptr(kv_pages), _ptr(block_table), _ptr(cache_seqlens),
-                                            _ptr(ref_counts), _ptr(num_used), _ptr(workspace), _stream(stream)),
+    _check(load_library().mla_compact_pages(ctypes.byref(p), kv_pages.data_ptr(), block_table.data_ptr(), cache_seqlens.data_ptr(),
+                                            ref_counts.data_ptr(), num_used.data_ptr(), _ptr(workspace), _stream(stream)),
            "mla_compact_pages")
 
 
@@ -539,7 +567,7 @@ class ChunkAttention:
     def attend(self, q_nope_absorbed, q_rope, kv_pages, block_table, scale, out=None, lse=None, stream=None):
         import torch
         if self.seqlens is None:
-            raise MlaError(MLA_ERR_WORKSPACE, "ChunkAttention.attend before plan")
+            _refuse("ChunkAttention.attend before plan", MLA_ERR_WORKSPACE)
         if out is None:
             out = torch.empty_like(q_nope_absorbed)
         if lse is None:
@@ -567,25 +595,21 @@ class PagePool:
         return (torch.full((p.batch, p.max_pages_per_seq), -1, **kw), torch.zeros(p.batch, **kw),
                 torch.zeros(p.num_pages, **kw))
 
-    def _outcome(self, n: int):
-        import torch
-        return torch.empty(n, dtype=torch.int32, device=self.device)
-
     def copy(self, kv_pages, src_pages, dst_pages, stream=None):
         mla_copy_pages(self.p, kv_pages, src_pages, dst_pages, stream)
 
     def fork(self, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns new_pages int32 [n]: the child's own page, -1 (none needed), -2 (refused), -3 (no page left)."""
         if parents.numel() > self.max_forks:
-            raise MlaError(MLA_ERR_WORKSPACE, "PagePool.fork: more forks than max_forks")
-        new_pages = self._outcome(parents.numel())
+            _refuse("PagePool.fork: more forks than max_forks", MLA_ERR_WORKSPACE)
+        new_pages = parents.new_empty(parents.shape)
         _fork(self.p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, self.workspace,
               stream)
         return new_pages
 
     def reserve(self, num_new, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns served int32 [batch]: 1 (done), 0 (not enough pages), -2 (refused)."""
-        served = self._outcome(self.p.batch)
+        served = num_new.new_empty(num_new.shape)
         _reserve(self.p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
         return served
 
@@ -594,6 +618,6 @@ class PagePool:
 
     def compact(self, kv_pages, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns the number of used pages, int32 [1] on the device."""
-        used = self._outcome(1)
+        used = cache_seqlens.new_empty(1)
         _compact(self.p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
         return used
