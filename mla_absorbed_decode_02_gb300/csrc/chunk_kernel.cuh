@@ -152,12 +152,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
   return ok != 0;
 }
-// Bounded wait by a converged warp (the lanes agree but for a wait that runs out, and then all leave).
-__device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  return wait_one<true>(bar, parity, w, site);
-}
-
 // One tile of a unit's work.
 struct ChunkTileRef {
   ChunkBlock b;
@@ -303,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 #pragma unroll 1
       for (int d = 0; d < 9; ++d, advance()) {
         if (turn != warp) continue;
-        if (!wait_uniform(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
+        if (!wait_warp<true>(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
         const uint32_t full = lead0 + 8 * (CB_FULL + slot), dst = base + CK_RING + slot * kCkSlot;
         if (el) {
           if (np == 0) {
@@ -326,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 #pragma unroll 1
         for (int n = 0; n < 2; ++n, advance()) {
           if (turn != warp) continue;
-          if (!wait_uniform(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
+          if (!wait_warp<true>(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
           const uint32_t full = lead0 + 8 * (CB_FULL + slot), dst = base + CK_RING + slot * kCkSlot;
           const int z = 4 * n + 2 * (int)rank;  // dims 256 n + 128 rank, in blocks of 64
           if (key0 + 64 <= some) {
@@ -397,68 +391,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       const uint64_t desc_v = smem_desc(base + CK_RING, kCkBlk, 1024, kSwizzle128B);
       const bool el = elect_one();
       uint32_t slot = 0, phase = 0, g = 0, piece = 0;
-      auto advance = [&]() {
+      uint32_t at = 0;  // the slot at hand
+      // Each lane waits for itself: a vote on every slot costs 3% of the kernel.  Lanes can part only
+      // where a wait runs out; no lane waits for another before all have left these loops.
+      auto wait = [&](uint32_t b, uint32_t parity, int site) -> bool { return wait_one<true>(b, parity, wc, site); };
+      // (bytes that a copy brought are the barrier's to order; rows that a warp of the other CTA wrote --
+      // `written` -- need an acquire of the pair's scope)
+      auto take = [&](bool written) -> bool {
+        const uint32_t full = bar(CB_FULL + slot);
+        if (!((!written && mbar_try_wait(full, phase)) || wait(full, phase, kSiteCkRing))) return false;
+        at = slot;
         if (++slot == kCkSlots) {
           slot = 0;
           phase ^= 1;
         }
+        return true;
       };
       auto qk = [&](const ChunkTileRef& r, uint32_t t) -> bool {
         if (r.first) {
-          if (!wait_uniform(bar(CB_Q_FULL), piece & 1, wc, kSiteCkQ)) return false;
+          if (!wait(bar(CB_Q_FULL), piece & 1, kSiteCkQ)) return false;
           ++piece;
         }
-        if (t >= 2 && !wait_uniform(bar(CB_S_EMPTY + (t & 1)), ((t >> 1) - 1) & 1, wc, kSiteCkScores)) return false;
+        if (t >= 2 && !wait(bar(CB_S_EMPTY + (t & 1)), ((t >> 1) - 1) & 1, kSiteCkScores)) return false;
+        tc_fence_after();
         const uint32_t d_tmem = tmem + CT_S + 128 * (t & 1);
 #pragma unroll
         for (int d = 0; d < 9; ++d) {
-          if (!wait_uniform(bar(CB_FULL + slot), phase, wc, kSiteCkRing)) return false;
-          tc_fence_after();
-          const uint64_t da = desc_q + d * (kCkBlk >> 4), db = desc_k + slot * (kCkSlot >> 4);
+          if (!take(false)) return false;
+          const uint64_t da = desc_q + d * (kCkBlk >> 4), db = desc_k + at * (kCkSlot >> 4);
           if (el) {
             mma2_bf16_ss(d_tmem, da, db, id_qk, d ? 1u : 0u);
             mma2_bf16_ss(d_tmem, da + 2, db + 2, id_qk, 1u);
             mma2_bf16_ss(d_tmem, da + 4, db + 4, id_qk, 1u);
             mma2_bf16_ss(d_tmem, da + 6, db + 6, id_qk, 1u);
-            mma2_commit_both(bar(CB_EMPTY + slot));
+            mma2_commit_both(bar(CB_EMPTY + at));
           }
-          __syncwarp();
-          advance();
         }
         if (el) {
           mma2_commit_both(bar(CB_S_FULL + (t & 1)));
           if (r.last) mma2_commit_both(bar(CB_Q_EMPTY));
         }
-        __syncwarp();
         return true;
       };
       auto pv = [&](const ChunkTileRef& r, uint32_t t) -> bool {
-        if (!wait_uniform(bar(CB_P_FULL), t & 1, wc, kSiteCkP)) return false;
-        const int np = r.pages();
+        if (!wait(bar(CB_P_FULL), t & 1, kSiteCkP)) return false;
+        tc_fence_after();
+        const int np = r.pages(), some = chunk_visible(r.b, 0, args.causal);
 #pragma unroll 1
         for (int kb = 0; kb < np; ++kb) {
+          const bool written = kChunkTile * r.tile + 64 * kb + 64 > some;  // the copying warp looked through it
           const int steps = (min(r.vis - kChunkTile * r.tile - 64 * kb, 64) + 15) >> 4;
           const uint32_t acc = !r.first || kb > 0 ? 1u : 0u;
           const uint64_t da = desc_p + kb * (kCkBlk >> 4);
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            if (!wait_uniform(bar(CB_FULL + slot), phase, wc, kSiteCkRing)) return false;
-            tc_fence_after();
+            if (!take(written)) return false;
             const uint32_t d_tmem = tmem + CT_O + 128 * n;
-            const uint64_t db = desc_v + slot * (kCkSlot >> 4);
+            const uint64_t db = desc_v + at * (kCkSlot >> 4);
             if (el) {
               mma2_bf16_ss(d_tmem, da, db, id_pv, acc);
               if (steps > 1) mma2_bf16_ss(d_tmem, da + 2, db + 128, id_pv, 1u);
               if (steps > 2) mma2_bf16_ss(d_tmem, da + 4, db + 256, id_pv, 1u);
               if (steps > 3) mma2_bf16_ss(d_tmem, da + 6, db + 384, id_pv, 1u);
-              mma2_commit_both(bar(CB_EMPTY + slot));
+              mma2_commit_both(bar(CB_EMPTY + at));
             }
-            __syncwarp();
-            advance();
           }
         }
         if (el) mma2_commit_both(bar(CB_P_FREE));
-        __syncwarp();
         return true;
       };
       ChunkTileRef a, b;
@@ -499,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
           tma_prefetch_2d(&args.map_qr, 0, row);
         }
         __syncwarp();
-        if (!wait_uniform(bar(CB_Q_EMPTY), (piece - 1) & 1, wc, kSiteCkQ)) break;
+        if (!wait_warp<true>(bar(CB_Q_EMPTY), (piece - 1) & 1, wc, kSiteCkQ)) break;
       }
       if (el) {
         mbar_arrive_expect_tx_remote(full, 9 * kCkBlk);
