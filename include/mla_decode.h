@@ -335,7 +335,8 @@ typedef struct mla_chunk_params {
   int32_t causal;            /* nonzero: token i of b sees keys 0 .. L_b - n_b + i; zero: all L_b */
   int32_t kv_dtype;          /* mla_kv_dtype */
   int32_t num_units;         /* work units (one CTA pair each); 0 = as many as fit at once */
-  int32_t timeout_us;        /* limit of every bounded wait inside the kernels; 0 = 2,000,000 us */
+  int32_t timeout_us;        /* limit of every bounded wait inside the kernels; 0 = 2,000,000 us.  A wait can
+                                last as long as a unit's largest piece, about 3.3 us per 256 keys */
   int64_t max_kv_tokens;     /* FP8 cache: room for the expanded rows in the workspace, in tokens: at
                                 least the sum of 64 * ceil(L_b / 64) over the sequences with n_b > 0
                                 (a plan that needs more is refused).  bf16 cache: not used */
@@ -377,7 +378,8 @@ int32_t mla_chunk_schedule(const mla_chunk_params* p, const int32_t* cu_seqlens,
  *   out              device bf16 [T][H][512], latent outputs (W_UV is not applied)
  *   lse              device float32 [T][H], natural log; a token that sees no key gets out = 0,
  *                    lse = -inf.  Rows of tokens at or past cu_seqlens[B] are left as they were
- *   sched            device, from mla_chunk_schedule with the same p
+ *   sched            device, from mla_chunk_schedule with the same p (metadata of other params sets
+ *                    MLA_ERR_WORKSPACE in the device error word, and nothing is written)
  *   workspace        device, workspace_bytes, 256-byte aligned; not shared by calls that overlap
  * Scores, softmax statistics and sums are float32; P is bf16 for the P.V product.  A row of the
  * cache that is not finite makes NaN of the tokens that see it and of no others.  Cache rows past
@@ -394,7 +396,7 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
  * 0x4D4C4143, [1] = units, [2] = block capacity, [3] = blocks, [4] = partial slots, [5] = budget of
  * cost positions per unit, [6] = tokens per block, [7] = split blocks, [8] = pages of the sequences
  * with new tokens, [9] = 1: no more blocks than units, each unit has one share of one block, and [5]
- * is the most tiles of a share; [10..15] = 0; then per unit 8 ints {first block, first tile, last block, end tile,
+ * is the most tiles of a share; [10] = B, [11] = causal, [12..15] = 0; then per unit 8 ints {first block, first tile, last block, end tile,
  * split index of the first piece, 0, 0, 0} (first block -1: no work); then per block 8 ints {first
  * token, tokens, sequence, keys the first token sees before clipping, L, tiles of 256 keys, splits,
  * first slot}; then the split blocks, and the first page of each sequence.
@@ -475,7 +477,7 @@ int32_t mla_fork_sequences(const mla_pool_params* p, void* kv_pages, const int32
  * table row lacks are taken, and its length grows by num_new[b].
  *   served  device int32 [batch]: 1: done; 0: not enough free pages (sequences are served in order, up to
  *           the first whose pages are not there; later ones that need no page are served); -2: refused (a
- *           negative count, or a length past the block table; sets MLA_ERR_INVALID_ARG in the device error word)
+ *           negative count or length, or one past the block table; sets MLA_ERR_INVALID_ARG in the device error word)
  * A sequence that is not served keeps its length and pages.  A last page that others share must not be
  * grown into: mla_fork_sequences leaves none.
  */
@@ -485,7 +487,8 @@ int32_t mla_reserve_pages(const mla_pool_params* p, const int32_t* num_new, int3
 /*
  * Ends sequences (device int32 [num_sequences], rows of the block table; a row named twice is ended
  * once): each of its pages loses one reference, its table entries become -1 and its length 0.  A row
- * out of range, or a page without a reference, sets MLA_ERR_INVALID_ARG in the device error word.
+ * out of range, a length outside 0 .. 64 * max_pages_per_seq (both left as they are), or a page without a
+ * reference sets MLA_ERR_INVALID_ARG in the device error word.
  */
 int32_t mla_free_sequences(const mla_pool_params* p, const int32_t* sequences, int32_t num_sequences, int32_t* block_table,
                            int32_t* cache_seqlens, int32_t* ref_counts, void* stream);

@@ -303,6 +303,17 @@ def _refuse(what: str, status: int = MLA_ERR_INVALID_ARG):
     raise MlaError(status, what)
 
 
+def _expect_device(call: str, first, *others):
+    """All on the current CUDA device: a pointer of the host or of another device must not reach a kernel."""
+    import torch
+    d = first.get_device()
+    for t in others:
+        if t.get_device() != d:
+            _refuse(call + ": tensors on different devices")
+    if d < 0 or d != torch._C._cuda_getDevice():
+        _refuse(call + ": tensors are not on the current CUDA device")
+
+
 def _expect_pool(call: str, t, p, num_layers: int = 1, layer_stride: int = 0):
     """The pools' pages: large enough for the last layer's last page, rows not strided."""
     pool = p.num_pages * (64 * 1152 if p.kv_dtype == MLA_KV_BF16 else 64 * 656)
@@ -339,7 +350,10 @@ def mla_chunk_schedule(p: MlaChunkParams, cu_seqlens, cache_seqlens, sched, stre
         _refuse("mla_chunk_schedule: cu_seqlens")
     if _bad(cache_seqlens, i32, (p.batch,)):
         _refuse("mla_chunk_schedule: cache_seqlens")
-    _check(load_library().mla_chunk_schedule(ctypes.byref(p), cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), _ptr(sched),
+    if sched is None or sched.numel() * sched.element_size() < mla_chunk_workspace_size(p)[0]:
+        _refuse("mla_chunk_schedule: sched", MLA_ERR_WORKSPACE)
+    _expect_device("mla_chunk_schedule", cu_seqlens, cache_seqlens, sched)
+    _check(load_library().mla_chunk_schedule(ctypes.byref(p), cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), sched.data_ptr(),
                                              _stream(stream)), "mla_chunk_schedule")
 
 
@@ -347,6 +361,14 @@ def mla_chunk_attend(p: MlaChunkParams, q_nope_absorbed, q_rope, kv_pages, block
                      out, lse, sched, workspace, stream=None):
     """Attention of ragged chunks over the paged cache: q bf16 [T, H, 512] and [T, H, 64], out bf16 [T, H, 512],
     lse float32 [T, H]."""
+    sb, wb = mla_chunk_workspace_size(p)
+    for name, t, n in (("sched", sched, sb), ("workspace", workspace, wb)):
+        if t is None or t.numel() * t.element_size() < n:
+            _refuse("mla_chunk_attend: " + name, MLA_ERR_WORKSPACE)
+    _attend(p, q_nope_absorbed, q_rope, kv_pages, block_table, cache_seqlens, scale, out, lse, sched, workspace, stream)
+
+
+def _attend(p, q_nope_absorbed, q_rope, kv_pages, block_table, cache_seqlens, scale, out, lse, sched, workspace, stream):
     T, H, B = p.max_tokens, p.num_heads, p.batch
     i32, f32, bf16 = _dtypes()
     if _bad(q_nope_absorbed, bf16, (T, H, 512)):
@@ -362,6 +384,8 @@ def mla_chunk_attend(p: MlaChunkParams, q_nope_absorbed, q_rope, kv_pages, block
     if _bad(lse, f32, (T, H)):
         _refuse("mla_chunk_attend: lse")
     _expect_pool("mla_chunk_attend", kv_pages, p)
+    _expect_device("mla_chunk_attend", q_nope_absorbed, q_rope, kv_pages, block_table, cache_seqlens, out, lse, sched,
+                   workspace)
     _check(load_library().mla_chunk_attend(ctypes.byref(p), _ptr(q_nope_absorbed), _ptr(q_rope), _ptr(kv_pages),
                                            _ptr(block_table), _ptr(cache_seqlens), float(scale), _ptr(out), _ptr(lse),
                                            _ptr(sched), _ptr(workspace), _stream(stream)), "mla_chunk_attend")
@@ -386,6 +410,7 @@ def mla_append_kv(p: MlaPoolParams, latent, k_rope, cu_seqlens, cache_seqlens, b
     _expect_pool("mla_append_kv", kv_pages, p)
     if latent.shape[0] == 0:
         return
+    _expect_device("mla_append_kv", latent, k_rope, cu_seqlens, cache_seqlens, block_table, kv_pages)
     # (one row: its stride says nothing)
     ls, rs = (int(t.stride(0)) if t.shape[0] > 1 else n for t, n in ((latent, 512), (k_rope, 64)))
     _check(load_library().mla_append_kv(ctypes.byref(p), int(latent.shape[0]), latent.data_ptr(), ls, k_rope.data_ptr(), rs,
@@ -430,6 +455,7 @@ def mla_copy_pages(p: MlaPoolParams, kv_pages, src_pages, dst_pages, stream=None
     _expect_pool("mla_copy_pages", kv_pages, p, p.num_layers, p.layer_stride)
     if n == 0:
         return
+    _expect_device("mla_copy_pages", kv_pages, src_pages, dst_pages)
     _check(load_library().mla_copy_pages(ctypes.byref(p), kv_pages.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(), n,
                                          _stream(stream)), "mla_copy_pages")
 
@@ -452,6 +478,8 @@ def _fork(p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts
     _expect_pool("mla_fork_sequences", kv_pages, p, p.num_layers, p.layer_stride)
     if n == 0:
         return
+    _expect_device("mla_fork_sequences", kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages,
+                   workspace)
     _check(load_library().mla_fork_sequences(ctypes.byref(p), kv_pages.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
                                              block_table.data_ptr(), cache_seqlens.data_ptr(), ref_counts.data_ptr(),
                                              new_pages.data_ptr(), _ptr(workspace), _stream(stream)),
@@ -471,6 +499,7 @@ def _reserve(p, num_new, block_table, cache_seqlens, ref_counts, served, workspa
     if _bad(served, i32, (p.batch,)):
         _refuse("mla_reserve_pages: served")
     _expect_tables("mla_reserve_pages", p, block_table, cache_seqlens, ref_counts)
+    _expect_device("mla_reserve_pages", num_new, block_table, cache_seqlens, ref_counts, served, workspace)
     _check(load_library().mla_reserve_pages(ctypes.byref(p), num_new.data_ptr(), block_table.data_ptr(), cache_seqlens.data_ptr(),
                                             ref_counts.data_ptr(), served.data_ptr(), _ptr(workspace), _stream(stream)),
            "mla_reserve_pages")
@@ -482,6 +511,7 @@ def mla_free_sequences(p: MlaPoolParams, sequences, block_table, cache_seqlens, 
     _expect_tables("mla_free_sequences", p, block_table, cache_seqlens, ref_counts)
     if n == 0:
         return
+    _expect_device("mla_free_sequences", sequences, block_table, cache_seqlens, ref_counts)
     _check(load_library().mla_free_sequences(ctypes.byref(p), sequences.data_ptr(), n, block_table.data_ptr(),
                                              cache_seqlens.data_ptr(), ref_counts.data_ptr(), _stream(stream)),
            "mla_free_sequences")
@@ -499,6 +529,7 @@ def _compact(p, kv_pages, block_table, cache_seqlens, ref_counts, num_used, work
         _refuse("mla_compact_pages: num_used")
     _expect_tables("mla_compact_pages", p, block_table, cache_seqlens, ref_counts)
     _expect_pool("mla_compact_pages", kv_pages, p, p.num_layers, p.layer_stride)
+    _expect_device("mla_compact_pages", kv_pages, block_table, cache_seqlens, ref_counts, num_used, workspace)
     _check(load_library().mla_compact_pages(ctypes.byref(p), kv_pages.data_ptr(), block_table.data_ptr(), cache_seqlens.data_ptr(),
                                             ref_counts.data_ptr(), num_used.data_ptr(), _ptr(workspace), _stream(stream)),
            "mla_compact_pages")
@@ -572,8 +603,8 @@ class ChunkAttention:
             out = torch.empty_like(q_nope_absorbed)
         if lse is None:
             lse = torch.empty(q_nope_absorbed.shape[:2], dtype=torch.float32, device=q_nope_absorbed.device)
-        mla_chunk_attend(self.p, q_nope_absorbed, q_rope, kv_pages, block_table, self.seqlens, scale, out, lse,
-                         self.sched, self.workspace, stream)
+        _attend(self.p, q_nope_absorbed, q_rope, kv_pages, block_table, self.seqlens, scale, out, lse, self.sched,
+                self.workspace, stream)
         return out, lse
 
 

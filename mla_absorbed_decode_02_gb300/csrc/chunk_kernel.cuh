@@ -249,7 +249,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   const ChunkLayout lay = chunk_layout(args.num_units, args.capacity, args.batch);
   const int32_t* rec = sched + lay.units + kUnitInts * (blockIdx.x >> 1);
   const bool bad_meta = sched[kChMagic] != kChunkMagic || sched[kChUnits] != args.num_units ||
-                        sched[kChCapacity] != args.capacity || sched[kChTokens] != chunk_tokens_per_block(args.H);
+                        sched[kChCapacity] != args.capacity || sched[kChTokens] != chunk_tokens_per_block(args.H) ||
+                        sched[kChBatch] != args.batch || sched[kChCausal] != args.causal;
   const bool idle = bad_meta || rec[0] < 0;  // the same in both CTAs
   if (bad_meta && tid == 0) atomicCAS(&g_mla_error, 0, 5);
   pdl_launch_dependents();
@@ -717,12 +718,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 // ----------------------------------------------------------------- merge of split blocks
 // out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  grid (U, 2 CTAs x 8 warps of
 // the attention): a block of eight warps merges the 32 rows x 128 dims that one of its warps wrote, each
-// warp 16 of the dims (32 bytes of a bf16 row), four splits in flight.
+// warp 16 of the dims (32 bytes of a bf16 row).  Merging inside the attention kernel instead, by whichever
+// unit comes last (a counter per warp), took as long: 7 us more there against 9 us here.
 __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, int U, int capacity, int batch, int H,
                                                                 const float* o_acc, const float* lse_acc,
                                                                 __nv_bfloat16* out, float* lse) {
   pdl_wait_prerequisites();
-  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity ||
+  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity || sched[kChBatch] != batch ||
       (int)blockIdx.x >= sched[kChNumSplit])
     return;
   const ChunkLayout lay = chunk_layout(U, capacity, batch);
@@ -733,22 +735,17 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
   const float* lsrc = lse_acc + (int64_t)b.offset * kChunkRows + row;
   const float4* src = reinterpret_cast<const float4*>(o_acc) + (((int64_t)b.offset * 16 + blockIdx.y) * 32 + 4 * j) * 32 + lane;
   constexpr int64_t kStep = 16 * 32 * 32;  // float4 per split
-  float M = -INFINITY;
+  // one pass, two splits in flight with their lse (most split blocks have two): running maximum and sum
+  float M = -INFINITY, S = 0.f;
   bool nan = false;  // a partial of NaN keys: the maximum would not show it
-  for (int i = 0; i < b.splits; ++i) {
-    const float x = lsrc[(int64_t)i * kChunkRows];
-    nan |= isnan(x);
-    M = fmaxf(M, x);
-  }
-  float S = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < b.splits; i0 += 4) {
-    float4 v[4][4];
-    float x[4];
+  for (int i0 = 0; i0 < b.splits; i0 += 2) {
+    float4 v[2][4];
+    float x[2], top = M;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const bool in = i0 + k < b.splits;
       x[k] = in ? lsrc[(int64_t)(i0 + k) * kChunkRows] : -INFINITY;
 #pragma unroll
@@ -756,7 +753,17 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
         v[k][f] = in ? __ldcs(src + (i0 + k) * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
+      nan |= isnan(x[k]);
+      top = fmaxf(top, x[k]);
+    }
+    const float scale = top == M ? 1.f : expf(M - top);  // (0 before the first keys)
+    M = top;
+    S *= scale;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[f] = make_float4(acc[f].x * scale, acc[f].y * scale, acc[f].z * scale, acc[f].w * scale);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
       const float wk = M == -INFINITY ? 0.f : expf(x[k] - M);
       S += wk;
 #pragma unroll
@@ -790,7 +797,7 @@ __global__ void __launch_bounds__(256) mla_chunk_expand_kernel(const int32_t* sc
                                                                __nv_bfloat16* rows) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity) return;
+  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity || sched[kChBatch] != batch) return;
   const ChunkLayout lay = chunk_layout(U, capacity, batch);
   const int32_t* page_off = sched + lay.page_off;
   const int total = sched[kChPages], warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -964,6 +971,8 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     sched[kChNumSplit] = (int32_t)ns;
     sched[kChPages] = (int32_t)pages;
     sched[kChShares] = shares;
+    sched[kChBatch] = B;
+    sched[kChCausal] = causal;
     sched[kChMagic] = kChunkMagic;
   }
 }

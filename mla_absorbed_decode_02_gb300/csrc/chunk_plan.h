@@ -52,7 +52,7 @@ MLA_HD inline int32_t chunk_share_tiles(int32_t longest, int32_t least, int64_t 
 }
 
 // header words
-enum { kChMagic = 0, kChUnits, kChCapacity, kChBlocks, kChSlots, kChBudget, kChTokens, kChNumSplit, kChPages, kChShares };
+enum { kChMagic = 0, kChUnits, kChCapacity, kChBlocks, kChSlots, kChBudget, kChTokens, kChNumSplit, kChPages, kChShares, kChBatch, kChCausal };
 
 // Block record.
 struct ChunkBlock {
@@ -267,6 +267,8 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
   sched[kChNumSplit] = ns;
   sched[kChPages] = (int32_t)pages;
   sched[kChShares] = shares;
+  sched[kChBatch] = B;
+  sched[kChCausal] = causal;
   return true;
 }
 

@@ -367,15 +367,16 @@ __global__ void __launch_bounds__(128) mla_free_kernel(PoolArgs p, const int32_t
     if (threadIdx.x == 0) pool_error(1);
     return;
   }
-  if (threadIdx.x == 0) len_sh = atomicExch(&seqlens[b], 0);
-  __syncthreads();
-  const int64_t L = len_sh;
-  if (L < 0 || L > (int64_t)p.max_pages * kPageRows) {
-    if (threadIdx.x == 0) pool_error(1);
-    return;
+  if (threadIdx.x == 0) {
+    const int L = seqlens[b];
+    const bool ok = L >= 0 && (int64_t)L <= (int64_t)p.max_pages * kPageRows;
+    if (!ok) pool_error(1);
+    len_sh = ok ? atomicExch(&seqlens[b], 0) : 0;
   }
+  __syncthreads();
+  const int L = len_sh;
   int32_t* row = block_table + (int64_t)b * p.max_pages;
-  for (int j = threadIdx.x; j < pages_held((int)L); j += blockDim.x) {
+  for (int j = threadIdx.x; j < pages_held(L); j += blockDim.x) {
     const int page = row[j];
     row[j] = -1;
     if (page < 0 || page >= p.num_pages)

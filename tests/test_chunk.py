@@ -130,25 +130,52 @@ def test_workspace_does_not_grow_with_the_tokens():
 
 
 def test_attend_refuses_bad_arguments():
-    """Types and shapes in the binding, pointers and the scale in the library: nothing is launched."""
+    """Types, shapes and sizes in the binding: nothing is launched.  (Tensors of the host are themselves refused,
+    last of all.)"""
     import torch
     p = _params(batch=1, max_tokens=4, num_heads=2, num_pages=2, max_pages_per_seq=2)
+    sb, wb = _lib.mla_chunk_workspace_size(p)
     good = dict(q_nope_absorbed=torch.zeros(4, 2, 512, dtype=torch.bfloat16), q_rope=torch.zeros(4, 2, 64, dtype=torch.bfloat16),
                 kv_pages=torch.zeros(2, 64, 576, dtype=torch.bfloat16), block_table=torch.zeros(1, 2, dtype=torch.int32),
                 cache_seqlens=torch.zeros(1, dtype=torch.int32), scale=SCALE, out=torch.zeros(4, 2, 512, dtype=torch.bfloat16),
-                lse=torch.zeros(4, 2), sched=torch.zeros(4096, dtype=torch.int32), workspace=torch.zeros(4096, dtype=torch.uint8))
-    bad = [dict(q_nope_absorbed=good["q_nope_absorbed"].float()), dict(q_nope_absorbed=good["q_nope_absorbed"][:3]),
-           dict(q_rope=good["q_rope"].transpose(0, 1)), dict(kv_pages=good["kv_pages"][:1]), dict(out=good["out"].float()),
-           dict(lse=good["lse"].T), dict(block_table=good["block_table"].long()), dict(cache_seqlens=torch.zeros(2, dtype=torch.int32)),
-           dict(scale=0.0), dict(scale=float("nan")), dict(sched=None), dict(workspace=None), dict(out=None)]
-    for b in bad:
-        with pytest.raises(MlaError) as e:
+                lse=torch.zeros(4, 2), sched=torch.zeros(sb // 4, dtype=torch.int32), workspace=torch.zeros(wb, dtype=torch.uint8))
+    bad = [(dict(q_nope_absorbed=good["q_nope_absorbed"].float()), "q_nope_absorbed"), (dict(q_nope_absorbed=good["q_nope_absorbed"][:3]), "q_nope_absorbed"),
+           (dict(q_rope=good["q_rope"].transpose(0, 1)), "q_rope"), (dict(kv_pages=good["kv_pages"][:1]), "kv_pages"), (dict(out=good["out"].float()), "out"),
+           (dict(lse=good["lse"].T), "lse"), (dict(block_table=good["block_table"].long()), "block_table"),
+           (dict(cache_seqlens=torch.zeros(2, dtype=torch.int32)), "cache_seqlens"), (dict(sched=None), "sched"), (dict(workspace=None), "workspace"),
+           (dict(sched=good["sched"][1:]), "sched"), (dict(workspace=good["workspace"][1:]), "workspace"), (dict(out=None), "out"), ({}, "device")]
+    for b, word in bad:
+        with pytest.raises(MlaError, match=word) as e:
             _lib.mla_chunk_attend(p, **{**good, **b}, stream=0)
-        assert e.value.status == _lib.MLA_ERR_INVALID_ARG, b
-    for b in (dict(cu_seqlens=None), dict(cu_seqlens=torch.zeros(1, dtype=torch.int32)), dict(cache_seqlens=torch.zeros(1))):
-        with pytest.raises(MlaError):
-            _lib.mla_chunk_schedule(p, **{**dict(cu_seqlens=torch.zeros(2, dtype=torch.int32), cache_seqlens=good["cache_seqlens"],
-                                                 sched=good["sched"]), **b}, stream=0)
+        assert e.value.status in (_lib.MLA_ERR_INVALID_ARG, _lib.MLA_ERR_WORKSPACE), b
+    plan = dict(cu_seqlens=torch.zeros(2, dtype=torch.int32), cache_seqlens=good["cache_seqlens"], sched=good["sched"])
+    for b, word in ((dict(cu_seqlens=None), "cu_seqlens"), (dict(cu_seqlens=torch.zeros(1, dtype=torch.int32)), "cu_seqlens"),
+                    (dict(cache_seqlens=torch.zeros(1)), "cache_seqlens"), (dict(sched=good["sched"][1:]), "sched"), ({}, "device")):
+        with pytest.raises(MlaError, match=word):
+            _lib.mla_chunk_schedule(p, **{**plan, **b}, stream=0)
+
+
+def test_library_refuses_bad_pointers_and_scales():
+    """The C entries: null and misaligned pointers, a scale that is not positive and finite."""
+    import ctypes
+    lib, p = _lib.load_library(), _params(num_units=1)
+    buf = ctypes.create_string_buffer(4096)
+    base = (ctypes.addressof(buf) + 255) // 256 * 256
+    good = [base] * 5 + [SCALE] + [base] * 4 + [0]          # q, q_rope, kv, table, lens | out, lse, sched, workspace, stream
+    for k in (0, 1, 2, 3, 4, 6, 7, 8, 9):
+        for bad in (0, base + 2):
+            args = list(good)
+            args[k] = bad
+            assert lib.mla_chunk_attend(ctypes.byref(p), *args) == _lib.MLA_ERR_INVALID_ARG, (k, bad)
+    for scale in (0.0, -1.0, math.inf, math.nan):
+        args = list(good)
+        args[5] = scale
+        assert lib.mla_chunk_attend(ctypes.byref(p), *args) == _lib.MLA_ERR_INVALID_ARG
+    for k in range(3):
+        args = [base, base, base, 0]
+        args[k] = 0
+        assert lib.mla_chunk_schedule(ctypes.byref(p), *args) == _lib.MLA_ERR_INVALID_ARG
+    assert lib.mla_chunk_attend(None, *good) == _lib.MLA_ERR_INVALID_ARG
 
 
 # ------------------------------------------------------------------ the kernels (GPU)
@@ -271,6 +298,27 @@ def test_units_share_and_split_the_work(units, H, kv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("units", [3, 9, 40, 76])
+def test_the_same_bits_every_time(units):
+    """Repeated calls with one plan give the same bits, whatever the plan splits; another plan moves them by no
+    more than the rounding of the partials."""
+    import torch
+    q = Problem([40, 3, 1, 77], [1500, 9000, 12000, 2000], 40, seed=units, num_units=units)
+    attn = _lib.ChunkAttention(q.p)
+    attn.plan(q.d_cu, q.d_L)
+    first = None
+    for _ in range(6):
+        out, lse = attn.attend(q.d_q, q.d_qr, q.pool, q.d_bt, SCALE)
+        torch.cuda.synchronize()
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert _lib.mla_device_error(clear=True) == 0
+    one = Problem([40, 3, 1, 77], [1500, 9000, 12000, 2000], 40, seed=units, num_units=1).run()
+    assert (first[1] - one[1]).abs().max() <= 2e-6 * one[1].abs().max()
+    assert (first[0].float() - one[0].float()).norm() <= 2.0 ** -8 * one[0].float().norm()
+
+
+@pytest.mark.gpu
 def test_without_the_causal_rule():
     Problem([4, 9], [130, 600], 16, seed=3, causal=False).check()
 
@@ -354,6 +402,12 @@ def test_refused_plan_writes_nothing(lens):
     assert _lib.mla_device_error(clear=True) == _lib.MLA_ERR_WORKSPACE
     assert (out == 7).all() and (lse == 7).all()
     q.check(attn)                                  # the same buffers serve a good plan afterwards
+    other = MlaChunkParams.from_buffer_copy(q.p)   # a plan of other params
+    other.causal = 0
+    attn.p = other
+    attn.attend(q.d_q, q.d_qr, q.pool, q.d_bt, SCALE, out=out, lse=lse)
+    assert _lib.mla_device_error(clear=True) == _lib.MLA_ERR_WORKSPACE
+    assert (out == 7).all() and (lse == 7).all()
 
 
 @pytest.mark.gpu

@@ -76,17 +76,44 @@ def test_calls_refuse_bad_arguments():
     good = [q, x[:, :512], x[:, 512:], i32(7), lens, bt, pool]
     for at, v in ((1, x[:, :500]), (1, x[:, :512].float()), (2, x[:2, 512:]), (2, None), (3, i32(6)), (4, None), (5, bt.long()), (6, pool[0, :5])):
         bad.append((_lib.mla_append_kv, tuple(v if k == at else a for k, a in enumerate(good))))
-    odd = torch.zeros(4, 579, dtype=torch.bfloat16)                     # rows that do not start on 16 bytes
-    bad.append((_lib.mla_append_kv, (q, odd[:, :512], x[:, 512:], i32(7), lens, bt, pool)))
     for call, args in bad:
         with pytest.raises(MlaError) as e:
             call(*args, stream=0)
         assert e.value.status in (_lib.MLA_ERR_INVALID_ARG, _lib.MLA_ERR_WORKSPACE), call
+    # tensors of the host are refused, last of all
+    for call, args in ((_lib.mla_copy_pages, (p, pool, three, three)), (_lib.mla_fork_sequences, (p, pool, three, three, bt, lens, ref, three, ws)),
+                       (_lib.mla_reserve_pages, (p, lens, bt, lens, ref, lens, ws)), (_lib.mla_free_sequences, (p, three, bt, lens, ref)),
+                       (_lib.mla_compact_pages, (p, pool, bt, lens, ref, i32(1), ws)), (_lib.mla_append_kv, tuple(good))):
+        with pytest.raises(MlaError, match="device"):
+            call(*args, stream=0)
     # nothing to do: no launch
     _lib.mla_copy_pages(p, pool, i32(0), i32(0), stream=0)
     _lib.mla_fork_sequences(p, pool, i32(0), i32(0), bt, lens, ref, i32(0), ws, stream=0)
     _lib.mla_free_sequences(p, i32(0), bt, lens, ref, stream=0)
     _lib.mla_append_kv(q, x[:0, :512], x[:0, 512:], i32(7), lens, bt, pool, stream=0)
+
+
+def test_library_refuses_bad_pointers_and_strides():
+    """The C entries themselves: null and misaligned pointers, negative counts, row strides that the 16-byte
+    accesses cannot take."""
+    import ctypes
+    lib, p = _lib.load_library(), ctypes.byref(_params())
+    buf = ctypes.create_string_buffer(4096)
+    g = (ctypes.addressof(buf) + 255) // 256 * 256
+    calls = {"mla_append_kv": [4, g, 576, g, 576, g, g, g, g, 0], "mla_copy_pages": [g, g, g, 2, 0],
+             "mla_fork_sequences": [g, g, g, 2, g, g, g, g, g, 0], "mla_reserve_pages": [g, g, g, g, g, g, 0],
+             "mla_free_sequences": [g, 2, g, g, g, 0], "mla_compact_pages": [g, g, g, g, g, g, 0]}
+    for name, args in calls.items():
+        for k, v in enumerate(args[:-1]):
+            for bad in ((0, g + 2) if v == g else (-1,)):
+                a = list(args)
+                a[k] = bad
+                assert getattr(lib, name)(p, *a) == _lib.MLA_ERR_INVALID_ARG, (name, k, bad)
+        assert getattr(lib, name)(None, *args) == _lib.MLA_ERR_INVALID_ARG
+    for k, stride in ((2, 511), (2, 516), (4, 63), (4, 70)):
+        a = list(calls["mla_append_kv"])
+        a[k] = stride
+        assert lib.mla_append_kv(p, *a) == _lib.MLA_ERR_INVALID_ARG
 
 
 # ------------------------------------------------------------------ a plain model of the pool
@@ -104,7 +131,7 @@ class Model:
     def reserve(self, n):
         served, left, short = [], self.free_pages(), False
         for b in range(self.p.batch):
-            if n[b] < 0 or int(self.L[b]) + int(n[b]) > 64 * self.p.max_pages_per_seq:
+            if n[b] < 0 or self.L[b] < 0 or int(self.L[b]) + int(n[b]) > 64 * self.p.max_pages_per_seq:
                 served.append(-2)
                 continue
             a, e = -(-int(self.L[b]) // 64), -(-(int(self.L[b]) + int(n[b])) // 64)
@@ -300,6 +327,14 @@ def test_copy_and_pages_out_of_range():
     s.check(error=_lib.MLA_ERR_INVALID_ARG)
     s.pool.free(s.dev([6, -1]), *s.tables())
     s.check(error=_lib.MLA_ERR_INVALID_ARG)
+    s.reserve([10, 70, 0, 0, 0, 0])
+    for wrong in (-3, 64 * 8 + 1):                 # lengths that cannot be: nothing is touched
+        s.L[0] = s.m.L[0] = wrong
+        s.pool.free(s.dev([0]), *s.tables())
+        s.pool.compact(s.d, *s.tables())
+        assert s.pool.reserve(s.dev([1] * 6), *s.tables()).tolist() == s.m.reserve([1] * 6)
+        assert s.pool.fork(s.d, s.dev([0]), s.dev([5]), *s.tables()).tolist() == [-2]
+        s.check(error=_lib.MLA_ERR_INVALID_ARG)
 
 
 # ------------------------------------------------------------------ append
