@@ -248,10 +248,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   const int32_t* sched = args.sched;
   const ChunkLayout lay = chunk_layout(args.num_units, args.capacity, args.batch);
   const int32_t* rec = sched + lay.units + kUnitInts * (blockIdx.x >> 1);
-  const bool bad_meta = sched[kChMagic] != kChunkMagic || sched[kChUnits] != args.num_units ||
-                        sched[kChCapacity] != args.capacity || sched[kChTokens] != chunk_tokens_per_block(args.H) ||
-                        sched[kChBatch] != args.batch || sched[kChCausal] != args.causal;
-  const bool idle = bad_meta || rec[0] < 0;  // the same in both CTAs
+  // (header and record in whole vectors: one memory latency for all of it)
+  const int4 h0 = reinterpret_cast<const int4*>(sched)[0], h1 = reinterpret_cast<const int4*>(sched)[1],
+             h2 = reinterpret_cast<const int4*>(sched)[2], r0 = reinterpret_cast<const int4*>(rec)[0];
+  static_assert(kChMagic == 0 && kChUnits == 1 && kChCapacity == 2 && kChTokens == 6 && kChBatch == 10 && kChCausal == 11, "header");
+  const bool bad_meta = h0.x != kChunkMagic || h0.y != args.num_units || h0.z != args.capacity ||
+                        h1.z != chunk_tokens_per_block(args.H) || h2.z != args.batch || h2.w != args.causal;
+  const bool idle = bad_meta || r0.x < 0;  // the same in both CTAs
   if (bad_meta && tid == 0) atomicCAS(&g_mla_error, 0, 5);
   pdl_launch_dependents();
 
