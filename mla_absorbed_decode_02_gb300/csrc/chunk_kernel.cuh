@@ -271,25 +271,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     // ================================================================ page copies
     const int32_t* page_off = sched + lay.page_off;
     const bool el = elect_one();
-    // ring position (the waits of the first round pass: "the phase before" of a fresh barrier) and
-    // whose turn it is
-    uint32_t slot = 0, phase = 1, n_raw = 0;
-    int turn = 0;
+    // Slots are taken in turn: warp i the slots i, i + 6, ... of the whole stream.  The ring position
+    // of the section at hand (a tile's K or V slots): its first slot, that slot's phase (the waits of the
+    // first round pass: "the phase before" of a fresh barrier) and its number modulo the warps.
+    int first_slot = 0, first_turn = 0;
+    uint32_t first_phase = 1, n_raw = 0;
     bool ok = true;
-    auto advance = [&]() {
-      if (++slot == kCkSlots) {
-        slot = 0;
-        phase ^= 1;
-      }
-      turn = turn == kCkCopyWarps - 1 ? 0 : turn + 1;
+    uint32_t slot = 0, phase = 0;
+    auto locate = [&](int k) {  // slot k < 14 - kCkSlots + 1 of the section
+      const int q = first_slot + k, wraps = (q >= kCkSlots) + (q >= 2 * kCkSlots);
+      slot = q - kCkSlots * wraps;
+      phase = first_phase ^ (wraps & 1);
     };
-    // lane j < 4: physical page of the tile's page j
+    auto mine = [&]() -> int {  // this warp's first slot of the section
+      const int k = warp - first_turn;
+      return k < 0 ? k + kCkCopyWarps : k;
+    };
+    auto leave = [&](int n) {  // the section had n <= 9 slots
+      locate(n);
+      first_slot = slot;
+      first_phase = phase;
+      first_turn = (first_turn + n) % kCkCopyWarps;
+    };
+    // lane j < 4: physical page of the tile's page j, as the table has it (looked at when it is used, so
+    // that the load's latency is not waited for)
     auto page_of = [&](const ChunkTileRef& r) -> int {
       const int lp = 4 * r.tile + lane;
       if (lane >= 4 || lane >= r.pages()) return 0;
       if (args.expanded) return page_off[r.b.seq] + lp;
-      int page = args.block_table[(int64_t)r.b.seq * args.max_pages + lp];
-      if (page < 0 || page >= args.num_pages) {  // outside the contract: reported, and another page read
+      return args.block_table[(int64_t)r.b.seq * args.max_pages + lp];
+    };
+    auto checked = [&](int page) -> int {
+      if (!args.expanded && (page < 0 || page >= args.num_pages)) {  // outside the contract: reported, another page read
         atomicCAS(&g_mla_error, 0, 1);
         page = 0;
       }
@@ -299,8 +312,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       const int np = min(max(r.pages() - 2 * (int)rank, 0), 2);
       const int y0 = 64 * __shfl_sync(0xffffffffu, page, 2 * rank), y1 = 64 * __shfl_sync(0xffffffffu, page, 2 * rank + 1);
 #pragma unroll 1
-      for (int d = 0; d < 9; ++d, advance()) {
-        if (turn != warp) continue;
+      for (int d = mine(); d < 9; d += kCkCopyWarps) {
+        locate(d);
         if (!wait_warp<true>(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
         const uint32_t full = lead0 + 8 * (CB_FULL + slot), dst = base + CK_RING + slot * kCkSlot;
         if (el) {
@@ -314,54 +327,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
         }
         __syncwarp();
       }
+      leave(9);
       return true;
     };
     auto copy_v = [&](const ChunkTileRef& r, int page) -> bool {
       const int np = r.pages(), some = chunk_visible(r.b, 0, args.causal);  // keys every row of the block sees
 #pragma unroll 1
-      for (int kb = 0; kb < np; ++kb) {
+      for (int k = mine(); k < 2 * np; k += kCkCopyWarps) {
+        const int kb = k >> 1, n = k & 1;
         const int y = 64 * __shfl_sync(0xffffffffu, page, kb), key0 = kChunkTile * r.tile + 64 * kb;
-#pragma unroll 1
-        for (int n = 0; n < 2; ++n, advance()) {
-          if (turn != warp) continue;
-          if (!wait_warp<true>(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
-          const uint32_t full = lead0 + 8 * (CB_FULL + slot), dst = base + CK_RING + slot * kCkSlot;
-          const int z = 4 * n + 2 * (int)rank;  // dims 256 n + 128 rank, in blocks of 64
-          if (key0 + 64 <= some) {
-            if (el) {
-              mbar_arrive_expect_tx_remote(full, kCkSlot);
-              tma2_load_3d(dst, &args.map_v, full, 0, y, z);
-            }
-            __syncwarp();
-            continue;
-          }
-          // some row does not see all of this page: rows [from, to) of it are looked through
-          const uint32_t raw = bar(CB_RAW + warp);
+        locate(k);
+        if (!wait_warp<true>(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
+        const uint32_t full = lead0 + 8 * (CB_FULL + slot), dst = base + CK_RING + slot * kCkSlot;
+        const int z = 4 * n + 2 * (int)rank;  // dims 256 n + 128 rank, in blocks of 64
+        if (key0 + 64 <= some) {
           if (el) {
-            mbar_arrive_expect_tx(raw, kCkSlot);
-            tma2_load_3d(dst, &args.map_v, map_to_rank(raw, rank), 0, y, z);
+            mbar_arrive_expect_tx_remote(full, kCkSlot);
+            tma2_load_3d(dst, &args.map_v, full, 0, y, z);
           }
           __syncwarp();
-          if (!wait_warp(raw, n_raw & 1, wc, kSiteCkRaw)) return false;
-          ++n_raw;
-          const int from = max(some - key0, 0), seen = min(r.vis - key0, 64), to = (seen + 15) & ~15;
-          for (int i = from * 16 + lane; i < to * 16; i += 32) {  // 16-byte chunks: two blocks of 8 a row
-            const int row = i >> 4;
-            const uint32_t a = dst + ((i >> 3) & 1) * kCkBlk + row * 128 + (i & 7) * 16;
-            uint32_t v[4];
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
-            bool bad = row >= seen;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              bad |= (v[q] & 0x7F80u) == 0x7F80u || (v[q] & 0x7F800000u) == 0x7F800000u;
-            if (bad) asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0u) : "memory");
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(full);
-          __syncwarp();
+          continue;
         }
+        // some row does not see all of this page: rows [from, to) of it are looked through
+        const uint32_t raw = bar(CB_RAW + warp);
+        if (el) {
+          mbar_arrive_expect_tx(raw, kCkSlot);
+          tma2_load_3d(dst, &args.map_v, map_to_rank(raw, rank), 0, y, z);
+        }
+        __syncwarp();
+        if (!wait_warp(raw, n_raw & 1, wc, kSiteCkRaw)) return false;
+        ++n_raw;
+        const int from = max(some - key0, 0), seen = min(r.vis - key0, 64), to = (seen + 15) & ~15;
+        for (int i = from * 16 + lane; i < to * 16; i += 32) {  // 16-byte chunks: two blocks of 8 a row
+          const int row = i >> 4;
+          const uint32_t a = dst + ((i >> 3) & 1) * kCkBlk + row * 128 + (i & 7) * 16;
+          uint32_t v[4];
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
+          bool bad = row >= seen;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            bad |= (v[q] & 0x7F80u) == 0x7F80u || (v[q] & 0x7F800000u) == 0x7F800000u;
+          if (bad) asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0u) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(full);
+        __syncwarp();
       }
+      leave(2 * np);
       return true;
     };
     // the order of the MMA warp: K of the next tile, then V of the current one (the other way at a block's
@@ -372,10 +385,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     int pa = page_of(a), pb = 0, pc = 0;
     has_b = cur.next(b);
     if (has_b) pb = page_of(b);
+    pa = checked(pa);
     ok = copy_k(a, pa);
     while (ok) {
       has_c = has_b && cur.next(c);
       if (has_c) pc = page_of(c);
+      pb = checked(pb);
       if (has_b && !b.first && !(ok = copy_k(b, pb))) break;
       if (!(ok = copy_v(a, pa)) || !has_b) break;
       if (b.first && !(ok = copy_k(b, pb))) break;
