@@ -748,74 +748,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 }
 
 // ----------------------------------------------------------------- merge of split blocks
-// out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  grid (U, 2 CTAs x 8 warps of
-// the attention): a block of eight warps merges the 32 rows x 128 dims that one of its warps wrote, each
-// warp 16 of the dims (32 bytes of a bf16 row).  Merging inside the attention kernel instead, by whichever
+// out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  Items are (split block, one of
+// the 2 x 8 warps that wrote it): eight warps merge its 32 rows x 128 dims, each 16 of the dims (32 bytes
+// of a bf16 row).  Three blocks per SM stride over the items (a block for each: 0.6 us more where there is
+// nothing to merge).  Merging inside the attention kernel instead, by whichever
 // unit comes last (a counter per warp), took as long: 7 us more there against 9 us here.
 __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, int U, int capacity, int batch, int H,
                                                                 const float* o_acc, const float* lse_acc,
                                                                 __nv_bfloat16* out, float* lse) {
   pdl_wait_prerequisites();
-  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity || sched[kChBatch] != batch ||
-      (int)blockIdx.x >= sched[kChNumSplit])
+  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity || sched[kChBatch] != batch)
     return;
   const ChunkLayout lay = chunk_layout(U, capacity, batch);
-  const ChunkBlock b = reinterpret_cast<const ChunkBlock*>(sched + lay.blocks)[sched[lay.split_list + blockIdx.x]];
-  const int rank = blockIdx.y >> 3, wi = blockIdx.y & 7, lane = threadIdx.x & 31, j = threadIdx.x >> 5;
-  const int L = 32 * (wi & 3) + lane, row = 64 * rank + (L & 63);
-  if (row >= b.ntok * H) return;
-  const float* lsrc = lse_acc + (int64_t)b.offset * kChunkRows + row;
-  const float4* src = reinterpret_cast<const float4*>(o_acc) + (((int64_t)b.offset * 16 + blockIdx.y) * 32 + 4 * j) * 32 + lane;
-  constexpr int64_t kStep = 16 * 32 * 32;  // float4 per split
-  // one pass, two splits in flight with their lse (most split blocks have two): running maximum and sum
-  float M = -INFINITY, S = 0.f;
-  bool nan = false;  // a partial of NaN keys: the maximum would not show it
-  float4 acc[4];
+  const int items = 16 * sched[kChNumSplit];
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    const ChunkBlock b = reinterpret_cast<const ChunkBlock*>(sched + lay.blocks)[sched[lay.split_list + (it >> 4)]];
+    const int rank = (it >> 3) & 1, wi = it & 7, lane = threadIdx.x & 31, j = threadIdx.x >> 5;
+    const int L = 32 * (wi & 3) + lane, row = 64 * rank + (L & 63);
+    if (row >= b.ntok * H) continue;
+    const float* lsrc = lse_acc + (int64_t)b.offset * kChunkRows + row;
+    const float4* src = reinterpret_cast<const float4*>(o_acc) + (((int64_t)b.offset * 16 + (it & 15)) * 32 + 4 * j) * 32 + lane;
+    constexpr int64_t kStep = 16 * 32 * 32;  // float4 per split
+    // one pass, two splits in flight with their lse (most split blocks have two): running maximum and sum
+    float M = -INFINITY, S = 0.f;
+    bool nan = false;  // a partial of NaN keys: the maximum would not show it
+    float4 acc[4];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < b.splits; i0 += 2) {
-    float4 v[2][4];
-    float x[2], top = M;
+    for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < b.splits; i0 += 2) {
+      float4 v[2][4];
+      float x[2], top = M;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const bool in = i0 + k < b.splits;
-      x[k] = in ? lsrc[(int64_t)(i0 + k) * kChunkRows] : -INFINITY;
+      for (int k = 0; k < 2; ++k) {
+        const bool in = i0 + k < b.splits;
+        x[k] = in ? lsrc[(int64_t)(i0 + k) * kChunkRows] : -INFINITY;
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
-        v[k][f] = in ? __ldcs(src + (i0 + k) * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+        for (int f = 0; f < 4; ++f)
+          v[k][f] = in ? __ldcs(src + (i0 + k) * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      nan |= isnan(x[k]);
-      top = fmaxf(top, x[k]);
-    }
-    const float scale = top == M ? 1.f : expf(M - top);  // (0 before the first keys)
-    M = top;
-    S *= scale;
+      for (int k = 0; k < 2; ++k) {
+        nan |= isnan(x[k]);
+        top = fmaxf(top, x[k]);
+      }
+      const float scale = top == M ? 1.f : expf(M - top);  // (0 before the first keys)
+      M = top;
+      S *= scale;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) acc[f] = make_float4(acc[f].x * scale, acc[f].y * scale, acc[f].z * scale, acc[f].w * scale);
+      for (int f = 0; f < 4; ++f) acc[f] = make_float4(acc[f].x * scale, acc[f].y * scale, acc[f].z * scale, acc[f].w * scale);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float wk = M == -INFINITY ? 0.f : expf(x[k] - M);
-      S += wk;
+      for (int k = 0; k < 2; ++k) {
+        const float wk = M == -INFINITY ? 0.f : expf(x[k] - M);
+        S += wk;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        acc[f].x += wk * v[k][f].x;
-        acc[f].y += wk * v[k][f].y;
-        acc[f].z += wk * v[k][f].z;
-        acc[f].w += wk * v[k][f].w;
+        for (int f = 0; f < 4; ++f) {
+          acc[f].x += wk * v[k][f].x;
+          acc[f].y += wk * v[k][f].y;
+          acc[f].z += wk * v[k][f].z;
+          acc[f].w += wk * v[k][f].w;
+        }
       }
     }
-  }
-  const float inv = nan ? NAN : M == -INFINITY ? 0.f : 1.f / S;
-  const int64_t q_row = (int64_t)b.tok0 * H + row;
-  uint4* dst = reinterpret_cast<uint4*>(out + q_row * 512 + 256 * (wi >> 2) + 128 * (L >> 6) + 16 * j);
+    const float inv = nan ? NAN : M == -INFINITY ? 0.f : 1.f / S;
+    const int64_t q_row = (int64_t)b.tok0 * H + row;
+    uint4* dst = reinterpret_cast<uint4*>(out + q_row * 512 + 256 * (wi >> 2) + 128 * (L >> 6) + 16 * j);
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
-    dst[f] = make_uint4(pack_bf16(acc[2 * f].x * inv, acc[2 * f].y * inv), pack_bf16(acc[2 * f].z * inv, acc[2 * f].w * inv),
-                        pack_bf16(acc[2 * f + 1].x * inv, acc[2 * f + 1].y * inv),
-                        pack_bf16(acc[2 * f + 1].z * inv, acc[2 * f + 1].w * inv));
-  if (j == 0 && (wi >> 2) == 0 && L < 64) lse[q_row] = nan ? NAN : M == -INFINITY ? -INFINITY : M + logf(S);
+    for (int f = 0; f < 2; ++f)
+      dst[f] = make_uint4(pack_bf16(acc[2 * f].x * inv, acc[2 * f].y * inv), pack_bf16(acc[2 * f].z * inv, acc[2 * f].w * inv),
+                          pack_bf16(acc[2 * f + 1].x * inv, acc[2 * f + 1].y * inv),
+                          pack_bf16(acc[2 * f + 1].z * inv, acc[2 * f + 1].w * inv));
+    if (j == 0 && (wi >> 2) == 0 && L < 64) lse[q_row] = nan ? NAN : M == -INFINITY ? -INFINITY : M + logf(S);
+  }
 }
 
 // ----------------------------------------------------------------- FP8 rows -> bf16 rows
