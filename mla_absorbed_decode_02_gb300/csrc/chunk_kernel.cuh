@@ -748,76 +748,133 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 }
 
 // ----------------------------------------------------------------- merge of split blocks
-// out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  Items are (split block, one of
-// the 2 x 8 warps that wrote it): eight warps merge its 32 rows x 128 dims, each 16 of the dims (32 bytes
-// of a bf16 row).  Three blocks per SM stride over the items (a block for each: 0.6 us more where there is
-// nothing to merge).  Merging inside the attention kernel instead, by whichever
-// unit comes last (a counter per warp), took as long: 7 us more there against 9 us here.
+// out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  Three blocks of eight warps per SM
+// stride over the items.
+//   Stretches (most split blocks have two pieces): an item is the 32 rows x 128 dims that one of the 2 x 8
+//   warps of the attention wrote; a warp takes 16 of the dims (32 bytes of a bf16 row), two pieces in flight.
+//   Shares (few blocks, each in up to as many pieces as there are units): an item is 8 of those dims; the
+//   eight warps take every eighth piece each and meet in shared memory.
+// Merging inside the attention kernel instead, by whichever unit comes last (a counter per warp), took as
+// long: 7 us more there against 9 us here.
+template <int kCols>
+struct ChunkMerge {  // running log-sum-exp merge of one row's float4 columns
+  float M = -INFINITY, S = 0.f;
+  bool nan = false;  // a partial of NaN keys: the maximum would not show it
+  float4 acc[kCols];
+  __device__ ChunkMerge() {
+#pragma unroll
+    for (int f = 0; f < kCols; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // partials k: sums of weights s_k and of weighted rows v_k, both relative to exp(x_k)
+  template <int kN>
+  __device__ void add(const float (&x)[kN], const float (&s)[kN], const float4 (&v)[kN][kCols]) {
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      nan |= isnan(x[k]);
+      top = fmaxf(top, x[k]);
+    }
+    const float scale = top == M ? 1.f : expf(M - top);  // (0 before the first keys)
+    M = top;
+    S *= scale;
+#pragma unroll
+    for (int f = 0; f < kCols; ++f) acc[f] = make_float4(acc[f].x * scale, acc[f].y * scale, acc[f].z * scale, acc[f].w * scale);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const float wk = M == -INFINITY ? 0.f : expf(x[k] - M);
+      S += wk * s[k];
+#pragma unroll
+      for (int f = 0; f < kCols; ++f) {
+        acc[f].x += wk * v[k][f].x;
+        acc[f].y += wk * v[k][f].y;
+        acc[f].z += wk * v[k][f].z;
+        acc[f].w += wk * v[k][f].w;
+      }
+    }
+  }
+  __device__ void store(__nv_bfloat16* dst, float* lse_row) const {
+    const float inv = nan ? NAN : M == -INFINITY ? 0.f : 1.f / S;
+#pragma unroll
+    for (int f = 0; f < kCols; f += 2)
+      *reinterpret_cast<uint4*>(dst + 4 * f) =
+          make_uint4(pack_bf16(acc[f].x * inv, acc[f].y * inv), pack_bf16(acc[f].z * inv, acc[f].w * inv),
+                     pack_bf16(acc[f + 1].x * inv, acc[f + 1].y * inv), pack_bf16(acc[f + 1].z * inv, acc[f + 1].w * inv));
+    if (lse_row) *lse_row = nan ? NAN : M == -INFINITY ? -INFINITY : M + logf(S);
+  }
+};
+
 __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, int U, int capacity, int batch, int H,
                                                                 const float* o_acc, const float* lse_acc,
                                                                 __nv_bfloat16* out, float* lse) {
+  __shared__ float4 sh_acc[8][2][32];
+  __shared__ float sh_m[8][32], sh_s[8][32];
   pdl_wait_prerequisites();
   if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity || sched[kChBatch] != batch)
     return;
   const ChunkLayout lay = chunk_layout(U, capacity, batch);
-  const int items = 16 * sched[kChNumSplit];
+  const bool shares = sched[kChShares] != 0;
+  const int per = shares ? 256 : 16, items = per * sched[kChNumSplit], lane = threadIdx.x & 31, j = threadIdx.x >> 5;
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
-    const ChunkBlock b = reinterpret_cast<const ChunkBlock*>(sched + lay.blocks)[sched[lay.split_list + (it >> 4)]];
-    const int rank = (it >> 3) & 1, wi = it & 7, lane = threadIdx.x & 31, j = threadIdx.x >> 5;
-    const int L = 32 * (wi & 3) + lane, row = 64 * rank + (L & 63);
-    if (row >= b.ntok * H) continue;
-    const float* lsrc = lse_acc + (int64_t)b.offset * kChunkRows + row;
-    const float4* src = reinterpret_cast<const float4*>(o_acc) + (((int64_t)b.offset * 16 + (it & 15)) * 32 + 4 * j) * 32 + lane;
-    constexpr int64_t kStep = 16 * 32 * 32;  // float4 per split
-    // one pass, two splits in flight with their lse (most split blocks have two): running maximum and sum
-    float M = -INFINITY, S = 0.f;
-    bool nan = false;  // a partial of NaN keys: the maximum would not show it
-    float4 acc[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < b.splits; i0 += 2) {
-      float4 v[2][4];
-      float x[2], top = M;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const bool in = i0 + k < b.splits;
-        x[k] = in ? lsrc[(int64_t)(i0 + k) * kChunkRows] : -INFINITY;
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-          v[k][f] = in ? __ldcs(src + (i0 + k) * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        nan |= isnan(x[k]);
-        top = fmaxf(top, x[k]);
-      }
-      const float scale = top == M ? 1.f : expf(M - top);  // (0 before the first keys)
-      M = top;
-      S *= scale;
-#pragma unroll
-      for (int f = 0; f < 4; ++f) acc[f] = make_float4(acc[f].x * scale, acc[f].y * scale, acc[f].z * scale, acc[f].w * scale);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float wk = M == -INFINITY ? 0.f : expf(x[k] - M);
-        S += wk;
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          acc[f].x += wk * v[k][f].x;
-          acc[f].y += wk * v[k][f].y;
-          acc[f].z += wk * v[k][f].z;
-          acc[f].w += wk * v[k][f].w;
-        }
-      }
-    }
-    const float inv = nan ? NAN : M == -INFINITY ? 0.f : 1.f / S;
+    const ChunkBlock b = reinterpret_cast<const ChunkBlock*>(sched + lay.blocks)[sched[lay.split_list + it / per]];
+    const int writer = it & 15, wi = writer & 7, L = 32 * (wi & 3) + lane, row = 64 * (writer >> 3) + (L & 63);
+    const bool on = row < b.ntok * H;
+    const int col = shares ? 2 * ((it >> 4) & 15) : 4 * j;  // float4 columns [col, col + 2 or 4) of the 32
     const int64_t q_row = (int64_t)b.tok0 * H + row;
-    uint4* dst = reinterpret_cast<uint4*>(out + q_row * 512 + 256 * (wi >> 2) + 128 * (L >> 6) + 16 * j);
+    __nv_bfloat16* dst = out + q_row * 512 + 256 * (wi >> 2) + 128 * (L >> 6) + 4 * col;
+    float* lse_row = wi < 2 && col == 0 ? lse + q_row : nullptr;  // (one of the four lanes that hold the row)
+    const float* lsrc = lse_acc + (int64_t)b.offset * kChunkRows + row;
+    const float4* src = reinterpret_cast<const float4*>(o_acc) + (((int64_t)b.offset * 16 + writer) * 32 + col) * 32 + lane;
+    constexpr int64_t kStep = 16 * 32 * 32;  // float4 per piece
+    if (!shares) {
+      ChunkMerge<4> m;
+      for (int i0 = 0; on && i0 < b.splits; i0 += 2) {
+        float4 v[2][4];
+        float x[2], s[2];
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
-      dst[f] = make_uint4(pack_bf16(acc[2 * f].x * inv, acc[2 * f].y * inv), pack_bf16(acc[2 * f].z * inv, acc[2 * f].w * inv),
-                          pack_bf16(acc[2 * f + 1].x * inv, acc[2 * f + 1].y * inv),
-                          pack_bf16(acc[2 * f + 1].z * inv, acc[2 * f + 1].w * inv));
-    if (j == 0 && (wi >> 2) == 0 && L < 64) lse[q_row] = nan ? NAN : M == -INFINITY ? -INFINITY : M + logf(S);
+        for (int k = 0; k < 2; ++k) {
+          const bool in = i0 + k < b.splits;
+          x[k] = in ? lsrc[(int64_t)(i0 + k) * kChunkRows] : -INFINITY;
+          s[k] = 1.f;
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            v[k][f] = in ? __ldcs(src + (i0 + k) * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        m.add(x, s, v);
+      }
+      if (on) m.store(dst, lse_row);
+      continue;
+    }
+    ChunkMerge<2> m;
+    for (int i0 = j; on && i0 < b.splits; i0 += 32) {  // four of this warp's pieces in flight
+      float4 v[4][2];
+      float x[4], s[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + 8 * k;
+        const bool in = i < b.splits;
+        x[k] = in ? lsrc[(int64_t)i * kChunkRows] : -INFINITY;
+        s[k] = 1.f;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) v[k][f] = in ? __ldcs(src + i * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      m.add(x, s, v);
+    }
+    __syncthreads();  // (the item before has been read)
+    sh_acc[j][0][lane] = m.acc[0];
+    sh_acc[j][1][lane] = m.acc[1];
+    sh_m[j][lane] = m.nan ? NAN : m.M;
+    sh_s[j][lane] = m.S;
+    __syncthreads();
+    if (j == 0 && on) {
+      ChunkMerge<2> t;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float x[2] = {sh_m[i][lane], sh_m[i + 1][lane]}, s[2] = {sh_s[i][lane], sh_s[i + 1][lane]};
+        const float4 v[2][2] = {{sh_acc[i][0][lane], sh_acc[i][1][lane]}, {sh_acc[i + 1][0][lane], sh_acc[i + 1][1][lane]}};
+        t.add(x, s, v);
+      }
+      t.store(dst, lse_row);
+    }
   }
 }
 
