@@ -182,24 +182,29 @@ struct ChunkCursor {
   bool open;
   ChunkBlock b;
   int vis;
-  __device__ void init(const ChunkBlock* blk_records, const int32_t* rec, int causal_) {
+  __device__ void set_block(int4 lo, int4 hi) {
+    b.tok0 = lo.x; b.ntok = lo.y; b.seq = lo.z; b.base = lo.w;
+    b.len = hi.x; b.nt = hi.y; b.splits = hi.z; b.offset = hi.w;
+  }
+  // r: the unit's record {first block, first tile, last block, end tile | split, ... | the first block}
+  __device__ void init(const ChunkBlock* blk_records, int4 r0, int split, int4 lo, int4 hi, int causal_) {
     blocks = blk_records;
     causal = causal_;
-    blk = blk0 = rec[0];
-    tile0 = rec[1];
-    blk1 = rec[2];
-    tile1 = rec[3];
-    split0 = rec[4];
+    blk = blk0 = r0.x;
+    tile0 = r0.y;
+    blk1 = r0.z;
+    tile1 = r0.w;
+    split0 = split;
     open = false;
+    set_block(lo, hi);
   }
   __device__ bool next(ChunkTileRef& r) {
     if (!open || t >= end) {
-      if (open) ++blk;
-      if (blk > blk1) return false;
-      const int4* src = reinterpret_cast<const int4*>(blocks + blk);
-      const int4 lo = src[0], hi = src[1];
-      b.tok0 = lo.x; b.ntok = lo.y; b.seq = lo.z; b.base = lo.w;
-      b.len = hi.x; b.nt = hi.y; b.splits = hi.z; b.offset = hi.w;
+      if (open) {
+        if (++blk > blk1) return false;
+        const int4* src = reinterpret_cast<const int4*>(blocks + blk);
+        set_block(src[0], src[1]);
+      }
       vis = chunk_visible(b, b.ntok - 1, causal);
       t = blk == blk0 ? tile0 : 0;
       end = blk == blk1 ? tile1 : b.nt;
@@ -261,10 +266,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   pdl_wait_prerequisites();
   const int32_t* sched = args.sched;
   const ChunkLayout lay = chunk_layout(args.num_units, args.capacity, args.batch);
-  const int32_t* rec = sched + lay.units + kUnitInts * (blockIdx.x >> 1);
+  const int4* rec = reinterpret_cast<const int4*>(sched + lay.units + kChunkUnitInts * (blockIdx.x >> 1));
   // (header and record in whole vectors: one memory latency for all of it)
   const int4 h0 = reinterpret_cast<const int4*>(sched)[0], h1 = reinterpret_cast<const int4*>(sched)[1],
-             h2 = reinterpret_cast<const int4*>(sched)[2], r0 = reinterpret_cast<const int4*>(rec)[0];
+             h2 = reinterpret_cast<const int4*>(sched)[2], r0 = rec[0], r1 = rec[1], r2 = rec[2], r3 = rec[3];
   static_assert(kChMagic == 0 && kChUnits == 1 && kChCapacity == 2 && kChTokens == 6 && kChBatch == 10 && kChCausal == 11, "header");
   const bool bad_meta = h0.x != kChunkMagic || h0.y != args.num_units || h0.z != args.capacity ||
                         h1.z != chunk_tokens_per_block(args.H) || h2.z != args.batch || h2.w != args.causal;
@@ -278,7 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   wc.timeout_ns = args.timeout_ns;
   const uint32_t lead0 = map_to_rank(bar(0), 0);  // the leader's barrier i is at lead0 + 8 i
   ChunkCursor cur;
-  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), rec, args.causal);
+  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), r0, r1.x, r2, r3, args.causal);
 
   if (idle) {
   } else if (warp < kCkCopyWarps) {
@@ -752,8 +757,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 // stride over the items.
 //   Stretches (most split blocks have two pieces): an item is the 32 rows x 128 dims that one of the 2 x 8
 //   warps of the attention wrote; a warp takes 16 of the dims (32 bytes of a bf16 row), two pieces in flight.
-//   Shares (few blocks, each in up to as many pieces as there are units): an item is 8 of those dims; the
-//   eight warps take every eighth piece each and meet in shared memory.
+//   Shares (few blocks, each in up to as many pieces as there are units): an item is 4 of those dims; the
+//   eight warps take every eighth piece each, ten in flight, and meet in shared memory.
 // Merging inside the attention kernel instead, by whichever unit comes last (a counter per warp), took as
 // long: 7 us more there against 9 us here.
 template <int kCols>
@@ -794,11 +799,19 @@ struct ChunkMerge {  // running log-sum-exp merge of one row's float4 columns
   }
   __device__ void store(__nv_bfloat16* dst, float* lse_row) const {
     const float inv = nan ? NAN : M == -INFINITY ? 0.f : 1.f / S;
+    uint32_t o[2 * kCols];
 #pragma unroll
-    for (int f = 0; f < kCols; f += 2)
-      *reinterpret_cast<uint4*>(dst + 4 * f) =
-          make_uint4(pack_bf16(acc[f].x * inv, acc[f].y * inv), pack_bf16(acc[f].z * inv, acc[f].w * inv),
-                     pack_bf16(acc[f + 1].x * inv, acc[f + 1].y * inv), pack_bf16(acc[f + 1].z * inv, acc[f + 1].w * inv));
+    for (int f = 0; f < kCols; ++f) {
+      o[2 * f] = pack_bf16(acc[f].x * inv, acc[f].y * inv);
+      o[2 * f + 1] = pack_bf16(acc[f].z * inv, acc[f].w * inv);
+    }
+    if constexpr (kCols == 1) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+    } else {
+#pragma unroll
+      for (int f = 0; f < kCols / 2; ++f)
+        *reinterpret_cast<uint4*>(dst + 8 * f) = make_uint4(o[4 * f], o[4 * f + 1], o[4 * f + 2], o[4 * f + 3]);
+    }
     if (lse_row) *lse_row = nan ? NAN : M == -INFINITY ? -INFINITY : M + logf(S);
   }
 };
@@ -806,19 +819,24 @@ struct ChunkMerge {  // running log-sum-exp merge of one row's float4 columns
 __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, int U, int capacity, int batch, int H,
                                                                 const float* o_acc, const float* lse_acc,
                                                                 __nv_bfloat16* out, float* lse) {
-  __shared__ float4 sh_acc[8][2][32];
+  __shared__ float4 sh_acc[8][32];
   __shared__ float sh_m[8][32], sh_s[8][32];
   pdl_wait_prerequisites();
-  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity || sched[kChBatch] != batch)
-    return;
   const ChunkLayout lay = chunk_layout(U, capacity, batch);
-  const bool shares = sched[kChShares] != 0;
-  const int per = shares ? 256 : 16, items = per * sched[kChNumSplit], lane = threadIdx.x & 31, j = threadIdx.x >> 5;
+  const int4 h0 = reinterpret_cast<const int4*>(sched)[0], h1 = reinterpret_cast<const int4*>(sched)[1],
+             h2 = reinterpret_cast<const int4*>(sched)[2];
+  static_assert(kChNumSplit == 7 && kChShares == 9, "header");
+  if (h0.x != kChunkMagic || h0.y != U || h0.z != capacity || h2.z != batch) return;
+  const bool shares = h2.y != 0;
+  const int per = shares ? 512 : 16, items = per * h1.w, lane = threadIdx.x & 31, j = threadIdx.x >> 5;
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
-    const ChunkBlock b = reinterpret_cast<const ChunkBlock*>(sched + lay.blocks)[sched[lay.split_list + it / per]];
+    const int4* rec = reinterpret_cast<const int4*>(sched + lay.split_list) + 2 * (it / per);
+    const int4 lo = rec[0], hi = rec[1];
+    ChunkBlock b;
+    b.tok0 = lo.x; b.ntok = lo.y; b.splits = hi.z; b.offset = hi.w;
     const int writer = it & 15, wi = writer & 7, L = 32 * (wi & 3) + lane, row = 64 * (writer >> 3) + (L & 63);
     const bool on = row < b.ntok * H;
-    const int col = shares ? 2 * ((it >> 4) & 15) : 4 * j;  // float4 columns [col, col + 2 or 4) of the 32
+    const int col = shares ? (it >> 4) & 31 : 4 * j;  // float4 columns [col, col + 1 or 4) of the 32
     const int64_t q_row = (int64_t)b.tok0 * H + row;
     __nv_bfloat16* dst = out + q_row * 512 + 256 * (wi >> 2) + 128 * (L >> 6) + 4 * col;
     float* lse_row = wi < 2 && col == 0 ? lse + q_row : nullptr;  // (one of the four lanes that hold the row)
@@ -844,35 +862,36 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
       if (on) m.store(dst, lse_row);
       continue;
     }
-    ChunkMerge<2> m;
-    for (int i0 = j; on && i0 < b.splits; i0 += 32) {  // four of this warp's pieces in flight
-      float4 v[4][2];
-      float x[4], s[4];
+    ChunkMerge<1> m;
+    for (int i0 = j; on && i0 < b.splits; i0 += 80) {  // ten of this warp's pieces in flight
+      float4 v[10][1];
+      float x[10], s[10];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 10; ++k) {
         const int i = i0 + 8 * k;
         const bool in = i < b.splits;
         x[k] = in ? lsrc[(int64_t)i * kChunkRows] : -INFINITY;
         s[k] = 1.f;
-#pragma unroll
-        for (int f = 0; f < 2; ++f) v[k][f] = in ? __ldcs(src + i * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[k][0] = in ? __ldcs(src + i * kStep) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       m.add(x, s, v);
     }
     __syncthreads();  // (the item before has been read)
-    sh_acc[j][0][lane] = m.acc[0];
-    sh_acc[j][1][lane] = m.acc[1];
+    sh_acc[j][lane] = m.acc[0];
     sh_m[j][lane] = m.nan ? NAN : m.M;
     sh_s[j][lane] = m.S;
     __syncthreads();
     if (j == 0 && on) {
-      ChunkMerge<2> t;
+      ChunkMerge<1> t;
+      float4 v[8][1];
+      float x[8], s[8];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float x[2] = {sh_m[i][lane], sh_m[i + 1][lane]}, s[2] = {sh_s[i][lane], sh_s[i + 1][lane]};
-        const float4 v[2][2] = {{sh_acc[i][0][lane], sh_acc[i][1][lane]}, {sh_acc[i + 1][0][lane], sh_acc[i + 1][1][lane]}};
-        t.add(x, s, v);
+      for (int i = 0; i < 8; ++i) {
+        x[i] = sh_m[i][lane];
+        s[i] = sh_s[i][lane];
+        v[i][0] = sh_acc[i][lane];
       }
+      t.add(x, s, v);
       t.store(dst, lse_row);
     }
   }
@@ -1036,7 +1055,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     if (k < nb) {
       blocks[k].splits = s;
       blocks[k].offset = (int32_t)o;
-      if (s > 1) sched[l.split_list + ns + le] = (int32_t)k;
+      if (s > 1) reinterpret_cast<ChunkBlock*>(sched + l.split_list)[ns + le] = blocks[k];
     }
     ns += sum;
     if (shares) {
@@ -1047,7 +1066,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
   }
   __syncthreads();
   for (int u = tid; u < U; u += 1024) {
-    int32_t* rec = sched + l.units + kUnitInts * u;
+    int32_t* rec = sched + l.units + kChunkUnitInts * u;
     if (shares)
       chunk_share_unit(blocks, pos, (int)nb, at, u, rec);
     else

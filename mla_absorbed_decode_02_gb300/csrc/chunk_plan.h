@@ -24,6 +24,7 @@ namespace mla {
 constexpr int32_t kChunkMagic = 0x4D4C4143;  // "MLAC"
 constexpr int kChunkHeader = 16;              // int32 header words
 constexpr int kChunkBlockInts = 8;            // int32 words per block record
+constexpr int kChunkUnitInts = 16;            // int32 words per unit record
 constexpr int kChunkRows = 128;               // rows of a block (MMA M of a CTA pair)
 constexpr int kChunkTile = 256;               // keys of a tile (four pages)
 // Cost positions of a tile, and of a piece beyond its tiles (the query load, the epilogue, the
@@ -83,9 +84,9 @@ MLA_HD inline int64_t chunk_block_capacity(int64_t max_tokens, int batch, int H)
 MLA_HD inline ChunkLayout chunk_layout(int U, int64_t cap, int batch) {
   ChunkLayout l;
   l.units = kChunkHeader;
-  l.blocks = l.units + (int64_t)kUnitInts * U;
+  l.blocks = l.units + (int64_t)kChunkUnitInts * U;
   l.split_list = l.blocks + kChunkBlockInts * cap;
-  l.page_off = l.split_list + U;
+  l.page_off = l.split_list + (int64_t)kChunkBlockInts * U;
   l.blk_off = l.page_off + batch + 1;
   l.pos = l.blk_off + batch + 1;
   l.total = l.pos + cap;
@@ -133,11 +134,12 @@ MLA_HD inline int chunk_find(const int32_t* off, int n, int32_t v) {
   return a;
 }
 
-// Unit u's record {first block, first tile, last block, end tile, split index of the first piece}.
+// Unit u's record {first block, first tile, last block, end tile, split index of the first piece, 0, 0, 0,
+// the first block's record} (the kernels read what they need of the plan in one memory latency).
 MLA_HD inline void chunk_unit(const ChunkBlock* blocks, const int32_t* pos, int NB, int64_t total, int64_t budget, int u,
                               int32_t* rec) {
   rec[0] = -1;
-  for (int i = 1; i < kUnitInts; ++i) rec[i] = 0;
+  for (int i = 1; i < kChunkUnitInts; ++i) rec[i] = 0;
   const int64_t lo = (int64_t)u * budget, hi = lo + budget;
   if (lo >= total || NB == 0) return;
   int a = 0, b = NB;  // first block whose last tile lies at or past lo
@@ -160,6 +162,7 @@ MLA_HD inline void chunk_unit(const ChunkBlock* blocks, const int32_t* pos, int 
   rec[2] = c;
   rec[3] = (int32_t)end;
   rec[4] = (int32_t)(u - first0 / budget);
+  *reinterpret_cast<ChunkBlock*>(rec + kUnitInts) = blocks[a];
 }
 
 // (The budget is at least a tile's cost -- with more blocks than units it always is -- so every unit between
@@ -179,7 +182,7 @@ MLA_HD inline int32_t chunk_shares(int32_t nt, int32_t m) {
 MLA_HD inline void chunk_share_unit(const ChunkBlock* blocks, const int32_t* pos, int NB, int64_t total, int u,
                                     int32_t* rec) {
   rec[0] = -1;
-  for (int i = 1; i < kUnitInts; ++i) rec[i] = 0;
+  for (int i = 1; i < kChunkUnitInts; ++i) rec[i] = 0;
   if (u >= total) return;
   const int k = chunk_find(pos, NB, u), i = u - pos[k];
   const int32_t nt = blocks[k].nt, s = blocks[k].splits, even = (nt + s - 1) / s;
@@ -187,6 +190,7 @@ MLA_HD inline void chunk_share_unit(const ChunkBlock* blocks, const int32_t* pos
   rec[1] = i * even;
   rec[3] = nt < (i + 1) * even ? nt : (i + 1) * even;
   rec[4] = i;
+  *reinterpret_cast<ChunkBlock*>(rec + kUnitInts) = blocks[k];
 }
 
 // Host twin: writes sched as the scheduler kernel does; false (and a header without the magic
@@ -247,11 +251,11 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
     at += blocks[k].splits;
     if (blocks[k].splits > 1) {
       slots += blocks[k].splits;
-      sched[l.split_list + ns++] = k;
+      reinterpret_cast<ChunkBlock*>(sched + l.split_list)[ns++] = blocks[k];
     }
   }
   for (int u = 0; u < U; ++u) {
-    int32_t* rec = sched + l.units + kUnitInts * u;
+    int32_t* rec = sched + l.units + kChunkUnitInts * u;
     if (shares)
       chunk_share_unit(blocks, pos, (int)nb, at, u, rec);
     else

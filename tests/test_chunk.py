@@ -38,9 +38,9 @@ def _params(**kw):
 
 def _parse(sched, U):
     cap = sched[2]
-    units = sched[16:16 + 8 * U].reshape(U, 8)
-    blocks = sched[16 + 8 * U:16 + 8 * U + 8 * cap].reshape(cap, 8)[:sched[3]]
-    return units, blocks, sched[16 + 8 * U + 8 * cap:][:sched[7]]
+    units = sched[16:16 + 16 * U].reshape(U, 16)
+    blocks = sched[16 + 16 * U:16 + 16 * U + 8 * cap].reshape(cap, 8)[:sched[3]]
+    return units, blocks, sched[16 + 16 * U + 8 * cap:][:8 * sched[7]].reshape(-1, 8)
 
 
 @pytest.mark.parametrize("H", [1, 7, 16, 64, 96, 128])
@@ -72,6 +72,7 @@ def test_plan_covers_every_tile_once(H, U, seed):
     for rec in units:
         if rec[0] < 0:
             continue
+        assert np.array_equal(rec[8:], blocks[rec[0]])
         for k in range(rec[0], rec[2] + 1):
             t0 = rec[1] if k == rec[0] else 0
             t1 = rec[3] if k == rec[2] else blocks[k][5]
@@ -82,7 +83,7 @@ def test_plan_covers_every_tile_once(H, U, seed):
         assert [t for a, b, _ in parts for t in range(a, b)] == list(range(blocks[k][5]))
         assert [s for _, _, s in parts] == list(range(len(parts))) and blocks[k][6] == len(parts)
         if len(parts) > 1:
-            assert blocks[k][7] == slots and k in split
+            assert blocks[k][7] == slots and any(np.array_equal(r, blocks[k]) for r in split)
             slots += len(parts)
     assert sched[4] == slots <= 2 * max(U - 1, 0) and len(split) == sum(len(v) > 1 for v in seen.values())
     assert sched[8] == sum(-(-int(x) // 64) for x, m in zip(L, n) if m > 0)
@@ -124,7 +125,7 @@ def test_bad_params(kw, status):
 def test_workspace_does_not_grow_with_the_tokens():
     sb, wb = _lib.mla_chunk_workspace_size(_params(num_units=76, max_tokens=8192, num_heads=128))
     assert wb == 2 * 76 * 128 * 513 * 4
-    assert sb == 4 * (16 + 8 * 76 + 8 * 8192 + 76 + 4 + 4 + 8192)
+    assert sb == 4 * (16 + 16 * 76 + 8 * 8192 + 8 * 76 + 4 + 4 + 8192)
     _, wf = _lib.mla_chunk_workspace_size(_params(num_units=76, kv_dtype=_lib.MLA_KV_FP8_E4M3, max_kv_tokens=1000))
     assert wf == wb + 15 * 64 * 1152
 
