@@ -220,7 +220,7 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
       return st;
   }
   if ((st = launch_after(stream, dim3(2 * U), kCkThreads, kCkSmem, mla_chunk_kernel, a))) return st;
-  const int64_t items = (int64_t)U * 512, most = (int64_t)d->sm_count * 3;  // at most U blocks are split
+  const int64_t items = (int64_t)U * 128, most = (int64_t)d->sm_count * 3;  // at most U blocks are split
   return launch_after(stream, dim3((unsigned)(items < most ? items : most)), 256, 0, mla_chunk_combine_kernel, sc, U, (int)bufs.cap, p->batch,
                       p->num_heads, (const float*)a.o_acc, (const float*)a.lse_acc, a.out, lse);
 }

@@ -754,11 +754,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 
 // ----------------------------------------------------------------- merge of split blocks
 // out = sum_i exp(lse_i - lse) out_i over the units that shared a block.  Three blocks of eight warps per SM
-// stride over the items.
-//   Stretches (most split blocks have two pieces): an item is the 32 rows x 128 dims that one of the 2 x 8
-//   warps of the attention wrote; a warp takes 16 of the dims (32 bytes of a bf16 row), two pieces in flight.
-//   Shares (few blocks, each in up to as many pieces as there are units): an item is 4 of those dims; the
-//   eight warps take every eighth piece each, ten in flight, and meet in shared memory.
+// stride over the items.  An item is the 32 rows x 128 dims that one of the 2 x 8 warps of the attention wrote,
+// or a quarter of them by pieces:
+//   Fewer than eight pieces a block on average: a warp takes 16 of the dims (32 bytes of a bf16 row) over all
+//   pieces, two in flight; nothing is exchanged.  24 blocks of three pieces 66 us with the attention, 75 the
+//   other way; 75 blocks of two 202 against 225.
+//   Eight or more (then there are few blocks, and a warp of a row's own would run alone through them): an item
+//   is 16 of the dims, each warp takes every eighth piece, and they meet in shared memory.  One block of 74
+//   pieces 52 us with the attention, 84 the other way; 2 of 32 16 against 29; 8 of 8 28.6 against 29.0.
 // Merging inside the attention kernel instead, by whichever unit comes last (a counter per warp), took as
 // long: 7 us more there against 9 us here.
 template <int kCols>
@@ -819,16 +822,16 @@ struct ChunkMerge {  // running log-sum-exp merge of one row's float4 columns
 __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, int U, int capacity, int batch, int H,
                                                                 const float* o_acc, const float* lse_acc,
                                                                 __nv_bfloat16* out, float* lse) {
-  __shared__ float4 sh_acc[8][32];
+  __shared__ float4 sh_acc[8][4][32];
   __shared__ float sh_m[8][32], sh_s[8][32];
   pdl_wait_prerequisites();
   const ChunkLayout lay = chunk_layout(U, capacity, batch);
   const int4 h0 = reinterpret_cast<const int4*>(sched)[0], h1 = reinterpret_cast<const int4*>(sched)[1],
              h2 = reinterpret_cast<const int4*>(sched)[2];
-  static_assert(kChNumSplit == 7 && kChShares == 9, "header");
+  static_assert(kChSlots == 4 && kChNumSplit == 7 && kChBatch == 10, "header");
   if (h0.x != kChunkMagic || h0.y != U || h0.z != capacity || h2.z != batch) return;
-  const bool shares = h2.y != 0;
-  const int per = shares ? 512 : 16, items = per * h1.w, lane = threadIdx.x & 31, j = threadIdx.x >> 5;
+  const bool fine = h1.x >= 8 * h1.w;  // slots against split blocks
+  const int per = fine ? 128 : 16, step = fine ? 8 : 1, items = per * h1.w, lane = threadIdx.x & 31, j = threadIdx.x >> 5;
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
     const int4* rec = reinterpret_cast<const int4*>(sched + lay.split_list) + 2 * (it / per);
     const int4 lo = rec[0], hi = rec[1];
@@ -836,52 +839,39 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
     b.tok0 = lo.x; b.ntok = lo.y; b.splits = hi.z; b.offset = hi.w;
     const int writer = it & 15, wi = writer & 7, L = 32 * (wi & 3) + lane, row = 64 * (writer >> 3) + (L & 63);
     const bool on = row < b.ntok * H;
-    const int col = shares ? (it >> 4) & 31 : 4 * j;  // float4 columns [col, col + 1 or 4) of the 32
+    const int col = fine ? 4 * ((it >> 4) & 7) : 4 * j;  // float4 columns [col, col + 4) of the 32
     const int64_t q_row = (int64_t)b.tok0 * H + row;
     __nv_bfloat16* dst = out + q_row * 512 + 256 * (wi >> 2) + 128 * (L >> 6) + 4 * col;
     float* lse_row = wi < 2 && col == 0 ? lse + q_row : nullptr;  // (one of the four lanes that hold the row)
     const float* lsrc = lse_acc + (int64_t)b.offset * kChunkRows + row;
     const float4* src = reinterpret_cast<const float4*>(o_acc) + (((int64_t)b.offset * 16 + writer) * 32 + col) * 32 + lane;
     constexpr int64_t kStep = 16 * 32 * 32;  // float4 per piece
-    if (!shares) {
-      ChunkMerge<4> m;
-      for (int i0 = 0; on && i0 < b.splits; i0 += 2) {
-        float4 v[2][4];
-        float x[2], s[2];
+    ChunkMerge<4> m;
+    for (int i0 = fine ? j : 0; on && i0 < b.splits; i0 += 2 * step) {
+      float4 v[2][4];
+      float x[2], s[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const bool in = i0 + k < b.splits;
-          x[k] = in ? lsrc[(int64_t)(i0 + k) * kChunkRows] : -INFINITY;
-          s[k] = 1.f;
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-            v[k][f] = in ? __ldcs(src + (i0 + k) * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        m.add(x, s, v);
-      }
-      if (on) m.store(dst, lse_row);
-      continue;
-    }
-    ChunkMerge<1> m;
-    for (int i0 = j; on && i0 < b.splits; i0 += 80) {  // ten of this warp's pieces in flight
-      float4 v[10][1];
-      float x[10], s[10];
-#pragma unroll
-      for (int k = 0; k < 10; ++k) {
-        const int i = i0 + 8 * k;
+      for (int k = 0; k < 2; ++k) {
+        const int i = i0 + k * step;
         const bool in = i < b.splits;
         x[k] = in ? lsrc[(int64_t)i * kChunkRows] : -INFINITY;
         s[k] = 1.f;
-        v[k][0] = in ? __ldcs(src + i * kStep) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) v[k][f] = in ? __ldcs(src + i * kStep + 32 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       m.add(x, s, v);
     }
+    if (!fine) {
+      if (on) m.store(dst, lse_row);
+      continue;
+    }
     __syncthreads();  // (the item before has been read)
-    sh_acc[j][lane] = m.acc[0];
     sh_m[j][lane] = m.nan ? NAN : m.M;
     sh_s[j][lane] = m.S;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) sh_acc[j][f][lane] = m.acc[f];
     __syncthreads();
-    if (j == 0 && on) {
+    if (j < 4 && on) {
       ChunkMerge<1> t;
       float4 v[8][1];
       float x[8], s[8];
@@ -889,10 +879,10 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
       for (int i = 0; i < 8; ++i) {
         x[i] = sh_m[i][lane];
         s[i] = sh_s[i][lane];
-        v[i][0] = sh_acc[i][lane];
+        v[i][0] = sh_acc[i][j][lane];
       }
       t.add(x, s, v);
-      t.store(dst, lse_row);
+      t.store(dst + 4 * j, j == 0 ? lse_row : nullptr);
     }
   }
 }
