@@ -198,6 +198,7 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
         (st = encode_map(&a.map_v, bf, 3, kv, dv, sv, box3, CU_TENSOR_MAP_SWIZZLE_128B)))
       return st;
   }
+  a.kv = static_cast<const uint8_t*>(kv);
   a.block_table = block_table;
   a.sched = sc;
   a.out = static_cast<__nv_bfloat16*>(out);
