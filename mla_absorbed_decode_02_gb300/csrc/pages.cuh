@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max
   lo += k;
   const int first = __shfl_sync(0xffffffffu, start, k), n = __shfl_sync(0xffffffffu, start, k + 1) - first;
   const int64_t pos = (int64_t)__shfl_sync(0xffffffffu, len, k) - n + (t - first);
-  if (n < 0 || pos < 0 || pos >= (int64_t)p.max_pages * kPageRows) {
+  if (n < 0 || t < first || pos < 0 || pos >= (int64_t)p.max_pages * kPageRows) {
     if (lane == 0) pool_error(1);
     return;
   }

@@ -419,6 +419,21 @@ def test_append_outside_the_table_is_refused():
     assert torch.equal(pool, want)
 
 
+@pytest.mark.gpu
+def test_append_of_tokens_before_the_first_sequence_is_refused():
+    """cu[0] past 0: the tokens before it belong to no sequence and go nowhere; the others are written."""
+    import torch
+    p, lat, rope, cu, lens, bt, pool, at, x = _append_case(MLA_KV_BF16, [3, 2], [9, 2], seed=8)
+    want = pool.clone()
+    cu[0], lens[0] = 2, 7                         # one token is left of the first three: row 6
+    want[at[0][0], 6] = x[2].view(torch.uint8)
+    pg, r = (torch.tensor(v, device="cuda") for v in zip(*at[3:]))
+    want[pg, r] = x[3:5].view(torch.uint8)
+    _lib.mla_append_kv(p, lat, rope, cu, lens, bt, pool)
+    assert _lib.mla_device_error(clear=True) == _lib.MLA_ERR_INVALID_ARG
+    assert torch.equal(pool, want)
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", [MLA_KV_BF16, MLA_KV_FP8_E4M3])
