@@ -378,7 +378,8 @@ int32_t mla_chunk_schedule(const mla_chunk_params* p, const int32_t* cu_seqlens,
  *   out              device bf16 [T][H][512], latent outputs (W_UV is not applied)
  *   lse              device float32 [T][H], natural log; a token that sees no key gets out = 0,
  *                    lse = -inf.  Rows of tokens at or past cu_seqlens[B] are left as they were
- *   sched            device, from mla_chunk_schedule with the same p (metadata of other params sets
+ *   sched            device, from mla_chunk_schedule with the same p (a plan made with another
+ *                    B, T, H, max_pages_per_seq, causal, max_kv_tokens or unit count sets
  *                    MLA_ERR_WORKSPACE in the device error word, and nothing is written)
  *   workspace        device, workspace_bytes, 256-byte aligned; not shared by calls that overlap
  * Scores, softmax statistics and sums are float32; P is bf16 for the P.V product.  A row of the
@@ -396,10 +397,12 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
  * 0x4D4C4143, [1] = units, [2] = block capacity, [3] = blocks, [4] = partial slots, [5] = budget of
  * cost positions per unit, [6] = tokens per block, [7] = split blocks, [8] = pages of the sequences
  * with new tokens, [9] = 1: no more blocks than units, each unit has one share of one block, and [5]
- * is the most tiles of a share; [10] = B, [11] = causal, [12..15] = 0; then per unit 16 ints {first block, first tile, last block, end tile,
- * split index of the first piece, 0, 0, 0, the first block's record} (first block -1: no work); then
- * per block 8 ints {first token, tokens, sequence, keys the first token sees before clipping, L, tiles
- * of 256 keys, splits, first slot}; then the split blocks' records, and the first page of each sequence.
+ * is the most tiles of a share; [10] = B, [11] = causal, [12] = T, [13] = H, [14] = max_pages_per_seq, [15] =
+ * FP8: max_kv_tokens / 64, bf16: INT32_MAX; then per unit 16 ints {first block, first tile, last block,
+ * end tile, split index of the first piece, 0, 0, 0, the first block's record} (first block -1: no
+ * work); then per block 8 ints {first token, tokens, sequence, keys the first token sees before clipping,
+ * L, tiles of 256 keys, splits, first slot}; then the split blocks' records, and the first page of each
+ * sequence.
  * MLA_ERR_INVALID_ARG where the scheduler kernel refuses.
  */
 int32_t mla_chunk_plan_host(const mla_chunk_params* p, int32_t num_units, const int32_t* cu_seqlens,
@@ -427,7 +430,7 @@ typedef struct mla_pool_params {
 /*
  * Appends the rows of ragged new tokens to the cache of one layer (num_layers and layer_stride are
  * not used): token cu[b] + i goes to row L_b - n_b + i of sequence b, through the block table.
- *   max_tokens     rows of latent and k_rope; tokens at or past cu_seqlens[B] are not read
+ *   max_tokens     rows of latent and k_rope; those at or past cu_seqlens[B] go nowhere
  *   latent         device bf16, row t at latent + t * latent_stride elements: 512 latent values
  *   k_rope         device bf16, row t at k_rope + t * rope_stride elements: 64 RoPE key values
  *                  (strides: multiples of 8 elements, so the two parts of one [T][576] array will do)

@@ -204,26 +204,20 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.H = p->num_heads;
-  a.causal = p->causal != 0;
-  a.max_pages = p->max_pages_per_seq;
+  a.key = {U, (int32_t)bufs.cap, p->batch, p->causal != 0, p->max_tokens, p->num_heads, p->max_pages_per_seq, (int32_t)chunk_kv_pages(p)};
   a.num_pages = p->num_pages;
-  a.num_units = U;
-  a.capacity = (int32_t)bufs.cap;
-  a.batch = p->batch;
   a.expanded = fp8;
   a.timeout_ns = (uint64_t)(p->timeout_us > 0 ? p->timeout_us : 2000000) * 1000ull;
   if (fp8) {
     const int64_t pages = p->max_kv_tokens / 64, most = (int64_t)d->sm_count * 8;
-    if ((st = launch_after(stream, dim3((unsigned)(pages < most ? pages : most)), 256, 0, mla_chunk_expand_kernel, sc, U,
-                           (int)bufs.cap, p->batch, static_cast<const uint8_t*>(kv_pages), block_table,
-                           p->max_pages_per_seq, p->num_pages, cache_seqlens, static_cast<__nv_bfloat16*>(rows))))
+    if ((st = launch_after(stream, dim3((unsigned)(pages < most ? pages : most)), 256, 0, mla_chunk_expand_kernel, sc, a.key,
+                           static_cast<const uint8_t*>(kv_pages), block_table, p->num_pages, cache_seqlens, static_cast<__nv_bfloat16*>(rows))))
       return st;
   }
   if ((st = launch_after(stream, dim3(2 * U), kCkThreads, kCkSmem, mla_chunk_kernel, a))) return st;
   const int64_t items = (int64_t)U * 128, most = (int64_t)d->sm_count * 3;  // at most U blocks are split
-  return launch_after(stream, dim3((unsigned)(items < most ? items : most)), 256, 0, mla_chunk_combine_kernel, sc, U, (int)bufs.cap, p->batch,
-                      p->num_heads, (const float*)a.o_acc, (const float*)a.lse_acc, a.out, lse);
+  return launch_after(stream, dim3((unsigned)(items < most ? items : most)), 256, 0, mla_chunk_combine_kernel, sc,
+                      a.key, (const float*)a.o_acc, (const float*)a.lse_acc, a.out, lse);
 }
 
 int32_t mla_append_kv(const mla_pool_params* p, int64_t max_tokens, const void* latent, int64_t latent_stride,

@@ -96,7 +96,8 @@ struct ChunkArgs {
   float* o_acc;         // split partials, normalised, 128 x 512 each in the accumulators' order
   float* lse_acc;       // [slots][128]
   float scale_log2;
-  int32_t H, causal, max_pages, num_pages, num_units, capacity, batch;
+  ChunkKey key;
+  int32_t num_pages;
   int32_t expanded;     // the cache rows are the expanded ones: page = page_off[seq] + logical page
   uint64_t timeout_ns;
 };
@@ -178,6 +179,14 @@ struct ChunkTileRef {
   bool first, last;
   __device__ int pages() const { return min(max((vis - kChunkTile * tile + 63) >> 6, 0), 4); }
 };
+
+// The header's words 0..3, 8..11 and 12..15 against the call's.
+__device__ __forceinline__ bool chunk_plan_is(int4 h0, int4 h2, int4 h3, const ChunkKey& k) {
+  static_assert(kChMagic == 0 && kChUnits == 1 && kChCapacity == 2 && kChBatch == 10 && kChCausal == 11 && kChMaxTokens == 12 &&
+                kChHeads == 13 && kChMaxPages == 14 && kChKvPages == 15, "header");
+  return h0.x == kChunkMagic && h0.y == k.units && h0.z == k.capacity && h2.z == k.batch && h2.w == k.causal &&
+         h3.x == k.max_tokens && h3.y == k.heads && h3.z == k.max_pages && h3.w == k.kv_pages;
+}
 
 // Walks the unit's tiles in order, across blocks.
 struct ChunkCursor {
@@ -269,14 +278,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   }
   pdl_wait_prerequisites();
   const int32_t* sched = args.sched;
-  const ChunkLayout lay = chunk_layout(args.num_units, args.capacity, args.batch);
+  const ChunkLayout lay = chunk_layout(args.key.units, args.key.capacity, args.key.batch);
   const int4* rec = reinterpret_cast<const int4*>(sched + lay.units + kChunkUnitInts * (blockIdx.x >> 1));
   // (header and record in whole vectors: one memory latency for all of it)
-  const int4 h0 = reinterpret_cast<const int4*>(sched)[0], h1 = reinterpret_cast<const int4*>(sched)[1],
-             h2 = reinterpret_cast<const int4*>(sched)[2], r0 = rec[0], r1 = rec[1], r2 = rec[2], r3 = rec[3];
-  static_assert(kChMagic == 0 && kChUnits == 1 && kChCapacity == 2 && kChTokens == 6 && kChBatch == 10 && kChCausal == 11, "header");
-  const bool bad_meta = h0.x != kChunkMagic || h0.y != args.num_units || h0.z != args.capacity ||
-                        h1.z != chunk_tokens_per_block(args.H) || h2.z != args.batch || h2.w != args.causal;
+  const int4 h0 = reinterpret_cast<const int4*>(sched)[0], h2 = reinterpret_cast<const int4*>(sched)[2],
+             h3 = reinterpret_cast<const int4*>(sched)[3], r0 = rec[0], r1 = rec[1], r2 = rec[2], r3 = rec[3];
+  const bool bad_meta = !chunk_plan_is(h0, h2, h3, args.key);
   const bool idle = bad_meta || r0.x < 0;  // the same in both CTAs
   if (bad_meta && tid == 0) atomicCAS(&g_mla_error, 0, 5);
   pdl_launch_dependents();
@@ -287,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   wc.timeout_ns = args.timeout_ns;
   const uint32_t lead0 = map_to_rank(bar(0), 0);  // the leader's barrier i is at lead0 + 8 i
   ChunkCursor cur;
-  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), r0, r1.x, r2, r3, args.causal);
+  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), r0, r1.x, r2, r3, args.key.causal);
 
   if (idle) {
   } else if (warp < kCkCopyWarps) {
@@ -322,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       const int lp = 4 * r.tile + lane;
       if (lane >= 4 || lane >= r.pages()) return 0;
       if (args.expanded) return page_off[r.b.seq] + lp;
-      return args.block_table[(int64_t)r.b.seq * args.max_pages + lp];
+      return args.block_table[(int64_t)r.b.seq * args.key.max_pages + lp];
     };
     auto checked = [&](int page) -> int {
       if (!args.expanded && (page < 0 || page >= args.num_pages)) {  // outside the contract: reported, another page read
@@ -364,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       return true;
     };
     auto copy_v = [&](const ChunkTileRef& r, int page) -> bool {
-      const int np = r.pages(), some = chunk_visible(r.b, 0, args.causal);  // keys every row of the block sees
+      const int np = r.pages(), some = chunk_visible(r.b, 0, args.key.causal);  // keys every row of the block sees
 #pragma unroll 1
       for (int k = mine(); k < 2 * np; k += kCkCopyWarps) {
         const int kb = k >> 1, n = k & 1;
@@ -489,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       auto pv = [&](const ChunkTileRef& r, uint32_t t) -> bool {
         if (!wait(bar(CB_P_FULL), t & 1, kSiteCkP)) return false;
         tc_fence_after();
-        const int np = r.pages(), some = chunk_visible(r.b, 0, args.causal);
+        const int np = r.pages(), some = chunk_visible(r.b, 0, args.key.causal);
 #pragma unroll 1
         for (int kb = 0; kb < np; ++kb) {
           const bool written = kChunkTile * r.tile + 64 * kb + 64 > some;  // the copying warp looked through it
@@ -544,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     const uint32_t full = lead0 + 8 * CB_Q_FULL;
     const bool el = elect_one();
     while (cur.next(r)) {
-      const int row = r.b.tok0 * args.H + 64 * (int)rank;
+      const int row = r.b.tok0 * args.key.heads + 64 * (int)rank;
       if (piece > 0) {
         if (el) {
           tma_prefetch_3d(&args.map_q, 0, row, 0);
@@ -586,11 +593,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       if (!wait_warp(bar(CB_SUM), pieces & 1, wc, kSiteCkRed)) return false;
       ++pieces;
       const float l = sums[row] + sums[64 + row] + sums[128 + row] + sums[192 + row];
-      const int rows = e.b.ntok * args.H - (r - lane);  // rows of this warp's 32 that the block has
+      const int rows = e.b.ntok * args.key.heads - (r - lane);  // rows of this warp's 32 that the block has
       const bool split = e.b.splits > 1;
       const bool none = e.vis == 0;  // no tile had keys: the accumulator was never written
       const uint64_t inv = splat_f32x2(l == 0.f ? 0.f : 1.f / l);
-      const int64_t q_row = (int64_t)e.b.tok0 * args.H + r, slot = e.b.offset + e.split;
+      const int64_t q_row = (int64_t)e.b.tok0 * args.key.heads + r, slot = e.b.offset + e.split;
       const uint32_t acc = tmem + lane_off + CT_O + 128 * w;
       if (split) {
         // partials stay in the accumulator's order, [slot][CTA][warp][4 columns][lane]: whole 512-byte
@@ -660,9 +667,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     uint32_t g = 0;
     for (; ok && cur.next(a); ++g) {
       if (a.first) {
-        const int j = r / args.H;  // this row's token of the block
-        lim = j < a.b.ntok ? chunk_visible(a.b, j, args.causal) : 0;
-        some = chunk_visible(a.b, 0, args.causal);
+        const int j = r / args.key.heads;  // this row's token of the block
+        lim = j < a.b.ntok ? chunk_visible(a.b, j, args.key.causal) : 0;
+        some = chunk_visible(a.b, 0, args.key.causal);
       }
       const uint32_t sb = g & 1;
       if (!(ok = wait_warp<true>(bar(CB_S_FULL + sb), (g >> 1) & 1, wc, kSiteCkScores))) break;
@@ -675,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       __syncwarp();
       // (relaxed: the scores are in registers; nothing was written that the MMA warp reads)
       if (lane == 0) mbar_arrive_remote_relaxed(lead0 + 8 * (CB_S_EMPTY + sb), sv[0] ^ sv[63]);
-      if (kChunkTile * (a.tile + 1) > some || r >= a.b.ntok * args.H) {
+      if (kChunkTile * (a.tile + 1) > some || r >= a.b.ntok * args.key.heads) {
         // keys this row sees of the thread's 64; a seen score of -inf comes of a key that is not
         // finite (and whose value row was zeroed): the row becomes NaN
         const int nv = lim - (kChunkTile * a.tile + 64 * part);
@@ -834,17 +841,16 @@ struct ChunkMerge {  // running log-sum-exp merge of one row's float4 columns
   }
 };
 
-__global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, int U, int capacity, int batch, int H,
-                                                                const float* o_acc, const float* lse_acc,
-                                                                __nv_bfloat16* out, float* lse) {
+__global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* sched, ChunkKey key, const float* o_acc,
+                                                                const float* lse_acc, __nv_bfloat16* out, float* lse) {
   __shared__ float4 sh_acc[8][4][32];
   __shared__ float sh_m[8][32], sh_s[8][32];
   pdl_wait_prerequisites();
-  const ChunkLayout lay = chunk_layout(U, capacity, batch);
-  const int4 h0 = reinterpret_cast<const int4*>(sched)[0], h1 = reinterpret_cast<const int4*>(sched)[1],
-             h2 = reinterpret_cast<const int4*>(sched)[2];
-  static_assert(kChSlots == 4 && kChNumSplit == 7 && kChBatch == 10, "header");
-  if (h0.x != kChunkMagic || h0.y != U || h0.z != capacity || h2.z != batch) return;
+  const ChunkLayout lay = chunk_layout(key.units, key.capacity, key.batch);
+  const int H = key.heads;
+  const int4 *h = reinterpret_cast<const int4*>(sched), h0 = h[0], h1 = h[1], h2 = h[2], h3 = h[3];
+  static_assert(kChSlots == 4 && kChNumSplit == 7, "header");
+  if (!chunk_plan_is(h0, h2, h3, key)) return;
   const bool fine = h1.x >= 8 * h1.w;  // slots against split blocks
   const int per = fine ? 128 : 16, step = fine ? 8 : 1, items = per * h1.w, lane = threadIdx.x & 31, j = threadIdx.x >> 5;
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
@@ -907,19 +913,19 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
 // pages (sequence b's from page_off[b]): value = bf16(code x scale), RoPE copied.  A chunk's rows
 // read every cached row many times over, so 1808 bytes of traffic a cached token stand against
 // 278,528 FLOP per new token at 128 heads.  A warp takes a row: lane l the codes [16 l, 16 l + 16).
-__global__ void __launch_bounds__(256) mla_chunk_expand_kernel(const int32_t* sched, int U, int capacity, int batch,
-                                                               const uint8_t* pages, const int32_t* block_table,
-                                                               int max_pages, int num_pages, const int32_t* lens,
+__global__ void __launch_bounds__(256) mla_chunk_expand_kernel(const int32_t* sched, ChunkKey key, const uint8_t* pages,
+                                                               const int32_t* block_table, int num_pages, const int32_t* lens,
                                                                __nv_bfloat16* rows) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  if (sched[kChMagic] != kChunkMagic || sched[kChUnits] != U || sched[kChCapacity] != capacity || sched[kChBatch] != batch) return;
-  const ChunkLayout lay = chunk_layout(U, capacity, batch);
+  const int4* h = reinterpret_cast<const int4*>(sched);
+  if (!chunk_plan_is(h[0], h[2], h[3], key)) return;
+  const ChunkLayout lay = chunk_layout(key.units, key.capacity, key.batch);
   const int32_t* page_off = sched + lay.page_off;
   const int total = sched[kChPages], warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int pg = blockIdx.x; pg < total; pg += gridDim.x) {
-    const int b = chunk_find(page_off, batch, pg), lp = pg - page_off[b];
-    int page = block_table[(int64_t)b * max_pages + lp];
+    const int b = chunk_find(page_off, key.batch, pg), lp = pg - page_off[b];
+    int page = block_table[(int64_t)b * key.max_pages + lp];
     if (page < 0 || page >= num_pages) {
       if (threadIdx.x == 0) atomicCAS(&g_mla_error, 0, 1);
       page = 0;
@@ -1078,8 +1084,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
       chunk_unit(blocks, pos, (int)nb, total, budget, u, rec);
   }
   if (tid == 0) {
-    sched[kChUnits] = U;
-    sched[kChCapacity] = (int32_t)cap;
+    chunk_write_key(sched, {U, (int32_t)cap, B, causal, (int32_t)max_tokens, H, max_pages, (int32_t)max_kv_pages});
     sched[kChBlocks] = (int32_t)nb;
     sched[kChSlots] = (int32_t)slots;
     sched[kChBudget] = (int32_t)budget;
@@ -1087,8 +1092,6 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     sched[kChNumSplit] = (int32_t)ns;
     sched[kChPages] = (int32_t)pages;
     sched[kChShares] = shares;
-    sched[kChBatch] = B;
-    sched[kChCausal] = causal;
     sched[kChMagic] = kChunkMagic;
   }
 }

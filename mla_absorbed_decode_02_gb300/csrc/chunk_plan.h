@@ -53,7 +53,26 @@ MLA_HD inline int32_t chunk_share_tiles(int32_t longest, int32_t least, int64_t 
 }
 
 // header words
-enum { kChMagic = 0, kChUnits, kChCapacity, kChBlocks, kChSlots, kChBudget, kChTokens, kChNumSplit, kChPages, kChShares, kChBatch, kChCausal };
+enum {
+  kChMagic = 0, kChUnits, kChCapacity, kChBlocks, kChSlots, kChBudget, kChTokens, kChNumSplit, kChPages, kChShares, kChBatch,
+  kChCausal, kChMaxTokens, kChHeads, kChMaxPages, kChKvPages
+};
+
+// What a plan was made for.  The kernels that use it compare all of it: every index they form is
+// bounded by the plan's own limits, not by the lengths.
+struct ChunkKey {
+  int32_t units, capacity, batch, causal, max_tokens, heads, max_pages, kv_pages;
+};
+MLA_HD inline void chunk_write_key(int32_t* sched, const ChunkKey& k) {
+  sched[kChUnits] = k.units;
+  sched[kChCapacity] = k.capacity;
+  sched[kChBatch] = k.batch;
+  sched[kChCausal] = k.causal;
+  sched[kChMaxTokens] = k.max_tokens;
+  sched[kChHeads] = k.heads;
+  sched[kChMaxPages] = k.max_pages;
+  sched[kChKvPages] = k.kv_pages;
+}
 
 // Block record.
 struct ChunkBlock {
@@ -262,8 +281,7 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
       chunk_unit(blocks, pos, (int)nb, total, budget, u, rec);
   }
   sched[kChMagic] = kChunkMagic;
-  sched[kChUnits] = U;
-  sched[kChCapacity] = (int32_t)cap;
+  chunk_write_key(sched, {U, (int32_t)cap, B, causal, (int32_t)max_tokens, H, max_pages, (int32_t)max_kv_pages});
   sched[kChBlocks] = (int32_t)nb;
   sched[kChSlots] = slots;
   sched[kChBudget] = (int32_t)budget;
@@ -271,8 +289,6 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
   sched[kChNumSplit] = ns;
   sched[kChPages] = (int32_t)pages;
   sched[kChShares] = shares;
-  sched[kChBatch] = B;
-  sched[kChCausal] = causal;
   return true;
 }
 

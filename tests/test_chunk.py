@@ -412,6 +412,35 @@ def test_refused_plan_writes_nothing(lens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kv, change", [("bf16", dict(causal=0)), ("bf16", dict(num_heads=15)), ("bf16", dict(max_tokens=4)),
+                                        ("bf16", dict(num_units=9)), ("bf16", dict(max_pages_per_seq=46)), ("fp8", dict(max_kv_tokens=64 * 51)),
+                                        ("bf16", dict(batch=1)), ("fp8", dict(kv_dtype=_lib.MLA_KV_BF16))])
+def test_plan_of_other_params(kv, change):
+    """A plan made for one set of params and used with another writes nothing, whichever of them differs: neither
+    the attention nor the merge of the split blocks (there are some) takes an index from it."""
+    import ctypes
+
+    import torch
+    q = Problem([2, 3], [300, 47 * 64], 16, kv, num_units=8)
+    attn = _lib.ChunkAttention(q.p)
+    q.check(attn)
+    assert int(attn.sched[7]) > 0                  # split blocks
+    other = MlaChunkParams.from_buffer_copy(q.p)
+    for k, v in change.items():
+        assert getattr(q.p, k) != v
+        setattr(other, k, v)
+    out = torch.full_like(q.d_q, 7.0)
+    lse = torch.full(q.d_q.shape[:2], 7.0, device="cuda")
+    ptr = lambda *ts: [ctypes.c_void_p(t.data_ptr()) for t in ts]  # noqa: E731
+    st = _lib.load_library().mla_chunk_attend(
+        ctypes.byref(other), *ptr(q.d_q, q.d_qr, q.pool, q.d_bt, q.d_L), ctypes.c_float(SCALE),
+        *ptr(out, lse, attn.sched, _lib.ChunkAttention(q.p).workspace), ctypes.c_void_p(_lib._stream(None)))
+    assert st == 0
+    assert _lib.mla_device_error(clear=True) == _lib.MLA_ERR_WORKSPACE
+    assert (out == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_captured_and_on_two_streams(kv):
     """Two problems, each with buffers of its own, captured into graphs and replayed at the same time on two
