@@ -25,12 +25,14 @@
 // run the softmax.  A row's 256 scores lie in four threads, which agree on its maximum through
 // shared memory; O is rescaled only when the maximum grows by more than 2^8.
 //
-// Measured: 512 tokens x 128 heads after 32,768 rows in 2.8-2.9 ms, 1620-1690 TFLOP/s (88% of the
-// measured cuBLAS rate, 97% of its sustained rate); 4 x ~450 tokens x 16 heads after ~3000 rows in
-// 148 us, 1346 TFLOP/s; the tensor cores' own time for a tile is 4352 cycles of ~5900.  What is left
-// is each slot's wait (~75 cycles, in which the one issuing thread feeds nothing) and the turnaround
-// of a slot: MMA done, both CTAs told, copy issued, L2, both CTAs' bytes counted -- seven slots
-// barely cover it, and shared memory has no room for an eighth.
+// Measured: 512 tokens x 128 heads after 32,768 rows in 2.71-2.84 ms, 1660-1740 TFLOP/s (91% of the
+// measured cuBLAS rate, 100% of its sustained rate); 4 x ~450 tokens x 16 heads after ~3000 rows in 138
+// us, 1445 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 202 us, 1350 TFLOP/s.  The tensor cores' own
+// time for a tile is 4352 cycles of ~5750.  What is left is each slot's wait (~75 cycles, in which the one
+// issuing thread feeds nothing) and the turnaround of a slot: MMA done, both CTAs told, copy issued, L2,
+// both CTAs' bytes counted -- seven slots barely cover it, and shared memory has no room for an eighth.
+// With many short blocks add the change of block (~3/4 of a tile: the last softmax and the first have no
+// MMAs beside them), launch and merge (~15 us).
 //
 // Rows of a block see different numbers of keys where it holds several tokens.  P is zero past a
 // row's limit, but 0 x NaN is NaN, so in the pages that some row does not see in full the copying
@@ -913,6 +915,8 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
 // pages (sequence b's from page_off[b]): value = bf16(code x scale), RoPE copied.  A chunk's rows
 // read every cached row many times over, so 1808 bytes of traffic a cached token stand against
 // 278,528 FLOP per new token at 128 heads.  A warp takes a row: lane l the codes [16 l, 16 l + 16).
+// 63,900 rows in 26 us, 4.5 TB/s, 3% of the attention over them; two or eight rows of a warp in flight
+// instead of four, or half a page a block, changed nothing.
 __global__ void __launch_bounds__(256) mla_chunk_expand_kernel(const int32_t* sched, ChunkKey key, const uint8_t* pages,
                                                                const int32_t* block_table, int num_pages, const int32_t* lens,
                                                                __nv_bfloat16* rows) {
@@ -982,6 +986,7 @@ __device__ __forceinline__ int64_t block_scan_1024(int64_t v, int64_t* sh, int64
 }
 
 // One CTA of 1024 threads; the phases of chunk_plan_host with the sums in parallel.
+// 7-8 us from 8 to 225 blocks: dependent trips to L2 and barriers, once a step for all layers.
 __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu, const int32_t* lens, int B,
                                                                int64_t max_tokens, int H, int causal, int max_pages,
                                                                int64_t max_kv_pages, int U, int64_t cap, int32_t* sched) {
