@@ -69,8 +69,7 @@ enum : uint32_t {
   CB_Q_FULL = CB_RAW + kCkCopyWarps,  // leader
   CB_Q_EMPTY,
   CB_S_FULL,                          // + tile parity
-  CB_S_EMPTY = CB_S_FULL + 2,         // + tile parity, leader: one arrival per softmax warp
-  CB_P_FULL = CB_S_EMPTY + 2,         // leader: one arrival per softmax warp
+  CB_P_FULL = CB_S_FULL + 2,          // leader: one arrival per softmax warp; its scores are read, too
   CB_P_FREE,                          // PV done
   CB_RED,                             // + tile parity: row maxima in shared memory, one arrival per softmax warp
   CB_SUM = CB_RED + 2,                // row sums in shared memory
@@ -265,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     for (uint32_t i = 0; i < kCkBars; ++i) {
       uint32_t count = 1;
       if (i < CB_EMPTY || i == CB_Q_FULL) count = 2;                                    // one per CTA
-      if (i == CB_S_EMPTY || i == CB_S_EMPTY + 1 || i == CB_P_FULL) count = 16;         // 8 softmax warps per CTA
+      if (i == CB_P_FULL) count = 16;                                                   // 8 softmax warps per CTA
       if (i >= CB_RED && i <= CB_SUM) count = 8;
       mbar_init(bar(i), count);
     }
@@ -485,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
           if (!wait(bar(CB_Q_FULL), piece & 1, kSiteCkQ)) return false;
           ++piece;
         }
-        if (t >= 2 && !wait(bar(CB_S_EMPTY + (t & 1)), ((t >> 1) - 1) & 1, kSiteCkScores)) return false;
+        // (tile t - 2's scores are read: its P has been waited for)
         tc_fence_after();
         const uint32_t d_tmem = tmem + CT_S + 128 * (t & 1);
 #pragma unroll
@@ -693,10 +692,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       tmem_ld32(tmem + lane_off + CT_S + 128 * sb + 64 * w, *reinterpret_cast<uint32_t(*)[32]>(sv));
       tmem_ld32(tmem + lane_off + CT_S + 128 * sb + 64 * w + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
       tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      // (relaxed: the scores are in registers; nothing was written that the MMA warp reads)
-      if (lane == 0) mbar_arrive_remote_relaxed(lead0 + 8 * (CB_S_EMPTY + sb), sv[0] ^ sv[63]);
       if (kChunkTile * (a.tile + 1) > some || r >= a.b.ntok * args.key.heads) {
         // keys this row sees of the thread's 64; a seen score of -inf comes of a key that is not
         // finite (and whose value row was zeroed): the row becomes NaN
