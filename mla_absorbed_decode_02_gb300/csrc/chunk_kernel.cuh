@@ -25,14 +25,13 @@
 // run the softmax.  A row's 256 scores lie in four threads, which agree on its maximum through
 // shared memory; O is rescaled only when the maximum grows by more than 2^8.
 //
-// Measured: 512 tokens x 128 heads after 32,768 rows in 2.71-2.84 ms, 1660-1740 TFLOP/s (91% of the
-// measured cuBLAS rate, 100% of its sustained rate); 4 x ~450 tokens x 16 heads after ~3000 rows in 138
-// us, 1445 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 202 us, 1350 TFLOP/s.  The tensor cores' own
-// time for a tile is 4352 cycles of ~5750.  What is left is each slot's wait (~75 cycles, in which the one
-// issuing thread feeds nothing) and the turnaround of a slot: MMA done, both CTAs told, copy issued, L2,
-// both CTAs' bytes counted -- seven slots barely cover it, and shared memory has no room for an eighth.
-// With many short blocks add the change of block (~3/4 of a tile: the last softmax and the first have no
-// MMAs beside them), launch and merge (~15 us).
+// Measured: 512 tokens x 128 heads after 32,768 rows in 2.63-2.66 ms, 1770-1790 TFLOP/s (95% of the
+// measured cuBLAS rate), 2.73 ms when held for seconds (cuBLAS then: 2.76): the power cap; 4 x ~450 tokens
+// x 16 heads after ~3000 rows in 133 us, 1500 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 198 us, 1380
+// TFLOP/s.  A long append's tile takes 4760 cycles, of which the tensor cores' own are 4352; the prompts'
+// 5220 and the streams' 5780, where slots wait for pages from L2 and HBM.  With many short blocks add the change
+// of block (~3/4 of a tile: the last softmax and the first have no MMAs beside them), launch and
+// merge (~15 us).
 //
 // Rows of a block see different numbers of keys where it holds several tokens.  P is zero past a
 // row's limit, but 0 x NaN is NaN, so in the pages that some row does not see in full the copying
