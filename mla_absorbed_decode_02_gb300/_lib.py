@@ -578,6 +578,18 @@ class Decoder:
         return out, lse
 
 
+def _new(like, shape, dtype, stream):
+    """A result that `stream` writes: its memory comes from that stream's pool, not from what the current stream has
+    let go of but may still be using."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 class ChunkAttention:
     """Convenience wrapper of the chunk attention: owns the plan and the workspace of one problem shape."""
 
@@ -586,7 +598,7 @@ class ChunkAttention:
         self.p = p
         self.device = torch.device("cuda" if device is None else device)
         sb, wb = mla_chunk_workspace_size(p)
-        self.sched = torch.zeros(sb // 4, dtype=torch.int32, device=self.device)
+        self.sched = torch.empty(sb // 4, dtype=torch.int32, device=self.device)  # (nothing to wait for on any stream)
         self.workspace = torch.empty(wb, dtype=torch.uint8, device=self.device)
         self.seqlens = None
 
@@ -596,13 +608,12 @@ class ChunkAttention:
         self.seqlens = cache_seqlens
 
     def attend(self, q_nope_absorbed, q_rope, kv_pages, block_table, scale, out=None, lse=None, stream=None):
-        import torch
         if self.seqlens is None:
             _refuse("ChunkAttention.attend before plan", MLA_ERR_WORKSPACE)
         if out is None:
-            out = torch.empty_like(q_nope_absorbed)
+            out = _new(q_nope_absorbed, q_nope_absorbed.shape, _dtypes()[2], stream)
         if lse is None:
-            lse = torch.empty(q_nope_absorbed.shape[:2], dtype=torch.float32, device=q_nope_absorbed.device)
+            lse = _new(q_nope_absorbed, q_nope_absorbed.shape[:2], _dtypes()[1], stream)
         _attend(self.p, q_nope_absorbed, q_rope, kv_pages, block_table, self.seqlens, scale, out, lse, self.sched,
                 self.workspace, stream)
         return out, lse
@@ -633,14 +644,14 @@ class PagePool:
         """Returns new_pages int32 [n]: the child's own page, -1 (none needed), -2 (refused), -3 (no page left)."""
         if parents.numel() > self.max_forks:
             _refuse("PagePool.fork: more forks than max_forks", MLA_ERR_WORKSPACE)
-        new_pages = parents.new_empty(parents.shape)
+        new_pages = _new(parents, parents.shape, parents.dtype, stream)
         _fork(self.p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, self.workspace,
               stream)
         return new_pages
 
     def reserve(self, num_new, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns served int32 [batch]: 1 (done), 0 (not enough pages), -2 (refused)."""
-        served = num_new.new_empty(num_new.shape)
+        served = _new(num_new, num_new.shape, num_new.dtype, stream)
         _reserve(self.p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
         return served
 
@@ -649,6 +660,6 @@ class PagePool:
 
     def compact(self, kv_pages, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns the number of used pages, int32 [1] on the device."""
-        used = cache_seqlens.new_empty(1)
+        used = _new(cache_seqlens, (1,), cache_seqlens.dtype, stream)
         _compact(self.p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
         return used

@@ -434,6 +434,31 @@ def test_append_of_tokens_before_the_first_sequence_is_refused():
     assert torch.equal(pool, want)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("as_pointer", [False, True])
+def test_results_for_another_stream(as_pointer):
+    """A call on another stream takes no memory for its result that kernels waiting on the current stream still read."""
+    import torch
+    p = MlaPoolParams.make(8, 64, 4)
+    up = _lib.PagePool(p)
+    bt, lens, ref = up.new_tables()
+    new = torch.full((8,), 3, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    _lib.mla_reserve_pages(p, new, bt, lens, ref, torch.empty_like(new), up.workspace)   # loads the kernel
+    torch.cuda.synchronize()
+    x = torch.full((8,), 5, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)              # about a tenth of a second
+    y = x * 2
+    where = x.data_ptr()
+    del x                                       # its memory is free to the current stream, after y
+    served = up.reserve(new, bt, lens, ref, stream=side.cuda_stream if as_pointer else side)
+    assert served.data_ptr() != where
+    torch.cuda.synchronize()
+    assert (y == 10).all() and (served == 1).all() and (lens == 6).all()
+    assert _lib.mla_device_error(clear=True) == 0
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", [MLA_KV_BF16, MLA_KV_FP8_E4M3])
