@@ -25,9 +25,9 @@
 // run the softmax.  A row's 256 scores lie in four threads, which agree on its maximum through
 // shared memory; O is rescaled only when the maximum grows by more than 2^8.
 //
-// Measured: 512 tokens x 128 heads after 32,768 rows in 2.63-2.66 ms, 1770-1790 TFLOP/s (95% of the
+// Measured: 512 tokens x 128 heads after 32,768 rows in 2.60-2.66 ms, 1770-1810 TFLOP/s (95% of the
 // measured cuBLAS rate), 2.73 ms when held for seconds (cuBLAS then: 2.76): the power cap; 4 x ~450 tokens
-// x 16 heads after ~3000 rows in 133 us, 1500 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 198 us, 1380
+// x 16 heads after ~3000 rows in 131 us, 1525 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 197 us, 1385
 // TFLOP/s.  A long append's tile takes 4760 cycles, of which the tensor cores' own are 4352; the prompts'
 // 5220 and the streams' 5780, where slots wait for pages from L2 and HBM.  With many short blocks add the change
 // of block (~3/4 of a tile: the last softmax and the first have no MMAs beside them), launch and
@@ -49,6 +49,7 @@ namespace mla {
 constexpr int kCkThreads = 512;
 constexpr int kCkCopyWarps = 6;
 constexpr int kCkSlots = 7;
+constexpr int kCkSweepBlocks = 4;
 constexpr uint32_t kCkBlk = 8192;                            // [64 rows][64 bf16], 128-byte swizzle
 constexpr uint32_t kCkSlot = 2 * kCkBlk;
 constexpr uint32_t CK_Q = 0;                                 // 9 blocks: 64 rows x 576 dims
@@ -350,12 +351,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       return page;
     };
     // The rows of a tile in one sweep into L2: the copies take 128 or 256 bytes of each row at a time, and where
-    // nothing else has brought the rows they wait on HBM.  One block of a sequence does it, the one of its
-    // last token: 48 sequences of one token over 8192 keys 106 against 119 us; by all blocks, 512 tokens
-    // of one sequence lose 1%.
+    // nothing else has brought the rows they wait on HBM.  Done by the last block of a sequence of few blocks:
+    // 64 sequences of one token over 8192 keys, 16 heads 122 against 134 us; 24 of four blocks 205 against 211.
+    // From six blocks on, which bring the rows for each other, it gains nothing, and in a piece of a prompt, a
+    // sequence of 57, it costs (134 against 131 us).
+    auto sweeps = [&](const ChunkTileRef& r) -> bool {
+      if (r.b.base + r.b.ntok - 1 != r.b.len) return false;  // not the sequence's last
+      return r.blk < kCkSweepBlocks || cur.blocks[r.blk - kCkSweepBlocks].seq != r.b.seq;
+    };
     auto prefetch = [&](const ChunkTileRef& r, int page) {
       const bool here = (uint32_t)(lane - 2 * (int)rank) < 2u && lane < r.pages();
-      if (here && r.tile % kCkCopyWarps == warp && r.b.base + r.b.ntok - 1 == r.b.len)
+      if (here && r.tile % kCkCopyWarps == warp)
         prefetch_l2(args.kv + (int64_t)page * (64 * 1152), min(r.vis - kChunkTile * r.tile - 64 * lane, 64) * 1152);
       __syncwarp();
     };
@@ -438,11 +444,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     if (has_b) pb = page_of(b);
     pa = checked(pa);
     ok = copy_k(a, pa);
+    bool sweep = sweeps(a);
     while (ok) {
       has_c = has_b && cur.next(c);
       if (has_c) pc = page_of(c);
       pb = checked(pb);
-      if (has_b) prefetch(b, pb);
+      if (has_b && b.first) sweep = sweeps(b);
+      if (has_b && sweep) prefetch(b, pb);
       if (has_b && !b.first && !(ok = copy_k(b, pb))) break;
       if (!(ok = copy_v(a, pa)) || !has_b) break;
       if (b.first && !(ok = copy_k(b, pb))) break;
