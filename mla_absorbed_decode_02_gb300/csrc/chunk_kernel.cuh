@@ -27,7 +27,7 @@
 //
 // Measured: 512 tokens x 128 heads after 32,768 rows in 2.60-2.66 ms, 1770-1810 TFLOP/s (95% of the
 // measured cuBLAS rate), 2.73 ms when held for seconds (cuBLAS then: 2.76): the power cap; 4 x ~450 tokens
-// x 16 heads after ~3000 rows in 131 us, 1525 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 197 us, 1385
+// x 16 heads after ~3000 rows in 130 us, 1535 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 198 us, 1380
 // TFLOP/s.  A long append's tile takes 4760 cycles, of which the tensor cores' own are 4352; the prompts'
 // 5220 and the streams' 5780, where slots wait for pages from L2 and HBM.  With many short blocks add the change
 // of block (~3/4 of a tile: the last softmax and the first have no MMAs beside them), launch and
