@@ -203,7 +203,7 @@ __device__ __forceinline__ bool chunk_plan_is(int4 h0, int4 h2, int4 h3, const C
 // Walks the unit's tiles in order, across blocks.
 struct ChunkCursor {
   const ChunkBlock* blocks;
-  int causal, blk, blk0, blk1, tile0, tile1, split0, t, end;
+  int causal, blk, blk0, blk1, tile0, tile1, split0, t, end, step, next_step;
   bool open;
   ChunkBlock b;
   int vis;
@@ -211,22 +211,28 @@ struct ChunkCursor {
     b.tok0 = lo.x; b.ntok = lo.y; b.seq = lo.z; b.base = lo.w;
     b.len = hi.x; b.nt = hi.y; b.splits = hi.z; b.offset = hi.w;
   }
-  // r: the unit's record {first block, first tile, last block, end tile | split, ... | the first block}
-  __device__ void init(const ChunkBlock* blk_records, int4 r0, int split, int4 lo, int4 hi, int causal_) {
+  // r: the unit's record {first block, first tile, last block, end tile | split, steps beyond 1 | the first block}
+  __device__ void init(const ChunkBlock* blk_records, int4 r0, int4 r1, int4 lo, int4 hi, int causal_) {
     blocks = blk_records;
     causal = causal_;
     blk = blk0 = r0.x;
     tile0 = r0.y;
     blk1 = r0.z;
     tile1 = r0.w;
-    split0 = split;
+    split0 = r1.x;
+    step = 1 + r1.y;
+    next_step = 1 + r1.z;
     open = false;
     set_block(lo, hi);
   }
   __device__ bool next(ChunkTileRef& r) {
     if (!open || t >= end) {
       if (open) {
-        if (++blk > blk1) return false;
+        blk += step;
+        if (blk > blk1) return false;
+        const int s = step;
+        step = next_step;
+        next_step = s;
         const int4* src = reinterpret_cast<const int4*>(blocks + blk);
         set_block(src[0], src[1]);
       }
@@ -306,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   wc.timeout_ns = args.timeout_ns;
   const uint32_t lead0 = map_to_rank(bar(0), 0);  // the leader's barrier i is at lead0 + 8 i
   ChunkCursor cur;
-  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), r0, r1.x, r2, r3, args.key.causal);
+  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), r0, r1, r2, r3, args.key.causal);
 
   if (idle) {
   } else if (warp < kCkCopyWarps) {
@@ -1007,6 +1013,8 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
                                                                int64_t max_kv_pages, int U, int64_t cap, int32_t* sched) {
   __shared__ int64_t sh[32];
   __shared__ int bad, sh_share;
+  __shared__ int sort_key[kChunkSortSeqs], sort_blocks[kChunkSortSeqs], sort_at[kChunkSortSeqs];
+  __shared__ unsigned long long sh_most;
   const int tid = threadIdx.x, tb = chunk_tokens_per_block(H);
   const ChunkLayout l = chunk_layout(U, cap, B);
   ChunkBlock* blocks = reinterpret_cast<ChunkBlock*>(sched + l.blocks);
@@ -1037,16 +1045,30 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     page_off[B] = (int32_t)pages;
     blk_off[B] = (int32_t)nb;
   }
+  const bool sorted = nb > U && B <= kChunkSortSeqs;
+  if (sorted && tid < B) {
+    const int32_t n = cu[tid + 1] - cu[tid];
+    sort_key[tid] = chunk_sort_key(n, lens[tid]);
+    sort_blocks[tid] = chunk_seq_blocks(n, tb);
+  }
+  if (tid == 0) sh_most = 0;
+  __syncthreads();
+  if (sorted && tid < B) {
+    int at = 0;
+    for (int o = 0; o < B; ++o)
+      if (chunk_sorts_before(sort_key[o], o, sort_key[tid], tid)) at += sort_blocks[o];
+    sort_at[tid] = at;
+  }
+  __syncthreads();
+  for (int64_t k = tid; k < nb; k += 1024) {
+    const int b = chunk_find(blk_off, B, (int32_t)k), first = blk_off[b];
+    blocks[sorted ? sort_at[b] + (k - first) : k] = chunk_make_block(cu, lens, b, (int)k, first, tb, causal);
+  }
   __syncthreads();
   int64_t total = 0;
   for (int64_t k0 = 0; k0 < nb; k0 += 1024) {
     const int64_t k = k0 + tid;
-    int32_t cost = 0;
-    if (k < nb) {
-      const int b = chunk_find(blk_off, B, (int32_t)k);
-      blocks[k] = chunk_make_block(cu, lens, b, (int)k, blk_off[b], tb, causal);
-      cost = chunk_cost(blocks[k].nt);
-    }
+    const int32_t cost = k < nb ? chunk_cost(blocks[k].nt) : 0;
     const int64_t e = block_scan_1024(cost, sh, &sum);
     if (k < nb) pos[k] = (int32_t)(total + e);
     total += sum;
@@ -1073,10 +1095,16 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     shares = sh_share > 0;
     if (shares) budget = sh_share;
   }
+  if (sorted)
+    for (int u = tid; u < U; u += 1024) atomicMax(&sh_most, (unsigned long long)chunk_deal_cost(blocks, (int)nb, U, u));
+  __syncthreads();
+  const bool dealt = sorted && chunk_is_dealt((int64_t)sh_most, budget, pages);
+  if (dealt) budget = (int64_t)sh_most;
   int64_t slots = 0, ns = 0, at = 0;
   for (int64_t k0 = 0; k0 < nb; k0 += 1024) {
     const int64_t k = k0 + tid;
     const int32_t s = k >= nb ? 0
+                      : dealt ? 1
                       : shares ? chunk_shares(blocks[k].nt, (int32_t)budget)
                                : chunk_splits(pos[k], blocks[k].nt, budget);
     const int64_t oe = block_scan_1024(s > 1 ? s : 0, sh, &sum);
@@ -1098,7 +1126,9 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
   __syncthreads();
   for (int u = tid; u < U; u += 1024) {
     int32_t* rec = sched + l.units + kChunkUnitInts * u;
-    if (shares)
+    if (dealt)
+      chunk_deal_unit(blocks, (int)nb, U, u, rec);
+    else if (shares)
       chunk_share_unit(blocks, pos, (int)nb, at, u, rec);
     else
       chunk_unit(blocks, pos, (int)nb, total, budget, u, rec);
@@ -1111,7 +1141,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     sched[kChTokens] = tb;
     sched[kChNumSplit] = (int32_t)ns;
     sched[kChPages] = (int32_t)pages;
-    sched[kChShares] = shares;
+    sched[kChShares] = dealt ? 2 : shares;
     sched[kChMagic] = kChunkMagic;
   }
 }

@@ -12,6 +12,16 @@
 // needs no merging, or at most m tiles of one, m the least that the units suffice for -- and the
 // plan is the one of the three whose longest unit costs least.
 //
+// Where there are more blocks than units they can be dealt instead, whole, in rounds: unit u takes the
+// u-th block, then the (2 U - 1 - u)-th, the (2 U + u)-th, ... of the sequences in order of their length, the
+// longest first.  Nothing is split or merged, and the blocks of a sequence, side by side in a round, read the same
+// keys at the same time: in stretches they start at any of its tiles, and where the keys are more than L2 holds
+// HBM brings them once for each.  So dealing is taken up to 5/4 of the stretches' cost (tiles and pieces):
+// 24 sequences of 12 tokens x 128 heads over 8192 keys 389 against 573 us at 1.03 of the cost, 20 of 9 286
+// against 336 at 1.22, 32 of 1..24 over up to 7492 184 against 198 at 1.09; 39 of 6 380 against 366 at 1.27.  Keys
+// that L2 holds anyway leave the pieces and the merge: 11/10.  Prompt pieces on 16 heads 125 against 130 us at
+// 1.04, 12 of 10 over 2048 51 against 57 at 1.06; over 4096 101 against 97 at 1.15.
+//
 // The per-item functions are shared by the scheduler kernel (which runs the prefix sums in
 // parallel) and the host twin.
 #pragma once
@@ -50,6 +60,19 @@ MLA_HD inline int32_t chunk_share_tiles(int32_t longest, int32_t least, int64_t 
   const int64_t stretch = budget >= kChunkTileCost ? budget + kChunkPieceCost + merge : INT64_MAX;
   if (whole <= share && whole <= stretch) return longest;
   return share <= stretch ? least : 0;
+}
+
+// The order of the blocks: by sequence, the longest first (with more blocks than units and no more sequences
+// than this; each counts those before it).
+constexpr int kChunkSortSeqs = 1024;
+MLA_HD inline int32_t chunk_sort_key(int32_t n, int32_t len) { return n > 0 ? (len + kChunkTile - 1) / kChunkTile : -1; }
+MLA_HD inline bool chunk_sorts_before(int32_t key_a, int a, int32_t key_b, int b) {
+  return key_a > key_b || (key_a == key_b && a < b);
+}
+constexpr int kChunkNearPages = 896;  // 64 MB of rows: what either half of the L2 holds of its own
+MLA_HD inline bool chunk_is_dealt(int64_t most, int64_t budget, int64_t pages) {
+  const int64_t stretch = budget + kChunkPieceCost + (int64_t)kChunkTileCost * kChunkMergeCost;
+  return most <= stretch + stretch / (pages > kChunkNearPages ? 4 : 10);
 }
 
 // header words
@@ -153,7 +176,8 @@ MLA_HD inline int chunk_find(const int32_t* off, int n, int32_t v) {
   return a;
 }
 
-// Unit u's record {first block, first tile, last block, end tile, split index of the first piece, 0, 0, 0,
+// Unit u's record {first block, first tile, last block, end tile, split index of the first piece, steps between
+// its blocks beyond 1 (in turn, where they are dealt), 0,
 // the first block's record} (the kernels read what they need of the plan in one memory latency).
 MLA_HD inline void chunk_unit(const ChunkBlock* blocks, const int32_t* pos, int NB, int64_t total, int64_t budget, int u,
                               int32_t* rec) {
@@ -212,6 +236,23 @@ MLA_HD inline void chunk_share_unit(const ChunkBlock* blocks, const int32_t* pos
   *reinterpret_cast<ChunkBlock*>(rec + kUnitInts) = blocks[k];
 }
 
+// Unit u's blocks where they are dealt: u, then steps of 2 (U - 1 - u) + 1 and 2 u + 1 in turn (NB > U).
+MLA_HD inline int64_t chunk_deal_cost(const ChunkBlock* blocks, int NB, int U, int u) {
+  int64_t cost = 0;
+  int step = 2 * (U - 1 - u) + 1;
+  for (int64_t i = u; i < NB; i += step, step = 2 * U - step) cost += chunk_cost(blocks[i].nt);
+  return cost;
+}
+MLA_HD inline void chunk_deal_unit(const ChunkBlock* blocks, int NB, int U, int u, int32_t* rec) {
+  for (int i = 0; i < kChunkUnitInts; ++i) rec[i] = 0;
+  rec[0] = u;
+  rec[2] = NB - 1;
+  rec[3] = blocks[NB - 1].nt;
+  rec[5] = 2 * (U - 1 - u);
+  rec[6] = 2 * u;
+  *reinterpret_cast<ChunkBlock*>(rec + kUnitInts) = blocks[u];
+}
+
 // Host twin: writes sched as the scheduler kernel does; false (and a header without the magic
 // word) where the lengths are refused.
 inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64_t max_tokens, int H, int causal,
@@ -237,11 +278,17 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
   if (!ok) return false;
   page_off[B] = (int32_t)pages;
   blk_off[B] = (int32_t)nb;
+  const bool sorted = nb > U && B <= kChunkSortSeqs;
+  for (int b = 0; b < B; ++b) {
+    const int32_t n = cu[b + 1] - cu[b], key = chunk_sort_key(n, lens[b]);
+    int at = sorted ? 0 : blk_off[b];
+    for (int o = 0; sorted && o < B; ++o)
+      if (chunk_sorts_before(chunk_sort_key(cu[o + 1] - cu[o], lens[o]), o, key, b)) at += chunk_seq_blocks(cu[o + 1] - cu[o], tb);
+    for (int i = 0; i < chunk_seq_blocks(n, tb); ++i) blocks[at + i] = chunk_make_block(cu, lens, b, i, 0, tb, causal);
+  }
   int64_t total = 0;
   int32_t longest = 1;
   for (int k = 0; k < nb; ++k) {
-    const int b = chunk_find(blk_off, B, k);
-    blocks[k] = chunk_make_block(cu, lens, b, k, blk_off[b], tb, causal);
     if (blocks[k].nt > longest) longest = blocks[k].nt;
     pos[k] = (int32_t)total;
     total += chunk_cost(blocks[k].nt);
@@ -261,10 +308,17 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
     shares = m > 0;
     if (shares) budget = m;
   }
+  int64_t most = 0;
+  for (int u = 0; sorted && u < U; ++u) {
+    const int64_t c = chunk_deal_cost(blocks, (int)nb, U, u);
+    if (c > most) most = c;
+  }
+  const bool dealt = sorted && chunk_is_dealt(most, budget, pages);
+  if (dealt) budget = most;
   int64_t at = 0;
   int32_t slots = 0, ns = 0;
   for (int k = 0; k < nb; ++k) {
-    blocks[k].splits = shares ? chunk_shares(blocks[k].nt, (int32_t)budget) : chunk_splits(pos[k], blocks[k].nt, budget);
+    blocks[k].splits = dealt ? 1 : shares ? chunk_shares(blocks[k].nt, (int32_t)budget) : chunk_splits(pos[k], blocks[k].nt, budget);
     blocks[k].offset = slots;
     if (shares) pos[k] = (int32_t)at;
     at += blocks[k].splits;
@@ -275,7 +329,9 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
   }
   for (int u = 0; u < U; ++u) {
     int32_t* rec = sched + l.units + kChunkUnitInts * u;
-    if (shares)
+    if (dealt)
+      chunk_deal_unit(blocks, (int)nb, U, u, rec);
+    else if (shares)
       chunk_share_unit(blocks, pos, (int)nb, at, u, rec);
     else
       chunk_unit(blocks, pos, (int)nb, total, budget, u, rec);
@@ -288,7 +344,7 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
   sched[kChTokens] = tb;
   sched[kChNumSplit] = ns;
   sched[kChPages] = (int32_t)pages;
-  sched[kChShares] = shares;
+  sched[kChShares] = dealt ? 2 : shares;
   return true;
 }
 

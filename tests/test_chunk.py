@@ -58,26 +58,40 @@ def test_plan_covers_every_tile_once(H, U, seed):
     tb = max(1, 128 // H)
     assert sched[0] == 0x4D4C4143 and sched[1] == U and sched[6] == tb
     units, blocks, split = _parse(sched, U)
-    # every new token in one block, in order, blocks within a sequence
+    # every new token in one block, blocks within a sequence; the longest sequences first where they are sorted
     assert sum(b[1] for b in blocks) == cu[-1]
+    if len(blocks) > U:
+        order = [(-(-(-ln // 256)), seq, tok0) for tok0, _, seq, _, ln, *_ in blocks.tolist()]
+        assert order == sorted(order)
     at = 0
-    for tok0, ntok, seq, base, ln, nt, splits, off in blocks:
+    for tok0, ntok, seq, base, ln, nt, splits, off in sorted(blocks.tolist()):
         assert tok0 == at and 1 <= ntok <= tb and cu[seq] <= tok0 and tok0 + ntok <= cu[seq + 1]
         assert ln == L[seq] and base == L[seq] - n[seq] + (tok0 - cu[seq]) + 1
         vis = min(max(base + ntok - 1, 0), ln)
         assert nt == max(1, -(-vis // 256))
         at += ntok
     # units take disjoint stretches that cover all tiles; splits are counted in order
-    seen = {k: [] for k in range(len(blocks))}
-    for rec in units:
+    seen, owner = {k: [] for k in range(len(blocks))}, {}
+    for u, rec in enumerate(units):
         if rec[0] < 0:
             continue
         assert np.array_equal(rec[8:], blocks[rec[0]])
-        for k in range(rec[0], rec[2] + 1):
+        k, steps = int(rec[0]), [1 + int(rec[5]), 1 + int(rec[6])]
+        if sched[9] == 2:
+            assert sum(steps) == 2 * U
+        else:
+            assert steps == [1, 1]
+        visited = []
+        while k <= rec[2]:
+            visited.append(k)
+            k += steps[0]
+            steps.reverse()
+        for k in visited:
             t0 = rec[1] if k == rec[0] else 0
             t1 = rec[3] if k == rec[2] else blocks[k][5]
             assert t0 < t1
             seen[k].append((t0, t1, rec[4] if k == rec[0] else 0))
+            owner[k] = u
     slots = 0
     for k, parts in seen.items():
         assert [t for a, b, _ in parts for t in range(a, b)] == list(range(blocks[k][5]))
@@ -85,8 +99,27 @@ def test_plan_covers_every_tile_once(H, U, seed):
         if len(parts) > 1:
             assert blocks[k][7] == slots and any(np.array_equal(r, blocks[k]) for r in split)
             slots += len(parts)
+    if sched[9] == 2:
+        assert slots == 0 and sched[5] == max(sum(3 + 4 * (t1 - t0) for k in seen for t0, t1, _ in seen[k] if owner[k] == u) for u in range(U))
     assert sched[4] == slots <= 2 * max(U - 1, 0) and len(split) == sum(len(v) > 1 for v in seen.values())
     assert sched[8] == sum(-(-int(x) // 64) for x, m in zip(L, n) if m > 0)
+
+
+def test_plans_of_each_kind():
+    """Shares or whole blocks where there are no more blocks than units, blocks dealt in rounds where that costs at
+    most 5/4 of stretches (11/10 where the rows fit the L2), stretches else and with more sequences than are sorted."""
+    def kind(n, L, H, U):
+        cu = np.concatenate([[0], np.cumsum(n)])
+        p = _params(batch=len(n), max_tokens=int(cu[-1]), num_heads=H, num_units=U, max_pages_per_seq=200)
+        return _lib.mla_chunk_plan_host(p, U, cu, L)[9]
+    assert kind([4], [4000], 16, 8) == 1
+    assert kind([12] * 24, [8192] * 24, 128, 76) == 2        # 288 blocks: four rounds
+    assert kind([4] * 24, [8192] * 24, 128, 76) == 0         # 96 blocks: the second round would be a quarter full
+    assert kind([9] * 20, [8192] * 20, 128, 76) == 2         # 1.22 of the stretches, 2560 pages
+    assert kind([9] * 20, [2048] * 20, 128, 76) == 0         # 1.12, 640 pages
+    assert kind([1] * 1024, [900] * 1024, 128, 76) == 2
+    assert kind([1] * 1025, [900] * 1025, 128, 76) == 0
+    assert kind([2] * 5, [12000, 300, 300, 300, 300], 128, 8) == 0   # one sequence far longer than the rest
 
 
 @pytest.mark.parametrize("cu,lens,kw", [
