@@ -400,11 +400,11 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
  * is the most tiles of a share; [9] = 2: whole blocks dealt in rounds, [5] is the greatest cost of a
  * unit; [10] = B, [11] = causal, [12] = T, [13] = H, [14] = max_pages_per_seq, [15] = FP8:
  * max_kv_tokens / 64, bf16: INT32_MAX; then per unit 16 ints {first block, first tile, last block, end
- * tile, split index of the first piece, two steps (beyond 1) taken in turn from block to block, 0, the first
- * block's record} (first block -1: no work); then per block 8 ints {first token, tokens, sequence, keys
- * the first token sees before clipping, L, tiles of 256 keys, splits, first slot} (with more blocks
- * than units and at most 1024 sequences the longest sequence's first); then the split blocks'
- * records, and the first page of each sequence.
+ * tile, split index of the first piece, 0, 0, 0, the first block's record} (first block -1: no work); then
+ * per block 8 ints {first token, tokens, sequence, keys the first token sees before clipping, L, tiles
+ * of 256 keys, splits, first slot} (dealt: unit after unit; else with more blocks than units and at most
+ * 1024 sequences the longest sequence's first); then the split blocks' records, and the first page
+ * of each sequence.
  * MLA_ERR_INVALID_ARG where the scheduler kernel refuses.
  */
 int32_t mla_chunk_plan_host(const mla_chunk_params* p, int32_t num_units, const int32_t* cu_seqlens,

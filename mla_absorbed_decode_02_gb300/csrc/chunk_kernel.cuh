@@ -203,7 +203,7 @@ __device__ __forceinline__ bool chunk_plan_is(int4 h0, int4 h2, int4 h3, const C
 // Walks the unit's tiles in order, across blocks.
 struct ChunkCursor {
   const ChunkBlock* blocks;
-  int causal, blk, blk0, blk1, tile0, tile1, split0, t, end, step, next_step;
+  int causal, blk, blk0, blk1, tile0, tile1, split0, t, end;
   bool open;
   ChunkBlock b;
   int vis;
@@ -211,28 +211,22 @@ struct ChunkCursor {
     b.tok0 = lo.x; b.ntok = lo.y; b.seq = lo.z; b.base = lo.w;
     b.len = hi.x; b.nt = hi.y; b.splits = hi.z; b.offset = hi.w;
   }
-  // r: the unit's record {first block, first tile, last block, end tile | split, steps beyond 1 | the first block}
-  __device__ void init(const ChunkBlock* blk_records, int4 r0, int4 r1, int4 lo, int4 hi, int causal_) {
+  // r: the unit's record {first block, first tile, last block, end tile | split, ... | the first block}
+  __device__ void init(const ChunkBlock* blk_records, int4 r0, int split, int4 lo, int4 hi, int causal_) {
     blocks = blk_records;
     causal = causal_;
     blk = blk0 = r0.x;
     tile0 = r0.y;
     blk1 = r0.z;
     tile1 = r0.w;
-    split0 = r1.x;
-    step = 1 + r1.y;
-    next_step = 1 + r1.z;
+    split0 = split;
     open = false;
     set_block(lo, hi);
   }
   __device__ bool next(ChunkTileRef& r) {
     if (!open || t >= end) {
       if (open) {
-        blk += step;
-        if (blk > blk1) return false;
-        const int s = step;
-        step = next_step;
-        next_step = s;
+        if (++blk > blk1) return false;
         const int4* src = reinterpret_cast<const int4*>(blocks + blk);
         set_block(src[0], src[1]);
       }
@@ -312,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
   wc.timeout_ns = args.timeout_ns;
   const uint32_t lead0 = map_to_rank(bar(0), 0);  // the leader's barrier i is at lead0 + 8 i
   ChunkCursor cur;
-  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), r0, r1, r2, r3, args.key.causal);
+  if (!idle) cur.init(reinterpret_cast<const ChunkBlock*>(sched + lay.blocks), r0, r1.x, r2, r3, args.key.causal);
 
   if (idle) {
   } else if (warp < kCkCopyWarps) {
@@ -363,7 +357,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
     // sequence of 57, it costs (134 against 131 us).
     auto sweeps = [&](const ChunkTileRef& r) -> bool {
       if (r.b.base + r.b.ntok - 1 != r.b.len) return false;  // not the sequence's last
-      return r.blk < kCkSweepBlocks || cur.blocks[r.blk - kCkSweepBlocks].seq != r.b.seq;
+      const int32_t* off = sched + lay.blk_off + r.b.seq;
+      return off[1] - off[0] <= kCkSweepBlocks;
     };
     auto prefetch = [&](const ChunkTileRef& r, int page) {
       const bool here = (uint32_t)(lane - 2 * (int)rank) < 2u && lane < r.pages();
@@ -1014,7 +1009,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
   __shared__ int64_t sh[32];
   __shared__ int bad, sh_share;
   __shared__ int sort_key[kChunkSortSeqs], sort_blocks[kChunkSortSeqs], sort_at[kChunkSortSeqs];
-  __shared__ unsigned long long sh_most;
+  __shared__ int load[kChunkDealUnits], unit_at[kChunkDealUnits], sh_most;
   const int tid = threadIdx.x, tb = chunk_tokens_per_block(H);
   const ChunkLayout l = chunk_layout(U, cap, B);
   ChunkBlock* blocks = reinterpret_cast<ChunkBlock*>(sched + l.blocks);
@@ -1065,14 +1060,18 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     blocks[sorted ? sort_at[b] + (k - first) : k] = chunk_make_block(cu, lens, b, (int)k, first, tb, causal);
   }
   __syncthreads();
-  int64_t total = 0;
-  for (int64_t k0 = 0; k0 < nb; k0 += 1024) {
-    const int64_t k = k0 + tid;
-    const int32_t cost = k < nb ? chunk_cost(blocks[k].nt) : 0;
-    const int64_t e = block_scan_1024(cost, sh, &sum);
-    if (k < nb) pos[k] = (int32_t)(total + e);
-    total += sum;
-  }
+  auto positions = [&]() -> int64_t {  // the blocks' places on the line, and its length
+    int64_t all = 0;
+    for (int64_t k0 = 0; k0 < nb; k0 += 1024) {
+      const int64_t k = k0 + tid;
+      const int32_t cost = k < nb ? chunk_cost(blocks[k].nt) : 0;
+      const int64_t e = block_scan_1024(cost, sh, &sum);
+      if (k < nb) pos[k] = (int32_t)(all + e);
+      all += sum;
+    }
+    return all;
+  };
+  const int64_t total = positions();
   if (total > kMaxPlanPositions) return refuse();
   __syncthreads();
   bool shares = nb <= U;
@@ -1095,11 +1094,43 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
     shares = sh_share > 0;
     if (shares) budget = sh_share;
   }
-  if (sorted)
-    for (int u = tid; u < U; u += 1024) atomicMax(&sh_most, (unsigned long long)chunk_deal_cost(blocks, (int)nb, U, u));
-  __syncthreads();
-  const bool dealt = sorted && chunk_is_dealt((int64_t)sh_most, budget, pages);
-  if (dealt) budget = (int64_t)sh_most;
+  bool dealt = false;
+  if (sorted && U <= kChunkDealUnits) {
+    int32_t* owner = pos;  // (for a while)
+    int mine = 0, count = 0;
+    for (int64_t k0 = 0; k0 < nb; k0 += U) {
+      if (tid < U) load[tid] = mine;
+      __syncthreads();
+      if (tid < U) {
+        int64_t k = k0;
+        for (int v = 0; v < U; ++v) k += load[v] < mine || (load[v] == mine && v < tid);
+        if (k < nb) {
+          mine += chunk_cost(blocks[k].nt);
+          ++count;
+          owner[k] = tid;
+        }
+      }
+      __syncthreads();
+    }
+    if (tid < U) atomicMax(&sh_most, mine);
+    const int64_t first = block_scan_1024(count, sh, &sum);
+    if (tid < U) unit_at[tid] = (int)first;
+    __syncthreads();
+    dealt = chunk_is_dealt(sh_most, budget, pages);
+    if (dealt) {  // the blocks of a unit one after another
+      budget = sh_most;
+      for (int64_t k = tid; k < nb; k += 1024) {
+        const int b = chunk_find(blk_off, B, (int32_t)k), lead = blk_off[b];
+        const int64_t s = sort_at[b] + (k - lead);
+        blocks[unit_at[owner[s]] + s / U] = chunk_make_block(cu, lens, b, (int)k, lead, tb, causal);
+      }
+      __syncthreads();
+      for (int u = tid; u < U; u += 1024) load[u] = u + 1 < U ? unit_at[u + 1] : (int)nb;
+    }
+    __syncthreads();
+    positions();
+    __syncthreads();
+  }
   int64_t slots = 0, ns = 0, at = 0;
   for (int64_t k0 = 0; k0 < nb; k0 += 1024) {
     const int64_t k = k0 + tid;
@@ -1127,7 +1158,7 @@ __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu
   for (int u = tid; u < U; u += 1024) {
     int32_t* rec = sched + l.units + kChunkUnitInts * u;
     if (dealt)
-      chunk_deal_unit(blocks, (int)nb, U, u, rec);
+      chunk_deal_unit(blocks, unit_at[u], load[u], rec);
     else if (shares)
       chunk_share_unit(blocks, pos, (int)nb, at, u, rec);
     else

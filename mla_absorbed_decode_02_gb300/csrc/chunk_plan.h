@@ -12,9 +12,9 @@
 // needs no merging, or at most m tiles of one, m the least that the units suffice for -- and the
 // plan is the one of the three whose longest unit costs least.
 //
-// Where there are more blocks than units they can be dealt instead, whole, in rounds: unit u takes the
-// u-th block, then the (2 U - 1 - u)-th, the (2 U + u)-th, ... of the sequences in order of their length, the
-// longest first.  Nothing is split or merged, and the blocks of a sequence, side by side in a round, read the same
+// Where there are more blocks than units they can be dealt instead, whole, in rounds of one for each unit: the
+// sequences' blocks in order of their length, the longest first, and in a round the longest to the unit
+// that has least.  Nothing is split or merged, and the blocks of a sequence, side by side in a round, read the same
 // keys at the same time: in stretches they start at any of its tiles, and where the keys are more than L2 holds
 // HBM brings them once for each.  So dealing is taken up to 5/4 of the stretches' cost (tiles and pieces):
 // 24 sequences of 12 tokens x 128 heads over 8192 keys 389 against 573 us at 1.03 of the cost, 20 of 9 286
@@ -26,6 +26,7 @@
 // parallel) and the host twin.
 #pragma once
 #include <cstdint>
+#include <vector>
 
 #include "plan.h"
 
@@ -64,7 +65,7 @@ MLA_HD inline int32_t chunk_share_tiles(int32_t longest, int32_t least, int64_t 
 
 // The order of the blocks: by sequence, the longest first (with more blocks than units and no more sequences
 // than this; each counts those before it).
-constexpr int kChunkSortSeqs = 1024;
+constexpr int kChunkSortSeqs = 1024, kChunkDealUnits = 1024;
 MLA_HD inline int32_t chunk_sort_key(int32_t n, int32_t len) { return n > 0 ? (len + kChunkTile - 1) / kChunkTile : -1; }
 MLA_HD inline bool chunk_sorts_before(int32_t key_a, int a, int32_t key_b, int b) {
   return key_a > key_b || (key_a == key_b && a < b);
@@ -176,8 +177,7 @@ MLA_HD inline int chunk_find(const int32_t* off, int n, int32_t v) {
   return a;
 }
 
-// Unit u's record {first block, first tile, last block, end tile, split index of the first piece, steps between
-// its blocks beyond 1 (in turn, where they are dealt), 0,
+// Unit u's record {first block, first tile, last block, end tile, split index of the first piece, 0, 0, 0,
 // the first block's record} (the kernels read what they need of the plan in one memory latency).
 MLA_HD inline void chunk_unit(const ChunkBlock* blocks, const int32_t* pos, int NB, int64_t total, int64_t budget, int u,
                               int32_t* rec) {
@@ -236,21 +236,13 @@ MLA_HD inline void chunk_share_unit(const ChunkBlock* blocks, const int32_t* pos
   *reinterpret_cast<ChunkBlock*>(rec + kUnitInts) = blocks[k];
 }
 
-// Unit u's blocks where they are dealt: u, then steps of 2 (U - 1 - u) + 1 and 2 u + 1 in turn (NB > U).
-MLA_HD inline int64_t chunk_deal_cost(const ChunkBlock* blocks, int NB, int U, int u) {
-  int64_t cost = 0;
-  int step = 2 * (U - 1 - u) + 1;
-  for (int64_t i = u; i < NB; i += step, step = 2 * U - step) cost += chunk_cost(blocks[i].nt);
-  return cost;
-}
-MLA_HD inline void chunk_deal_unit(const ChunkBlock* blocks, int NB, int U, int u, int32_t* rec) {
+// The record of a unit that was dealt the blocks [first, end).
+MLA_HD inline void chunk_deal_unit(const ChunkBlock* blocks, int first, int end, int32_t* rec) {
   for (int i = 0; i < kChunkUnitInts; ++i) rec[i] = 0;
-  rec[0] = u;
-  rec[2] = NB - 1;
-  rec[3] = blocks[NB - 1].nt;
-  rec[5] = 2 * (U - 1 - u);
-  rec[6] = 2 * u;
-  *reinterpret_cast<ChunkBlock*>(rec + kUnitInts) = blocks[u];
+  rec[0] = first;
+  rec[2] = end - 1;
+  rec[3] = blocks[end - 1].nt;
+  *reinterpret_cast<ChunkBlock*>(rec + kUnitInts) = blocks[first];
 }
 
 // Host twin: writes sched as the scheduler kernel does; false (and a header without the magic
@@ -308,13 +300,33 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
     shares = m > 0;
     if (shares) budget = m;
   }
-  int64_t most = 0;
-  for (int u = 0; sorted && u < U; ++u) {
-    const int64_t c = chunk_deal_cost(blocks, (int)nb, U, u);
-    if (c > most) most = c;
+  bool dealt = false;
+  std::vector<std::vector<ChunkBlock>> hand(sorted && U <= kChunkDealUnits ? U : 0);
+  if (!hand.empty()) {
+    std::vector<int64_t> load(U, 0);
+    for (int64_t k0 = 0; k0 < nb; k0 += U) {
+      const std::vector<int64_t> had = load;
+      for (int u = 0; u < U; ++u) {
+        int64_t k = k0;
+        for (int v = 0; v < U; ++v) k += had[v] < had[u] || (had[v] == had[u] && v < u);
+        if (k >= nb) continue;
+        hand[u].push_back(blocks[k]);
+        load[u] += chunk_cost(blocks[k].nt);
+      }
+    }
+    int64_t most = 0;
+    for (int64_t c : load) most = c > most ? c : most;
+    dealt = chunk_is_dealt(most, budget, pages);
+    if (dealt) {
+      budget = most;
+      int64_t k = 0;
+      for (const auto& h : hand)
+        for (const ChunkBlock& b : h) {
+          pos[k] = k ? pos[k - 1] + chunk_cost(blocks[k - 1].nt) : 0;
+          blocks[k++] = b;
+        }
+    }
   }
-  const bool dealt = sorted && chunk_is_dealt(most, budget, pages);
-  if (dealt) budget = most;
   int64_t at = 0;
   int32_t slots = 0, ns = 0;
   for (int k = 0; k < nb; ++k) {
@@ -327,11 +339,13 @@ inline bool chunk_plan_host(const int32_t* cu, const int32_t* lens, int B, int64
       reinterpret_cast<ChunkBlock*>(sched + l.split_list)[ns++] = blocks[k];
     }
   }
+  int dealt_at = 0;
   for (int u = 0; u < U; ++u) {
     int32_t* rec = sched + l.units + kChunkUnitInts * u;
-    if (dealt)
-      chunk_deal_unit(blocks, (int)nb, U, u, rec);
-    else if (shares)
+    if (dealt) {
+      chunk_deal_unit(blocks, dealt_at, dealt_at + (int)hand[u].size(), rec);
+      dealt_at += (int)hand[u].size();
+    } else if (shares)
       chunk_share_unit(blocks, pos, (int)nb, at, u, rec);
     else
       chunk_unit(blocks, pos, (int)nb, total, budget, u, rec);

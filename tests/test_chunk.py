@@ -60,7 +60,7 @@ def test_plan_covers_every_tile_once(H, U, seed):
     units, blocks, split = _parse(sched, U)
     # every new token in one block, blocks within a sequence; the longest sequences first where they are sorted
     assert sum(b[1] for b in blocks) == cu[-1]
-    if len(blocks) > U:
+    if len(blocks) > U and sched[9] != 2:
         order = [(-(-(-ln // 256)), seq, tok0) for tok0, _, seq, _, ln, *_ in blocks.tolist()]
         assert order == sorted(order)
     at = 0
@@ -76,17 +76,7 @@ def test_plan_covers_every_tile_once(H, U, seed):
         if rec[0] < 0:
             continue
         assert np.array_equal(rec[8:], blocks[rec[0]])
-        k, steps = int(rec[0]), [1 + int(rec[5]), 1 + int(rec[6])]
-        if sched[9] == 2:
-            assert sum(steps) == 2 * U
-        else:
-            assert steps == [1, 1]
-        visited = []
-        while k <= rec[2]:
-            visited.append(k)
-            k += steps[0]
-            steps.reverse()
-        for k in visited:
+        for k in range(rec[0], rec[2] + 1):
             t0 = rec[1] if k == rec[0] else 0
             t1 = rec[3] if k == rec[2] else blocks[k][5]
             assert t0 < t1
@@ -411,7 +401,7 @@ def test_agrees_with_the_decode():
 def test_plan_on_the_device_is_the_host_plan(kv):
     import torch
     rng = np.random.default_rng(8)
-    for B, H in ((1, 128), (40, 16), (1500, 7), (3000, 128)):
+    for B, H in ((1, 128), (40, 16), (1500, 7), (3000, 128), (30, 128), (40, 128), (300, 64), (1024, 128)):
         n = rng.integers(0, 6, B)
         L = n + rng.integers(0, 3000, B)
         cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
