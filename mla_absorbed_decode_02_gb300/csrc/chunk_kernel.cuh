@@ -25,13 +25,13 @@
 // run the softmax.  A row's 256 scores lie in four threads, which agree on its maximum through
 // shared memory; O is rescaled only when the maximum grows by more than 2^8.
 //
-// Measured: 512 tokens x 128 heads after 32,768 rows in 2.60-2.66 ms, 1770-1810 TFLOP/s (95% of the
-// measured cuBLAS rate), 2.73 ms when held for seconds (cuBLAS then: 2.76): the power cap; 4 x ~450 tokens
-// x 16 heads after ~3000 rows in 130 us, 1535 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 198 us, 1380
-// TFLOP/s.  A long append's tile takes 4760 cycles, of which the tensor cores' own are 4352; the prompts'
-// 5220 and the streams' 5780, where slots wait for pages from L2 and HBM.  With many short blocks add the change
-// of block (~3/4 of a tile: the last softmax and the first have no MMAs beside them), launch and
-// merge (~15 us).
+// Measured: 512 tokens x 128 heads after 32,768 rows in 2.52-2.56 ms, 1840-1870 TFLOP/s (the measured cuBLAS
+// rate), 2.62 ms when held for seconds (cuBLAS then: 2.76): the power cap; 4 x ~450 tokens x 16 heads after
+// ~3000 rows in 124 us, 1610 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 172 us, 1590 TFLOP/s.  A long
+// append's tile takes 4840 cycles, of which the tensor cores' own are 4352; the prompts' 5110 and the
+// streams' 5670, where slots wait for pages from L2 and HBM.  With many short blocks add the change of block
+// (~3/4 of a tile: the last softmax and the first have no MMAs beside them), what the units' shares
+// differ by, and the launches.
 //
 // Rows of a block see different numbers of keys where it holds several tokens.  P is zero past a
 // row's limit, but 0 x NaN is NaN, so in the pages that some row does not see in full the copying
@@ -798,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
 // or a quarter of them by pieces:
 //   Fewer than eight pieces a block on average: a warp takes 16 of the dims (32 bytes of a bf16 row) over all
 //   pieces, two in flight; nothing is exchanged.  24 blocks of three pieces 66 us with the attention, 75 the
-//   other way; 75 blocks of two 202 against 225.
+//   other way; 75 blocks of two 202 against 225 (dealt out whole since then, they need none).
 //   Eight or more (then there are few blocks, and a warp of a row's own would run alone through them): an item
 //   is 16 of the dims, each warp takes every eighth piece, and they meet in shared memory.  One block of 74
 //   pieces 52 us with the attention, 84 the other way; 2 of 32 16 against 29; 8 of 8 28.6 against 29.0.
@@ -1002,7 +1002,8 @@ __device__ __forceinline__ int64_t block_scan_1024(int64_t v, int64_t* sh, int64
 }
 
 // One CTA of 1024 threads; the phases of chunk_plan_host with the sums in parallel.
-// 7-8 us from 8 to 225 blocks: dependent trips to L2 and barriers, once a step for all layers.
+// 10 us with 8 blocks, 15-23 with 225 to 580 to deal (cold): dependent trips to L2 and barriers, once a step
+// for all layers.
 __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu, const int32_t* lens, int B,
                                                                int64_t max_tokens, int H, int causal, int max_pages,
                                                                int64_t max_kv_pages, int U, int64_t cap, int32_t* sched) {

@@ -18,8 +18,8 @@
 // keys at the same time: in stretches they start at any of its tiles, and where the keys are more than L2 holds
 // HBM brings them once for each.  So dealing is taken up to 5/4 of the stretches' cost (tiles and pieces):
 // 24 sequences of 12 tokens x 128 heads over 8192 keys 389 against 573 us at 1.03 of the cost, 20 of 9 286
-// against 336 at 1.22, 32 of 1..24 over up to 7492 184 against 198 at 1.09; 39 of 6 380 against 366 at 1.27.  Keys
-// that L2 holds anyway leave the pieces and the merge: 11/10.  Prompt pieces on 16 heads 125 against 130 us at
+// against 336 at 1.22, 32 of 1..24 over up to 7492 172 against 198 at 1.03; 39 of 6 380 against 366 at 1.27.  Keys
+// that L2 holds anyway leave the pieces and the merge: 11/10.  Prompt pieces on 16 heads 124 against 130 us at
 // 1.04, 12 of 10 over 2048 51 against 57 at 1.06; over 4096 101 against 97 at 1.15.
 //
 // The per-item functions are shared by the scheduler kernel (which runs the prefix sums in
