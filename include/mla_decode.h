@@ -405,7 +405,7 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
  * of 256 keys, splits, first slot} (dealt: unit after unit; else with more blocks than units and at most
  * 1024 sequences the longest sequence's first); then the split blocks' records, and the first page
  * of each sequence.
- * MLA_ERR_INVALID_ARG where the scheduler kernel refuses.
+ * MLA_ERR_INVALID_ARG where the scheduler kernel refuses, MLA_ERR_WORKSPACE where host memory runs out.
  */
 int32_t mla_chunk_plan_host(const mla_chunk_params* p, int32_t num_units, const int32_t* cu_seqlens,
                             const int32_t* cache_seqlens, void* sched);

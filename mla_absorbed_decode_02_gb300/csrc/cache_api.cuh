@@ -2,6 +2,7 @@
 // launches).  Part of mla_decode.cu: it uses that file's device table and map encoder.
 #pragma once
 #include <initializer_list>
+#include <new>
 
 namespace {
 
@@ -128,10 +129,14 @@ int32_t mla_chunk_plan_host(const mla_chunk_params* p, int32_t num_units, const 
   int32_t st = check_chunk(p);
   if (st != MLA_OK) return st;
   if (num_units < 1 || num_units > 65535 || !cu_seqlens || !cache_seqlens || !sched) return MLA_ERR_INVALID_ARG;
-  return chunk_plan_host(cu_seqlens, cache_seqlens, p->batch, p->max_tokens, p->num_heads, p->causal != 0,
-                         p->max_pages_per_seq, chunk_kv_pages(p), num_units, static_cast<int32_t*>(sched))
-             ? MLA_OK
-             : MLA_ERR_INVALID_ARG;
+  try {
+    return chunk_plan_host(cu_seqlens, cache_seqlens, p->batch, p->max_tokens, p->num_heads, p->causal != 0,
+                           p->max_pages_per_seq, chunk_kv_pages(p), num_units, static_cast<int32_t*>(sched))
+               ? MLA_OK
+               : MLA_ERR_INVALID_ARG;
+  } catch (const std::bad_alloc&) {  // no room to deal the blocks in
+    return MLA_ERR_WORKSPACE;
+  }
 }
 
 int32_t mla_chunk_schedule(const mla_chunk_params* p, const int32_t* cu_seqlens, const int32_t* cache_seqlens, void* sched,

@@ -314,6 +314,23 @@ def test_matches_float64(kv, H, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,L,H,units,kind", [
+    ([2, 2, 3], [300, 520, 700], 128, 2, 2),           # dealt: seven blocks in four rounds
+    ([40, 3, 0, 17], [1000, 3, 0, 260], 16, 3, 2),
+    ([1] * 11, list(range(0, 1100, 100)), 64, 4, 2),   # one without a key among them
+    ([3], [2600], 128, 2, 0),                          # stretches: two rounds would leave a unit idle in the second
+    ([1, 1, 1], [5000, 64, 70], 128, 2, 0),
+    ([2], [700], 128, 5, 1),                           # shares
+])
+def test_each_kind_of_plan(kv, n, L, H, units, kind):
+    q = Problem(n, L, H, kv, seed=40 + units, num_units=units, pad=1)
+    attn = _lib.ChunkAttention(q.p)
+    q.check(attn)
+    assert int(attn.sched[9]) == kind
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("units", [1, 2, 7, 76])
 @pytest.mark.parametrize("H,kv", [(16, "bf16"), (128, "fp8")])
 def test_units_share_and_split_the_work(units, H, kv):
