@@ -49,7 +49,7 @@ namespace mla {
 constexpr int kCkThreads = 512;
 constexpr int kCkCopyWarps = 6;
 constexpr int kCkSlots = 7;
-constexpr int kCkSweepBlocks = 4;
+constexpr int kCkPageBytes = 64 * 1152;
 constexpr uint32_t kCkBlk = 8192;                            // [64 rows][64 bf16], 128-byte swizzle
 constexpr uint32_t kCkSlot = 2 * kCkBlk;
 constexpr uint32_t CK_Q = 0;                                 // 9 blocks: 64 rows x 576 dims
@@ -350,28 +350,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       }
       return page;
     };
-    // The rows of a tile in one sweep into L2: the copies take 128 or 256 bytes of each row at a time, and where
-    // nothing else has brought the rows they wait on HBM.  Done by the last block of a sequence of few blocks:
-    // 64 sequences of one token over 8192 keys, 16 heads 122 against 134 us; 24 of four blocks 205 against 211.
-    // From six blocks on, which bring the rows for each other, it gains nothing, and in a piece of a prompt, a
-    // sequence of 57, it costs (134 against 131 us).
-    auto sweeps = [&](const ChunkTileRef& r) -> bool {
-      if (r.b.base + r.b.ntok - 1 != r.b.len) return false;  // not the sequence's last
+    // The copies take 128 or 256 bytes of a row at a time, and where nothing else has brought the rows they wait
+    // on HBM: the last block of a sequence brings them into L2 in order.
+    //   The sequence's only block: a tile's rows in one sweep, right before their copies (64 sequences of one
+    //   token over 8192 keys, 16 heads 122 against 134 us; a tile earlier it is 147).
+    //   With other blocks beside it: a tile ahead, in pieces of 8 KB spread over the slots of the tile before (20
+    //   sequences of 16 tokens x 128 heads over 8192 keys 418 against 454 us, 64 of 2 over 4096 97 against 107; in
+    //   one sweep it costs, prompt pieces 134 against 131 us).
+    enum { kNoPrefetch, kSweep, kAhead };
+    auto bring = [&](const ChunkTileRef& r) -> int {
+      if (r.b.base + r.b.ntok - 1 != r.b.len) return kNoPrefetch;  // not the sequence's last
       const int32_t* off = sched + lay.blk_off + r.b.seq;
-      return off[1] - off[0] <= kCkSweepBlocks;
+      return off[1] - off[0] == 1 ? kSweep : kAhead;
     };
-    auto prefetch = [&](const ChunkTileRef& r, int page) {
+    auto sweep = [&](const ChunkTileRef& r, int page) {
       const bool here = (uint32_t)(lane - 2 * (int)rank) < 2u && lane < r.pages();
       if (here && r.tile % kCkCopyWarps == warp)
-        prefetch_l2(args.kv + (int64_t)page * (64 * 1152), min(r.vis - kChunkTile * r.tile - 64 * lane, 64) * 1152);
+        prefetch_l2(args.kv + (int64_t)page * kCkPageBytes, min(r.vis - kChunkTile * r.tile - 64 * lane, 64) * 1152);
       __syncwarp();
     };
-    auto copy_k = [&](const ChunkTileRef& r, int page) -> bool {
+    // (ahead: tile n's rows are prefetched meanwhile)
+    auto copy_k = [&](const ChunkTileRef& r, int page, const ChunkTileRef& n, int n_page, bool ahead) -> bool {
       const int np = min(max(r.pages() - 2 * (int)rank, 0), 2);
       const int y0 = 64 * __shfl_sync(0xffffffffu, page, 2 * rank), y1 = 64 * __shfl_sync(0xffffffffu, page, 2 * rank + 1);
+      const int n0 = __shfl_sync(0xffffffffu, n_page, 2 * rank), n1 = __shfl_sync(0xffffffffu, n_page, 2 * rank + 1);
+      const int n_np = ahead ? min(max(n.pages() - 2 * (int)rank, 0), 2) : 0;
 #pragma unroll 1
       for (int d = mine(); d < 9; d += kCkCopyWarps) {
         locate(d);
+        if (el && n_np > 0) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // two of the 18 pieces of 8 KB of the CTA's two pages
+            const int piece = 2 * d + h, second = piece >= 9;
+            if (second < n_np)
+              prefetch_l2(args.kv + (int64_t)(second ? n1 : n0) * kCkPageBytes + (piece - 9 * second) * 8192, 8192);
+          }
+        }
+        __syncwarp();
         if (!wait_warp<true>(bar(CB_EMPTY + slot), phase, wc, kSiteCkRing)) return false;
         const uint32_t full = lead0 + 8 * (CB_FULL + slot), dst = base + CK_RING + slot * kCkSlot;
         if (el) {
@@ -436,30 +451,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       return true;
     };
     // the order of the MMA warp: K of the next tile, then V of the current one (the other way at a block's
-    // end); a tile's page numbers are read one tile ahead of their use
-    ChunkTileRef a, b, c;
-    bool has_b, has_c;
+    // end); a tile's page numbers are read two tiles ahead of their use
+    ChunkTileRef a, b, c, d;
+    bool has_b, has_c, has_d;
     cur.next(a);
-    int pa = page_of(a), pb = 0, pc = 0;
+    int pa = page_of(a), pb = 0, pc = 0, pd = 0;
     has_b = cur.next(b);
     if (has_b) pb = page_of(b);
+    has_c = has_b && cur.next(c);
+    if (has_c) pc = page_of(c);
     pa = checked(pa);
-    ok = copy_k(a, pa);
-    bool sweep = sweeps(a);
+    ok = copy_k(a, pa, a, 0, false);
+    int bring_b = bring(has_b ? b : a), bring_c = has_c && c.first ? bring(c) : bring_b;
+    if (has_b) pb = checked(pb);
     while (ok) {
-      has_c = has_b && cur.next(c);
-      if (has_c) pc = page_of(c);
-      pb = checked(pb);
-      if (has_b && b.first) sweep = sweeps(b);
-      if (has_b && sweep) prefetch(b, pb);
-      if (has_b && !b.first && !(ok = copy_k(b, pb))) break;
+      has_d = has_c && cur.next(d);
+      if (has_d) pd = page_of(d);
+      if (has_c) pc = checked(pc);
+      if (has_b && bring_b == kSweep) sweep(b, pb);
+      const bool ahead = has_c && bring_c == kAhead;
+      if (has_b && !b.first && !(ok = copy_k(b, pb, c, pc, ahead))) break;
       if (!(ok = copy_v(a, pa)) || !has_b) break;
-      if (b.first && !(ok = copy_k(b, pb))) break;
+      if (b.first && !(ok = copy_k(b, pb, c, pc, ahead))) break;
       a = b;
       pa = pb;
       b = c;
       pb = pc;
+      bring_b = bring_c;
+      c = d;
+      pc = pd;
+      if (has_d && d.first) bring_c = bring(d);
       has_b = has_c;
+      has_c = has_d;
     }
   } else if (warp == 6) {
     // ================================================================ MMAs
