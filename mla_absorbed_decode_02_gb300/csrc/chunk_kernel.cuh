@@ -25,9 +25,9 @@
 // run the softmax.  A row's 256 scores lie in four threads, which agree on its maximum through
 // shared memory; O is rescaled only when the maximum grows by more than 2^8.
 //
-// Measured: 512 tokens x 128 heads after 32,768 rows in 2.52-2.56 ms, 1840-1870 TFLOP/s (the measured cuBLAS
-// rate), 2.62 ms when held for seconds (cuBLAS then: 2.76): the power cap; 4 x ~450 tokens x 16 heads after
-// ~3000 rows in 124 us, 1610 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 172 us, 1590 TFLOP/s.  A long
+// Measured: 512 tokens x 128 heads after 32,768 rows in 2.50-2.56 ms, 1840-1880 TFLOP/s (the measured cuBLAS
+// rate), 2.61 ms when held for seconds (cuBLAS then: 2.76): the power cap; 4 x ~450 tokens x 16 heads after
+// ~3000 rows in 122 us, 1630 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 167 us, 1630 TFLOP/s.  A long
 // append's tile takes 4840 cycles, of which the tensor cores' own are 4352; the prompts' 5110 and the
 // streams' 5670, where slots wait for pages from L2 and HBM.  With many short blocks add the change of block
 // (~3/4 of a tile: the last softmax and the first have no MMAs beside them), what the units' shares
