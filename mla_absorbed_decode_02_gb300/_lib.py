@@ -578,16 +578,16 @@ class Decoder:
         return out, lse
 
 
-def _new(like, shape, dtype, stream):
-    """A result that `stream` writes: its memory comes from that stream's pool, not from what the current stream has
-    let go of but may still be using."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+def _new(like, stream, shape=None, dtype=None):
+    """A result that `stream` writes, of this tensor's shape and type or those given: its memory comes from that
+    stream's pool, not from what the current stream has let go of but may still be using."""
     import torch
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
+        with torch.cuda.stream(stream):
+            return _new(like, None, shape, dtype)
+    return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype)  # (1.3 against 2.6 us)
 
 
 class ChunkAttention:
@@ -611,9 +611,9 @@ class ChunkAttention:
         if self.seqlens is None:
             _refuse("ChunkAttention.attend before plan", MLA_ERR_WORKSPACE)
         if out is None:
-            out = _new(q_nope_absorbed, q_nope_absorbed.shape, _dtypes()[2], stream)
+            out = _new(q_nope_absorbed, stream)
         if lse is None:
-            lse = _new(q_nope_absorbed, q_nope_absorbed.shape[:2], _dtypes()[1], stream)
+            lse = _new(q_nope_absorbed, stream, q_nope_absorbed.shape[:2], _dtypes()[1])
         _attend(self.p, q_nope_absorbed, q_rope, kv_pages, block_table, self.seqlens, scale, out, lse, self.sched,
                 self.workspace, stream)
         return out, lse
@@ -644,14 +644,14 @@ class PagePool:
         """Returns new_pages int32 [n]: the child's own page, -1 (none needed), -2 (refused), -3 (no page left)."""
         if parents.numel() > self.max_forks:
             _refuse("PagePool.fork: more forks than max_forks", MLA_ERR_WORKSPACE)
-        new_pages = _new(parents, parents.shape, parents.dtype, stream)
+        new_pages = _new(parents, stream)
         _fork(self.p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, self.workspace,
               stream)
         return new_pages
 
     def reserve(self, num_new, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns served int32 [batch]: 1 (done), 0 (not enough pages), -2 (refused)."""
-        served = _new(num_new, num_new.shape, num_new.dtype, stream)
+        served = _new(num_new, stream)
         _reserve(self.p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
         return served
 
@@ -660,6 +660,6 @@ class PagePool:
 
     def compact(self, kv_pages, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns the number of used pages, int32 [1] on the device."""
-        used = _new(cache_seqlens, (1,), cache_seqlens.dtype, stream)
+        used = _new(cache_seqlens, stream, (1,))
         _compact(self.p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
         return used
