@@ -17,10 +17,10 @@
 // that has least.  Nothing is split or merged, and the blocks of a sequence, side by side in a round, read the same
 // keys at the same time: in stretches they start at any of its tiles, and where the keys are more than L2 holds
 // HBM brings them once for each.  So dealing is taken up to 5/4 of the stretches' cost (tiles and pieces):
-// 24 sequences of 12 tokens x 128 heads over 8192 keys 389 against 573 us at 1.03 of the cost, 20 of 9 286
-// against 336 at 1.22, 32 of 1..24 over up to 7492 172 against 198 at 1.03; 39 of 6 380 against 366 at 1.27.  Keys
-// that L2 holds anyway leave the pieces and the merge: 11/10.  Prompt pieces on 16 heads 124 against 130 us at
-// 1.04, 12 of 10 over 2048 51 against 57 at 1.06; over 4096 101 against 97 at 1.15.
+// 50 sequences of 5 tokens x 128 heads over 8192 keys 370 against 441 us at 1.19 of the cost, 57 of 1..10
+// over 400 to 8100 112 against 132 at 1.08, 39 of 6 over 8192 364 against 366 at 1.26, 16 of 10 266 against
+// 251 at 1.37.  Keys that L2 holds anyway leave the pieces and the merge: 11/10.  Prompt pieces on 16 heads
+// 124 against 130 us at 1.04, 12 of 10 over 2048 51 against 57 at 1.06; over 4096 101 against 97 at 1.15.
 //
 // The per-item functions are shared by the scheduler kernel (which runs the prefix sums in
 // parallel) and the host twin.
