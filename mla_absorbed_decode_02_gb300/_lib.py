@@ -590,21 +590,37 @@ def _new(like, stream, shape=None, dtype=None):
     return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype)  # (1.3 against 2.6 us)
 
 
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
 class ChunkAttention:
-    """Convenience wrapper of the chunk attention: owns the plan and the workspace of one problem shape."""
+    """Convenience wrapper of the chunk attention: owns the plan and the workspace of one problem shape, and a copy of
+    its params (`p` reads as a copy too; other params may be set where the buffers hold them)."""
 
     def __init__(self, p: MlaChunkParams, device=None):
         import torch
-        self.p = p
+        self._p = type(p).from_buffer_copy(p)
         self.device = torch.device("cuda" if device is None else device)
-        sb, wb = mla_chunk_workspace_size(p)
+        sb, wb = mla_chunk_workspace_size(self._p)
         self.sched = torch.empty(sb // 4, dtype=torch.int32, device=self.device)  # (nothing to wait for on any stream)
         self.workspace = torch.empty(wb, dtype=torch.uint8, device=self.device)
         self.seqlens = None
 
+    @property
+    def p(self) -> MlaChunkParams:
+        return type(self._p).from_buffer_copy(self._p)
+
+    @p.setter
+    def p(self, p: MlaChunkParams):
+        sb, wb = mla_chunk_workspace_size(p)
+        if sb > _nbytes(self.sched) or wb > _nbytes(self.workspace):
+            _refuse("ChunkAttention.p: larger than what the wrapper was made for", MLA_ERR_WORKSPACE)
+        self._p = type(p).from_buffer_copy(p)
+
     def plan(self, cu_seqlens, cache_seqlens, stream=None):
         """The plan of a step's lengths; the tensors are read again by attend()."""
-        mla_chunk_schedule(self.p, cu_seqlens, cache_seqlens, self.sched, stream)
+        mla_chunk_schedule(self._p, cu_seqlens, cache_seqlens, self.sched, stream)
         self.seqlens = cache_seqlens
 
     def attend(self, q_nope_absorbed, q_rope, kv_pages, block_table, scale, out=None, lse=None, stream=None):
@@ -614,52 +630,67 @@ class ChunkAttention:
             out = _new(q_nope_absorbed, stream)
         if lse is None:
             lse = _new(q_nope_absorbed, stream, q_nope_absorbed.shape[:2], _dtypes()[1])
-        _attend(self.p, q_nope_absorbed, q_rope, kv_pages, block_table, self.seqlens, scale, out, lse, self.sched,
+        _attend(self._p, q_nope_absorbed, q_rope, kv_pages, block_table, self.seqlens, scale, out, lse, self.sched,
                 self.workspace, stream)
         return out, lse
 
 
 class PagePool:
     """Convenience wrapper of the page upkeep: owns the workspace of one pool shape, for calls that fork at most
-    max_forks sequences.  The tables belong to the caller."""
+    max_forks sequences, and a copy of its params (`p` reads as a copy too; other params may be set where the
+    workspace holds them).  The tables belong to the caller."""
 
     def __init__(self, p: MlaPoolParams, max_forks: int = 1024, device=None):
         import torch
-        self.p = p
+        self._p = type(p).from_buffer_copy(p)
         self.device = torch.device("cuda" if device is None else device)
-        self.max_forks = int(max_forks)
-        self.workspace = torch.empty(mla_pool_workspace_size(p, self.max_forks), dtype=torch.uint8, device=self.device)
+        self._max_forks = int(max_forks)
+        self.workspace = torch.empty(mla_pool_workspace_size(self._p, self._max_forks), dtype=torch.uint8, device=self.device)
+
+    @property
+    def p(self) -> MlaPoolParams:
+        return type(self._p).from_buffer_copy(self._p)
+
+    @p.setter
+    def p(self, p: MlaPoolParams):
+        if mla_pool_workspace_size(p, self._max_forks) > _nbytes(self.workspace):
+            _refuse("PagePool.p: larger than what the wrapper was made for", MLA_ERR_WORKSPACE)
+        self._p = type(p).from_buffer_copy(p)
+
+    @property
+    def max_forks(self) -> int:
+        return self._max_forks
 
     def new_tables(self):
         """An empty pool's (block_table, cache_seqlens, ref_counts)."""
         import torch
-        p, kw = self.p, dict(dtype=torch.int32, device=self.device)
+        p, kw = self._p, dict(dtype=torch.int32, device=self.device)
         return (torch.full((p.batch, p.max_pages_per_seq), -1, **kw), torch.zeros(p.batch, **kw),
                 torch.zeros(p.num_pages, **kw))
 
     def copy(self, kv_pages, src_pages, dst_pages, stream=None):
-        mla_copy_pages(self.p, kv_pages, src_pages, dst_pages, stream)
+        mla_copy_pages(self._p, kv_pages, src_pages, dst_pages, stream)
 
     def fork(self, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns new_pages int32 [n]: the child's own page, -1 (none needed), -2 (refused), -3 (no page left)."""
-        if parents.numel() > self.max_forks:
+        if parents.numel() > self._max_forks:
             _refuse("PagePool.fork: more forks than max_forks", MLA_ERR_WORKSPACE)
         new_pages = _new(parents, stream)
-        _fork(self.p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, self.workspace,
+        _fork(self._p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, self.workspace,
               stream)
         return new_pages
 
     def reserve(self, num_new, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns served int32 [batch]: 1 (done), 0 (not enough pages), -2 (refused)."""
         served = _new(num_new, stream)
-        _reserve(self.p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
+        _reserve(self._p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
         return served
 
     def free(self, sequences, block_table, cache_seqlens, ref_counts, stream=None):
-        mla_free_sequences(self.p, sequences, block_table, cache_seqlens, ref_counts, stream)
+        mla_free_sequences(self._p, sequences, block_table, cache_seqlens, ref_counts, stream)
 
     def compact(self, kv_pages, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns the number of used pages, int32 [1] on the device."""
         used = _new(cache_seqlens, stream, (1,))
-        _compact(self.p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
+        _compact(self._p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
         return used
