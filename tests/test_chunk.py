@@ -511,3 +511,30 @@ def test_captured_and_on_two_streams(kv):
     assert _lib.mla_device_error(clear=True) == 0
     for (g, st, out, lse, _), (o, l) in zip(state, want):
         assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,units", [(16, 1), (128, 0), (128, 9)])
+@pytest.mark.parametrize("kv,dim", [("bf16", 7), ("bf16", 300), ("bf16", 515), ("fp8", 515)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, 3e38])
+@pytest.mark.parametrize("row", [5, 300, 640, 717])
+def test_one_score_that_is_not_finite(H, units, kv, dim, value, row):
+    """One value of one key: infinite, or finite where its product with the query leaves float32.  Whatever the sign of
+    the score, whichever tile the key lies in (three are seen in full by every token, in the last some tokens see
+    less), and whether the block is split: the tokens that see the key get NaN, the others keep their bits."""
+    import torch
+    n, L = 6, 720
+    q = Problem([n], [L], H, kv, seed=23, num_units=units)
+    sign = torch.where(torch.arange(H, device="cuda") % 2 == 0, 100.0, -100.0).to(torch.bfloat16)   # scores of either sign
+    (q.d_q if dim < 512 else q.d_qr)[:, :, dim % 512] = sign
+    want, want_lse = q.run()
+    assert want.isfinite().all() and want_lse.isfinite().all()
+    where = int(q.bt[0, row // 64]) * 64 + row % 64
+    if kv == "bf16":
+        q.pool.view(-1, 576)[where, dim] = value
+    else:
+        q.pool.view(-1, 656)[where, 528:].view(torch.bfloat16)[dim - 512] = value
+    got, got_lse = q.run()
+    first = max(0, row - (L - n))                 # the first token that sees the key
+    assert torch.equal(got[:first], want[:first]) and torch.equal(got_lse[:first], want_lse[:first])
+    assert got_lse[first:].isnan().all() and got[first:].isnan().all()
