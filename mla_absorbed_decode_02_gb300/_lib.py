@@ -594,7 +594,67 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-class ChunkAttention:
+_idle_streams = {}
+
+
+def _idle_stream(index: int):
+    """A stream of the library's own (torch's are shared out in turn) on which nothing is ever launched."""
+    import torch
+    with _lock:
+        if index not in _idle_streams:
+            handle = ctypes.c_void_p()
+            torch.cuda.check_error(int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(handle))))
+            _idle_streams[index] = torch.cuda.ExternalStream(handle.value, device=index)
+        return _idle_streams[index]
+
+
+class _Owner:
+    """Buffers that a wrapper's calls use on any stream, in any order.
+
+    torch gives memory that was freed on a stream back to allocations on that stream at once, while its kernels may
+    still use it; an allocation for use on another stream must not get such memory.  So the buffers are allocated
+    for a stream that runs nothing: all that comes from there was a wrapper's before, and a wrapper's buffers
+    are free again only when the streams that it was called on (record_stream) have come to where it was
+    dropped.  Streams that torch does not own may be gone by then, and are not waited for: a wrapper used on one is
+    kept until its work there is done."""
+
+    def _own(self, *sizes_and_types):
+        import torch
+        new = lambda: [torch.empty(n, dtype=t, device=self.device) for n, t in sizes_and_types]  # noqa: E731
+        self._streams = set()
+        if self.device.type != "cuda" or torch.cuda.is_current_stream_capturing():  # (the graph's own memory)
+            self._buffers = new()
+        else:
+            index = self.device.index
+            with torch.cuda.stream(_idle_stream(torch.cuda.current_device() if index is None else index)):
+                self._buffers = new()
+        return self._buffers
+
+    def _on(self, stream):
+        """The handle of the stream of a call, which the buffers are kept for."""
+        if self.device.type != "cuda":
+            return stream
+        handle = _stream(stream)
+        if handle not in self._streams:
+            self._keep_for(stream, handle)
+        return handle
+
+    def _keep_for(self, stream, handle):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif handle == 0:
+            stream = torch.cuda.default_stream()
+        if isinstance(stream, torch.cuda.Stream) and (handle == 0 or stream.stream_id != handle):  # (not an external one)
+            with torch.cuda.stream(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    return  # (a graph's user keeps the wrapper)
+            for t in self._buffers:
+                t.record_stream(stream)
+        self._streams.add(handle)
+
+
+class ChunkAttention(_Owner):
     """Convenience wrapper of the chunk attention: owns the plan and the workspace of one problem shape, and a copy of
     its params (`p` reads as a copy too; other params may be set where the buffers hold them)."""
 
@@ -603,8 +663,7 @@ class ChunkAttention:
         self._p = type(p).from_buffer_copy(p)
         self.device = torch.device("cuda" if device is None else device)
         sb, wb = mla_chunk_workspace_size(self._p)
-        self.sched = torch.empty(sb // 4, dtype=torch.int32, device=self.device)  # (nothing to wait for on any stream)
-        self.workspace = torch.empty(wb, dtype=torch.uint8, device=self.device)
+        self.sched, self.workspace = self._own((sb // 4, torch.int32), (wb, torch.uint8))
         self.seqlens = None
 
     @property
@@ -620,7 +679,7 @@ class ChunkAttention:
 
     def plan(self, cu_seqlens, cache_seqlens, stream=None):
         """The plan of a step's lengths; the tensors are read again by attend()."""
-        mla_chunk_schedule(self._p, cu_seqlens, cache_seqlens, self.sched, stream)
+        mla_chunk_schedule(self._p, cu_seqlens, cache_seqlens, self.sched, self._on(stream))
         self.seqlens = cache_seqlens
 
     def attend(self, q_nope_absorbed, q_rope, kv_pages, block_table, scale, out=None, lse=None, stream=None):
@@ -631,11 +690,11 @@ class ChunkAttention:
         if lse is None:
             lse = _new(q_nope_absorbed, stream, q_nope_absorbed.shape[:2], _dtypes()[1])
         _attend(self._p, q_nope_absorbed, q_rope, kv_pages, block_table, self.seqlens, scale, out, lse, self.sched,
-                self.workspace, stream)
+                self.workspace, self._on(stream))
         return out, lse
 
 
-class PagePool:
+class PagePool(_Owner):
     """Convenience wrapper of the page upkeep: owns the workspace of one pool shape, for calls that fork at most
     max_forks sequences, and a copy of its params (`p` reads as a copy too; other params may be set where the
     workspace holds them).  The tables belong to the caller."""
@@ -645,7 +704,7 @@ class PagePool:
         self._p = type(p).from_buffer_copy(p)
         self.device = torch.device("cuda" if device is None else device)
         self._max_forks = int(max_forks)
-        self.workspace = torch.empty(mla_pool_workspace_size(self._p, self._max_forks), dtype=torch.uint8, device=self.device)
+        self.workspace, = self._own((mla_pool_workspace_size(self._p, self._max_forks), torch.uint8))
 
     @property
     def p(self) -> MlaPoolParams:
@@ -677,13 +736,13 @@ class PagePool:
             _refuse("PagePool.fork: more forks than max_forks", MLA_ERR_WORKSPACE)
         new_pages = _new(parents, stream)
         _fork(self._p, kv_pages, parents, children, block_table, cache_seqlens, ref_counts, new_pages, self.workspace,
-              stream)
+              self._on(stream))
         return new_pages
 
     def reserve(self, num_new, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns served int32 [batch]: 1 (done), 0 (not enough pages), -2 (refused)."""
         served = _new(num_new, stream)
-        _reserve(self._p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, stream)
+        _reserve(self._p, num_new, block_table, cache_seqlens, ref_counts, served, self.workspace, self._on(stream))
         return served
 
     def free(self, sequences, block_table, cache_seqlens, ref_counts, stream=None):
@@ -692,5 +751,5 @@ class PagePool:
     def compact(self, kv_pages, block_table, cache_seqlens, ref_counts, stream=None):
         """Returns the number of used pages, int32 [1] on the device."""
         used = _new(cache_seqlens, stream, (1,))
-        _compact(self._p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, stream)
+        _compact(self._p, kv_pages, block_table, cache_seqlens, ref_counts, used, self.workspace, self._on(stream))
         return used
