@@ -448,6 +448,16 @@ int32_t mla_append_kv(const mla_pool_params* p, int64_t max_tokens, const void* 
                       const void* k_rope, int64_t rope_stride, const int32_t* cu_seqlens, const int32_t* cache_seqlens,
                       const int32_t* block_table, void* kv_pages, void* stream);
 
+/*
+ * The same for a step whose pages may have run out: tokens of a sequence with served[b] != 1 (device
+ * int32 [batch], as mla_reserve_pages writes it) go nowhere, and are no error.  Such a sequence still has
+ * its old length, so that without `served` its tokens would overwrite the last n_b rows it holds.
+ */
+int32_t mla_append_served_kv(const mla_pool_params* p, int64_t max_tokens, const void* latent, int64_t latent_stride,
+                             const void* k_rope, int64_t rope_stride, const int32_t* cu_seqlens,
+                             const int32_t* cache_seqlens, const int32_t* block_table, const int32_t* served,
+                             void* kv_pages, void* stream);
+
 /* Bytes of the device workspace of fork (of at most max_forks), reserve and compact.  Host only. */
 int32_t mla_pool_workspace_size(const mla_pool_params* p, int32_t max_forks, size_t* workspace_bytes);
 
@@ -484,7 +494,8 @@ int32_t mla_fork_sequences(const mla_pool_params* p, void* kv_pages, const int32
  *   served  device int32 [batch]: 1: done; 0: not enough free pages (sequences are served in order, up to
  *           the first whose pages are not there; later ones that need no page are served); -2: refused (a
  *           negative count or length, or one past the block table; sets MLA_ERR_INVALID_ARG in the device error word)
- * A sequence that is not served keeps its length and pages.  A last page that others share must not be
+ * A sequence that is not served keeps its length and pages.  Its tokens of the step may stay in the token
+ * buffers: mla_append_served_kv leaves them out, and what the attention gives for them has no meaning.  A last page that others share must not be
  * grown into: mla_fork_sequences leaves none.
  */
 int32_t mla_reserve_pages(const mla_pool_params* p, const int32_t* num_new, int32_t* block_table, int32_t* cache_seqlens,

@@ -124,6 +124,7 @@ def load_library():
             "mla_chunk_schedule": ([C, vp, vp, vp, vp], i32),
             "mla_chunk_attend": ([C, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp], i32),
             "mla_append_kv": ([K, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp], i32),
+            "mla_append_served_kv": ([K, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp], i32),
             "mla_pool_workspace_size": ([K, i32, ctypes.POINTER(sz)], i32),
             "mla_copy_pages": ([K, vp, vp, vp, i32, vp], i32),
             "mla_fork_sequences": ([K, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp], i32),
@@ -391,9 +392,11 @@ def _attend(p, q_nope_absorbed, q_rope, kv_pages, block_table, cache_seqlens, sc
                                            _ptr(sched), _ptr(workspace), _stream(stream)), "mla_chunk_attend")
 
 
-def mla_append_kv(p: MlaPoolParams, latent, k_rope, cu_seqlens, cache_seqlens, block_table, kv_pages, stream=None):
+def mla_append_kv(p: MlaPoolParams, latent, k_rope, cu_seqlens, cache_seqlens, block_table, kv_pages, stream=None,
+                  served=None):
     """Rows of ragged new tokens into the pages: latent bf16 [T, 512] and k_rope bf16 [T, 64], rows of either may be
-    strided (the two parts of one [T, 576] array)."""
+    strided (the two parts of one [T, 576] array).  With served (int32 [B], from mla_reserve_pages) the tokens of
+    sequences that did not get their pages go nowhere."""
     i32, _, bf16 = _dtypes()
     B = p.batch
     for name, t, n in (("latent", latent, 512), ("k_rope", k_rope, 64)):
@@ -407,12 +410,20 @@ def mla_append_kv(p: MlaPoolParams, latent, k_rope, cu_seqlens, cache_seqlens, b
         _refuse("mla_append_kv: cache_seqlens")
     if _bad(block_table, i32, (B, p.max_pages_per_seq)):
         _refuse("mla_append_kv: block_table")
+    if served is not None and _bad(served, i32, (B,)):
+        _refuse("mla_append_kv: served")
     _expect_pool("mla_append_kv", kv_pages, p)
     if latent.shape[0] == 0:
         return
     _expect_device("mla_append_kv", latent, k_rope, cu_seqlens, cache_seqlens, block_table, kv_pages)
     # (one row: its stride says nothing)
     ls, rs = (int(t.stride(0)) if t.shape[0] > 1 else n for t, n in ((latent, 512), (k_rope, 64)))
+    if served is not None:
+        _expect_device("mla_append_kv", served)
+        _check(load_library().mla_append_served_kv(ctypes.byref(p), int(latent.shape[0]), latent.data_ptr(), ls, k_rope.data_ptr(), rs,
+                                                   cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(),
+                                                   served.data_ptr(), kv_pages.data_ptr(), _stream(stream)), "mla_append_served_kv")
+        return
     _check(load_library().mla_append_kv(ctypes.byref(p), int(latent.shape[0]), latent.data_ptr(), ls, k_rope.data_ptr(), rs,
                                         cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(), kv_pages.data_ptr(),
                                         _stream(stream)), "mla_append_kv")

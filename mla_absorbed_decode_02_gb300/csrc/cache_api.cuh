@@ -108,6 +108,28 @@ bool all_int_arrays(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+int32_t append_kv(const mla_pool_params* p, int64_t max_tokens, const void* latent, int64_t latent_stride,
+                  const void* k_rope, int64_t rope_stride, const int32_t* cu_seqlens, const int32_t* cache_seqlens,
+                  const int32_t* block_table, const int32_t* served, void* kv_pages, void* stream) {
+  int32_t st = check_pool(p);
+  if (st != MLA_OK) return st;
+  if (max_tokens < 0 || !latent || !k_rope || !cu_seqlens || !cache_seqlens || !block_table || !kv_pages)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(latent) || !aligned16(k_rope) || !aligned16(kv_pages) || !aligned(cu_seqlens, 4) ||
+      !aligned(cache_seqlens, 4) || !aligned(block_table, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (latent_stride < 512 || latent_stride % 8 != 0 || rope_stride < 64 || rope_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (max_tokens > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (max_tokens == 0) return MLA_OK;
+  const dim3 grid((unsigned)((max_tokens + 7) / 8));
+  const __nv_bfloat16 *c = static_cast<const __nv_bfloat16*>(latent), *r = static_cast<const __nv_bfloat16*>(k_rope);
+  const bool fp8 = p->kv_dtype == MLA_KV_FP8_E4M3;
+  auto* kernel = served ? (fp8 ? mla_append_kernel<true, true> : mla_append_kernel<false, true>)
+                        : (fp8 ? mla_append_kernel<true, false> : mla_append_kernel<false, false>);
+  return launch_after(stream, grid, 256, 0, kernel, pool_args(p), max_tokens, c, latent_stride, r, rope_stride, cu_seqlens,
+                      cache_seqlens, block_table, served, static_cast<uint8_t*>(kv_pages));
+}
+
 }  // namespace
 
 extern "C" {
@@ -228,21 +250,17 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
 int32_t mla_append_kv(const mla_pool_params* p, int64_t max_tokens, const void* latent, int64_t latent_stride,
                       const void* k_rope, int64_t rope_stride, const int32_t* cu_seqlens, const int32_t* cache_seqlens,
                       const int32_t* block_table, void* kv_pages, void* stream) {
-  int32_t st = check_pool(p);
-  if (st != MLA_OK) return st;
-  if (max_tokens < 0 || !latent || !k_rope || !cu_seqlens || !cache_seqlens || !block_table || !kv_pages)
-    return MLA_ERR_INVALID_ARG;
-  if (!aligned16(latent) || !aligned16(k_rope) || !aligned16(kv_pages) || !aligned(cu_seqlens, 4) ||
-      !aligned(cache_seqlens, 4) || !aligned(block_table, 4))
-    return MLA_ERR_INVALID_ARG;
-  if (latent_stride < 512 || latent_stride % 8 != 0 || rope_stride < 64 || rope_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
-  if (max_tokens > INT32_MAX) return MLA_ERR_UNSUPPORTED;
-  if (max_tokens == 0) return MLA_OK;
-  const dim3 grid((unsigned)((max_tokens + 7) / 8));
-  const __nv_bfloat16 *c = static_cast<const __nv_bfloat16*>(latent), *r = static_cast<const __nv_bfloat16*>(k_rope);
-  return launch_after(stream, grid, 256, 0, p->kv_dtype == MLA_KV_BF16 ? mla_append_kernel<false> : mla_append_kernel<true>,
-                      pool_args(p), max_tokens, c, latent_stride, r, rope_stride, cu_seqlens, cache_seqlens, block_table,
-                      static_cast<uint8_t*>(kv_pages));
+  return append_kv(p, max_tokens, latent, latent_stride, k_rope, rope_stride, cu_seqlens, cache_seqlens, block_table, nullptr,
+                   kv_pages, stream);
+}
+
+int32_t mla_append_served_kv(const mla_pool_params* p, int64_t max_tokens, const void* latent, int64_t latent_stride,
+                             const void* k_rope, int64_t rope_stride, const int32_t* cu_seqlens,
+                             const int32_t* cache_seqlens, const int32_t* block_table, const int32_t* served,
+                             void* kv_pages, void* stream) {
+  if (!served || !aligned(served, 4)) return MLA_ERR_INVALID_ARG;
+  return append_kv(p, max_tokens, latent, latent_stride, k_rope, rope_stride, cu_seqlens, cache_seqlens, block_table, served,
+                   kv_pages, stream);
 }
 
 int32_t mla_pool_workspace_size(const mla_pool_params* p, int32_t max_forks, size_t* workspace_bytes) {

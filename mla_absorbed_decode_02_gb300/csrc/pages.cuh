@@ -17,6 +17,8 @@
 namespace mla {
 
 constexpr int kPageRows = 64;
+// What reserve writes for a sequence.
+constexpr int kReserveDone = 1, kReserveNoPages = 0, kReserveRefused = -2;
 
 struct PoolArgs {
   int32_t batch, num_pages, max_pages, num_layers, row_bytes;
@@ -80,13 +82,15 @@ __device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&
 // Token t of the ragged buffer belongs to the sequence b with cu[b] <= t < cu[b + 1] and goes to
 // row L_b - n_b + (t - cu[b]) of that sequence.  A warp takes a token: its row is loaded first,
 // then the sequence is found by a 32-way search (one round for up to 31 sequences, two for up to
-// ~1000).  64 rows in 1.9 us; 22,500 rows quantised in 10.2 us, 4.0 TB/s (11.4 us with
-// the divisions): the search and the launch are the rest.
-template <bool kFp8>
+// ~1000).  kServed: the tokens of a sequence that did not get its pages go nowhere -- its length is
+// still the old one, and row L_b - n_b one that it (or, in a shared page, another) holds; a kernel of
+// its own, since as a question at run time it cost the other 7%.  64 rows in 1.9 us; 22,500 rows
+// quantised in 10.2 us, 4.0 TB/s (11.4 us with the divisions): the search and the launch are the rest.
+template <bool kFp8, bool kServed>
 __global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max_tokens, const __nv_bfloat16* latent,
                                                          int64_t latent_stride, const __nv_bfloat16* rope,
                                                          int64_t rope_stride, const int32_t* cu, const int32_t* lens,
-                                                         const int32_t* block_table, uint8_t* pages) {
+                                                         const int32_t* block_table, const int32_t* served, uint8_t* pages) {
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   pdl_wait_prerequisites();
@@ -105,12 +109,14 @@ __global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max
     hi = min(hi, lo + step * (k + 1));
     lo = lo + step * k;
   }
-  // the last round: lane j holds cu[lo + j] and the length of sequence lo + j
+  // the last round: lane j holds cu[lo + j], the length of sequence lo + j and whether it takes its tokens
   const int32_t start = lo + lane <= p.batch ? cu[lo + lane] : INT32_MAX;
   const int32_t len = lo + lane < p.batch ? lens[lo + lane] : 0;
+  const bool takes = kServed && lo + lane < p.batch && served[lo + lane] == kReserveDone;
   if (t >= end) return;  // rows behind the last sequence
   const uint32_t le = __ballot_sync(0xffffffffu, lo + lane < hi && start <= t);
   const int k = le ? 31 - __clz(le) : 0;  // (at most 30: the next sequence's start is a lane's too)
+  if (kServed && !((__ballot_sync(0xffffffffu, takes) >> k) & 1)) return;
   lo += k;
   const int first = __shfl_sync(0xffffffffu, start, k), n = __shfl_sync(0xffffffffu, start, k + 1) - first;
   const int64_t pos = (int64_t)__shfl_sync(0xffffffffu, len, k) - n + (t - first);
@@ -319,8 +325,6 @@ __global__ void __launch_bounds__(256) mla_fork_kernel(PoolArgs p, uint8_t* page
 }
 
 // ----------------------------------------------------------------- reserve
-constexpr int kReserveDone = 1, kReserveNoPages = 0, kReserveRefused = -2;
-
 // One CTA.  Sequence b needs pages for num_new[b] more rows.  Those served are the sequences up to
 // the first whose pages are no longer there, and all that need none.  ws: pages needed by the
 // sequences before b [batch + 1].

@@ -545,3 +545,102 @@ def test_upkeep_captured_on_another_stream():
     assert _lib.mla_device_error(clear=True) == 0
     for a, b in zip(want + s.tables() + (s.d,), got + t.tables() + (t.d,)):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ steps whose pages run out
+def test_append_refuses_a_bad_served():
+    import ctypes
+
+    import torch
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    p, x = _params(num_layers=1), torch.zeros(4, 576, dtype=torch.bfloat16)
+    good = (p, x[:, :512], x[:, 512:], i32(7), i32(6), i32(6, 8), torch.zeros(32, 64, 656, dtype=torch.uint8))
+    for served in (i32(5), i32(7), i32(6).long(), i32(12)[::2], i32(6, 1)):
+        with pytest.raises(MlaError, match="served") as e:
+            _lib.mla_append_kv(*good, stream=0, served=served)
+        assert e.value.status == _lib.MLA_ERR_INVALID_ARG
+    with pytest.raises(MlaError, match="device"):
+        _lib.mla_append_kv(*good, stream=0, served=i32(6))
+    buf = ctypes.create_string_buffer(4096)
+    g = (ctypes.addressof(buf) + 255) // 256 * 256
+    args = [4, g, 576, g, 576, g, g, g, g, g, 0]       # ... block_table, served, kv_pages, stream
+    for k, v in enumerate(args[:-1]):
+        for bad in ((0, g + 2) if v == g else (-1,)):
+            a = list(args)
+            a[k] = bad
+            assert _lib.load_library().mla_append_served_kv(ctypes.byref(p), *a) == _lib.MLA_ERR_INVALID_ARG, (k, bad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", [MLA_KV_BF16, MLA_KV_FP8_E4M3])
+@pytest.mark.parametrize("batch", [1, 31, 32, 33, 700, 2100])
+def test_append_leaves_out_what_is_not_served(kv, batch):
+    """Only tokens of sequences whose `served` is 1 are written, for every depth of the search; the lengths and
+    pages of the others are not looked at."""
+    import torch
+    rng = np.random.default_rng(batch)
+    n = rng.integers(0, 4, batch)
+    n[-1] = 2
+    served = rng.choice([1, 1, 0, -2], batch)
+    served[-1] = 0 if batch == 1 else 1
+    p, lat, rope, cu, lens, bt, pool, at, x = _append_case(kv, n, n + rng.integers(0, 100, batch), seed=batch + kv, pad=3)
+    want = pool.clone()
+    _lib.mla_append_kv(p, lat, rope, cu, lens, bt, want)
+    d_served = torch.from_numpy(served.astype(np.int32)).cuda()
+    plain = pool.clone()
+    _lib.mla_append_kv(p, lat, rope, cu, lens, bt, plain, served=torch.ones_like(d_served))
+    assert torch.equal(plain, want)
+    skipped = [a for a, b in zip(at, np.repeat(np.arange(batch), n)) if served[b] != 1]
+    if skipped:
+        pg, r = (torch.tensor(v, device="cuda") for v in zip(*skipped))
+        want[pg, r] = pool[pg, r]
+    lens[d_served == -2], bt[d_served == 0] = -5, -1     # neither is read
+    _lib.mla_append_kv(p, lat, rope, cu, lens, bt, pool, served=d_served)
+    torch.cuda.synchronize()
+    assert _lib.mla_device_error(clear=True) == 0
+    assert torch.equal(pool, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", [MLA_KV_BF16, MLA_KV_FP8_E4M3])
+def test_a_step_whose_pages_run_out(kv):
+    """reserve, append and attention of one step with its token buffers as they were laid out: the sequence that gets
+    no page keeps its rows, and those that share pages with it keep theirs; the others' results are those of a pool
+    with pages enough."""
+    import torch
+    B, H, M = 4, 16, 4
+    g = torch.Generator("cuda").manual_seed(kv)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    row = (576, torch.bfloat16) if kv == MLA_KV_BF16 else (656, torch.uint8)
+    first, second = [128, 0, 70, 5], [3, 9, 100, 30]
+    token = lambda n, w: torch.randn(n, *w, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    x1, x2, q, qr = token(203, (576,)), token(142, (576,)), token(142, (H, 512)), token(142, (H, 64))
+    cu1, cu2 = dev([0, 128, 128, 198, 203]), dev([0, 3, 12, 112, 142])
+    got = {}
+    for P in (16, 6):
+        p = MlaPoolParams.make(B, P, M, kv_dtype=kv)
+        up = _lib.PagePool(p)
+        t = up.new_tables()
+        bt, L, ref = t
+        pool = torch.zeros(P, 64, row[0], dtype=row[1], device="cuda")
+        served = up.reserve(dev(first), *t)
+        _lib.mla_append_kv(p, x1[:, :512], x1[:, 512:], cu1, L, bt, pool, served=served)
+        assert up.fork(pool, dev([0]), dev([1]), *t).tolist() == [-1]    # 1 shares both pages of 0; 5 pages are held
+        before = pool.clone()
+        served = up.reserve(dev(second), *t)                             # of six pages one is left: 0's
+        assert served.tolist() == ([1] * 4 if P == 16 else [1, 0, 0, 1])
+        attn = _lib.ChunkAttention(_lib.MlaChunkParams.make(B, 142, H, P, M, kv_dtype=kv, max_kv_tokens=B * M * 64))
+        attn.plan(cu2, L)
+        _lib.mla_append_kv(p, x2[:, :512], x2[:, 512:], cu2, L, bt, pool, served=served)
+        out, lse = attn.attend(q, qr, pool, bt, 192 ** -0.5)
+        torch.cuda.synchronize()
+        assert _lib.mla_device_error(clear=True) == 0
+        got[P] = out, lse
+        if P == 6:
+            assert L.tolist() == [131, 128, 70, 35]
+            for b, rows in ((0, 128), (1, 128), (2, 70), (3, 5)):         # what was cached before the step
+                held = bt[b, :-(-rows // 64)].long()
+                assert torch.equal(pool[held].flatten(0, 1)[:rows], before[held].flatten(0, 1)[:rows])
+    for b in (0, 3):
+        for a, e in zip(got[16], got[6]):
+            assert torch.equal(a[cu2[b]:cu2[b + 1]], e[cu2[b]:cu2[b + 1]])
