@@ -538,3 +538,13 @@ def test_one_score_that_is_not_finite(H, units, kv, dim, value, row):
     first = max(0, row - (L - n))                 # the first token that sees the key
     assert torch.equal(got[:first], want[:first]) and torch.equal(got_lse[:first], want_lse[:first])
     assert got_lse[first:].isnan().all() and got[first:].isnan().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,L,H,units", [([4, 9], [130, 600], 128, 0), ([1, 0, 17, 3], [1, 50, 1025, 2], 40, 3), ([5, 2], [3, 0], 128, 2),
+                                         ([30, 1], [260, 2000], 7, 9), ([2] * 9, [64 * k + 1 for k in range(9)], 64, 4)])
+def test_without_the_causal_rule_everywhere(kv, n, L, H, units):
+    """Every new token sees all L_b keys, those of later tokens among them: both row types, several blocks a sequence,
+    split and dealt blocks, fewer rows than new tokens."""
+    Problem(n, L, H, kv, seed=50 + units, causal=False, pad=2, num_units=units).check()
