@@ -158,12 +158,20 @@ def _ptr(t) -> int:
     return int(t.data_ptr())
 
 
+_raw = None  # torch._C, once CUDA is up and it gives raw streams
+
+
 def _stream(stream) -> int:
+    global _raw
+    if type(stream) is int:
+        return stream
     if stream is None:
-        import torch
-        if torch.cuda.is_initialized() and hasattr(torch._C, "_cuda_getCurrentRawStream"):
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())  # 0.2 us; the Stream object costs 3
-        return int(torch.cuda.current_stream().cuda_stream)
+        if _raw is None:
+            import torch
+            if not (torch.cuda.is_initialized() and hasattr(torch._C, "_cuda_getCurrentRawStream")):
+                return int(torch.cuda.current_stream().cuda_stream)
+            _raw = torch._C
+        return _raw._cuda_getCurrentRawStream(_raw._cuda_getDevice())  # 0.2 us; the Stream object costs 3
     return int(getattr(stream, "cuda_stream", stream))
 
 
@@ -641,10 +649,8 @@ class _Owner:
                 self._buffers = new()
         return self._buffers
 
-    def _on(self, stream):
+    def _on(self, stream) -> int:
         """The handle of the stream of a call, which the buffers are kept for."""
-        if self.device.type != "cuda":
-            return stream
         handle = _stream(stream)
         if handle not in self._streams:
             self._keep_for(stream, handle)
@@ -652,6 +658,8 @@ class _Owner:
 
     def _keep_for(self, stream, handle):
         import torch
+        if self.device.type != "cuda":
+            return
         if stream is None:
             stream = torch.cuda.current_stream()
         elif handle == 0:

@@ -35,9 +35,9 @@ def test_params_changed_after_a_chunk_wrapper_was_made(monkeypatch):
     assert attn.p.max_kv_tokens == 6400 and larger.p.max_kv_tokens == 12800
     import torch
     x = torch.zeros(8, 16, 512, dtype=torch.bfloat16)
-    attn.plan(None, x)
-    attn.attend(x, None, None, None, 1.0)
-    larger.plan(None, x)
+    attn.plan(None, x, stream=0)
+    attn.attend(x, None, None, None, 1.0, out=x, lse=x, stream=0)
+    larger.plan(None, x, stream=0)
     assert used == [6400, 6400, 12800]
     with pytest.raises(MlaError) as e:
         attn.p = p
@@ -59,9 +59,10 @@ def test_params_changed_after_a_pool_wrapper_was_made(monkeypatch):
     pool.p.num_pages = 10000
     import torch
     ids, lens = torch.zeros(8, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
-    pool.fork(None, ids, ids, None, lens, None)
-    pool.reserve(lens, None, lens, None)
-    pool.compact(None, None, lens, None)
+    monkeypatch.setattr(_lib, "_new", lambda like, *a: like)
+    pool.fork(None, ids, ids, None, lens, None, stream=0)
+    pool.reserve(lens, None, lens, None, stream=0)
+    pool.compact(None, None, lens, None, stream=0)
     assert used == [(100, 4)] * 3
     bt, L, ref = pool.new_tables()
     assert bt.shape == (4, 8) and L.shape == (4,) and ref.shape == (100,)
