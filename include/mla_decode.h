@@ -382,11 +382,11 @@ int32_t mla_chunk_schedule(const mla_chunk_params* p, const int32_t* cu_seqlens,
  *                    B, T, H, max_pages_per_seq, causal, max_kv_tokens or unit count sets
  *                    MLA_ERR_WORKSPACE in the device error word, and nothing is written)
  *   workspace        device, workspace_bytes, 256-byte aligned; not shared by calls that overlap
- * Scores, softmax statistics and sums are float32; P is bf16 for the P.V product.  A key whose score
- * is not finite in float32 (its row of the cache holds NaN or an infinity, or the product with the
- * query overflows, to either side) makes NaN of out and lse of the tokens and heads that see it, and
- * of no others.  Cache rows past L_b may hold any bits.  The kernels run on stream, each a programmatic dependent of the one
- * before, and can be captured into a graph.
+ * Scores, softmax statistics and sums are float32; P is bf16 for the P.V product.  Where the product
+ * of a token's query and a key that it sees is not finite in float32 (the row of the cache holds NaN
+ * or an infinity, or the product overflows, to either side), out and lse of that token and head are
+ * NaN, and no others.  Cache rows past L_b may hold any bits.  The kernels run on stream, each a
+ * programmatic dependent of the one before, and can be captured into a graph.
  */
 int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed, const void* q_rope, const void* kv_pages,
                          const int32_t* block_table, const int32_t* cache_seqlens, float scale, void* out, float* lse,

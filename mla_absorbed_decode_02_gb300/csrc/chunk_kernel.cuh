@@ -720,17 +720,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       if (!(ok = wait_warp<true>(bar(CB_S_FULL + sb), (g >> 1) & 1, wc, kSiteCkScores))) break;
       tc_fence_after();
       uint32_t sv[64];
-      tmem_ld32(tmem + lane_off + CT_S + 128 * sb + 64 * w, *reinterpret_cast<uint32_t(*)[32]>(sv));
-      tmem_ld32(tmem + lane_off + CT_S + 128 * sb + 64 * w + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+      float least[2];
+      tmem_ld32_min(tmem + lane_off + CT_S + 128 * sb + 64 * w, *reinterpret_cast<uint32_t(*)[32]>(sv), least[0]);
+      tmem_ld32_min(tmem + lane_off + CT_S + 128 * sb + 64 * w + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32), least[1]);
       tmem_wait_ld();
-      const bool part_seen = kChunkTile * (a.tile + 1) > some || r >= a.b.ntok * args.key.heads;
-      if (part_seen) {
-        // keys this row sees of the thread's 64; a seen score of -inf makes the row NaN (as `odd` does below; what
-        // is not finite in such a key's value row was zeroed)
+      // A seen score of -inf makes the row NaN.  (The maximum and exp(-inf) = 0 would lose it, and whether a token feels
+      // such a key would depend on the tile it lies in; +inf and NaN show by themselves.)  The least score comes with
+      // the load: found by instructions of its own it cost 1% of prompt pieces and 2-3% of a long append.
+      if (kChunkTile * (a.tile + 1) > some || r >= a.b.ntok * args.key.heads) {
+        // keys this row sees of the thread's 64 (what is not finite in their value rows was zeroed)
         const int nv = lim - (kChunkTile * a.tile + 64 * part);
 #pragma unroll
         for (int j = 0; j < 64; ++j)
           sv[j] = j < nv ? (sv[j] == 0xFF800000u ? 0x7FC00000u : sv[j]) : 0xFF800000u;
+      } else if (fminf(least[0], least[1]) == -INFINITY) {
+        sv[0] = 0x7FC00000u;
       }
       float mt;
       {
@@ -756,17 +760,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
       uint32_t pp[32];
       float ls;
       {
-        // odd: 0, or NaN where a score is not finite.  (The maximum and exp(-inf) = 0 would lose a score of -inf, and
-        // whether a token feels such a key would depend on the tile it lies in.  Prompt pieces 123.5 against 122.9 us
-        // without it, a long append 2.57 against 2.53 ms; a running minimum of the scores instead takes 124.7 and 2.61.)
         const uint64_t s2 = splat_f32x2(sl2), nm = splat_f32x2(-m_use);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull}, odd = 0ull;
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           float x0, x1;
-          const uint64_t s01 = pack_b32x2(sv[2 * j], sv[2 * j + 1]);
-          unpack_f32x2(ffma_f32x2(s01, s2, nm), x0, x1);
-          odd = ffma_f32x2(s01, 0ull, odd);
+          unpack_f32x2(ffma_f32x2(pack_b32x2(sv[2 * j], sv[2 * j + 1]), s2, nm), x0, x1);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
           pp[j] = pack_bf16(p0, p1);
           acc[j & 3] = fadd_f32x2(acc[j & 3], pack_f32x2(p0, p1));
@@ -774,8 +773,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
         float z0, z1;
         unpack_f32x2(fadd_f32x2(fadd_f32x2(acc[0], acc[1]), fadd_f32x2(acc[2], acc[3])), z0, z1);
         ls = z0 + z1;
-        unpack_f32x2(odd, z0, z1);
-        if (!part_seen) ls += z0 + z1;
       }
       // PV of the tile before is done: P may be overwritten, O read and rescaled
       if (g > 0 && !(ok = wait_warp<true>(bar(CB_P_FREE), (g - 1) & 1, wc, kSiteCkPv))) break;
