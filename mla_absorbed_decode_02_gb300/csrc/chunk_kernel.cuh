@@ -25,9 +25,10 @@
 // run the softmax.  A row's 256 scores lie in four threads, which agree on its maximum through
 // shared memory; O is rescaled only when the maximum grows by more than 2^8.
 //
-// Measured: 512 tokens x 128 heads after 32,768 rows in 2.50-2.56 ms, 1840-1880 TFLOP/s (the measured cuBLAS
-// rate), 2.61 ms when held for seconds (cuBLAS then: 2.76): the power cap; 4 x ~450 tokens x 16 heads after
-// ~3000 rows in 122 us, 1630 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in 167 us, 1630 TFLOP/s.  A long
+// Measured, from a graph / through the Python entry on changing inputs: 512 tokens x 128 heads after 32,768 rows in
+// 2.50-2.56 / 2.60 ms, 1810-1880 TFLOP/s (the power cap; cuBLAS held for seconds would take 2.76); 4 x ~430 tokens x
+// 16 heads after ~3000 rows in 122-125 / 133 us, 1500-1630 TFLOP/s; 32 streams of 1..24 tokens x 128 heads in
+// 167-172 / 187 us, 1460-1640 TFLOP/s; the plan of the step, 10 to 24 us once for all layers, not counted.  A long
 // append's tile takes 4840 cycles, of which the tensor cores' own are 4352; the prompts' 5110 and the
 // streams' 5670, where slots wait for pages from L2 and HBM.  With many short blocks add the change of block
 // (~3/4 of a tile: the last softmax and the first have no MMAs beside them), what the units' shares
@@ -767,6 +768,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCkThreads, 1)
           float x0, x1;
           unpack_f32x2(ffma_f32x2(pack_b32x2(sv[2 * j], sv[2 * j + 1]), s2, nm), x0, x1);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          // P in bf16, the type of V in the tensor cores (half a step is 2^-8 of a weight at most, of either sign); the row's sum
+          // takes the float32 weights, so that lse is not rounded with them
           pp[j] = pack_bf16(p0, p1);
           acc[j & 3] = fadd_f32x2(acc[j & 3], pack_f32x2(p0, p1));
         }
@@ -960,7 +963,8 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
 // read every cached row many times over, so 1808 bytes of traffic a cached token stand against
 // 278,528 FLOP per new token at 128 heads.  A warp takes a row: lane l the codes [16 l, 16 l + 16).
 // 63,900 rows in 26 us, 4.5 TB/s, 3% of the attention over them; two or eight rows of a warp in flight
-// instead of four, or half a page a block, changed nothing.
+// instead of four, or half a page a block, changed nothing.  Where a row has one reader nothing pays for
+// it: 64 x 1 token x 16 heads over 8192 FP8 rows take 307 us, over bf16 rows 122.
 __global__ void __launch_bounds__(256) mla_chunk_expand_kernel(const int32_t* sched, ChunkKey key, const uint8_t* pages,
                                                                const int32_t* block_table, int num_pages, const int32_t* lens,
                                                                __nv_bfloat16* rows) {
@@ -1030,7 +1034,7 @@ __device__ __forceinline__ int64_t block_scan_1024(int64_t v, int64_t* sh, int64
 }
 
 // One CTA of 1024 threads; the phases of chunk_plan_host with the sums in parallel.
-// 10 us with 8 blocks, 15-23 with 225 to 580 to deal (cold): dependent trips to L2 and barriers, once a step
+// 10 us with 8 blocks, 14-24 with 225 to 580 to deal (cold): dependent trips to L2 and barriers, once a step
 // for all layers.
 __global__ void __launch_bounds__(1024) mla_chunk_sched_kernel(const int32_t* cu, const int32_t* lens, int B,
                                                                int64_t max_tokens, int H, int causal, int max_pages,

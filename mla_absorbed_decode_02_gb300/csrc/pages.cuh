@@ -8,8 +8,8 @@
 // by the inputs (the atomics are integer additions).
 //
 // Measured: compaction of 226 pages x 16 layers, 533 MB read and written, in 78 us (6.8 TB/s, 102% of
-// the measured copy rate); 300 pages x 8 layers, 202 MB, copied in 27-31 us; the kernels
-// that only keep books take 2-6 us.
+// the measured copy rate); 300 pages x 8 layers, 202 MB, copied in 27-32 us; the kernels
+// that only keep books take 4-8 us cold, 2-5 in a run of calls.
 #pragma once
 #include "chunk_kernel.cuh"  // block_scan_1024
 #include "common.cuh"
@@ -84,8 +84,9 @@ __device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&
 // then the sequence is found by a 32-way search (one round for up to 31 sequences, two for up to
 // ~1000).  kServed: the tokens of a sequence that did not get its pages go nowhere -- its length is
 // still the old one, and row L_b - n_b one that it (or, in a shared page, another) holds; a kernel of
-// its own, since as a question at run time it cost the other 7%.  64 rows in 1.9 us; 22,500 rows
-// quantised in 10.2 us, 4.0 TB/s (11.4 us with the divisions): the search and the launch are the rest.
+// its own, since as a question at run time it cost the other 7%.  From a graph 64 rows in 1.9-2.2 us;
+// 22,500 rows quantised in 10.2-10.6 us, 3.9 TB/s (11.4 us with the divisions; 11.0-11.3 cold), as bf16 in 9.5 us,
+// 5.5 TB/s: the search and the launch are the rest.
 template <bool kFp8, bool kServed>
 __global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max_tokens, const __nv_bfloat16* latent,
                                                          int64_t latent_stride, const __nv_bfloat16* rope,
