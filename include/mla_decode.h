@@ -63,6 +63,11 @@ typedef enum {
   MLA_KV_BF16 = 0,          /* page = [64][576] bf16: c (512) then k^R (64); 1152 bytes per token */
   MLA_KV_FP8_E4M3 = 1,      /* page = [64][656 bytes]: 512 E4M3 codes of c, then 4 float32 scales
                                (one per 128-code tile, value = code * scale), then k^R as 64 bf16 */
+  MLA_KV_INT4 = 2,          /* page = [64][416 bytes]: 512 four-bit codes of c (256 bytes), then 16 bf16 scales (one per
+                               32 values), then k^R as 64 bf16.  value = (code - 8) * scale, exact in bf16: a scale has
+                               four significant bits (its low four mantissa bits are zero).  The 32-bit word (little
+                               endian) of dims 8 w .. 8 w + 7 has the code of dim 8 w + 2 i in bits 4 i .. 4 i + 3 and of dim
+                               8 w + 2 i + 1 in bits 16 + 4 i .. 19 + 4 i, i = 0 .. 3 */
 } mla_kv_dtype;
 
 typedef enum {
@@ -83,14 +88,16 @@ typedef struct mla_decode_params {
                                 zero => every new token sees all L_b keys */
   int32_t kv_dtype;          /* mla_kv_dtype */
   int32_t out_dtype;         /* mla_out_dtype */
-  int32_t num_units;         /* work units (one cluster of 2G SMs each, G = the token group); 0 = as
-                                many as fit at once */
+  int32_t num_units;         /* work units (one cluster of 2G SMs each, G = the token group; INT4 cache: one SM
+                                each, two with more than 64 heads); 0 = as many as fit at once */
   int32_t timeout_us;        /* limit of every bounded wait inside the kernels; 0 = 2,000,000 us */
   int32_t token_group;       /* G: new tokens of a sequence decoded together on shared pages: each page
                                 is read from memory once for the G tokens (one CTA pair per token, a
                                 cluster of 2G CTAs, pages multicast to every pair); 1..4 and dividing
                                 s_q; 0 = 1.  Clusters of 4 / 8 CTAs occupy 144 / 120 of GB300's 152 SMs,
-                                so G > 1 pays where DRAM, not the SMs, bounds the decode */
+                                so G > 1 pays where DRAM, not the SMs, bounds the decode.
+                                INT4 cache: the G tokens' heads are rows of one CTA, G * num_heads <= 64 where
+                                G > 1 (else MLA_ERR_UNSUPPORTED); 0 = the most that divide s_q and fit */
   int32_t qk_fp8;            /* FP8 cache only, opt-in (0 or 1): 1 => QK runs on E4M3 codes on the FP8 tensor
                                 cores ("MLA inference: two computation paths and FlashMLA", exercise 2
                                 "An FP8 KV cache").  The query is then passed quantised like the cache:
@@ -127,7 +134,8 @@ int32_t mla_get_scheduler_metadata(const mla_decode_params* p, const int32_t* ca
  *   q_nope_absorbed  device bf16 [B][s_q][H][512]  absorbed query q~ (qk_fp8: the 656-byte rows of
  *                    mla_quantize_q_fp8)
  *   q_rope           device bf16 [B][s_q][H][64]   RoPE query q^R (qk_fp8: not read)
- *   kv_pages         device [num_pages][64][576] bf16, or [num_pages][64][656 bytes] FP8 rows
+ *   kv_pages         device [num_pages][64][576] bf16, [num_pages][64][656 bytes] FP8 rows, or
+ *                    [num_pages][64][416 bytes] INT4 rows
  *   block_table      device int32 [B][max_pages_per_seq]: physical page of logical page i of
  *                    sequence b; entries past ceil(L_b/64) are never read.  Every entry read
  *                    must be in [0, num_pages).
@@ -141,7 +149,9 @@ int32_t mla_get_scheduler_metadata(const mla_decode_params* p, const int32_t* ca
  *   lse              device float32 [B][s_q][H]; a token that sees no key gets out = 0, lse = -inf
  *   sched            device, from mla_get_scheduler_metadata with the same p and lengths
  *   workspace        device, workspace_bytes from mla_get_workspace_size
- * Cache rows of the last page past L_b are not used (they may hold any bits).
+ * Cache rows of the last page past L_b are not used (they may hold any bits).  INT4 cache: a block-table entry
+ * outside [0, num_pages) sets MLA_ERR_INVALID_ARG in the device error word and leaves that sequence's result
+ * undefined; a key whose row holds NaN makes NaN of the tokens that see it, and of no others.
  */
 int32_t mla_decode(const mla_decode_params* p, const void* q_nope_absorbed, const void* q_rope, const void* kv_pages,
                    const int32_t* block_table, const int32_t* cache_seqlens, float scale, void* out, float* lse,
@@ -201,6 +211,26 @@ int32_t mla_resolve_num_units(const mla_decode_params* p, int32_t* num_units);
  * launches nothing.  Both buffers 16-byte aligned; asynchronous on stream.
  */
 int32_t mla_quantize_kv_fp8(const void* kv_bf16, void* kv_fp8, int64_t num_tokens, void* stream);
+
+/*
+ * Writes the INT4 form of a bf16 cache, in the layout MLA_KV_INT4 reads.
+ *   kv_bf16   device bf16 [num_tokens][576]: latent c (512) then k^R (64)
+ *   kv_int4   device [num_tokens][416 bytes]: 256 bytes of codes, 16 bf16 scales, the 64 RoPE values unchanged
+ * Per 32 latent values: scale = amax / 7 rounded up to four significant bits and at least 2^-126 (1 where all are
+ * zero); code = 8 + x / scale rounded to nearest even, 1 .. 15.  Values of which one is not finite, or above 7 * 2^119, read
+ * back as NaN, all 32.  num_tokens = 0 launches nothing.  Both buffers 16-byte aligned; asynchronous on stream.
+ */
+int32_t mla_quantize_kv_int4(const void* kv_bf16, void* kv_int4, int64_t num_tokens, void* stream);
+
+/*
+ * The way back: rows of a cache of any format as bf16 rows.
+ *   kv_dtype  mla_kv_dtype of kv_rows
+ *   kv_rows   device [num_tokens] rows of 1152, 656 or 416 bytes (the pages of a pool are such rows, one after another)
+ *   kv_bf16   device bf16 [num_tokens][576]: FP8 values are code * scale rounded to bf16, INT4 values and the
+ *             64 RoPE values are exact; must not overlap kv_rows
+ * num_tokens = 0 launches nothing.  Both buffers 16-byte aligned; asynchronous on stream.
+ */
+int32_t mla_dequantize_kv(int32_t kv_dtype, const void* kv_rows, void* kv_bf16, int64_t num_tokens, void* stream);
 
 /*
  * The query of an FP8-QK decode (mla_decode_params.qk_fp8), quantised like a cache row:
@@ -337,7 +367,7 @@ typedef struct mla_chunk_params {
   int32_t num_units;         /* work units (one CTA pair each); 0 = as many as fit at once */
   int32_t timeout_us;        /* limit of every bounded wait inside the kernels; 0 = 2,000,000 us.  A wait can
                                 last as long as a unit's largest piece, about 3.3 us per 256 keys */
-  int64_t max_kv_tokens;     /* FP8 cache: room for the expanded rows in the workspace, in tokens: at
+  int64_t max_kv_tokens;     /* FP8 or INT4 cache: room for the expanded rows in the workspace, in tokens: at
                                 least the sum of 64 * ceil(L_b / 64) over the sequences with n_b > 0
                                 (a plan that needs more is refused).  bf16 cache: not used */
   int32_t reserved[4];       /* must be zero */
@@ -345,7 +375,7 @@ typedef struct mla_chunk_params {
 
 /*
  * Sizes of the two caller-provided device buffers: *sched_bytes for the plan, *workspace_bytes for
- * the split partials (float32) and, with an FP8 cache, the expanded rows (1152 bytes a token).
+ * the split partials (float32) and, with an FP8 or INT4 cache, the expanded rows (1152 bytes a token).
  * They depend on p alone, never on the lengths.  Needs a CUDA device only when p->num_units == 0.
  */
 int32_t mla_chunk_workspace_size(const mla_chunk_params* p, size_t* sched_bytes, size_t* workspace_bytes);
@@ -358,7 +388,7 @@ int32_t mla_chunk_workspace_size(const mla_chunk_params* p, size_t* sched_bytes,
  *   cache_seqlens  device int32 [B]: L_b with the n_b new tokens, 0 .. 64 * max_pages_per_seq; a
  *                  length below n_b leaves the first n_b - L_b tokens without keys
  *   sched          device, sched_bytes
- * Lengths outside these rules, or FP8 sequences past max_kv_tokens, set MLA_ERR_INVALID_ARG in the
+ * Lengths outside these rules, or FP8 or INT4 sequences past max_kv_tokens, set MLA_ERR_INVALID_ARG in the
  * device error word; the plan is then marked refused, mla_chunk_attend writes nothing and sets
  * MLA_ERR_WORKSPACE unless an error is set already.
  */
@@ -368,8 +398,8 @@ int32_t mla_chunk_schedule(const mla_chunk_params* p, const int32_t* cu_seqlens,
 /*
  * The attention.
  *   q_nope_absorbed  device bf16 [T][H][512]; q_rope device bf16 [T][H][64]
- *   kv_pages         device, the pool of mla_decode (bf16 or FP8 pages).  FP8 rows stand for
- *                    bf16(code * scale): they are expanded once per call into the workspace
+ *   kv_pages         device, the pool of mla_decode (bf16, FP8 or INT4 pages).  FP8 rows stand for
+ *                    bf16(code * scale); FP8 and INT4 rows are expanded once per call into the workspace
  *   block_table      device int32 [B][max_pages_per_seq]; entries past ceil(L_b / 64) are never read.
  *                    An entry outside [0, num_pages) sets MLA_ERR_INVALID_ARG in the device error
  *                    word and leaves that sequence's result undefined
@@ -399,7 +429,7 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
  * cost positions per unit, [6] = tokens per block, [7] = split blocks, [8] = pages of the sequences
  * with new tokens, [9] = 1: no more blocks than units, each unit has one share of one block, and [5]
  * is the most tiles of a share; [9] = 2: whole blocks dealt in rounds, [5] is the greatest cost of a
- * unit; [10] = B, [11] = causal, [12] = T, [13] = H, [14] = max_pages_per_seq, [15] = FP8:
+ * unit; [10] = B, [11] = causal, [12] = T, [13] = H, [14] = max_pages_per_seq, [15] = FP8, INT4:
  * max_kv_tokens / 64, bf16: INT32_MAX; then per unit 16 ints {first block, first tile, last block, end
  * tile, split index of the first piece, 0, 0, 0, the first block's record} (first block -1: no work); then
  * per block 8 ints {first token, tokens, sequence, keys the first token sees before clipping, L, tiles
@@ -424,7 +454,7 @@ typedef struct mla_pool_params {
   int32_t num_pages;         /* physical pages in each pool (>= 1) */
   int32_t page_size;         /* must be 64 */
   int32_t max_pages_per_seq; /* row length of block_table (>= 1) */
-  int32_t kv_dtype;          /* mla_kv_dtype: pages of 64 rows of 1152 or 656 bytes */
+  int32_t kv_dtype;          /* mla_kv_dtype: pages of 64 rows of 1152, 656 or 416 bytes */
   int32_t num_layers;        /* pools that share the table (1..16383) */
   int64_t layer_stride;      /* bytes, a multiple of 16, at least a pool's size; 0 = pools are packed */
   int32_t reserved[4];       /* must be zero */
@@ -440,7 +470,8 @@ typedef struct mla_pool_params {
  *   cu_seqlens, cache_seqlens, block_table   as for mla_chunk_schedule / mla_chunk_attend
  *   kv_pages       device, the layer's pool.  FP8: quantised by the rule of mla_quantize_kv_fp8 (the
  *                  same bytes for finite rows); a tile that holds a value that is not finite reads
- *                  back as NaN there (as NaN throughout, where the value is infinite)
+ *                  back as NaN there (as NaN throughout, where the value is infinite).  INT4: by the rule of
+ *                  mla_quantize_kv_int4
  * A token whose row lies outside the block table, or whose page is not in [0, num_pages), is not
  * written and sets MLA_ERR_INVALID_ARG in the device error word.
  */
@@ -457,6 +488,47 @@ int32_t mla_append_served_kv(const mla_pool_params* p, int64_t max_tokens, const
                              const void* k_rope, int64_t rope_stride, const int32_t* cu_seqlens,
                              const int32_t* cache_seqlens, const int32_t* block_table, const int32_t* served,
                              void* kv_pages, void* stream);
+
+/*
+ * The append as a model's layer has its rows: unrotated, and not yet normed.  In one launch, for every new token t
+ * at its position pos,
+ *     row   = [ c | rotate(k_rope[t], pos) ],  c = latent[t], or with norm_weight
+ *             c = bf16(latent[t] / sqrt(mean(latent[t]^2) + norm_eps) * norm_weight)
+ *     q_out[t][h] = rotate(q_rope[t][h], pos)              for the num_heads query heads
+ * and the row goes into the cache as mla_append_kv would put it ("MLA inference: two computation paths and FlashMLA", section
+ * "Two equivalent paths": rotary positions on the 64 RoPE dims alone, which the cache holds rotated).  With the
+ * angles' cosines c_i and sines s_i, i = 0 .. 31, a pair (x, y) becomes (x c_i - y s_i, y c_i + x s_i); the arithmetic is
+ * float32, each result is rounded to bf16 once.
+ */
+typedef struct mla_rotate_params {
+  int64_t max_tokens;        /* rows of latent, k_rope, q_rope and q_out; those at or past cu_seqlens[B] are left as they are */
+  int64_t latent_stride;     /* elements between rows; >= 512, a multiple of 8 */
+  int64_t rope_stride;       /* of k_rope; >= 64, a multiple of 8 */
+  int64_t q_token_stride;    /* of q_rope, elements between tokens and between heads: multiples of 8; one head's 64 values are */
+  int64_t q_head_stride;     /*   contiguous (so the last dims of a [T][H][192] array will do) */
+  int32_t num_heads;         /* query heads to rotate, 0 .. 65535; 0: keys alone, q_rope and q_out are not used */
+  int32_t interleaved;       /* pairs: 0 = (i, i + 32), 1 = (2 i, 2 i + 1) */
+  int32_t max_positions;     /* rows of cos_sin (>= 1) */
+  float norm_eps;            /* finite, >= 0; not used without norm_weight */
+  int32_t reserved[4];       /* must be zero */
+} mla_rotate_params;
+
+/*
+ *   latent, k_rope   device bf16, rows as for mla_append_kv
+ *   norm_weight      device bf16 [512], or NULL: latent is stored as it is
+ *   cos_sin          device float32 [max_positions][64]: 32 cosines, then 32 sines, of each position
+ *   positions        device int32 [max_tokens], or NULL: a token's position is its row in its sequence, L_b - n_b + i
+ *   q_rope           device bf16 (strides above); q_out device bf16 [max_tokens][num_heads][64], contiguous: the q_rope input
+ *                    of mla_decode and mla_chunk_attend; may be q_rope itself where that is contiguous, not overlap it otherwise
+ *   cu_seqlens, cache_seqlens, block_table, kv_pages   as for mla_append_kv
+ *   served           device int32 [batch], or NULL: as for mla_append_served_kv; left-out tokens' queries are left as they are
+ * A token whose row lies outside the block table, whose page is not in [0, num_pages), or whose position is not in
+ * [0, max_positions) sets MLA_ERR_INVALID_ARG in the device error word; neither its row nor its queries are written.
+ */
+int32_t mla_append_rotated_kv(const mla_pool_params* p, const mla_rotate_params* r, const void* latent, const void* k_rope,
+                              const void* norm_weight, const float* cos_sin, const int32_t* positions, const void* q_rope,
+                              void* q_out, const int32_t* cu_seqlens, const int32_t* cache_seqlens, const int32_t* block_table,
+                              const int32_t* served, void* kv_pages, void* stream);
 
 /* Bytes of the device workspace of fork (of at most max_forks), reserve and compact.  Host only. */
 int32_t mla_pool_workspace_size(const mla_pool_params* p, int32_t max_forks, size_t* workspace_bytes);

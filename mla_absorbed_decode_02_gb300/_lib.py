@@ -15,7 +15,8 @@ import numpy as np
 (MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA, MLA_ERR_TIMEOUT, MLA_ERR_WORKSPACE,
  MLA_ERR_SCRATCH_LIMIT) = range(7)
 MLA_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
-MLA_KV_BF16, MLA_KV_FP8_E4M3 = 0, 1
+MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_INT4 = 0, 1, 2
+_ROW_BYTES = (1152, 656, 416)  # of a cached token, by format
 MLA_OUT_BF16, MLA_OUT_F32 = 0, 1
 SCHED_MAGIC = 0x4D4C4131
 
@@ -84,6 +85,13 @@ class MlaPoolParams(ctypes.Structure):
         return cls(batch, num_pages, page_size, max_pages_per_seq, kv_dtype, num_layers, layer_stride)
 
 
+class MlaRotateParams(ctypes.Structure):
+    _fields_ = [("max_tokens", ctypes.c_int64), ("latent_stride", ctypes.c_int64), ("rope_stride", ctypes.c_int64),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("num_heads", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("max_positions", ctypes.c_int32), ("norm_eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32 * 4)]
+
+
 def load_library():
     """Load the built library (raises if it has not been built)."""
     global _lib
@@ -100,6 +108,7 @@ def load_library():
         X = ctypes.POINTER(MlaExtendParams)
         C = ctypes.POINTER(MlaChunkParams)
         K = ctypes.POINTER(MlaPoolParams)
+        R = ctypes.POINTER(MlaRotateParams)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         sig = {
             "mla_get_workspace_size": ([P, ctypes.POINTER(sz), ctypes.POINTER(sz)], i32),
@@ -113,6 +122,9 @@ def load_library():
             "mla_wait_selftest": ([i32, vp], i32),
             "mla_decode_noalloc": ([P, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp], i32),
             "mla_quantize_kv_fp8": ([vp, vp, ctypes.c_int64, vp], i32),
+            "mla_quantize_kv_int4": ([vp, vp, ctypes.c_int64, vp], i32),
+            "mla_dequantize_kv": ([i32, vp, vp, ctypes.c_int64, vp], i32),
+            "mla_append_rotated_kv": ([K, R] + [vp] * 13, i32),
             "mla_quantize_q_fp8": ([vp, vp, vp, ctypes.c_int64, vp], i32),
             "mla_absorb_query": ([i32, i32, i32, vp, vp, vp, vp], i32),
             "mla_project_output": ([i32, i32, i32, vp, vp, vp, vp], i32),
@@ -254,6 +266,36 @@ def mla_quantize_kv_fp8(kv_bf16, kv_fp8, num_tokens: int, stream=None):
            "mla_quantize_kv_fp8")
 
 
+def _rows_of(call, t, name, num_tokens, row_bytes):
+    """Checks a buffer of rows one after another, on the current device."""
+    if t is None or not t.is_contiguous() or num_tokens < 0 or t.numel() * t.element_size() < num_tokens * row_bytes:
+        _refuse(f"{call}: {name}")
+
+
+def mla_quantize_kv_int4(kv_bf16, kv_int4, num_tokens: int, stream=None):
+    """bf16 cache rows [n, 576] -> 416-byte INT4 rows [n, 416] (codes, scales, RoPE)."""
+    _rows_of("mla_quantize_kv_int4", kv_bf16, "kv_bf16", num_tokens, 1152)
+    _rows_of("mla_quantize_kv_int4", kv_int4, "kv_int4", num_tokens, 416)
+    if num_tokens == 0:
+        return
+    _expect_device("mla_quantize_kv_int4", kv_bf16, kv_int4)
+    _check(load_library().mla_quantize_kv_int4(_ptr(kv_bf16), _ptr(kv_int4), int(num_tokens), _stream(stream)),
+           "mla_quantize_kv_int4")
+
+
+def mla_dequantize_kv(kv_dtype: int, kv_rows, kv_bf16, num_tokens: int, stream=None):
+    """Rows of a cache of any format (MLA_KV_*, a pool's pages hold them one after another) -> bf16 rows [n, 576]."""
+    if not 0 <= kv_dtype < 3:
+        _refuse("mla_dequantize_kv: kv_dtype")
+    _rows_of("mla_dequantize_kv", kv_rows, "kv_rows", num_tokens, _ROW_BYTES[kv_dtype])
+    _rows_of("mla_dequantize_kv", kv_bf16, "kv_bf16", num_tokens, 1152)
+    if num_tokens == 0:
+        return
+    _expect_device("mla_dequantize_kv", kv_rows, kv_bf16)
+    _check(load_library().mla_dequantize_kv(kv_dtype, _ptr(kv_rows), _ptr(kv_bf16), int(num_tokens), _stream(stream)),
+           "mla_dequantize_kv")
+
+
 def mla_quantize_q_fp8(q_nope_absorbed, q_rope, q_fp8, num_rows: int, stream=None):
     """Query rows for an FP8-QK decode: q~ bf16 [n, 512] and q^R bf16 [n, 64] -> 656-byte rows [n, 656]."""
     _check(load_library().mla_quantize_q_fp8(_ptr(q_nope_absorbed), _ptr(q_rope), _ptr(q_fp8), int(num_rows),
@@ -325,7 +367,7 @@ def _expect_device(call: str, first, *others):
 
 def _expect_pool(call: str, t, p, num_layers: int = 1, layer_stride: int = 0):
     """The pools' pages: large enough for the last layer's last page, rows not strided."""
-    pool = p.num_pages * (64 * 1152 if p.kv_dtype == MLA_KV_BF16 else 64 * 656)
+    pool = p.num_pages * 64 * (_ROW_BYTES[p.kv_dtype] if 0 <= p.kv_dtype < 3 else 1152)
     if (t is None or not t.is_contiguous()
             or t.numel() * t.element_size() < (num_layers - 1) * (layer_stride or pool) + pool):
         _refuse(call + ": kv_pages")
@@ -435,6 +477,77 @@ def mla_append_kv(p: MlaPoolParams, latent, k_rope, cu_seqlens, cache_seqlens, b
     _check(load_library().mla_append_kv(ctypes.byref(p), int(latent.shape[0]), latent.data_ptr(), ls, k_rope.data_ptr(), rs,
                                         cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(), kv_pages.data_ptr(),
                                         _stream(stream)), "mla_append_kv")
+
+
+def mla_rope_table(max_positions: int, theta: float = 10000.0, device="cuda"):
+    """The cosines and sines that mla_append_rotated_kv reads, float32 [max_positions, 64]: 32 cosines, then 32 sines, of
+    pos * theta ** (-i / 32).  The angles are taken in float64: in float32 those of far positions are off by hundredths."""
+    import torch
+    pos = torch.arange(max_positions, dtype=torch.float64, device=device)
+    angle = pos[:, None] * theta ** (-torch.arange(32, dtype=torch.float64, device=device) / 32.0)
+    return torch.cat([angle.cos(), angle.sin()], -1).float()
+
+
+def mla_append_rotated_kv(p: MlaPoolParams, latent, k_rope, cos_sin, cu_seqlens, cache_seqlens, block_table, kv_pages,
+                          q_rope=None, q_out=None, positions=None, norm_weight=None, norm_eps: float = 1e-6,
+                          interleaved: bool = False, served=None, stream=None):
+    """mla_append_kv of rows as a model's layer has them: latent bf16 [T, 512] normed on the way where norm_weight (bf16 [512])
+    is given, k_rope bf16 [T, 64] rotated by cos_sin (float32 [positions, 64], mla_rope_table), and the queries' q_rope
+    bf16 [T, H, 64] (heads and tokens may be strided) rotated into q_out (bf16 [T, H, 64], made if not given).  A
+    token's position is its row in its sequence, or positions[t] (int32 [T]).  Returns q_out."""
+    i32, f32, bf16 = _dtypes()
+    B, call = p.batch, "mla_append_rotated_kv: "
+    for name, t, n in (("latent", latent, 512), ("k_rope", k_rope, 64)):
+        if t is None or t.dtype != bf16 or t.dim() != 2 or t.shape[1] != n or t.stride(1) != 1:
+            _refuse(call + name)
+    T = int(latent.shape[0])
+    if k_rope.shape[0] != T:
+        _refuse(call + "k_rope")
+    if cos_sin is None or cos_sin.dim() != 2 or _bad(cos_sin, f32, (cos_sin.shape[0], 64)) or cos_sin.shape[0] == 0:
+        _refuse(call + "cos_sin")
+    if _bad(cu_seqlens, i32, (B + 1,)):
+        _refuse(call + "cu_seqlens")
+    if _bad(cache_seqlens, i32, (B,)):
+        _refuse(call + "cache_seqlens")
+    if _bad(block_table, i32, (B, p.max_pages_per_seq)):
+        _refuse(call + "block_table")
+    if positions is not None and _bad(positions, i32, (T,)):
+        _refuse(call + "positions")
+    if norm_weight is not None and _bad(norm_weight, bf16, (512,)):
+        _refuse(call + "norm_weight")
+    if served is not None and _bad(served, i32, (B,)):
+        _refuse(call + "served")
+    H = 0
+    if q_rope is not None:
+        if q_rope.dtype != bf16 or q_rope.dim() != 3 or q_rope.shape[0] != T or q_rope.shape[2] != 64 or q_rope.stride(2) != 1:
+            _refuse(call + "q_rope")
+        H = int(q_rope.shape[1])
+        if q_out is None:
+            q_out = _new(q_rope, stream, (T, H, 64), bf16)
+        elif _bad(q_out, bf16, (T, H, 64)):
+            _refuse(call + "q_out")
+        # (read and written by the same threads where the two are one, by others where they merely overlap)
+        if T and H and not (q_out.data_ptr() == q_rope.data_ptr() and q_rope.is_contiguous()):
+            lo, out = q_rope.data_ptr(), q_out.data_ptr()
+            hi = lo + 2 * ((T - 1) * q_rope.stride(0) + (H - 1) * q_rope.stride(1) + 64)
+            if lo < out + q_out.numel() * 2 and out < hi:
+                _refuse(call + "q_out overlaps q_rope")
+    elif q_out is not None:
+        _refuse(call + "q_out without q_rope")
+    _expect_pool("mla_append_rotated_kv", kv_pages, p)
+    if T == 0:
+        return q_out
+    _expect_device("mla_append_rotated_kv", latent, k_rope, cos_sin, cu_seqlens, cache_seqlens, block_table, kv_pages,
+                   *(t for t in (positions, norm_weight, served, q_rope, q_out) if t is not None))
+    # (one row, or one head: its stride says nothing)
+    r = MlaRotateParams(T, int(latent.stride(0)) if T > 1 else 512, int(k_rope.stride(0)) if T > 1 else 64,
+                        int(q_rope.stride(0)) if H and T > 1 else 0, int(q_rope.stride(1)) if H > 1 else 0, H, int(bool(interleaved)),
+                        int(cos_sin.shape[0]), float(norm_eps))
+    _check(load_library().mla_append_rotated_kv(ctypes.byref(p), ctypes.byref(r), latent.data_ptr(), k_rope.data_ptr(), _ptr(norm_weight),
+                                                cos_sin.data_ptr(), _ptr(positions), _ptr(q_rope) if H else 0, _ptr(q_out) if H else 0,
+                                                cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(), _ptr(served),
+                                                kv_pages.data_ptr(), _stream(stream)), "mla_append_rotated_kv")
+    return q_out
 
 
 def mla_pool_workspace_size(p: MlaPoolParams, max_forks: int) -> int:

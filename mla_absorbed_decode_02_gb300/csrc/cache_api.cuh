@@ -19,6 +19,11 @@ int32_t launch_after(void* stream, dim3 grid, int threads, size_t smem, void (*k
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
+// Bytes of a cached token, 0 for what is no mla_kv_dtype.
+int kv_row_bytes(int32_t kv_dtype) {
+  return kv_dtype == MLA_KV_BF16 ? 1152 : kv_dtype == MLA_KV_FP8_E4M3 ? 656 : kv_dtype == MLA_KV_INT4 ? kI4Row : 0;
+}
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // ------------------------------------------------------------------ chunk attention
@@ -29,8 +34,8 @@ int32_t check_chunk(const mla_chunk_params* p) {
     return MLA_ERR_INVALID_ARG;
   for (int i = 0; i < 4; ++i)
     if (p->reserved[i] != 0) return MLA_ERR_INVALID_ARG;
-  if (p->kv_dtype != MLA_KV_BF16 && p->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
-  if (p->kv_dtype == MLA_KV_FP8_E4M3 && p->max_kv_tokens < 64) return MLA_ERR_INVALID_ARG;
+  if (kv_row_bytes(p->kv_dtype) == 0) return MLA_ERR_INVALID_ARG;
+  if (p->kv_dtype != MLA_KV_BF16 && p->max_kv_tokens < 64) return MLA_ERR_INVALID_ARG;
   if (p->page_size != 64 || p->num_heads > 128) return MLA_ERR_UNSUPPORTED;
   if ((int64_t)p->max_tokens * p->num_heads > INT32_MAX - 256 || (int64_t)p->num_pages * 64 > INT32_MAX ||
       p->max_kv_tokens > INT32_MAX - 64 || (int64_t)p->max_pages_per_seq * 64 > INT32_MAX - kChunkTile ||
@@ -64,13 +69,13 @@ ChunkBuffers chunk_buffers(const mla_chunk_params* p, int32_t U) {
   b.sched = sizeof(int32_t) * (size_t)chunk_layout(U, b.cap, p->batch).total;
   b.o_acc = (size_t)2 * U * kChunkRows * 512 * sizeof(float);
   b.lse_acc = (size_t)2 * U * kChunkRows * sizeof(float);
-  b.rows = p->kv_dtype == MLA_KV_FP8_E4M3 ? (size_t)(p->max_kv_tokens / 64) * 64 * 1152 : 0;
+  b.rows = p->kv_dtype != MLA_KV_BF16 ? (size_t)(p->max_kv_tokens / 64) * 64 * 1152 : 0;
   b.workspace = b.o_acc + align256(b.lse_acc) + b.rows;
   return b;
 }
 
 int64_t chunk_kv_pages(const mla_chunk_params* p) {  // pages a plan may name in all
-  return p->kv_dtype == MLA_KV_FP8_E4M3 ? p->max_kv_tokens / 64 : INT32_MAX;
+  return p->kv_dtype != MLA_KV_BF16 ? p->max_kv_tokens / 64 : INT32_MAX;
 }
 
 // ------------------------------------------------------------------ page pool
@@ -81,8 +86,8 @@ int32_t check_pool(const mla_pool_params* p) {
     return MLA_ERR_INVALID_ARG;
   for (int i = 0; i < 4; ++i)
     if (p->reserved[i] != 0) return MLA_ERR_INVALID_ARG;
-  if (p->kv_dtype != MLA_KV_BF16 && p->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
-  const int64_t packed = (int64_t)p->num_pages * 64 * (p->kv_dtype == MLA_KV_BF16 ? 1152 : 656);
+  if (kv_row_bytes(p->kv_dtype) == 0) return MLA_ERR_INVALID_ARG;
+  const int64_t packed = (int64_t)p->num_pages * 64 * kv_row_bytes(p->kv_dtype);
   if (p->layer_stride != 0 && (p->layer_stride < packed || p->layer_stride % 16 != 0)) return MLA_ERR_INVALID_ARG;
   if (p->page_size != 64) return MLA_ERR_UNSUPPORTED;
   if ((int64_t)p->num_pages * 64 > INT32_MAX || (int64_t)p->max_pages_per_seq * 64 > INT32_MAX || p->batch > (1 << 24) ||
@@ -97,7 +102,7 @@ PoolArgs pool_args(const mla_pool_params* p) {
   a.num_pages = p->num_pages;
   a.max_pages = p->max_pages_per_seq;
   a.num_layers = p->num_layers;
-  a.row_bytes = p->kv_dtype == MLA_KV_BF16 ? 1152 : 656;
+  a.row_bytes = kv_row_bytes(p->kv_dtype);
   a.layer_stride = p->layer_stride ? p->layer_stride : (int64_t)p->num_pages * 64 * a.row_bytes;
   return a;
 }
@@ -123,9 +128,9 @@ int32_t append_kv(const mla_pool_params* p, int64_t max_tokens, const void* late
   if (max_tokens == 0) return MLA_OK;
   const dim3 grid((unsigned)((max_tokens + 7) / 8));
   const __nv_bfloat16 *c = static_cast<const __nv_bfloat16*>(latent), *r = static_cast<const __nv_bfloat16*>(k_rope);
-  const bool fp8 = p->kv_dtype == MLA_KV_FP8_E4M3;
-  auto* kernel = served ? (fp8 ? mla_append_kernel<true, true> : mla_append_kernel<false, true>)
-                        : (fp8 ? mla_append_kernel<true, false> : mla_append_kernel<false, false>);
+  auto* kernel = p->kv_dtype == MLA_KV_INT4       ? (served ? mla_append_kernel<kKvInt4, true> : mla_append_kernel<kKvInt4, false>)
+                 : p->kv_dtype == MLA_KV_FP8_E4M3 ? (served ? mla_append_kernel<kKvFp8, true> : mla_append_kernel<kKvFp8, false>)
+                                                  : (served ? mla_append_kernel<kKvBf16, true> : mla_append_kernel<kKvBf16, false>);
   return launch_after(stream, grid, 256, 0, kernel, pool_args(p), max_tokens, c, latent_stride, r, rope_stride, cu_seqlens,
                       cache_seqlens, block_table, served, static_cast<uint8_t*>(kv_pages));
 }
@@ -204,7 +209,7 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
   const ChunkBuffers bufs = chunk_buffers(p, U);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int32_t* sc = static_cast<const int32_t*>(sched);
-  const bool fp8 = p->kv_dtype == MLA_KV_FP8_E4M3;
+  const bool expanded = p->kv_dtype != MLA_KV_BF16;
 
   ChunkArgs a;
   std::memset(&a, 0, sizeof a);
@@ -212,8 +217,8 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
   a.lse_acc = reinterpret_cast<float*>(ws + bufs.o_acc);
   void* rows = ws + bufs.o_acc + align256(bufs.lse_acc);
   const uint64_t q_rows = (uint64_t)p->max_tokens * p->num_heads;
-  const uint64_t kv_rows = fp8 ? (uint64_t)(p->max_kv_tokens / 64) * 64 : (uint64_t)p->num_pages * 64;
-  const void* kv = fp8 ? rows : kv_pages;
+  const uint64_t kv_rows = expanded ? (uint64_t)(p->max_kv_tokens / 64) * 64 : (uint64_t)p->num_pages * 64;
+  const void* kv = expanded ? rows : kv_pages;
   const uint32_t box2[2] = {64, 64}, box3[3] = {64, 64, 2}, boxq[3] = {64, 64, 8};
   {
     const uint64_t dq[3] = {64, q_rows, 8}, sq[2] = {1024, 128}, dr[2] = {64, q_rows}, sr[1] = {128};
@@ -233,11 +238,12 @@ int32_t mla_chunk_attend(const mla_chunk_params* p, const void* q_nope_absorbed,
   a.scale_log2 = scale * 1.4426950408889634f;
   a.key = {U, (int32_t)bufs.cap, p->batch, p->causal != 0, p->max_tokens, p->num_heads, p->max_pages_per_seq, (int32_t)chunk_kv_pages(p)};
   a.num_pages = p->num_pages;
-  a.expanded = fp8;
+  a.expanded = expanded;
   a.timeout_ns = (uint64_t)(p->timeout_us > 0 ? p->timeout_us : 2000000) * 1000ull;
-  if (fp8) {
+  if (expanded) {
     const int64_t pages = p->max_kv_tokens / 64, most = (int64_t)d->sm_count * 8;
-    if ((st = launch_after(stream, dim3((unsigned)(pages < most ? pages : most)), 256, 0, mla_chunk_expand_kernel, sc, a.key,
+    if ((st = launch_after(stream, dim3((unsigned)(pages < most ? pages : most)), 256, 0,
+                           p->kv_dtype == MLA_KV_INT4 ? mla_chunk_expand_kernel<kKvInt4> : mla_chunk_expand_kernel<kKvFp8>, sc, a.key,
                            static_cast<const uint8_t*>(kv_pages), block_table, p->num_pages, cache_seqlens, static_cast<__nv_bfloat16*>(rows))))
       return st;
   }
@@ -261,6 +267,89 @@ int32_t mla_append_served_kv(const mla_pool_params* p, int64_t max_tokens, const
   if (!served || !aligned(served, 4)) return MLA_ERR_INVALID_ARG;
   return append_kv(p, max_tokens, latent, latent_stride, k_rope, rope_stride, cu_seqlens, cache_seqlens, block_table, served,
                    kv_pages, stream);
+}
+
+int32_t mla_append_rotated_kv(const mla_pool_params* p, const mla_rotate_params* r, const void* latent, const void* k_rope,
+                              const void* norm_weight, const float* cos_sin, const int32_t* positions, const void* q_rope,
+                              void* q_out, const int32_t* cu_seqlens, const int32_t* cache_seqlens, const int32_t* block_table,
+                              const int32_t* served, void* kv_pages, void* stream) {
+  int32_t st = check_pool(p);
+  if (st != MLA_OK) return st;
+  if (!r || r->max_tokens < 0 || r->num_heads < 0 || r->max_positions < 1 || (r->interleaved != 0 && r->interleaved != 1))
+    return MLA_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (r->reserved[i] != 0) return MLA_ERR_INVALID_ARG;
+  if (!all_int_arrays({latent, k_rope, cos_sin, kv_pages}) || (norm_weight && !aligned16(norm_weight)) || !cu_seqlens ||
+      !cache_seqlens || !block_table || !aligned(cu_seqlens, 4) || !aligned(cache_seqlens, 4) || !aligned(block_table, 4) ||
+      !aligned(positions, 4) || !aligned(served, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (norm_weight && !(r->norm_eps >= 0.f && r->norm_eps < INFINITY)) return MLA_ERR_INVALID_ARG;
+  if (r->latent_stride < 512 || r->latent_stride % 8 != 0 || r->rope_stride < 64 || r->rope_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (r->num_heads > 0 && (!all_int_arrays({q_rope, q_out}) || r->q_token_stride % 8 != 0 || r->q_head_stride % 8 != 0 ||
+                           r->q_token_stride < 0 || r->q_head_stride < 0))
+    return MLA_ERR_INVALID_ARG;
+  if (r->max_tokens > INT32_MAX || r->num_heads > 65535) return MLA_ERR_UNSUPPORTED;
+  if (r->max_tokens == 0) return MLA_OK;
+  RotateArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.p = pool_args(p);
+  a.max_tokens = r->max_tokens;
+  a.latent_stride = r->latent_stride;
+  a.rope_stride = r->rope_stride;
+  a.q_token_stride = r->q_token_stride;
+  a.q_head_stride = r->q_head_stride;
+  a.latent = static_cast<const __nv_bfloat16*>(latent);
+  a.rope = static_cast<const __nv_bfloat16*>(k_rope);
+  a.weight = static_cast<const __nv_bfloat16*>(norm_weight);
+  a.q = static_cast<const __nv_bfloat16*>(q_rope);
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.cu = cu_seqlens;
+  a.lens = cache_seqlens;
+  a.block_table = block_table;
+  a.served = served;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.pages = static_cast<uint8_t*>(kv_pages);
+  a.eps = r->norm_eps;
+  a.heads = r->num_heads;
+  a.max_positions = r->max_positions;
+  a.warps = r->num_heads > 64 ? 4 : r->num_heads > 32 ? 2 : 1;
+  const dim3 grid((unsigned)((r->max_tokens * a.warps + 7) / 8));
+  const int pick = (served ? 1 : 0) + (r->interleaved ? 2 : 0);
+  using Kernel = void (*)(RotateArgs);
+#define MLA_ROTATE(F) {mla_append_rotated_kernel<F, false, false>, mla_append_rotated_kernel<F, true, false>, \
+                       mla_append_rotated_kernel<F, false, true>, mla_append_rotated_kernel<F, true, true>}
+  static const Kernel kernels[3][4] = {MLA_ROTATE(kKvBf16), MLA_ROTATE(kKvFp8), MLA_ROTATE(kKvInt4)};
+#undef MLA_ROTATE
+  return launch_after(stream, grid, 256, 0, kernels[p->kv_dtype][pick], a);
+}
+
+int32_t mla_quantize_kv_int4(const void* kv_bf16, void* kv_int4, int64_t num_tokens, void* stream) {
+  if (!kv_bf16 || !kv_int4 || num_tokens < 0 || !aligned16(kv_bf16) || !aligned16(kv_int4)) return MLA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return MLA_OK;
+  const int64_t blocks = (num_tokens + 7) / 8;
+  if (blocks > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  mla_quantize_int4_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const __nv_bfloat16*>(kv_bf16), static_cast<uint8_t*>(kv_int4), num_tokens);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int32_t mla_dequantize_kv(int32_t kv_dtype, const void* kv_rows, void* kv_bf16, int64_t num_tokens, void* stream) {
+  const int row = kv_row_bytes(kv_dtype);
+  if (row == 0 || !kv_rows || !kv_bf16 || num_tokens < 0 || !aligned16(kv_rows) || !aligned16(kv_bf16)) return MLA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return MLA_OK;
+  const int64_t blocks = (num_tokens + 7) / 8;
+  if (blocks > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (kv_dtype == MLA_KV_BF16)
+    return cudaMemcpyAsync(kv_bf16, kv_rows, (size_t)num_tokens * row, cudaMemcpyDeviceToDevice, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  const uint8_t* rows = static_cast<const uint8_t*>(kv_rows);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(kv_bf16);
+  if (kv_dtype == MLA_KV_FP8_E4M3)
+    mla_dequantize_kernel<kKvFp8><<<(unsigned)blocks, 256, 0, s>>>(rows, out, num_tokens);
+  else
+    mla_dequantize_kernel<kKvInt4><<<(unsigned)blocks, 256, 0, s>>>(rows, out, num_tokens);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int32_t mla_pool_workspace_size(const mla_pool_params* p, int32_t max_forks, size_t* workspace_bytes) {

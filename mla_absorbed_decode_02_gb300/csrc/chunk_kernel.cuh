@@ -44,6 +44,7 @@
 #include "chunk_plan.h"
 #include "common.cuh"
 #include "decode_kernel.cuh"  // packed float pairs, bf16 packing
+#include "int4_rows.cuh"
 
 namespace mla {
 
@@ -957,7 +958,38 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
   }
 }
 
-// ----------------------------------------------------------------- FP8 rows -> bf16 rows
+// ----------------------------------------------------------------- FP8 and INT4 rows -> bf16 rows
+// Formats of a cached token, as in mla_kv_dtype.
+enum : int { kKvBf16 = 0, kKvFp8 = 1, kKvInt4 = 2 };
+
+// A quantised row by a warp, 16 latent values a lane: bf16(code x scale), RoPE copied.
+template <int kFmt>
+__device__ __forceinline__ void expand_row(const uint8_t* src, __nv_bfloat16* dst, int lane) {
+  uint32_t o[8];
+  if constexpr (kFmt == kKvFp8) {
+    const uint4 c = *reinterpret_cast<const uint4*>(src + 16 * lane);
+    const float s = *reinterpret_cast<const float*>(src + 512 + 4 * (lane >> 3));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[q >> 1] >> (16 * (q & 1)));
+      const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3));  // exact
+      const float2 f = __half22float2(h);
+      o[q] = pack_bf16(f.x * s, f.y * s);
+    }
+  } else {
+    static_assert(kFmt == kKvInt4, "format");
+    const uint2 c = *reinterpret_cast<const uint2*>(src + 8 * lane);
+    const uint32_t s = *reinterpret_cast<const uint16_t*>(src + kI4Codes + (lane & ~1)), s2 = s | s << 16, a2 = int4_offset(s2);
+    expand_int4_word(c.x, s2, a2, reinterpret_cast<uint32_t(&)[4]>(o[0]));
+    expand_int4_word(c.y, s2, a2, reinterpret_cast<uint32_t(&)[4]>(o[4]));
+  }
+  uint4* d = reinterpret_cast<uint4*>(dst + 16 * lane);
+  d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  if (lane < 8) *reinterpret_cast<uint4*>(dst + 512 + 8 * lane) = *reinterpret_cast<const uint4*>(src + (kFmt == kKvFp8 ? 528 : kI4Rope) + 16 * lane);
+}
+
 // The pages of the sequences that have new tokens, expanded once per call into consecutive bf16
 // pages (sequence b's from page_off[b]): value = bf16(code x scale), RoPE copied.  A chunk's rows
 // read every cached row many times over, so 1808 bytes of traffic a cached token stand against
@@ -965,6 +997,7 @@ __global__ void __launch_bounds__(256) mla_chunk_combine_kernel(const int32_t* s
 // 63,900 rows in 26 us, 4.5 TB/s, 3% of the attention over them; two or eight rows of a warp in flight
 // instead of four, or half a page a block, changed nothing.  Where a row has one reader nothing pays for
 // it: 64 x 1 token x 16 heads over 8192 FP8 rows take 307 us, over bf16 rows 122.
+template <int kFmt>
 __global__ void __launch_bounds__(256) mla_chunk_expand_kernel(const int32_t* sched, ChunkKey key, const uint8_t* pages,
                                                                const int32_t* block_table, int num_pages, const int32_t* lens,
                                                                __nv_bfloat16* rows) {
@@ -985,23 +1018,8 @@ __global__ void __launch_bounds__(256) mla_chunk_expand_kernel(const int32_t* sc
     const int n = min(lens[b] - 64 * lp, 64);  // rows past the sequence's end are not expanded
 #pragma unroll 4
     for (int r = warp; r < n; r += 8) {
-      const uint8_t* src = pages + ((int64_t)page * 64 + r) * 656;
-      __nv_bfloat16* dst = rows + ((int64_t)pg * 64 + r) * 576;
-      const uint4 c = *reinterpret_cast<const uint4*>(src + 16 * lane);
-      const float s = *reinterpret_cast<const float*>(src + 512 + 4 * (lane >> 3));
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      uint32_t o[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[q >> 1] >> (16 * (q & 1)));
-        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3));  // exact
-        const float2 f = __half22float2(h);
-        o[q] = pack_bf16(f.x * s, f.y * s);
-      }
-      uint4* d = reinterpret_cast<uint4*>(dst + 16 * lane);
-      d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      if (lane < 8) *reinterpret_cast<uint4*>(dst + 512 + 8 * lane) = *reinterpret_cast<const uint4*>(src + 528 + 16 * lane);
+      constexpr int kRow = kFmt == kKvFp8 ? 656 : kI4Row;
+      expand_row<kFmt>(pages + ((int64_t)page * 64 + r) * kRow, rows + ((int64_t)pg * 64 + r) * 576, lane);
     }
   }
 }

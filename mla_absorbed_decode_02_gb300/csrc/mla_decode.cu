@@ -16,6 +16,7 @@
 #include "head_gemm.cuh"
 #include "extend_kernel.cuh"
 #include "chunk_kernel.cuh"
+#include "decode_int4.cuh"
 #include "pages.cuh"
 
 namespace mla {
@@ -230,6 +231,10 @@ int32_t device_info(DeviceInfo** out) {
                           (const void*)mla_decode_fp8qk_kernel})
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
         return MLA_ERR_CUDA;
+    if (cudaFuncSetAttribute(mla_decode_int4_n16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I4Smem<16>::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(mla_decode_int4_n32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I4Smem<32>::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(mla_decode_int4_n64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I4Smem<64>::kBytes) != cudaSuccess)
+      return MLA_ERR_CUDA;
     for (int G = 1; G <= 4; ++G) {  // GPCs hold whole clusters: bigger ones leave SMs idle
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * G * (d.sm_count / (2 * G)), 1, 1);
@@ -262,6 +267,23 @@ int32_t device_info(DeviceInfo** out) {
   return MLA_OK;
 }
 
+// New tokens per work block: the caller's token_group, else 1.  A group of G tokens reads each
+// page once instead of G times, but GPCs hold whole clusters: clusters of 4 CTAs fill 144 of
+// the 152 SMs, of 8 CTAs 120, so where the decode is bound by the SMs' work rather than by
+// DRAM (every s_q >= 2 workload measured) the per-token mode is the faster one.  On an INT4 cache the
+// tokens of a group are rows of one CTA and cost no more than one, so there it is as many as fit.
+int resolve_group(const mla_decode_params* p) {
+  if (p->token_group > 0) return p->token_group;
+  int G = 1;
+  if (p->kv_dtype == MLA_KV_INT4)
+    for (int g = 2; g <= p->s_q; ++g)
+      if (p->s_q % g == 0 && g * p->num_heads <= kI4MaxRows) G = g;
+  return G;
+}
+
+// INT4 cache: CTAs of a unit.
+int int4_parts(const mla_decode_params* p) { return p->num_heads > kI4MaxRows ? 2 : 1; }
+
 int32_t check_params(const mla_decode_params* p) {
   if (!p) return MLA_ERR_INVALID_ARG;
   if (p->batch < 1 || p->num_heads < 1 || p->num_pages < 1 || p->max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
@@ -271,19 +293,14 @@ int32_t check_params(const mla_decode_params* p) {
   if (p->qk_fp8 != 0 && (p->qk_fp8 != 1 || p->kv_dtype != MLA_KV_FP8_E4M3)) return MLA_ERR_INVALID_ARG;
   if (p->token_group < 0 || p->token_group > 4 || (p->token_group > 0 && p->s_q % p->token_group != 0))
     return MLA_ERR_INVALID_ARG;
-  if (p->kv_dtype != MLA_KV_BF16 && p->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (p->kv_dtype != MLA_KV_BF16 && p->kv_dtype != MLA_KV_FP8_E4M3 && p->kv_dtype != MLA_KV_INT4) return MLA_ERR_INVALID_ARG;
   if (p->out_dtype != MLA_OUT_BF16 && p->out_dtype != MLA_OUT_F32) return MLA_ERR_INVALID_ARG;
   if (p->page_size != 64 || p->s_q > 8 || p->num_heads > 128) return MLA_ERR_UNSUPPORTED;
   if ((int64_t)p->batch * p->s_q > (1 << 24) || (int64_t)p->num_pages * 64 > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if (p->qk_fp8 && p->token_group > 1) return MLA_ERR_UNSUPPORTED;
+  if (p->kv_dtype == MLA_KV_INT4 && p->token_group > 1 && p->token_group * p->num_heads > kI4MaxRows) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
-
-// New tokens per work block: the caller's token_group, else 1.  A group of G tokens reads each
-// page once instead of G times, but GPCs hold whole clusters: clusters of 4 CTAs fill 144 of
-// the 152 SMs, of 8 CTAs 120, so where the decode is bound by the SMs' work rather than by
-// DRAM (every s_q >= 2 workload measured) the per-token mode is the faster one.
-int resolve_group(const mla_decode_params* p) { return p->token_group > 0 ? p->token_group : 1; }
 
 int32_t resolve_units(const mla_decode_params* p, int32_t* U) {
   if (p->num_units > 0) {
@@ -293,7 +310,7 @@ int32_t resolve_units(const mla_decode_params* p, int32_t* U) {
   DeviceInfo* d = nullptr;
   int32_t st = device_info(&d);
   if (st != MLA_OK) return st;
-  *U = d->max_clusters[resolve_group(p)];
+  *U = p->kv_dtype == MLA_KV_INT4 ? d->sm_count / int4_parts(p) : d->max_clusters[resolve_group(p)];
   return MLA_OK;
 }
 
@@ -411,6 +428,59 @@ int32_t tensor_maps(const MapKey& k, DecodeArgs* a) {
   return MLA_OK;
 }
 
+// The decode kernel of an INT4 cache (arguments checked).
+int32_t launch_int4(const mla_decode_params* p, int32_t U, const void* q_nope, const void* q_rope, const void* kv_pages,
+                    const int32_t* block_table, const int32_t* cache_seqlens, float scale, void* out, float* lse,
+                    const void* sched, void* workspace, void* stream) {
+  const int H = p->num_heads, NQB = p->batch * p->s_q, G = resolve_group(p), parts = int4_parts(p);
+  const size_t slots = partial_slots(p, U);
+  Int4Args a;
+  std::memset(&a, 0, sizeof a);
+  a.parts = parts;
+  a.part_rows = parts > 1 ? (H + 1) / 2 : G * H;
+  const int N = a.part_rows <= 16 ? 16 : a.part_rows <= 32 ? 32 : 64;
+  const uint64_t rows = (uint64_t)NQB * H;
+  const uint64_t dq[3] = {64, rows, 8}, sq[2] = {1024, 128}, dr[2] = {64, rows}, sr[1] = {128};
+  const uint32_t bq[3] = {64, (uint32_t)N, 8}, br[2] = {64, (uint32_t)N};
+  int32_t st;
+  if ((st = encode_map(&a.map_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_nope, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      (st = encode_map(&a.map_qr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_rope, dr, sr, br, CU_TENSOR_MAP_SWIZZLE_128B)))
+    return st;
+  a.kv = static_cast<const uint8_t*>(kv_pages);
+  a.block_table = block_table;
+  a.seqlens = cache_seqlens;
+  a.sched = static_cast<const int32_t*>(sched);
+  a.out = out;
+  a.lse = lse;
+  a.o_acc = static_cast<float*>(workspace);
+  a.lse_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(slots * H * 512 * sizeof(float)));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.H = H;
+  a.s_q = p->s_q;
+  a.causal = p->causal != 0;
+  a.max_pages = p->max_pages_per_seq;
+  a.num_pages = p->num_pages;
+  a.out_f32 = p->out_dtype == MLA_OUT_F32;
+  a.num_units = U;
+  a.num_qb = NQB;
+  a.group = G;
+  a.timeout_ns = (uint64_t)(p->timeout_us > 0 ? p->timeout_us : 2000000) * 1000ull;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(parts * U, 1, 1);
+  cfg.blockDim = dim3(kI4Threads, 1, 1);
+  cfg.dynamicSmemBytes = N == 16 ? I4Smem<16>::kBytes : N == 32 ? I4Smem<32>::kBytes : I4Smem<64>::kBytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = N == 16   ? cudaLaunchKernelEx(&cfg, mla_decode_int4_n16_kernel, a)
+                        : N == 32 ? cudaLaunchKernelEx(&cfg, mla_decode_int4_n32_kernel, a)
+                                  : cudaLaunchKernelEx(&cfg, mla_decode_int4_n64_kernel, a);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -488,6 +558,8 @@ int32_t mla_decode_splitkv(const mla_decode_params* p, const void* q_nope_absorb
   if ((st = device_info(&dinfo)) != MLA_OK) return st;
   int32_t U = 0;
   if ((st = resolve_units(p, &U)) != MLA_OK) return st;
+  if (p->kv_dtype == MLA_KV_INT4)
+    return launch_int4(p, U, q_nope_absorbed, q_rope, kv_pages, block_table, cache_seqlens, scale, out, lse, sched, workspace, stream);
   const int H = p->num_heads, NQB = p->batch * p->s_q, G = resolve_group(p);
   const size_t slots = partial_slots(p, U);
 

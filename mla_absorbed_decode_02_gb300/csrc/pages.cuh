@@ -13,6 +13,7 @@
 #pragma once
 #include "chunk_kernel.cuh"  // block_scan_1024
 #include "common.cuh"
+#include "int4_rows.cuh"
 
 namespace mla {
 
@@ -80,27 +81,13 @@ __device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&
 
 // ----------------------------------------------------------------- append
 // Token t of the ragged buffer belongs to the sequence b with cu[b] <= t < cu[b + 1] and goes to
-// row L_b - n_b + (t - cu[b]) of that sequence.  A warp takes a token: its row is loaded first,
-// then the sequence is found by a 32-way search (one round for up to 31 sequences, two for up to
-// ~1000).  kServed: the tokens of a sequence that did not get its pages go nowhere -- its length is
-// still the old one, and row L_b - n_b one that it (or, in a shared page, another) holds; a kernel of
-// its own, since as a question at run time it cost the other 7%.  From a graph 64 rows in 1.9-2.2 us;
-// 22,500 rows quantised in 10.2-10.6 us, 3.9 TB/s (11.4 us with the divisions; 11.0-11.3 cold), as bf16 in 9.5 us,
-// 5.5 TB/s: the search and the launch are the rest.
-template <bool kFp8, bool kServed>
-__global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max_tokens, const __nv_bfloat16* latent,
-                                                         int64_t latent_stride, const __nv_bfloat16* rope,
-                                                         int64_t rope_stride, const int32_t* cu, const int32_t* lens,
-                                                         const int32_t* block_table, const int32_t* served, uint8_t* pages) {
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  pdl_wait_prerequisites();
-  pdl_launch_dependents();
-  if (t >= max_tokens) return;
-  const uint4* src = reinterpret_cast<const uint4*>(latent + t * latent_stride);
-  const uint4 a = src[kFp8 ? 2 * lane : lane], b = src[kFp8 ? 2 * lane + 1 : lane + 32];
-  uint4 kr = make_uint4(0, 0, 0, 0);
-  if (lane < 8) kr = *reinterpret_cast<const uint4*>(rope + t * rope_stride + 8 * lane);
+// row L_b - n_b + (t - cu[b]) of that sequence.  Called by a whole warp, which finds the sequence by a 32-way
+// search (one round for up to 31 sequences, two for up to ~1000).  False: the token lies behind the last sequence, or
+// (kServed) its sequence did not get its pages -- its length is still the old one, and row L_b - n_b one that it
+// (or, in a shared page, another) holds.  Else seq and pos, in the table or not.
+template <bool kServed>
+__device__ __forceinline__ bool find_token(const PoolArgs& p, int64_t t, const int32_t* cu, const int32_t* lens, const int32_t* served,
+                                           int lane, int& seq, int64_t& pos, bool& ok) {
   const int32_t end = cu[p.batch];
   int lo = 0, hi = p.batch;  // cu[lo] <= t < cu[hi]
   while (hi - lo > 31) {
@@ -114,37 +101,219 @@ __global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max
   const int32_t start = lo + lane <= p.batch ? cu[lo + lane] : INT32_MAX;
   const int32_t len = lo + lane < p.batch ? lens[lo + lane] : 0;
   const bool takes = kServed && lo + lane < p.batch && served[lo + lane] == kReserveDone;
-  if (t >= end) return;  // rows behind the last sequence
+  if (t >= end) return false;  // rows behind the last sequence
   const uint32_t le = __ballot_sync(0xffffffffu, lo + lane < hi && start <= t);
   const int k = le ? 31 - __clz(le) : 0;  // (at most 30: the next sequence's start is a lane's too)
-  if (kServed && !((__ballot_sync(0xffffffffu, takes) >> k) & 1)) return;
-  lo += k;
+  if (kServed && !((__ballot_sync(0xffffffffu, takes) >> k) & 1)) return false;
+  seq = lo + k;
   const int first = __shfl_sync(0xffffffffu, start, k), n = __shfl_sync(0xffffffffu, start, k + 1) - first;
-  const int64_t pos = (int64_t)__shfl_sync(0xffffffffu, len, k) - n + (t - first);
-  if (n < 0 || t < first || pos < 0 || pos >= (int64_t)p.max_pages * kPageRows) {
+  pos = (int64_t)__shfl_sync(0xffffffffu, len, k) - n + (t - first);
+  ok = n >= 0 && t >= first && pos >= 0 && pos < (int64_t)p.max_pages * kPageRows;
+  return true;
+}
+
+// 16 latent values of each lane (bf16 numbers) as codes and scales of a quantised row.
+template <int kFmt>
+__device__ __forceinline__ void write_codes(uint8_t* dst, int lane, const float (&x)[16]) {
+  if constexpr (kFmt == kKvFp8) {
+    float scale;
+    uint32_t c[4];
+    quantize_tile16<true>(x, c, scale);
+    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(c[0], c[1], c[2], c[3]);
+    if ((lane & 7) == 0) *reinterpret_cast<float*>(dst + 512 + 4 * (lane >> 3)) = scale;
+  } else {
+    static_assert(kFmt == kKvInt4, "format");
+    uint32_t c[2], scale;
+    quantize_int4_16(x, c, scale);
+    *reinterpret_cast<uint2*>(dst + 8 * lane) = make_uint2(c[0], c[1]);
+    if ((lane & 1) == 0) *reinterpret_cast<uint16_t*>(dst + kI4Codes + lane) = (uint16_t)scale;
+  }
+}
+template <int kFmt>
+constexpr int kRopeAt = kFmt == kKvBf16 ? 1024 : kFmt == kKvFp8 ? 528 : kI4Rope;
+
+// A warp takes a token: its row is loaded first, then its place found.  kServed is a kernel of its own, since as a question at
+// run time it cost the other 7%.  From a graph 64 rows in 1.9-2.2 us; 22,500 rows quantised in 10.2-10.6 us, 3.9 TB/s
+// (11.4 us with the divisions; 11.0-11.3 cold), as bf16 in 9.5 us, 5.5 TB/s: the search and the launch are the rest.
+template <int kFmt, bool kServed>
+__global__ void __launch_bounds__(256) mla_append_kernel(PoolArgs p, int64_t max_tokens, const __nv_bfloat16* latent,
+                                                         int64_t latent_stride, const __nv_bfloat16* rope,
+                                                         int64_t rope_stride, const int32_t* cu, const int32_t* lens,
+                                                         const int32_t* block_table, const int32_t* served, uint8_t* pages) {
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  if (t >= max_tokens) return;
+  const uint4* src = reinterpret_cast<const uint4*>(latent + t * latent_stride);
+  const uint4 a = src[kFmt != kKvBf16 ? 2 * lane : lane], b = src[kFmt != kKvBf16 ? 2 * lane + 1 : lane + 32];
+  uint4 kr = make_uint4(0, 0, 0, 0);
+  if (lane < 8) kr = *reinterpret_cast<const uint4*>(rope + t * rope_stride + 8 * lane);
+  int seq;
+  int64_t pos;
+  bool ok;
+  if (!find_token<kServed>(p, t, cu, lens, served, lane, seq, pos, ok)) return;
+  if (!ok) {
     if (lane == 0) pool_error(1);
     return;
   }
-  const int page = block_table[(int64_t)lo * p.max_pages + pos / kPageRows];
+  const int page = block_table[(int64_t)seq * p.max_pages + pos / kPageRows];
   if (page < 0 || page >= p.num_pages) {
     if (lane == 0) pool_error(1);
     return;
   }
   uint8_t* dst = pages + ((int64_t)page * kPageRows + pos % kPageRows) * p.row_bytes;
-  if (kFp8) {
-    float x[16], scale;
-    uint32_t c[4];
+  if constexpr (kFmt != kKvBf16) {
+    float x[16];
     widen16(a, b, x);
-    quantize_tile16<true>(x, c, scale);
-    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(c[0], c[1], c[2], c[3]);
-    if ((lane & 7) == 0) *reinterpret_cast<float*>(dst + 512 + 4 * (lane >> 3)) = scale;
-    if (lane < 8) *reinterpret_cast<uint4*>(dst + 528 + 16 * lane) = kr;
+    write_codes<kFmt>(dst, lane, x);
   } else {
     uint4* d = reinterpret_cast<uint4*>(dst);
     d[lane] = a;
     d[lane + 32] = b;
-    if (lane < 8) d[64 + lane] = kr;
   }
+  if (lane < 8) *reinterpret_cast<uint4*>(dst + kRopeAt<kFmt> + 16 * lane) = kr;
+}
+
+// ----------------------------------------------------------------- append of unrotated rows
+struct RotateArgs {
+  PoolArgs p;
+  int64_t max_tokens, latent_stride, rope_stride, q_token_stride, q_head_stride;
+  const __nv_bfloat16 *latent, *rope, *weight, *q;
+  const float* cos_sin;
+  const int32_t *positions, *cu, *lens, *block_table, *served;
+  __nv_bfloat16* q_out;
+  uint8_t* pages;
+  float eps;
+  int32_t heads, max_positions, warps;  // warps: of a token (1, 2, 4 or 8)
+};
+
+// Values 8 c .. 8 c + 7 (a) and 32 + 8 c .. 32 + 8 c + 7 (b) of a head, turned by their pairs' angles: cs holds the cosines and
+// sn the sines of the eight pairs that lie in a and b.
+__device__ __forceinline__ void rotate16(uint4& a, uint4& b, const float (&cs)[8], const float (&sn)[8], bool interleaved) {
+  float x[16];
+  widen16(a, b, x);
+  float y[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float u = interleaved ? x[2 * k] : x[k], v = interleaved ? x[2 * k + 1] : x[8 + k];
+    const float s = u * cs[k] - v * sn[k], t = v * cs[k] + u * sn[k];
+    if (interleaved) {
+      y[2 * k] = s;
+      y[2 * k + 1] = t;
+    } else {
+      y[k] = s;
+      y[8 + k] = t;
+    }
+  }
+  a = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+  b = make_uint4(pack_bf16(y[8], y[9]), pack_bf16(y[10], y[11]), pack_bf16(y[12], y[13]), pack_bf16(y[14], y[15]));
+}
+
+// `warps` warps take a token, each its share of the heads, the first one the row too.  Four lanes turn a head: lane c has
+// its values 8 c .. 8 c + 7 and 32 + 8 c .. (both pairings then lie within a lane), eight heads a warp at a time; their
+// angles are the same for every head.
+template <int kFmt, bool kServed, bool kInterleaved>
+__global__ void __launch_bounds__(256) mla_append_rotated_kernel(const __grid_constant__ RotateArgs g) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp & (g.warps - 1), c = lane & 3;
+  const int64_t t = (int64_t)blockIdx.x * (8 / g.warps) + warp / g.warps;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  if (t >= g.max_tokens) return;
+  uint4 a = make_uint4(0, 0, 0, 0), b = a, ra = a, rb = a;
+  if (share == 0) {
+    const uint4* src = reinterpret_cast<const uint4*>(g.latent + t * g.latent_stride);
+    a = src[2 * lane];
+    b = src[2 * lane + 1];
+    const uint4* r = reinterpret_cast<const uint4*>(g.rope + t * g.rope_stride);
+    ra = r[c];
+    rb = r[c + 4];
+  }
+  int seq;
+  int64_t row;
+  bool ok;
+  if (!find_token<kServed>(g.p, t, g.cu, g.lens, g.served, lane, seq, row, ok)) return;
+  const int64_t pos = g.positions ? g.positions[t] : row;
+  int page = -1;
+  if (ok) page = g.block_table[(int64_t)seq * g.p.max_pages + row / kPageRows];
+  if (!ok || page < 0 || page >= g.p.num_pages || pos < 0 || pos >= g.max_positions) {
+    if (lane == 0 && share == 0) pool_error(1);
+    return;
+  }
+  float cs[8], sn[8];
+  {
+    const float4* f = reinterpret_cast<const float4*>(g.cos_sin + pos * 64);
+    const int i0 = kInterleaved ? c : 2 * c, i1 = kInterleaved ? c + 4 : 2 * c + 1;
+    const float4 v[4] = {f[i0], f[i1], f[i0 + 8], f[i1 + 8]};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      cs[4 * k] = v[k].x; cs[4 * k + 1] = v[k].y; cs[4 * k + 2] = v[k].z; cs[4 * k + 3] = v[k].w;
+      sn[4 * k] = v[k + 2].x; sn[4 * k + 1] = v[k + 2].y; sn[4 * k + 2] = v[k + 2].z; sn[4 * k + 3] = v[k + 2].w;
+    }
+  }
+  if (share == 0) {
+    rotate16(ra, rb, cs, sn, kInterleaved);
+    if (g.weight) {
+      // float32 throughout, rounded to bf16 once: what a norm of its own would hand to the append
+      float x[16], w[16], sum = 0.f;
+      widen16(a, b, x);
+      const uint4* ws = reinterpret_cast<const uint4*>(g.weight);
+      widen16(ws[2 * lane], ws[2 * lane + 1], w);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) sum = fmaf(x[k], x[k], sum);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float inv = rsqrtf(sum * (1.f / 512.f) + g.eps);
+      uint32_t y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = pack_bf16(x[2 * k] * inv * w[2 * k], x[2 * k + 1] * inv * w[2 * k + 1]);
+      a = make_uint4(y[0], y[1], y[2], y[3]);
+      b = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+    uint8_t* dst = g.pages + ((int64_t)page * kPageRows + row % kPageRows) * g.p.row_bytes;
+    if constexpr (kFmt != kKvBf16) {
+      float x[16];
+      widen16(a, b, x);
+      write_codes<kFmt>(dst, lane, x);
+    } else {
+      reinterpret_cast<uint4*>(dst)[2 * lane] = a;
+      reinterpret_cast<uint4*>(dst)[2 * lane + 1] = b;
+    }
+    if (lane < 4) {
+      uint4* d = reinterpret_cast<uint4*>(dst + kRopeAt<kFmt>);
+      d[c] = ra;
+      d[c + 4] = rb;
+    }
+  }
+  const __nv_bfloat16* q = g.q + t * g.q_token_stride + 8 * c;
+  __nv_bfloat16* o = g.q_out + t * g.heads * 64 + 8 * c;
+#pragma unroll 2
+  for (int h = 8 * share + (lane >> 2); h < g.heads; h += 8 * g.warps) {
+    const __nv_bfloat16* src = q + h * g.q_head_stride;
+    uint4 x = *reinterpret_cast<const uint4*>(src), y = *reinterpret_cast<const uint4*>(src + 32);
+    rotate16(x, y, cs, sn, kInterleaved);
+    *reinterpret_cast<uint4*>(o + (int64_t)h * 64) = x;
+    *reinterpret_cast<uint4*>(o + (int64_t)h * 64 + 32) = y;
+  }
+}
+
+// ----------------------------------------------------------------- rows of any format
+// A warp takes a row.
+__global__ void __launch_bounds__(256) mla_quantize_int4_kernel(const __nv_bfloat16* kv, uint8_t* out, int64_t n) {
+  const int64_t tok = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (tok >= n) return;
+  const uint4* src = reinterpret_cast<const uint4*>(kv + tok * 576);
+  uint8_t* dst = out + tok * kI4Row;
+  float x[16];
+  widen16(src[2 * lane], src[2 * lane + 1], x);
+  write_codes<kKvInt4>(dst, lane, x);
+  if (lane < 8) *reinterpret_cast<uint4*>(dst + kI4Rope + 16 * lane) = src[64 + lane];
+}
+template <int kFmt>
+__global__ void __launch_bounds__(256) mla_dequantize_kernel(const uint8_t* rows, __nv_bfloat16* out, int64_t n) {
+  const int64_t tok = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (tok < n) expand_row<kFmt>(rows + tok * (kFmt == kKvFp8 ? 656 : kI4Row), out + tok * 576, threadIdx.x & 31);
 }
 
 // ----------------------------------------------------------------- moving bytes
