@@ -18,10 +18,10 @@
 // The quarters of a tile (128 dims, 32 KB) go through a ring of four slots (five up to 32 rows): a quarter is
 // expanded into its slot as soon as the output product of the tile before has left it.
 //
-// Roles (576 threads): warps 0..7 softmax (two warpgroups, half of the columns each; a thread holds one key, so a
+// Roles (five warpgroups): warps 0..7 softmax (two warpgroups, half of the columns each; a thread holds one key, so a
 // row's maximum lies across lanes: scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the
 // new maxima found and O rescaled); warps 8..15 read the pages into registers, a tile ahead, and expand them; warp 16
-// loads the queries; warp 17 issues the MMAs.
+// loads the queries; warp 17 issues the MMAs; two are idle and give their registers to the others.
 #pragma once
 #include "common.cuh"
 #include "decode_kernel.cuh"  // packed float pairs, bf16 packing, mma_bf16_ts
@@ -29,7 +29,7 @@
 
 namespace mla {
 
-constexpr int kI4Threads = 576;
+constexpr int kI4Threads = 640;
 constexpr int kI4MaxRows = 64;         // rows of a CTA
 constexpr int kI4Tile = 128;           // keys of a tile
 constexpr uint32_t kI4Blk = 16384;     // [128 keys][64 dims] bf16, 128-byte swizzle
@@ -39,6 +39,10 @@ template <int N>
 struct I4Smem {
   static constexpr int kSlots = N == 64 ? 4 : 5;
   static constexpr int kNc = N / 2;    // columns of a softmax warpgroup
+  // registers of a thread by warpgroup: 96 each at launch (65,536 over 640 threads), dealt out anew
+  static constexpr int kRegsSoftmax = N == 64 ? 112 : N == 32 ? 96 : 80, kRegsExpand = N == 64 ? 96 : N == 32 ? 104 : 112;
+  static constexpr int kRegsIssue = 480 - 2 * kRegsSoftmax - 2 * kRegsExpand;
+  static_assert(kRegsIssue >= 48 && kRegsIssue % 8 == 0, "registers");
   static constexpr uint32_t V = 0;
   static constexpr uint32_t Q = V + kSlots * kI4Slot;           // 9 blocks [N rows][64 dims]
   static constexpr uint32_t P = Q + 9 * N * 128;                // [128 keys][N]
@@ -59,7 +63,7 @@ enum : uint32_t {
   IB_Q_EMPTY,
   IB_S_FULL,                 // + tile parity
   IB_P_FULL = IB_S_FULL + 2, // one arrival per softmax warp
-  IB_PV,                     // the tile's output product is done
+  IB_PV,                     // a piece's last output product is done
   IB_FLAG,                   // + 2 warpgroup + tile parity: one arrival per warp
   IB_XCH = IB_FLAG + 4,      // + warpgroup
   IB_DRAIN = IB_XCH + 2,
@@ -189,11 +193,18 @@ __device__ __forceinline__ float reduce_columns(float (&v)[NC], int lane, Op op)
   return v[0];
 }
 
-__device__ __forceinline__ void ldg128(const uint8_t* p, uint32_t (&r)[4]) {
-  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p) : "memory");
+__device__ __forceinline__ void ldg128(const uint8_t* p, uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& w) {
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "l"(p) : "memory");
 }
-__device__ __forceinline__ void lds128f(uint32_t a, float (&r)[4]) {
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]) : "r"(a) : "memory");
+template <int kRegs>
+__device__ __forceinline__ void set_registers() {  // of a warpgroup; more than at launch once others have given theirs
+  if constexpr (kRegs > 96)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  else if constexpr (kRegs < 96)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+__device__ __forceinline__ void lds128f(uint32_t a, float& x, float& y, float& z, float& w) {
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x), "=f"(y), "=f"(z), "=f"(w) : "r"(a) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -204,6 +215,25 @@ __device__ __forceinline__ float lds32f(uint32_t a) {
   return v;
 }
 __device__ __forceinline__ void sts32f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+
+// The bounded waits of common.cuh in one piece: a warpgroup whose registers are dealt out anew makes no calls.
+__device__ __forceinline__ bool i4_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 31) == 0) {
+      if (*w.abort_local) return false;
+      if (globaltimer_ns() - t0 > w.timeout_ns) {
+        raise_abort(w, site);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool i4_wait_warp(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
+  return __all_sync(0xffffffffu, i4_wait(bar, parity, w, site));
+}
 
 template <int N>
 __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
@@ -261,116 +291,137 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
 
   if (idle) {
   } else if (warp >= 8 && warp < 16) {
+    set_registers<S::kRegsExpand>();
     // ================================================================ pages -> bf16
     // Codes: four lanes a key, 32 dims of a quarter each (16 bytes), the warp's keys 16 dw + lane / 4 (+ 8).  RoPE: a lane
-    // a key, half of its 64 values; they go to tensor memory as they are.
+    // a key, half of its 64 values; they go to tensor memory as they are.  A tile's bytes are asked for as the tile before
+    // is expanded, each into the registers that its bytes have left, and its pages a tile before that.
     const int dw = warp - 8, j = lane & 3, ckey = 16 * dw + (lane >> 2), cpage = dw >> 2;
     const int rkey = 32 * (warp & 3) + lane, rpage = (warp & 3) >> 1, rhalf = dw >> 2;
     const uint32_t rope_dst = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + TR + 16 * rhalf;
-    uint32_t code[8][4], scale[2][2], rope[4][4];
-    // physical page of the tile's page `which`; a page that the tile does not have reads as the first
-    auto page_of = [&](const I4Tile& r, int which) -> int {
+    uint32_t code[8][4], scale[4], rope[16];
+    // the table's entry for page `which` of a tile; a page that the tile does not have reads as the first
+    auto entry_of = [&](const I4Tile& r, int which) -> int {
       const int lp = (r.key0 >> 6) + (which < r.pages() ? which : 0);
-      int page = lp < args.max_pages ? args.block_table[(int64_t)r.seq * args.max_pages + lp] : -1;
+      return lp < args.max_pages ? args.block_table[(int64_t)r.seq * args.max_pages + lp] : -1;
+    };
+    auto row_of = [&](int page, int key) {
       if (page < 0 || page >= args.num_pages) {  // outside the contract: reported, another page read
         if (lane == 0) atomicCAS(&g_mla_error, 0, 1);
         page = 0;
       }
-      return page;
+      return args.kv + ((int64_t)page * 64 + (key & 63)) * kI4Row;
     };
-    auto row_of = [&](int page, int key) { return args.kv + ((int64_t)page * 64 + (key & 63)) * kI4Row; };
-    I4Tile a, n;
-    bool has = cur.next(a), ok = true;
-    {
-      const int pc = page_of(a, cpage), pr = page_of(a, rpage);
+    auto load_scales = [&](const uint8_t* src) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint8_t* src = row_of(pc, ckey + 8 * i);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) ldg128(src + 64 * m + 16 * j, code[2 * m + i]);
-        const uint2 s = *reinterpret_cast<const uint2*>(src + kI4Codes + 8 * j);
-        scale[i][0] = s.x;
-        scale[i][1] = s.y;
+        const uint2 v = *reinterpret_cast<const uint2*>(src + i * 8 * kI4Row + kI4Codes + 8 * j);
+        scale[2 * i] = v.x;
+        scale[2 * i + 1] = v.y;
       }
-      const uint8_t* src = row_of(pr, rkey) + kI4Rope + 64 * rhalf;
+    };
+    auto load_rope = [&](const uint8_t* src) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) ldg128(src + 16 * q, rope[q]);
-    }
-    uint32_t slot = 0, phase = 1;
-    for (uint32_t t = 0; ok && has; ++t) {
-      const bool has_n = cur.next(n);
-      const uint8_t *next_c = nullptr, *next_r = nullptr;
+      for (int q = 0; q < 4; ++q) ldg128(src + 16 * q, rope[4 * q], rope[4 * q + 1], rope[4 * q + 2], rope[4 * q + 3]);
+    };
+    I4Tile a, n, nn;
+    cur.next(a);
+    bool has_n = cur.next(n), ok = true;
+    int table_c = 0, table_r = 0;
+    {
+      const uint8_t* src = row_of(entry_of(a, cpage), ckey);
+      const uint8_t* src_r = row_of(entry_of(a, rpage), rkey) + kI4Rope + 64 * rhalf;
       if (has_n) {
-        next_c = row_of(page_of(n, cpage), ckey);
-        next_r = row_of(page_of(n, rpage), rkey) + kI4Rope + 64 * rhalf;
+        table_c = entry_of(n, cpage);
+        table_r = entry_of(n, rpage);
       }
-      const int some = a.vis - (args.causal ? args.group - 1 : 0) - a.key0;  // keys from here on are not seen by every token
-      uint32_t sc[2][2] = {{scale[0][0], scale[0][1]}, {scale[1][0], scale[1][1]}};
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (!(ok = wait_warp(bar(IB_EMPTY + slot), phase, wc, kSiteI4Ring))) break;
-        const uint32_t dst0 = base + S::V + slot * kI4Slot + (j >> 1) * kI4Blk;
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int key = ckey + 8 * i;
-          // the quad's lane m has the quarter's four scales
-          const uint32_t lo = __shfl_sync(0xffffffffu, sc[i][0], (lane & ~3) + m), hi = __shfl_sync(0xffffffffu, sc[i][1], (lane & ~3) + m);
-          uint32_t s2 = __byte_perm((j & 2) ? hi : lo, 0, (j & 1) ? 0x3232 : 0x1010);
-          if (key >= a.nkeys) {
-            s2 = 0;  // no key: the products must see zeros
-          } else if (key >= some && (s2 & 0x7F80u) == 0x7F80u) {
-            // a key that only some of the tokens see: its values must not reach the others (0 x NaN); the softmax
-            // gives NaN to those that see it
-            s2 = 0;
-            smem[S::POISON + 256 * (t & 1) + key] = smem[S::POISON + 256 * (t & 1) + 128 + key] = 1;
-          }
-          const uint32_t a2 = int4_offset(s2);
-          const uint32_t dst = dst0 + key * 128, x = (uint32_t)(4 * (j & 1)) ^ (uint32_t)(key & 7);
-          // lanes of the slot's second block write their chunks in another order, so that no two of a quad meet in a bank
           uint32_t (&w)[4] = code[2 * m + i];
-          const uint32_t turn = j & 2;
-          uint32_t v[4] = {turn ? w[2] : w[0], turn ? w[3] : w[1], turn ? w[0] : w[2], turn ? w[1] : w[3]};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[4];
-            expand_int4_word(v[q], s2, a2, o);
-            sts128(dst + ((x ^ (uint32_t)q ^ turn) << 4), o[0], o[1], o[2], o[3]);
-          }
-          if (has_n) ldg128(next_c + i * 8 * kI4Row + 64 * m + 16 * j, w);
+          ldg128(src + i * 8 * kI4Row + 64 * m + 16 * j, w[0], w[1], w[2], w[3]);
         }
-        if (m == 2) {  // (the scores of two tiles ago are done: this tile's first slot was waited for)
-          tmem_st_cols(rope_dst + 32 * (t & 1), reinterpret_cast<const uint32_t(&)[16]>(rope));
-          tmem_wait_st();
-          if (has_n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ldg128(next_r + 16 * q, rope[q]);
-        }
-        if (m == 0 && has_n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint2 s = *reinterpret_cast<const uint2*>(next_c + i * 8 * kI4Row + kI4Codes + 8 * j);
-            scale[i][0] = s.x;
-            scale[i][1] = s.y;
-          }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(IB_FULL + slot));
-        if (++slot == kSlots) {
-          slot = 0;
-          phase ^= 1;
+      load_scales(src);
+      load_rope(src_r);
+    }
+    uint32_t slot = 0, phase = 1;
+    for (uint32_t t = 0;; ++t) {
+      const uint8_t *next_c = nullptr, *next_r = nullptr;
+      const bool has_nn = has_n && cur.next(nn);
+      if (has_n) {
+        next_c = row_of(table_c, ckey);
+        next_r = row_of(table_r, rkey) + kI4Rope + 64 * rhalf;
+        if (has_nn) {
+          table_c = entry_of(nn, cpage);
+          table_r = entry_of(nn, rpage);
         }
       }
+      const int some = a.vis - (args.causal ? args.group - 1 : 0) - a.key0;  // keys from here on are not seen by every token
+      const uint32_t sc[4] = {scale[0], scale[1], scale[2], scale[3]};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        ok = ok && i4_wait_warp(bar(IB_EMPTY + slot), phase, wc, kSiteI4Ring);  // (the same in all lanes)
+        if (ok) {
+          const uint32_t dst0 = base + S::V + slot * kI4Slot + (j >> 1) * kI4Blk;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int key = ckey + 8 * i;
+            // the quad's lane m has the quarter's four scales
+            const uint32_t lo = __shfl_sync(0xffffffffu, sc[2 * i], (lane & ~3) + m), hi = __shfl_sync(0xffffffffu, sc[2 * i + 1], (lane & ~3) + m);
+            uint32_t s2 = __byte_perm((j & 2) ? hi : lo, 0, (j & 1) ? 0x3232 : 0x1010);
+            if (key >= a.nkeys) {
+              s2 = 0;  // no key: the products must see zeros
+            } else if (key >= some && (s2 & 0x7F80u) == 0x7F80u) {
+              // a key that only some of the tokens see: its values must not reach the others (0 x NaN); the softmax
+              // gives NaN to those that see it
+              s2 = 0;
+              smem[S::POISON + 256 * (t & 1) + key] = smem[S::POISON + 256 * (t & 1) + 128 + key] = 1;
+            }
+            const uint32_t a2 = int4_offset(s2);
+            const uint32_t dst = dst0 + key * 128, x = (uint32_t)(4 * (j & 1)) ^ (uint32_t)(key & 7);
+            // lanes of the slot's second block write their chunks in another order, so that no two of a quad meet in a bank
+            uint32_t (&w)[4] = code[2 * m + i];
+            const uint32_t turn = j & 2;
+            const uint32_t v[4] = {turn ? w[2] : w[0], turn ? w[3] : w[1], turn ? w[0] : w[2], turn ? w[1] : w[3]};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[4];
+              expand_int4_word(v[q], s2, a2, o);
+              sts128(dst + ((x ^ (uint32_t)q ^ turn) << 4), o[0], o[1], o[2], o[3]);
+            }
+            if (has_n) ldg128(next_c + i * 8 * kI4Row + 64 * m + 16 * j, w[0], w[1], w[2], w[3]);
+          }
+          if (m == 0 && has_n) load_scales(next_c);
+          if (m == 2) {  // (the scores of two tiles ago are done: this tile's first slot was waited for)
+            tmem_st_cols(rope_dst + 32 * (t & 1), rope);
+            tmem_wait_st();
+            if (has_n) load_rope(next_r);
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(IB_FULL + slot));
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok || !has_n) break;
       a = n;
-      has = has_n;
+      n = nn;
+      has_n = has_nn;
     }
-  } else if (warp == 16) {
+  } else if (warp >= 16) {
+    set_registers<S::kRegsIssue>();
+    if (warp == 16) {
     // ================================================================ queries
     I4Tile r;
     uint32_t piece = 0;
     const uint64_t keep = l2_policy_evict_last();
     while (cur.next(r)) {
-      if (piece > 0 && !wait_warp(bar(IB_Q_EMPTY), (piece - 1) & 1, wc, kSiteI4Q)) break;
+      if (piece > 0 && !i4_wait_warp(bar(IB_Q_EMPTY), (piece - 1) & 1, wc, kSiteI4Q)) break;
       if (lane == 0) {
         const int row = r.wb * block_rows + row0;
         mbar_arrive_expect_tx(bar(IB_Q_FULL), 9 * N * 128);
@@ -381,7 +432,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       ++piece;
       cur.skip_block();
     }
-  } else if (warp == 17) {
+    } else if (warp == 17) {
     // ================================================================ MMAs
     constexpr uint32_t id_qk = idesc_bf16_f32(128, N, 0, 0), id_pv = idesc_bf16_f32(128, N, 1, 1);
     const uint64_t desc_k = smem_desc(base + S::V, 16, 1024, kSwizzle128B), desc_q = smem_desc(base + S::Q, 16, 1024, kSwizzle128B);
@@ -393,7 +444,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     uint32_t slot = 0, phase = 0, pv_slot = 0, piece = 0;
     // Each lane waits for itself; lanes can part only where a wait runs out, and none waits for another before all have
     // left these loops.
-    auto wait = [&](uint32_t b, uint32_t parity, int site) -> bool { return wait_one(b, parity, wc, site); };
+    auto wait = [&](uint32_t b, uint32_t parity, int site) -> bool { return i4_wait(b, parity, wc, site); };
     auto qk_quarter = [&](const I4Tile& r, uint32_t t, int m) -> bool {
       if (m == 0 && r.first) {
         if (!wait(bar(IB_Q_FULL), piece & 1, kSiteI4Q)) return false;
@@ -438,7 +489,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         }
         if (++pv_slot == kSlots) pv_slot = 0;
       }
-      if (el) mma_commit(bar(IB_PV));
+      if (el && r.last) mma_commit(bar(IB_PV));
       return true;
     };
     I4Tile a, b;
@@ -468,18 +519,21 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     wd.timeout_ns = 100000000ull;
     volatile int no_abort = 0;
     wd.abort_local = &no_abort;
-    wait_warp(bar(IB_DRAIN), 0, wd, kSiteI4Drain);
+    i4_wait_warp(bar(IB_DRAIN), 0, wd, kSiteI4Drain);
+    }
   } else {
+    set_registers<S::kRegsSoftmax>();
     // ================================================================ softmax
     const int wg = warp >> 2, w = warp & 3, key = 32 * w + lane;
     const uint32_t lanes = (uint32_t)(32 * w) << 16;
+    constexpr int kC = NC < 16 ? NC : 16;               // columns at a time
     constexpr int kSpread = 32 / NC;                    // lanes that hold a column after reduce_columns
     const int mine = lane / kSpread, col0 = NC * wg;    // this lane's column of the warpgroup's
     const uint32_t mx = base + S::MAX + warp * NC * 4, fac = base + S::FAC + warp * NC * 4, xch = base + S::XCH + wg * 4 * NC * 4;
     const uint32_t prow = base + S::P + key * (2 * N);
     const uint32_t swz = N == 64 ? key & 7 : N == 32 ? (key >> 1) & 3 : (key >> 2) & 1;
     const float sl2 = args.scale_log2;
-    uint32_t slow = 0;
+    uint32_t exchanges = 0, piece = 0;
     float l[NC];
     bool ok = true;
     I4Tile a;
@@ -489,7 +543,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       if (lane % kSpread == 0) sts32f(at + (w * NC + mine) * 4, v);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(IB_XCH + wg));
-      return wait_warp(bar(IB_XCH + wg), slow++ & 1, wc, kSiteI4Flag);
+      return i4_wait_warp(bar(IB_XCH + wg), exchanges++ & 1, wc, kSiteI4Flag);
     };
     for (uint32_t t = 0; ok && cur.next(a); ++t) {
       if (a.first) {
@@ -498,7 +552,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         if (lane < NC) sts32f(mx + 4 * lane, -3.402823466e38f);  // (finite: a first score against it is no NaN)
         __syncwarp();
       }
-      if (!(ok = wait_warp(bar(IB_S_FULL + (t & 1)), (t >> 1) & 1, wc, kSiteI4Scores))) break;
+      if (!(ok = i4_wait_warp(bar(IB_S_FULL + (t & 1)), (t >> 1) & 1, wc, kSiteI4Scores))) break;
       tc_fence_after();
       const int some = a.vis - (args.causal ? args.group - 1 : 0) - a.key0;
       const bool masked = some < kI4Tile || a.nkeys < kI4Tile;
@@ -510,97 +564,113 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         bad = *poison != 0;
         if (bad) *poison = 0;
       }
-      auto load_scores = [&](float (&v)[NC]) {
-        uint32_t (&u)[NC] = reinterpret_cast<uint32_t(&)[NC]>(v);
-        tmem_ld_cols(tmem + lanes + TS + N * (t & 1) + col0, u);
+      // kC columns of scores from column c on
+      auto load_scores = [&](int c, float (&v)[kC]) {
+        uint32_t u[kC];
+        tmem_ld_cols(tmem + lanes + TS + N * (t & 1) + col0 + c, u);
         tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < kC; ++k) v[k] = __uint_as_float(u[k]);
         if (masked)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) u[c] = c < hidden ? 0xFF800000u : bad ? 0x7FC00000u : u[c];
+          for (int k = 0; k < kC; ++k) v[k] = c + k < hidden ? -INFINITY : bad ? __uint_as_float(0x7FC00000u) : v[k];
       };
-      float d[NC];
-      float top = -INFINITY;
       const uint64_t s2 = splat_f32x2(sl2);
-      auto scores = [&]() {  // against the maxima, in log2 units
-        load_scores(d);
+      auto scores = [&](int c, float (&v)[kC]) {  // against the maxima, in log2 units
+        load_scores(c, v);
 #pragma unroll
-        for (int q = 0; q < NC / 4; ++q) {
+        for (int q = 0; q < kC / 4; ++q) {
           float m4[4];
-          lds128f(mx + 16 * q, m4);
+          lds128f(mx + 4 * c + 16 * q, m4[0], m4[1], m4[2], m4[3]);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            unpack_f32x2(ffma_f32x2(pack_f32x2(d[4 * q + 2 * h], d[4 * q + 2 * h + 1]), s2, pack_f32x2(-m4[2 * h], -m4[2 * h + 1])),
-                         d[4 * q + 2 * h], d[4 * q + 2 * h + 1]);
+            unpack_f32x2(ffma_f32x2(pack_f32x2(v[4 * q + 2 * h], v[4 * q + 2 * h + 1]), s2, pack_f32x2(-m4[2 * h], -m4[2 * h + 1])),
+                         v[4 * q + 2 * h], v[4 * q + 2 * h + 1]);
         }
       };
-      scores();
+      float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NC; c += 2) top = fmax3(top, d[c], d[c + 1]);
+      for (int c = 0; c < NC; c += kC) {
+        float d[kC];
+        scores(c, d);
+#pragma unroll
+        for (int k = 0; k < kC; k += 2) top = fmax3(top, d[k], d[k + 1]);
+      }
       const bool over = __any_sync(0xffffffffu, top > 8.f);
       if (lane == 0) {
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + S::FLAG + 32 * (t & 1) + 4 * warp), "r"(over ? 1u : 0u) : "memory");
         mbar_arrive(bar(IB_FLAG + 2 * wg + (t & 1)));
       }
       __syncwarp();
-      if (!(ok = wait_warp(bar(IB_FLAG + 2 * wg + (t & 1)), (t >> 1) & 1, wc, kSiteI4Flag))) break;
+      if (!(ok = i4_wait_warp(bar(IB_FLAG + 2 * wg + (t & 1)), (t >> 1) & 1, wc, kSiteI4Flag))) break;
       float f4[4];
-      lds128f(base + S::FLAG + 32 * (t & 1) + 16 * wg, f4);
+      lds128f(base + S::FLAG + 32 * (t & 1) + 16 * wg, f4[0], f4[1], f4[2], f4[3]);
       const bool raise = (__float_as_uint(f4[0]) | __float_as_uint(f4[1]) | __float_as_uint(f4[2]) | __float_as_uint(f4[3])) != 0;
       if (raise) {
-        float v[NC];
-        load_scores(v);
+        float wm;
+        {
+          float v[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) v[c] *= sl2;
-        const float wm = reduce_columns<NC>(v, lane, [](float x, float y) { return fmaxf(x, y); });
+          for (int c = 0; c < NC; c += kC) {
+            float u[kC];
+            load_scores(c, u);
+#pragma unroll
+            for (int k = 0; k < kC; ++k) v[c + k] = u[k] * sl2;
+          }
+          wm = reduce_columns<NC>(v, lane, [](float x, float y) { return fmaxf(x, y); });
+        }
         if (!(ok = exchange(xch, wm))) break;
         float cm = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 4; ++k) cm = fmaxf(cm, lds32f(xch + (k * NC + mine) * 4));
         const float old = lds32f(mx + 4 * mine);
         const bool grow = cm > old + 8.f;
-        const float m_new = grow ? cm : old;
         __syncwarp();
         if (lane % kSpread == 0) {
-          sts32f(mx + 4 * mine, m_new);
+          sts32f(mx + 4 * mine, grow ? cm : old);
           sts32f(fac + 4 * mine, grow ? ex2_approx(old - cm) : 1.f);
         }
         __syncwarp();
-        scores();
-        if (!a.first) {
-          // the output so far, once the tile before has been added to it
-          if (!(ok = wait_warp(bar(IB_PV), (t - 1) & 1, wc, kSiteI4Pv))) break;
-          tc_fence_after();
-          float f[NC];
+        if (!a.first) {  // the output so far (the tile before has been added to it before this one's scores were done)
 #pragma unroll
-          for (int q = 0; q < NC / 4; ++q) lds128f(fac + 16 * q, *reinterpret_cast<float(*)[4]>(f + 4 * q));
+          for (int c = 0; c < NC; c += kC) {
+            float f[kC];
 #pragma unroll
-          for (int c = 0; c < NC; ++c) l[c] *= f[c];
+            for (int q = 0; q < kC / 4; ++q) lds128f(fac + 4 * c + 16 * q, f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+#pragma unroll
+            for (int k = 0; k < kC; ++k) l[c + k] *= f[k];
 #pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            uint32_t o[NC];
-            tmem_ld_cols(tmem + lanes + TO + N * m + col0, o);
-            tmem_wait_ld();
+            for (int m = 0; m < 4; ++m) {
+              uint32_t o[kC];
+              tmem_ld_cols(tmem + lanes + TO + N * m + col0 + c, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
-            tmem_st_cols(tmem + lanes + TO + N * m + col0, o);
+              for (int k = 0; k < kC; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[k]);
+              tmem_st_cols(tmem + lanes + TO + N * m + col0 + c, o);
+            }
           }
           tmem_wait_st();
         }
       }
-      uint32_t pp[NC / 2];
+      // (P is free: the output product of the tile before came before this tile's scores)
 #pragma unroll
-      for (int c = 0; c < NC; c += 2) {
-        const float p0 = ex2_approx(d[c]), p1 = ex2_approx(d[c + 1]);
-        // P in bf16, the type of the values in the tensor cores (half a step is 2^-8 of a weight at most, of either sign); the
-        // row's sum takes the float32 weights, so that lse is not rounded with them
-        pp[c / 2] = pack_bf16(p0, p1);
-        l[c] += p0;
-        l[c + 1] += p1;
+      for (int c = 0; c < NC; c += kC) {
+        float d[kC];
+        scores(c, d);
+        uint32_t pp[kC / 2];
+#pragma unroll
+        for (int k = 0; k < kC; k += 2) {
+          const float p0 = ex2_approx(d[k]), p1 = ex2_approx(d[k + 1]);
+          // P in bf16, the type of the values in the tensor cores (half a step is 2^-8 of a weight at most, of either sign); the
+          // row's sum takes the float32 weights, so that lse is not rounded with them
+          pp[k / 2] = pack_bf16(p0, p1);
+          l[c + k] += p0;
+          l[c + k + 1] += p1;
+        }
+#pragma unroll
+        for (int q = 0; q < kC / 8; ++q)
+          sts128(prow + (((uint32_t)((col0 + c) / 8 + q) ^ swz) << 4), pp[4 * q], pp[4 * q + 1], pp[4 * q + 2], pp[4 * q + 3]);
       }
-      if (t > 0 && !(ok = wait_warp(bar(IB_PV), (t - 1) & 1, wc, kSiteI4Pv))) break;  // P may be overwritten
-#pragma unroll
-      for (int q = 0; q < NC / 8; ++q)
-        sts128(prow + (((uint32_t)(wg * (NC / 8) + q) ^ swz) << 4), pp[4 * q], pp[4 * q + 1], pp[4 * q + 2], pp[4 * q + 3]);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -634,30 +704,33 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       }
       if (!on) row = -1;
       __syncwarp();
-      if (!(ok = wait_warp(bar(IB_PV), t & 1, wc, kSiteI4Pv))) break;
+      if (!(ok = i4_wait_warp(bar(IB_PV), piece++ & 1, wc, kSiteI4Pv))) break;
       tc_fence_after();
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
-        uint32_t o[NC];
-        tmem_ld_cols(tmem + lanes + TO + N * m + col0, o);
-        tmem_wait_ld();
-        float f[NC];
-#pragma unroll
-        for (int q = 0; q < NC / 4; ++q) lds128f(fac + 16 * q, *reinterpret_cast<float(*)[4]>(f + 4 * q));
         const int dim = 128 * m + 32 * w + lane;
 #pragma unroll
-        for (int c = 0; c < NC; c += 2) {
-          const float x0 = f[c] == 0.f ? 0.f : __uint_as_float(o[c]) * f[c], x1 = f[c + 1] == 0.f ? 0.f : __uint_as_float(o[c + 1]) * f[c + 1];
-          const int64_t r0 = __shfl_sync(0xffffffffu, row, c * kSpread), r1 = __shfl_sync(0xffffffffu, row, (c + 1) * kSpread);
-          if (split || args.out_f32) {
-            float* dst = split ? args.o_acc : static_cast<float*>(args.out);
-            if (r0 >= 0) dst[r0 * 512 + dim] = x0;
-            if (r1 >= 0) dst[r1 * 512 + dim] = x1;
-          } else {  // even lanes write two dims of the first row, odd lanes of the second
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
-            const int64_t to = (lane & 1) ? r1 : r0;
-            const uint32_t two = (lane & 1) ? pack_bf16(got, x1) : pack_bf16(x0, got);
-            if (to >= 0) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(args.out) + to * 512 + (dim & ~1)) = two;
+        for (int c = 0; c < NC; c += kC) {
+          uint32_t o[kC];
+          tmem_ld_cols(tmem + lanes + TO + N * m + col0 + c, o);
+          tmem_wait_ld();
+          float f[kC];
+#pragma unroll
+          for (int q = 0; q < kC / 4; ++q) lds128f(fac + 4 * c + 16 * q, f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+#pragma unroll
+          for (int k = 0; k < kC; k += 2) {
+            const float x0 = f[k] == 0.f ? 0.f : __uint_as_float(o[k]) * f[k], x1 = f[k + 1] == 0.f ? 0.f : __uint_as_float(o[k + 1]) * f[k + 1];
+            const int64_t r0 = __shfl_sync(0xffffffffu, row, (c + k) * kSpread), r1 = __shfl_sync(0xffffffffu, row, (c + k + 1) * kSpread);
+            if (split || args.out_f32) {
+              float* dst = split ? args.o_acc : static_cast<float*>(args.out);
+              if (r0 >= 0) dst[r0 * 512 + dim] = x0;
+              if (r1 >= 0) dst[r1 * 512 + dim] = x1;
+            } else {  // even lanes write two dims of the first row, odd lanes of the second
+              const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
+              const int64_t to = (lane & 1) ? r1 : r0;
+              const uint32_t two = (lane & 1) ? pack_bf16(got, x1) : pack_bf16(x0, got);
+              if (to >= 0) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(args.out) + to * 512 + (dim & ~1)) = two;
+            }
           }
         }
       }
