@@ -6,22 +6,30 @@
 // What bounds it: a key is 416 bytes and 2176 FLOP for each row (token and head) that reads it, so up to ~50 rows a key
 // HBM, beyond that the tensor cores; and a key's 512 values have to become bf16 in every SM that reads it.
 //
-// Work split.  The keys are the M dimension: S^T = K Q^T and O^T = C^T P^T.  A tile is 128 keys (two pages),
-// expanded once into shared memory as bf16, and that one copy is both products' A operand (K-major for the scores, MN-major for
-// the output), so a CTA needs no other's help: up to 64 rows are its N = 16, 32 or 64 columns, O^T is 4 x [128 dims x N]
-// in tensor memory.  A unit of the plan is one CTA, or two for 65 to 128 heads, which read the same pages at the
-// same time (the second from L2).  With several new tokens a sequence, as many as fit into 64 rows share every key.
+// Work split.  The keys are the M dimension: S^T = K Q^T and O^T = C^T P^T.  A tile is a page, 64 keys, expanded once
+// by a CTA that needs no other's help: up to 64 rows are its N = 16, 32 or 64 columns, O^T is 4 x [128 dims x N] in tensor
+// memory.  A unit of the plan is one CTA, or two for 65 to 128 heads, which read the same pages at the same time (the
+// second from L2).  With several new tokens a sequence, as many as fit into 64 rows share every key.
 //
-// MMA rates, M = 128, K = 16, cta_group::1: A from shared memory 39 / 40 / 48 cycles for N = 16 / 32 / 64 (4 KB of A and
-// 32 N bytes of B at 128 bytes a cycle, K- or MN-major alike, stores beside it cost nothing); A from tensor memory 12 / 17 / 32.
+// The scores' A operand, K [keys x 576], lies in tensor memory, the output's, C^T, in shared memory (MN-major, [64 keys][64
+// dims] blocks with the 128-byte swizzle): the expanding warps write both from the same registers.  MMA rates, M = 128, K = 16,
+// cta_group::1: A from shared memory 39 / 40 / 48 cycles for N = 16 / 32 / 64 (4 KB of A and 32 N bytes of B at 128 bytes a cycle,
+// K- or MN-major alike), from tensor memory 12 / 17 / 32.  With both products' A in shared memory its data path is what
+// runs out first.  Of the scores' 128 rows 64 are keys, lanes 0..15 of each of tensor memory's four quadrants (the 16-lane
+// loads and stores then keep every lane of a warp busy, four on a key); the others hold whatever was there.
 //
-// The quarters of a tile (128 dims, 32 KB) go through a ring of four slots (five up to 32 rows): a quarter is
-// expanded into its slot as soon as the output product of the tile before has left it.
+// Pages come by bulk copies into a ring in shared memory, as they are: loads into registers (64 bytes of a row at a time) kept
+// the load units busy for ~3000 cycles per 128 keys, which was more than everything else.  The four quarters of a tile (128 dims each)
+// are expanded by four warps each, into a ring of slots (16 KB each) in shared memory and of 64 columns each in tensor memory.
 //
-// Roles (five warpgroups): warps 0..7 softmax (two warpgroups, half of the columns each; a thread holds one key, so a
-// row's maximum lies across lanes: scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the
-// new maxima found and O rescaled); warps 8..15 read the pages into registers, a tile ahead, and expand them; warp 16
-// loads the queries; warp 17 issues the MMAs; two are idle and give their registers to the others.
+// Order of the values.  A lane expands 32 dims of a key, a quad of lanes a quarter, and the 16-lane stores deal a quad's words
+// out in turn: column 4 b + j of a quarter is word b of lane j.  So the scores run over the dims in that order, and the queries are
+// laid out in it when they are loaded.  The 16-lane loads deal the scores' columns out the same way: lane j of a quad has
+// rows 4 b + j, and its weights are neighbours in P, so that row 4 b + j of a warpgroup is column j NC / 4 + b of P and O^T.
+//
+// Roles (warps): softmax (one warpgroup, two for N = 64, half of the columns each; a row's maximum lies across lanes and
+// warps, so scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the new maxima found and O
+// rescaled); 16 warps expand; one copies the pages and writes the tiles' records, one issues the MMAs, two load the queries.
 #pragma once
 #include "common.cuh"
 #include "decode_kernel.cuh"  // packed float pairs, bf16 packing, mma_bf16_ts
@@ -29,54 +37,63 @@
 
 namespace mla {
 
-constexpr int kI4Threads = 640;
-constexpr int kI4MaxRows = 64;         // rows of a CTA
-constexpr int kI4Tile = 128;           // keys of a tile
-constexpr uint32_t kI4Blk = 16384;     // [128 keys][64 dims] bf16, 128-byte swizzle
+constexpr int kI4MaxRows = 64;           // rows of a CTA
+constexpr int kI4Tile = 64;              // keys of a tile
+constexpr int kI4Ahead = 8;              // tile records in shared memory
+constexpr uint32_t kI4Page = 64 * kI4Row;
+constexpr uint32_t kI4Blk = 8192;        // [64 keys][64 dims] bf16, 128-byte swizzle
 constexpr uint32_t kI4Slot = 2 * kI4Blk;
+static_assert(kI4Tile == kTile, "a tile of the plan is a page");
 
 template <int N>
 struct I4Smem {
-  static constexpr int kSlots = N == 64 ? 4 : 5;
-  static constexpr int kNc = N / 2;    // columns of a softmax warpgroup
-  // registers of a thread by warpgroup: 96 each at launch (65,536 over 640 threads), dealt out anew
-  static constexpr int kRegsSoftmax = N == 64 ? 112 : N == 32 ? 96 : 80, kRegsExpand = N == 64 ? 96 : N == 32 ? 104 : 112;
-  static constexpr int kRegsIssue = 480 - 2 * kRegsSoftmax - 2 * kRegsExpand;
-  static_assert(kRegsIssue >= 48 && kRegsIssue % 8 == 0, "registers");
+  static constexpr int kWg = N == 64 ? 2 : 1;                    // softmax warpgroups
+  static constexpr int kNc = N / kWg;                            // columns of each
+  static constexpr int kThreads = 128 * (kWg + 5);
+  static constexpr int kRaw = N == 64 ? 2 : 3;                   // pages as they came
+  static constexpr int kSlots = N == 64 ? 5 : N == 32 ? 6 : 7;   // quarters in shared memory
+  static constexpr int kA = N == 64 ? 2 : 4;                     // quarters in tensor memory
+  static constexpr int kS = N == 64 ? 1 : 2;                     // score buffers
   static constexpr uint32_t V = 0;
-  static constexpr uint32_t Q = V + kSlots * kI4Slot;           // 9 blocks [N rows][64 dims]
-  static constexpr uint32_t P = Q + 9 * N * 128;                // [128 keys][N]
-  static constexpr uint32_t FLAG = P + N * 256;                 // [tile parity][warp]: some score is far above the maximum
-  static constexpr uint32_t MAX = FLAG + 64;                    // [warp][kNc]: the running maxima, log2 units
-  static constexpr uint32_t FAC = MAX + 8 * kNc * 4;            // [warp][kNc]: factors of a rescale or of the output
-  static constexpr uint32_t XCH = FAC + 8 * kNc * 4;            // [maxima, sums][warpgroup][warp][kNc]
-  static constexpr uint32_t POISON = XCH + 16 * kNc * 4;        // [tile parity][warpgroup][128 keys]
-  static constexpr uint32_t BAR = POISON + 512;
-  static constexpr uint32_t kBytes = BAR + 256 + 1024;          // + alignment slack
+  static constexpr uint32_t Q = V + kSlots * kI4Slot;            // 9 blocks [N rows][64 dims]
+  static constexpr uint32_t P = Q + 9 * N * 128;                 // [64 keys][N]
+  static constexpr uint32_t RAW = P + N * 128;
+  static constexpr uint32_t FLAG = RAW + kRaw * kI4Page;         // [tile parity][warp]: some score is far above the maximum
+  static constexpr uint32_t MAX = FLAG + 64;                     // [warp][kNc]: the running maxima, log2 units
+  static constexpr uint32_t FAC = MAX + 4 * kWg * kNc * 4;       // [warp][kNc]: factors of a rescale or of the output
+  static constexpr uint32_t XCH = FAC + 4 * kWg * kNc * 4;       // [maxima, sums][warpgroup][warp][kNc]
+  static constexpr uint32_t POISON = XCH + 8 * kWg * kNc * 4;    // [tile parity][warpgroup][64 keys]
+  static constexpr uint32_t RING = POISON + 256;                 // kI4Ahead tile records of 32 bytes
+  static constexpr uint32_t BAR = RING + 32 * kI4Ahead;
+  static constexpr uint32_t kBytes = BAR + 512 + 1024;           // + alignment slack
   static_assert(kBytes <= 232448, "shared memory");
 };
 
 enum : uint32_t {
   IB_FULL = 0,               // + slot: one arrival per expanding warp
-  IB_EMPTY = IB_FULL + 5,    // + slot: the output product has read it
-  IB_Q_FULL = IB_EMPTY + 5,
+  IB_EMPTY = IB_FULL + 7,    // + slot: the output product has read it
+  IB_A_EMPTY = IB_EMPTY + 7, // + quarter of a tile: the scores' product has read it in tensor memory
+  IB_RAW = IB_A_EMPTY + 4,   // + page: landed
+  IB_RAW_EMPTY = IB_RAW + 3, // + page: one arrival per expanding warp
+  IB_Q_FULL = IB_RAW_EMPTY + 3,  // one arrival per loading warp
   IB_Q_EMPTY,
   IB_S_FULL,                 // + tile parity
   IB_P_FULL = IB_S_FULL + 2, // one arrival per softmax warp
   IB_PV,                     // a piece's last output product is done
   IB_FLAG,                   // + 2 warpgroup + tile parity: one arrival per warp
   IB_XCH = IB_FLAG + 4,      // + warpgroup
-  IB_DRAIN = IB_XCH + 2,
+  IB_TILE = IB_XCH + 2,      // + record: written
+  IB_TILE_READ = IB_TILE + kI4Ahead,  // + record: one arrival per softmax warp, the last readers
+  IB_DRAIN = IB_TILE_READ + kI4Ahead,
   kI4Bars
 };
 constexpr uint32_t kI4TmemSlot = 8 * kI4Bars, kI4Abort = kI4TmemSlot + 4;
-static_assert(kI4Abort + 4 <= 256, "barrier area");
+static_assert(kI4Abort + 4 <= 512, "barrier area");
 
-enum I4Site : int { kSiteI4Ring = 44, kSiteI4Q, kSiteI4Scores, kSiteI4P, kSiteI4Pv, kSiteI4Flag, kSiteI4Drain };
+enum I4Site : int { kSiteI4Ring = 44, kSiteI4Q, kSiteI4Scores, kSiteI4P, kSiteI4Pv, kSiteI4Flag, kSiteI4Drain, kSiteI4Tile, kSiteI4Raw };
 
 struct Int4Args {
-  CUtensorMap map_q;     // q~ rows: bf16 {64, rows, 8 blocks 128 bytes apart}, box {64, N, 8}, 128-byte swizzle
-  CUtensorMap map_qr;    // q^R rows: bf16 {64, rows}, box {64, N}
+  const __nv_bfloat16 *q_nope, *q_rope;
   const uint8_t* kv;
   const int32_t* block_table;
   const int32_t* seqlens;
@@ -91,11 +108,15 @@ struct Int4Args {
   uint64_t timeout_ns;
 };
 
+// A tile's record, as it lies in shared memory.
 struct I4Tile {
-  int wb, key0, nkeys;   // keys [key0, key0 + nkeys) are this tile's, nkeys <= 128
-  int seq, vis, split;   // vis: keys the block's last token sees
-  bool first, last;      // of the unit's piece of the block
-  __device__ int pages() const { return (nkeys + 63) >> 6; }
+  int flags, nkeys;      // the tile has keys 0 .. nkeys - 1 of the page
+  int some;              // keys of the tile that every token of the block sees (may lie outside 0 .. nkeys)
+  int wb, split;
+  enum { kValid = 1, kFirst = 2, kLast = 4 };  // first, last: of the unit's piece of the block
+  __device__ bool valid() const { return flags & kValid; }
+  __device__ bool first() const { return flags & kFirst; }
+  __device__ bool last() const { return flags & kLast; }
 };
 
 // Walks the unit's tiles in order, across blocks.
@@ -116,7 +137,7 @@ struct I4Cursor {
     t = end = 0;
   }
   __device__ bool next(I4Tile& r) {
-    r.first = false;
+    r.flags = 0;
     while (t >= end) {
       if (++wb > wb1) return false;
       const int qb = wb * G + G - 1;
@@ -124,84 +145,77 @@ struct I4Cursor {
       vis = visible_keys(seqlens[seq], s_q, qb % s_q, causal);
       t = wb == wb0 ? tile0 : 0;
       end = wb == wb1 ? tile1 : num_tiles(vis);
-      r.first = true;
+      r.flags = I4Tile::kFirst;
     }
     r.wb = wb;
-    r.seq = seq;
-    r.vis = vis;
     r.split = wb == wb0 ? split0 : 0;
-    r.key0 = kTile * t;
-    r.nkeys = min(min(vis, kTile * end) - kTile * t, kI4Tile);
-    t += 2;
-    r.last = t >= end;
+    r.nkeys = min(vis - kTile * t, kI4Tile);
+    r.some = vis - (causal ? G - 1 : 0) - kTile * t;
+    ++t;
+    r.flags |= I4Tile::kValid | (t >= end ? I4Tile::kLast : 0);
     return true;
   }
+  __device__ int page() const { return t - 1; }  // of the tile that next() gave
   __device__ void skip_block() { t = end; }
 };
 
-template <int NC>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[NC]) {
-  if constexpr (NC == 32) {
-    tmem_ld32(taddr, r);
-  } else if constexpr (NC == 16) {
-    tmem_ld16(taddr, r);
-  } else {
-    static_assert(NC == 8, "columns");
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+// 16 lanes x 16 columns of tensor memory and a warp: lane l has, in r[2 b + h], column 4 b + l % 4 of lane l / 4 + 8 h.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// The same for 2 K columns, K = 8 or 16 values a lane.
+template <int K>
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[K]) {
+  if constexpr (K == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr)
                  : "memory");
-  }
-}
-template <int NC>
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[NC]) {
-  if constexpr (NC == 32) {
-    tmem_st32(taddr, r);
-  } else if constexpr (NC == 16) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
   } else {
-    static_assert(NC == 8, "columns");
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+    static_assert(K == 16, "values");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
   }
 }
-
-// Reduces NC columns held by every lane over the 32 lanes; afterwards lane l has column l / (32 / NC).
-template <int NC, class Op>
-__device__ __forceinline__ float reduce_columns(float (&v)[NC], int lane, Op op) {
-  int n = NC;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    if (n > 1) {
-      n >>= 1;
-#pragma unroll
-      for (int k = 0; k < NC / 2; ++k)
-        if (k < n) {
-          const float send = (lane & o) ? v[k] : v[k + n], keep = (lane & o) ? v[k + n] : v[k];
-          v[k] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
-        }
-    } else {
-      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-    }
-  }
-  return v[0];
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Lane j of a quad has words r[0..3]; afterwards it has word j of the quad's lanes 0..3.
+__device__ __forceinline__ void quad_transpose(uint32_t (&r)[4], int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+  const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? r[0] : r[1], 1), y = __shfl_xor_sync(0xffffffffu, odd ? r[2] : r[3], 1);
+  const uint32_t b0 = odd ? x : r[0], b1 = odd ? r[1] : x, b2 = odd ? y : r[2], b3 = odd ? r[3] : y;
+  const uint32_t u = __shfl_xor_sync(0xffffffffu, high ? b0 : b2, 2), v = __shfl_xor_sync(0xffffffffu, high ? b1 : b3, 2);
+  r[0] = high ? u : b0;
+  r[1] = high ? v : b1;
+  r[2] = high ? b2 : u;
+  r[3] = high ? b3 : v;
 }
 
-__device__ __forceinline__ void ldg128(const uint8_t* p, uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& w) {
-  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "l"(p) : "memory");
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {  // multiples of 16
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
 }
-template <int kRegs>
-__device__ __forceinline__ void set_registers() {  // of a warpgroup; more than at launch once others have given theirs
-  if constexpr (kRegs > 96)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-  else if constexpr (kRegs < 96)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+__device__ __forceinline__ void lds128(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ void lds128f(uint32_t a, float& x, float& y, float& z, float& w) {
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x), "=f"(y), "=f"(z), "=f"(w) : "r"(a) : "memory");
@@ -216,31 +230,36 @@ __device__ __forceinline__ float lds32f(uint32_t a) {
 }
 __device__ __forceinline__ void sts32f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 
-// The bounded waits of common.cuh in one piece: a warpgroup whose registers are dealt out anew makes no calls.
-__device__ __forceinline__ bool i4_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 31) == 0) {
-      if (*w.abort_local) return false;
-      if (globaltimer_ns() - t0 > w.timeout_ns) {
+// The bounded waits of common.cuh in one piece; the timer is asked late, and rarely.
+__device__ __forceinline__ bool i4_wait_warp(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
+  bool ok = true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 255) == 0) {
+      if (*w.abort_local) {
+        ok = false;
+        break;
+      }
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > w.timeout_ns) {
         raise_abort(w, site);
-        return false;
+        ok = false;
+        break;
       }
     }
   }
-}
-__device__ __forceinline__ bool i4_wait_warp(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
-  return __all_sync(0xffffffffu, i4_wait(bar, parity, w, site));
+  return __all_sync(0xffffffffu, ok);
 }
 
 template <int N>
 __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   using S = I4Smem<N>;
-  constexpr int NC = S::kNc, kSlots = S::kSlots;
-  constexpr uint32_t TO = 0, TS = 4 * N, TR = 6 * N;  // tensor memory: O^T, two score buffers, two RoPE key buffers
-  static_assert(TR + 64 <= 512, "tensor memory");
+  constexpr int NC = S::kNc, B = NC / 4, kSlots = S::kSlots;  // B: columns of a lane
+  // tensor memory: O^T, score buffers, two buffers of the RoPE keys, the quarters of the latent keys
+  constexpr uint32_t TO = 0, TS = 4 * N, TR = TS + N * S::kS, TA = TR + 64;
+  static_assert(TA + 64 * S::kA <= 512, "tensor memory");
+  constexpr int kExpand = 4 * S::kWg, kIssue = kExpand + 16;  // first warps of the roles
   extern __shared__ uint8_t i4_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(i4_smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_addr(smem);
@@ -253,15 +272,18 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   if (tid == 0) {
     for (uint32_t i = 0; i < kI4Bars; ++i) {
       uint32_t count = 1;
-      if (i < IB_EMPTY || i == IB_P_FULL) count = 8;
-      if (i >= IB_FLAG && i < IB_DRAIN) count = 4;
+      if (i < IB_EMPTY) count = 4;
+      if (i >= IB_RAW_EMPTY && i < IB_Q_FULL) count = 16;
+      if (i == IB_Q_FULL) count = 2;
+      if (i == IB_P_FULL || (i >= IB_TILE_READ && i < IB_DRAIN)) count = 4 * S::kWg;
+      if (i >= IB_FLAG && i < IB_TILE) count = 4;
       mbar_init(bar(i), count);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (tid < 128) asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + S::POISON + 4 * tid), "r"(0u) : "memory");
-  if (warp == 17) {
+  if (tid < 64) asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + S::POISON + 4 * tid), "r"(0u) : "memory");
+  if (warp == kIssue + 1) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -270,10 +292,6 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (tid == 0) {
-    prefetch_tensormap(&args.map_q);
-    prefetch_tensormap(&args.map_qr);
-  }
   pdl_wait_prerequisites();
   const int32_t* sched = args.sched;
   const bool bad_meta = sched[0] != kSchedMagic || sched[1] != args.num_units || sched[2] != args.num_qb || sched[5] != args.group;
@@ -285,231 +303,269 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   wc.abort_local = abort_flag;
   wc.abort_peer = 0;
   wc.timeout_ns = args.timeout_ns;
-  I4Cursor cur;
-  if (!idle) cur.init(args, rec);
+  // the t-th tile's record
+  auto read_tile = [&](uint32_t t, I4Tile& r) -> bool {
+    const uint32_t at = base + S::RING + 32 * (t % kI4Ahead);
+    if (!i4_wait_warp(bar(IB_TILE + t % kI4Ahead), (t / kI4Ahead) & 1, wc, kSiteI4Tile)) return false;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.flags), "=r"(r.nkeys), "=r"(r.some), "=r"(r.wb) : "r"(at) : "memory");
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r.split) : "r"(at + 16) : "memory");
+    return true;
+  };
   const int block_rows = args.group * args.H, row0 = part * args.part_rows;
 
   if (idle) {
-  } else if (warp >= 8 && warp < 16) {
-    set_registers<S::kRegsExpand>();
+  } else if (warp >= kExpand && warp < kIssue) {
     // ================================================================ pages -> bf16
-    // Codes: four lanes a key, 32 dims of a quarter each (16 bytes), the warp's keys 16 dw + lane / 4 (+ 8).  RoPE: a lane
-    // a key, half of its 64 values; they go to tensor memory as they are.  A tile's bytes are asked for as the tile before
-    // is expanded, each into the registers that its bytes have left, and its pages a tile before that.
-    const int dw = warp - 8, j = lane & 3, ckey = 16 * dw + (lane >> 2), cpage = dw >> 2;
-    const int rkey = 32 * (warp & 3) + lane, rpage = (warp & 3) >> 1, rhalf = dw >> 2;
-    const uint32_t rope_dst = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + TR + 16 * rhalf;
-    uint32_t code[8][4], scale[4], rope[16];
-    // the table's entry for page `which` of a tile; a page that the tile does not have reads as the first
-    auto entry_of = [&](const I4Tile& r, int which) -> int {
-      const int lp = (r.key0 >> 6) + (which < r.pages() ? which : 0);
-      return lp < args.max_pages ? args.block_table[(int64_t)r.seq * args.max_pages + lp] : -1;
-    };
-    auto row_of = [&](int page, int key) {
+    // Four warps a quarter, 16 keys each: a quad has a key and, in the registers' other half, the key eight further; a lane 32 dims
+    // (16 bytes of codes).  Neighbouring quads take keys two apart: 416 bytes are 26 chunks of 16, so that the quads of an
+    // eight-lane phase read all eight bank groups.  (Row p of tensor memory's quadrant and of the slot is key perm(p).)
+    const int w = warp & 3, m = (warp - kExpand) >> 2, j = lane & 3, u = lane >> 2;
+    const int p0 = 16 * w + u, key0 = 16 * w + ((u & 4) | (u & 1) << 1 | (u & 2) >> 1);
+    const uint32_t tm = tmem + ((uint32_t)(32 * w) << 16);
+    constexpr uint32_t kNext = 8 * kI4Row;  // the second key
+    const uint32_t src_lane = base + S::RAW + key0 * kI4Row + 16 * j;
+    // chunk q of a lane's 32 dims in its slot; lanes of the slot's second block take their words in another order, so that no two
+    // of a quad meet in a bank
+    const uint32_t turn = j & 2;
+    uint32_t chunk[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      chunk[q] = base + S::V + (j >> 1) * kI4Blk + p0 * 128 + (((uint32_t)(4 * (j & 1)) ^ (uint32_t)(p0 & 7) ^ (uint32_t)q ^ turn) << 4);
+    // The quarter that had this one's columns of tensor memory before: quarter a_prev of the tile a_tiles ago.  A wait looks at a
+    // phase's parity alone, so it must come neither two phases early -- the tile before that is done, since the slot that is waited
+    // for first is free only after its output product -- nor two late: that quarter's next product comes after this one's.
+    static_assert(S::kA == 2 || S::kA == 4, "an earlier quarter of an earlier tile could be a phase further");
+    const int a_prev = (m + 4 - S::kA) & 3;
+    const uint32_t a_tiles = m >= S::kA ? 0 : 1;
+    uint32_t slot = m, phase = 1, as = m % S::kA, raw = 0, raw_phase = 0;
+    I4Tile a;
+    for (uint32_t t = 0; read_tile(t, a) && a.valid(); ++t) {
+      if (!i4_wait_warp(bar(IB_RAW + raw), raw_phase, wc, kSiteI4Raw)) break;
+      uint32_t code[2][4], s2[2], a2[2], rope[2][4];
+      const uint32_t src = src_lane + raw * kI4Page;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        lds128(src + i * kNext + 64 * m, code[i]);
+        s2[i] = lds16(src + i * kNext + kI4Codes + 8 * m - 14 * j);
+        if (m < 2) lds128(src + i * kNext + kI4Rope + 64 * m, rope[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s2[i] |= s2[i] << 16;
+        const int key = key0 + 8 * i;
+        if (key >= a.nkeys) {
+          s2[i] = 0;  // no key: the products must see zeros
+        } else if (key >= a.some && (s2[i] & 0x7F80u) == 0x7F80u) {
+          // a key that only some of the tokens see: its values must not reach the others (0 x NaN); the softmax
+          // gives NaN to those that see it
+          s2[i] = 0;
+          smem[S::POISON + 128 * (t & 1) + p0 + 8 * i] = smem[S::POISON + 128 * (t & 1) + 64 + p0 + 8 * i] = 1;
+        }
+        a2[i] = int4_offset(s2[i]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(IB_RAW_EMPTY + raw));
+      if (++raw == S::kRaw) {
+        raw = 0;
+        raw_phase ^= 1;
+      }
+      if (!i4_wait_warp(bar(IB_EMPTY + slot), phase, wc, kSiteI4Ring)) break;
+      if (t >= a_tiles && !i4_wait_warp(bar(IB_A_EMPTY + a_prev), (t - a_tiles) & 1, wc, kSiteI4Ring)) break;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[2][4], r[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          expand_int4_word(turn ? code[i][q ^ 2] : code[i][q], s2[i], a2[i], o[i]);
+          sts128(chunk[q] + slot * kI4Slot + i * 1024, o[i][0], o[i][1], o[i][2], o[i][3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[2 * k + i] = o[i][k];
+        }
+        tmem_st_16x16(tm + TA + 64 * as + 16 * q, r);
+      }
+      if (m < 2) {
+        // (this buffer's scores, of two tiles ago, are done: the slot that was waited for was read after them)
+        uint32_t r[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          r[2 * k] = rope[0][k];
+          r[2 * k + 1] = rope[1][k];
+        }
+        tmem_st_16x16(tm + TR + 32 * (t & 1) + 16 * m, r);
+      }
+      tmem_wait_st();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(IB_FULL + slot));
+      if ((slot += 4) >= kSlots) {
+        slot -= kSlots;
+        phase ^= 1;
+      }
+      as = (as + 4) % S::kA;
+    }
+  } else if (warp == kIssue) {
+    // ================================================================ pages and tile records
+    I4Cursor cur;
+    cur.init(args, rec);
+    I4Tile r;
+    bool more = true;
+    uint32_t raw = 0, raw_phase = 1;
+    for (uint32_t t = 0; more; ++t) {
+      more = cur.next(r);
+      int page = 0;
+      if (more) {
+        const int lp = cur.page();
+        page = lp < args.max_pages ? args.block_table[(int64_t)cur.seq * args.max_pages + lp] : -1;
+      }
+      if (t >= kI4Ahead && !i4_wait_warp(bar(IB_TILE_READ + t % kI4Ahead), (t / kI4Ahead - 1) & 1, wc, kSiteI4Tile)) break;
+      if (lane == 0) {
+        const uint32_t at = base + S::RING + 32 * (t % kI4Ahead);
+        sts128(at, r.flags, r.nkeys, r.some, r.wb);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 16), "r"(r.split) : "memory");
+        mbar_arrive(bar(IB_TILE + t % kI4Ahead));
+      }
+      __syncwarp();
+      if (!more) break;
       if (page < 0 || page >= args.num_pages) {  // outside the contract: reported, another page read
         if (lane == 0) atomicCAS(&g_mla_error, 0, 1);
         page = 0;
       }
-      return args.kv + ((int64_t)page * 64 + (key & 63)) * kI4Row;
-    };
-    auto load_scales = [&](const uint8_t* src) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint2 v = *reinterpret_cast<const uint2*>(src + i * 8 * kI4Row + kI4Codes + 8 * j);
-        scale[2 * i] = v.x;
-        scale[2 * i + 1] = v.y;
-      }
-    };
-    auto load_rope = [&](const uint8_t* src) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) ldg128(src + 16 * q, rope[4 * q], rope[4 * q + 1], rope[4 * q + 2], rope[4 * q + 3]);
-    };
-    I4Tile a, n, nn;
-    cur.next(a);
-    bool has_n = cur.next(n), ok = true;
-    int table_c = 0, table_r = 0;
-    {
-      const uint8_t* src = row_of(entry_of(a, cpage), ckey);
-      const uint8_t* src_r = row_of(entry_of(a, rpage), rkey) + kI4Rope + 64 * rhalf;
-      if (has_n) {
-        table_c = entry_of(n, cpage);
-        table_r = entry_of(n, rpage);
-      }
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t (&w)[4] = code[2 * m + i];
-          ldg128(src + i * 8 * kI4Row + 64 * m + 16 * j, w[0], w[1], w[2], w[3]);
-        }
-      load_scales(src);
-      load_rope(src_r);
-    }
-    uint32_t slot = 0, phase = 1;
-    for (uint32_t t = 0;; ++t) {
-      const uint8_t *next_c = nullptr, *next_r = nullptr;
-      const bool has_nn = has_n && cur.next(nn);
-      if (has_n) {
-        next_c = row_of(table_c, ckey);
-        next_r = row_of(table_r, rkey) + kI4Rope + 64 * rhalf;
-        if (has_nn) {
-          table_c = entry_of(nn, cpage);
-          table_r = entry_of(nn, rpage);
-        }
-      }
-      const int some = a.vis - (args.causal ? args.group - 1 : 0) - a.key0;  // keys from here on are not seen by every token
-      const uint32_t sc[4] = {scale[0], scale[1], scale[2], scale[3]};
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        ok = ok && i4_wait_warp(bar(IB_EMPTY + slot), phase, wc, kSiteI4Ring);  // (the same in all lanes)
-        if (ok) {
-          const uint32_t dst0 = base + S::V + slot * kI4Slot + (j >> 1) * kI4Blk;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int key = ckey + 8 * i;
-            // the quad's lane m has the quarter's four scales
-            const uint32_t lo = __shfl_sync(0xffffffffu, sc[2 * i], (lane & ~3) + m), hi = __shfl_sync(0xffffffffu, sc[2 * i + 1], (lane & ~3) + m);
-            uint32_t s2 = __byte_perm((j & 2) ? hi : lo, 0, (j & 1) ? 0x3232 : 0x1010);
-            if (key >= a.nkeys) {
-              s2 = 0;  // no key: the products must see zeros
-            } else if (key >= some && (s2 & 0x7F80u) == 0x7F80u) {
-              // a key that only some of the tokens see: its values must not reach the others (0 x NaN); the softmax
-              // gives NaN to those that see it
-              s2 = 0;
-              smem[S::POISON + 256 * (t & 1) + key] = smem[S::POISON + 256 * (t & 1) + 128 + key] = 1;
-            }
-            const uint32_t a2 = int4_offset(s2);
-            const uint32_t dst = dst0 + key * 128, x = (uint32_t)(4 * (j & 1)) ^ (uint32_t)(key & 7);
-            // lanes of the slot's second block write their chunks in another order, so that no two of a quad meet in a bank
-            uint32_t (&w)[4] = code[2 * m + i];
-            const uint32_t turn = j & 2;
-            const uint32_t v[4] = {turn ? w[2] : w[0], turn ? w[3] : w[1], turn ? w[0] : w[2], turn ? w[1] : w[3]};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t o[4];
-              expand_int4_word(v[q], s2, a2, o);
-              sts128(dst + ((x ^ (uint32_t)q ^ turn) << 4), o[0], o[1], o[2], o[3]);
-            }
-            if (has_n) ldg128(next_c + i * 8 * kI4Row + 64 * m + 16 * j, w[0], w[1], w[2], w[3]);
-          }
-          if (m == 0 && has_n) load_scales(next_c);
-          if (m == 2) {  // (the scores of two tiles ago are done: this tile's first slot was waited for)
-            tmem_st_cols(rope_dst + 32 * (t & 1), rope);
-            tmem_wait_st();
-            if (has_n) load_rope(next_r);
-          }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(IB_FULL + slot));
-          if (++slot == kSlots) {
-            slot = 0;
-            phase ^= 1;
-          }
-        }
-      }
-      if (!ok || !has_n) break;
-      a = n;
-      n = nn;
-      has_n = has_nn;
-    }
-  } else if (warp >= 16) {
-    set_registers<S::kRegsIssue>();
-    if (warp == 16) {
-    // ================================================================ queries
-    I4Tile r;
-    uint32_t piece = 0;
-    const uint64_t keep = l2_policy_evict_last();
-    while (cur.next(r)) {
-      if (piece > 0 && !i4_wait_warp(bar(IB_Q_EMPTY), (piece - 1) & 1, wc, kSiteI4Q)) break;
+      if (!i4_wait_warp(bar(IB_RAW_EMPTY + raw), raw_phase, wc, kSiteI4Raw)) break;
       if (lane == 0) {
-        const int row = r.wb * block_rows + row0;
-        mbar_arrive_expect_tx(bar(IB_Q_FULL), 9 * N * 128);
-        tma_load_3d(base + S::Q, &args.map_q, bar(IB_Q_FULL), 0, row, 0, keep);
-        tma_load_2d(base + S::Q + 8 * N * 128, &args.map_qr, bar(IB_Q_FULL), 0, row, keep);
+        mbar_arrive_expect_tx(bar(IB_RAW + raw), kI4Page);
+        bulk_load(base + S::RAW + raw * kI4Page, args.kv + (int64_t)page * kI4Page, kI4Page, bar(IB_RAW + raw));
       }
       __syncwarp();
+      if (++raw == S::kRaw) {
+        raw = 0;
+        raw_phase ^= 1;
+      }
+    }
+  } else if (warp > kIssue + 1) {
+    // ================================================================ queries
+    // Blocks of 64 values [N rows][128 bytes], 128-byte swizzle, the values in the order of the keys' tensor memory: chunk b of
+    // a quarter has word b of each of a quad's four lanes.  A quad takes four chunks.
+    const int loader = warp - kIssue - 2, j = lane & 3;
+    I4Cursor cur;
+    cur.init(args, rec);
+    I4Tile r;
+    uint32_t piece = 0;
+    while (cur.next(r)) {
+      if (piece > 0 && !i4_wait_warp(bar(IB_Q_EMPTY), (piece - 1) & 1, wc, kSiteI4Q)) break;
+      const int64_t first = (int64_t)r.wb * block_rows + row0;
+      const int rows = min(args.part_rows, block_rows - row0);
+#pragma unroll 6
+      for (int it = 8 * loader + (lane >> 2); it < 18 * N; it += 16) {  // (N is a multiple of 16: whole warps)
+        const int row = it / 18, u = it - 18 * row, m = u >> 2, q = u & 3;
+        const __nv_bfloat16* src = u < 16 ? args.q_nope + (first + row) * 512 + 128 * m + 32 * j + 8 * (q ^ (j & 2))
+                                          : args.q_rope + (first + row) * 64 + 32 * (u - 16) + 8 * j;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < rows) v = *reinterpret_cast<const uint4*>(src);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        quad_transpose(w, lane);
+        const int chunk = u < 16 ? 4 * q + j : 4 * (u - 16) + j;  // of the quarter's 16, of the RoPE block's 8
+        const int blk = u < 16 ? 2 * m + (chunk >> 3) : 8;
+        sts128(base + S::Q + blk * (N * 128) + row * 128 + (((uint32_t)chunk ^ (uint32_t)row) & 7) * 16, w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(IB_Q_FULL));
       ++piece;
       cur.skip_block();
     }
-    } else if (warp == 17) {
+  } else if (warp == kIssue + 1) {
     // ================================================================ MMAs
     constexpr uint32_t id_qk = idesc_bf16_f32(128, N, 0, 0), id_pv = idesc_bf16_f32(128, N, 1, 1);
-    const uint64_t desc_k = smem_desc(base + S::V, 16, 1024, kSwizzle128B), desc_q = smem_desc(base + S::Q, 16, 1024, kSwizzle128B);
-    const uint64_t desc_c = smem_desc(base + S::V, kI4Blk, 1024, kSwizzle128B);
-    const uint64_t desc_p = smem_desc(base + S::P, 16, N * 16, N == 64 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
+    // descriptors: an address 16 n bytes further is n more in the low word, the high words are constants
+    const uint64_t desc_q = smem_desc(0, 16, 1024, kSwizzle128B), desc_c = smem_desc(0, kI4Blk, 1024, kSwizzle128B);
+    const uint64_t desc_p = smem_desc(0, 16, N * 16, N == 64 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
+    const uint32_t at_q = (base + S::Q) >> 4, at_c = (base + S::V) >> 4, at_p = (base + S::P) >> 4;
+    auto at = [](uint64_t desc, uint32_t lo) { return desc | lo; };
     uint32_t el_;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el_));
     const bool el = el_ != 0;
-    uint32_t slot = 0, phase = 0, pv_slot = 0, piece = 0;
-    // Each lane waits for itself; lanes can part only where a wait runs out, and none waits for another before all have
-    // left these loops.
-    auto wait = [&](uint32_t b, uint32_t parity, int site) -> bool { return i4_wait(b, parity, wc, site); };
-    auto qk_quarter = [&](const I4Tile& r, uint32_t t, int m) -> bool {
-      if (m == 0 && r.first) {
+    uint32_t slot = 0, phase = 0, as = 0, pv_slot = 0, piece = 0;
+    auto wait = [&](uint32_t b, uint32_t parity, int site) -> bool { return i4_wait_warp(b, parity, wc, site); };
+    auto qk_quarter = [&](bool first, uint32_t t, int m) -> bool {
+      if (m == 0 && first) {
         if (!wait(bar(IB_Q_FULL), piece & 1, kSiteI4Q)) return false;
         ++piece;
       }
       if (!wait(bar(IB_FULL + slot), phase, kSiteI4Ring)) return false;
       tc_fence_after();
-      const uint32_t d = tmem + TS + N * (t & 1);
-      const uint64_t da = desc_k + slot * (kI4Slot >> 4), db = desc_q + m * (2 * N * 128 >> 4);
+      const uint32_t d = tmem + TS + N * (t % S::kS), a = tmem + TA + 64 * as;
+      const uint32_t lo = at_q + m * (2 * N * 128 >> 4);
       if (el) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_bf16_ss(d, da + (k >> 2) * (kI4Blk >> 4) + 2 * (k & 3), db + (k >> 2) * (N * 128 >> 4) + 2 * (k & 3), id_qk, m + k ? 1u : 0u);
+          mma_bf16_ts(d, a + 8 * k, at(desc_q, lo + (k >> 2) * (N * 128 >> 4) + 2 * (k & 3)), id_qk, m + k ? 1u : 0u);
+        mma_commit(bar(IB_A_EMPTY + m));
       }
       if (++slot == kSlots) {
         slot = 0;
         phase ^= 1;
       }
+      if (++as == S::kA) as = 0;
       return true;
     };
-    auto qk_rope = [&](const I4Tile& r, uint32_t t) {  // (the RoPE keys came with the last quarter)
+    auto qk_rope = [&](bool last, uint32_t t) {  // (the RoPE keys came with the first two quarters)
       if (el) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_bf16_ts(tmem + TS + N * (t & 1), tmem + TR + 32 * (t & 1) + 8 * k, desc_q + (8 * N * 128 >> 4) + 2 * k, id_qk, 1u);
+          mma_bf16_ts(tmem + TS + N * (t % S::kS), tmem + TR + 32 * (t & 1) + 8 * k, at(desc_q, at_q + (8 * N * 128 >> 4) + 2 * k), id_qk, 1u);
         mma_commit(bar(IB_S_FULL + (t & 1)));
-        if (r.last) mma_commit(bar(IB_Q_EMPTY));
+        if (last) mma_commit(bar(IB_Q_EMPTY));
       }
     };
-    auto pv = [&](const I4Tile& r, uint32_t t) -> bool {
-      if (!wait(bar(IB_P_FULL), t & 1, kSiteI4P)) return false;
+    auto pv = [&](bool first, bool last) {
       tc_fence_after();
-      const int steps = (r.nkeys + 15) >> 4;
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
-        const uint64_t da = desc_c + pv_slot * (kI4Slot >> 4);
+        const uint32_t lo = at_c + pv_slot * (kI4Slot >> 4);
         if (el) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < steps) mma_bf16_ss(tmem + TO + N * m, da + 128 * k, desc_p + (N * 32 >> 4) * k, id_pv, r.first && k == 0 ? 0u : 1u);
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ss(tmem + TO + N * m, at(desc_c, lo + 128 * k), at(desc_p, at_p + (N * 32 >> 4) * k), id_pv, first && k == 0 ? 0u : 1u);
           mma_commit(bar(IB_EMPTY + pv_slot));
         }
         if (++pv_slot == kSlots) pv_slot = 0;
       }
-      if (el && r.last) mma_commit(bar(IB_PV));
-      return true;
+      if (el && last) mma_commit(bar(IB_PV));
     };
-    I4Tile a, b;
-    cur.next(a);
-    bool ok = true;
-    for (int m = 0; ok && m < 4; ++m) ok = qk_quarter(a, 0, m);
-    if (ok) qk_rope(a, 0);
+    // (votes: what a record says is the same in all lanes, and known to be)
+    auto flag = [&](const I4Tile& r, int f) -> bool { return __any_sync(0xffffffffu, r.flags & f); };
+    I4Tile b;
+    bool ok = read_tile(0, b), first = true, last = false;
+    if (ok) last = flag(b, I4Tile::kLast);
+    for (int m = 0; ok && m < 4; ++m) ok = qk_quarter(true, 0, m);
+    if (ok) qk_rope(last, 0);
     for (uint32_t t = 0; ok; ++t) {
-      const bool more = cur.next(b);
-      // the spare slot's quarter before the output product: it runs beside the softmax (but not before a new query is there)
+      if (!(ok = read_tile(t + 1, b))) break;
+      const bool more = flag(b, I4Tile::kValid), b_first = flag(b, I4Tile::kFirst), b_last = flag(b, I4Tile::kLast);
+      // Beside the softmax run the next tile's quarters that the spare slots hold, as long as they are there first (not before a
+      // new query is, nor with one score buffer; and never all of a tile, so that a tile's scores come after the output product
+      // of the one before).
       int m = 0;
-      if (kSlots > 4 && more && !b.first) {
-        if (!(ok = qk_quarter(b, t + 1, 0))) break;
-        m = 1;
+      const int early = S::kS > 1 && more && !b_first ? kSlots - 4 : 0;
+      while (m < early) {
+        if (__any_sync(0xffffffffu, mbar_test_wait(bar(IB_P_FULL), t & 1))) break;
+        if (__any_sync(0xffffffffu, mbar_test_wait(bar(IB_FULL + slot), phase))) {
+          if (!(ok = qk_quarter(false, t + 1, m))) break;
+          ++m;
+        } else if (__any_sync(0xffffffffu, *abort_flag)) {  // (some other role's wait has run out)
+          ok = false;
+          break;
+        }
       }
-      if (!(ok = pv(a, t)) || !more) break;
-      for (; ok && m < 4; ++m) ok = qk_quarter(b, t + 1, m);
+      if (!ok || !(ok = wait(bar(IB_P_FULL), t & 1, kSiteI4P))) break;
+      pv(first, last);
+      if (!more) break;
+      for (; ok && m < 4; ++m) ok = qk_quarter(b_first, t + 1, m);
       if (!ok) break;
-      qk_rope(b, t + 1);
-      a = b;
+      qk_rope(b_last, t + 1);
+      first = b_first;
+      last = b_last;
     }
     __syncwarp();
     // no MMA may still run when the CTA leaves
@@ -520,82 +576,102 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     volatile int no_abort = 0;
     wd.abort_local = &no_abort;
     i4_wait_warp(bar(IB_DRAIN), 0, wd, kSiteI4Drain);
-    }
   } else {
-    set_registers<S::kRegsSoftmax>();
     // ================================================================ softmax
-    const int wg = warp >> 2, w = warp & 3, key = 32 * w + lane;
+    // A lane: rows (of the warpgroup's NC) 4 b + j, b < B, for the keys in places p0 and p0 + 8.  Arrays over rows are kept in the
+    // order of P's columns, j B + b.
+    const int wg = warp >> 2, w = warp & 3, j = lane & 3, u = lane >> 2, col0 = NC * wg;
+    const int p0 = 16 * w + u, key0 = 16 * w + ((u & 4) | (u & 1) << 1 | (u & 2) >> 1);
     const uint32_t lanes = (uint32_t)(32 * w) << 16;
-    constexpr int kC = NC < 16 ? NC : 16;               // columns at a time
-    constexpr int kSpread = 32 / NC;                    // lanes that hold a column after reduce_columns
-    const int mine = lane / kSpread, col0 = NC * wg;    // this lane's column of the warpgroup's
     const uint32_t mx = base + S::MAX + warp * NC * 4, fac = base + S::FAC + warp * NC * 4, xch = base + S::XCH + wg * 4 * NC * 4;
-    const uint32_t prow = base + S::P + key * (2 * N);
-    const uint32_t swz = N == 64 ? key & 7 : N == 32 ? (key >> 1) & 3 : (key >> 2) & 1;
+    constexpr uint32_t kSums = 4 * S::kWg * NC * 4;  // from the place of the maxima to that of the sums
     const float sl2 = args.scale_log2;
     uint32_t exchanges = 0, piece = 0;
-    float l[NC];
+    float l[B];
     bool ok = true;
     I4Tile a;
-    // the four warps' values of this lane's column, once all have written theirs (maxima and sums each in a place of their own:
-    // between two exchanges of a kind every warp has come past the flags, so that none still reads the one before)
-    auto exchange = [&](uint32_t at, float v) -> bool {
-      if (lane % kSpread == 0) sts32f(at + (w * NC + mine) * 4, v);
+    // reduces a lane's values over the quads, then over the warps: each lane has its columns' results.  (Maxima and sums each in a
+    // place of their own: between two exchanges of a kind every warp has come past the flags, so that none still reads the one before.)
+    auto exchange = [&](uint32_t at, float (&v)[B], bool sum) -> bool {
+      auto op = [sum](float x, float y) { return sum ? x + y : fmaxf(x, y); };
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v[b] = op(v[b], __shfl_xor_sync(0xffffffffu, v[b], o));
+      if (u == 0)
+#pragma unroll
+        for (int b = 0; b < B; ++b) sts32f(at + (w * NC + j * B + b) * 4, v[b]);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(IB_XCH + wg));
-      return i4_wait_warp(bar(IB_XCH + wg), exchanges++ & 1, wc, kSiteI4Flag);
-    };
-    for (uint32_t t = 0; ok && cur.next(a); ++t) {
-      if (a.first) {
+      if (!i4_wait_warp(bar(IB_XCH + wg), exchanges++ & 1, wc, kSiteI4Flag)) return false;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      for (int b = 0; b < B; ++b) {
+        const uint32_t c = at + (j * B + b) * 4;
+        v[b] = op(op(lds32f(c), lds32f(c + NC * 4)), op(lds32f(c + 2 * NC * 4), lds32f(c + 3 * NC * 4)));
+      }
+      return true;
+    };
+    for (uint32_t t = 0; (ok = read_tile(t, a)) && a.valid(); ++t) {
+      if (a.first()) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) l[b] = 0.f;
         if (lane < NC) sts32f(mx + 4 * lane, -3.402823466e38f);  // (finite: a first score against it is no NaN)
         __syncwarp();
       }
       if (!(ok = i4_wait_warp(bar(IB_S_FULL + (t & 1)), (t >> 1) & 1, wc, kSiteI4Scores))) break;
       tc_fence_after();
-      const int some = a.vis - (args.causal ? args.group - 1 : 0) - a.key0;
-      const bool masked = some < kI4Tile || a.nkeys < kI4Tile;
-      int hidden = 0;  // rows [0, hidden) of the warpgroup's columns do not see this key
-      bool bad = false;
-      if (masked) {
-        hidden = (key >= a.nkeys ? 1 << 20 : args.causal ? max(key - some + 1, 0) * args.H : 0) - row0 - col0;
-        uint8_t* poison = smem + S::POISON + 256 * (t & 1) + 128 * wg + key;
-        bad = *poison != 0;
-        if (bad) *poison = 0;
-      }
-      // kC columns of scores from column c on
-      auto load_scores = [&](int c, float (&v)[kC]) {
-        uint32_t u[kC];
-        tmem_ld_cols(tmem + lanes + TS + N * (t & 1) + col0 + c, u);
+      if (lane == 0) mbar_arrive(bar(IB_TILE_READ + t % kI4Ahead));
+      float d[2][B];
+      auto load_scores = [&]() {
+        uint32_t v[2 * B];
+        tmem_ld_16(tmem + lanes + TS + N * (t % S::kS) + col0, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < kC; ++k) v[k] = __uint_as_float(u[k]);
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) d[i][b] = __uint_as_float(v[2 * b + i]);
+      };
+      int hidden[2] = {0, 0};  // rows [0, hidden) of the warpgroup's do not see the key
+      bool bad[2] = {false, false};
+      const bool masked = a.some < kI4Tile || a.nkeys < kI4Tile;
+      if (masked)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int key = key0 + 8 * i;
+          hidden[i] = (key >= a.nkeys ? 1 << 20 : args.causal ? max(key - a.some + 1, 0) * args.H : 0) - row0 - col0;
+          uint8_t* poison = smem + S::POISON + 128 * (t & 1) + 64 * wg + p0 + 8 * i;
+          bad[i] = *poison != 0;
+          __syncwarp();
+          if (bad[i] && j == 0) *poison = 0;
+        }
+      auto mask_scores = [&]() {
         if (masked)
 #pragma unroll
-          for (int k = 0; k < kC; ++k) v[k] = c + k < hidden ? -INFINITY : bad ? __uint_as_float(0x7FC00000u) : v[k];
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+              d[i][b] = 4 * b + j < hidden[i] ? -INFINITY : bad[i] ? __uint_as_float(0x7FC00000u) : d[i][b];
       };
       const uint64_t s2 = splat_f32x2(sl2);
-      auto scores = [&](int c, float (&v)[kC]) {  // against the maxima, in log2 units
-        load_scores(c, v);
+      auto against_max = [&]() {  // in log2 units
 #pragma unroll
-        for (int q = 0; q < kC / 4; ++q) {
+        for (int q = 0; q < B / 4; ++q) {
           float m4[4];
-          lds128f(mx + 4 * c + 16 * q, m4[0], m4[1], m4[2], m4[3]);
+          lds128f(mx + 4 * (j * B + 4 * q), m4[0], m4[1], m4[2], m4[3]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            unpack_f32x2(ffma_f32x2(pack_f32x2(v[4 * q + 2 * h], v[4 * q + 2 * h + 1]), s2, pack_f32x2(-m4[2 * h], -m4[2 * h + 1])),
-                         v[4 * q + 2 * h], v[4 * q + 2 * h + 1]);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              unpack_f32x2(ffma_f32x2(pack_f32x2(d[i][4 * q + 2 * h], d[i][4 * q + 2 * h + 1]), s2, pack_f32x2(-m4[2 * h], -m4[2 * h + 1])),
+                           d[i][4 * q + 2 * h], d[i][4 * q + 2 * h + 1]);
         }
       };
+      load_scores();
+      mask_scores();
+      against_max();
       float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NC; c += kC) {
-        float d[kC];
-        scores(c, d);
-#pragma unroll
-        for (int k = 0; k < kC; k += 2) top = fmax3(top, d[k], d[k + 1]);
-      }
+      for (int b = 0; b < B; ++b) top = fmax3(top, d[0][b], d[1][b]);
       const bool over = __any_sync(0xffffffffu, top > 8.f);
       if (lane == 0) {
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + S::FLAG + 32 * (t & 1) + 4 * warp), "r"(over ? 1u : 0u) : "memory");
@@ -603,50 +679,44 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       }
       __syncwarp();
       if (!(ok = i4_wait_warp(bar(IB_FLAG + 2 * wg + (t & 1)), (t >> 1) & 1, wc, kSiteI4Flag))) break;
-      float f4[4];
-      lds128f(base + S::FLAG + 32 * (t & 1) + 16 * wg, f4[0], f4[1], f4[2], f4[3]);
-      const bool raise = (__float_as_uint(f4[0]) | __float_as_uint(f4[1]) | __float_as_uint(f4[2]) | __float_as_uint(f4[3])) != 0;
-      if (raise) {
-        float wm;
-        {
-          float v[NC];
+      uint32_t f4[4];
+      lds128(base + S::FLAG + 32 * (t & 1) + 16 * wg, f4);
+      if ((f4[0] | f4[1] | f4[2] | f4[3]) != 0) {
+        load_scores();
+        mask_scores();
+        float v[B];
 #pragma unroll
-          for (int c = 0; c < NC; c += kC) {
-            float u[kC];
-            load_scores(c, u);
+        for (int b = 0; b < B; ++b) v[b] = fmaxf(d[0][b], d[1][b]) * sl2;
+        if (!(ok = exchange(xch, v, false))) break;
 #pragma unroll
-            for (int k = 0; k < kC; ++k) v[c + k] = u[k] * sl2;
+        for (int b = 0; b < B; ++b) {
+          const uint32_t c = 4 * (j * B + b);
+          const float old = lds32f(mx + c);
+          const bool grow = v[b] > old + 8.f;
+          __syncwarp();
+          if (u == 0) {
+            sts32f(mx + c, grow ? v[b] : old);
+            sts32f(fac + c, grow ? ex2_approx(old - v[b]) : 1.f);
           }
-          wm = reduce_columns<NC>(v, lane, [](float x, float y) { return fmaxf(x, y); });
-        }
-        if (!(ok = exchange(xch, wm))) break;
-        float cm = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) cm = fmaxf(cm, lds32f(xch + (k * NC + mine) * 4));
-        const float old = lds32f(mx + 4 * mine);
-        const bool grow = cm > old + 8.f;
-        __syncwarp();
-        if (lane % kSpread == 0) {
-          sts32f(mx + 4 * mine, grow ? cm : old);
-          sts32f(fac + 4 * mine, grow ? ex2_approx(old - cm) : 1.f);
         }
         __syncwarp();
-        if (!a.first) {  // the output so far (the tile before has been added to it before this one's scores were done)
+        against_max();
+        if (!a.first()) {  // the output so far (the tile before has been added to it before this one's scores were done)
 #pragma unroll
-          for (int c = 0; c < NC; c += kC) {
-            float f[kC];
+          for (int b = 0; b < B; ++b) l[b] *= lds32f(fac + 4 * (j * B + b));
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 16) {
+            float f[16];
 #pragma unroll
-            for (int q = 0; q < kC / 4; ++q) lds128f(fac + 4 * c + 16 * q, f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-#pragma unroll
-            for (int k = 0; k < kC; ++k) l[c + k] *= f[k];
+            for (int q = 0; q < 4; ++q) lds128f(fac + 4 * c + 16 * q, f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
 #pragma unroll 1
             for (int m = 0; m < 4; ++m) {
-              uint32_t o[kC];
-              tmem_ld_cols(tmem + lanes + TO + N * m + col0 + c, o);
+              uint32_t o[16];
+              tmem_ld16(tmem + lanes + TO + N * m + col0 + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < kC; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[k]);
-              tmem_st_cols(tmem + lanes + TO + N * m + col0 + c, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[k]);
+              tmem_st16(tmem + lanes + TO + N * m + col0 + c, o);
             }
           }
           tmem_wait_st();
@@ -654,83 +724,82 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       }
       // (P is free: the output product of the tile before came before this tile's scores)
 #pragma unroll
-      for (int c = 0; c < NC; c += kC) {
-        float d[kC];
-        scores(c, d);
-        uint32_t pp[kC / 2];
+      for (int i = 0; i < 2; ++i) {
+        uint32_t pp[B / 2];
 #pragma unroll
-        for (int k = 0; k < kC; k += 2) {
-          const float p0 = ex2_approx(d[k]), p1 = ex2_approx(d[k + 1]);
+        for (int b = 0; b < B; b += 2) {
+          const float x0 = ex2_approx(d[i][b]), x1 = ex2_approx(d[i][b + 1]);
           // P in bf16, the type of the values in the tensor cores (half a step is 2^-8 of a weight at most, of either sign); the
           // row's sum takes the float32 weights, so that lse is not rounded with them
-          pp[k / 2] = pack_bf16(p0, p1);
-          l[c + k] += p0;
-          l[c + k + 1] += p1;
+          pp[b / 2] = pack_bf16(x0, x1);
+          l[b] += x0;
+          l[b + 1] += x1;
         }
-#pragma unroll
-        for (int q = 0; q < kC / 8; ++q)
-          sts128(prow + (((uint32_t)((col0 + c) / 8 + q) ^ swz) << 4), pp[4 * q], pp[4 * q + 1], pp[4 * q + 2], pp[4 * q + 3]);
+        const int p = p0 + 8 * i;
+        const uint32_t swz = N == 64 ? p & 7 : N == 32 ? (p >> 1) & 3 : (p >> 2) & 1, at = base + S::P + p * (2 * N);
+        if constexpr (B == 8)
+          sts128(at + (((uint32_t)(col0 / 8 + j) ^ swz) << 4), pp[0], pp[1], pp[2], pp[3]);
+        else
+          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(at + (((uint32_t)(j >> 1) ^ swz) << 4) + 8 * (j & 1)), "r"(pp[0]), "r"(pp[1]) : "memory");
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(IB_P_FULL));
-      if (!a.last) continue;
+      if (!a.last()) continue;
 
       // O / l of the finished piece -> its rows of out, or a split partial
-      const float wl = reduce_columns<NC>(l, lane, [](float x, float y) { return x + y; });
-      if (!(ok = exchange(xch + 8 * NC * 4, wl))) break;
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum += lds32f(xch + 8 * NC * 4 + (k * NC + mine) * 4);
-      const float m_run = lds32f(mx + 4 * mine);
-      const bool none = sum == 0.f;  // the row saw no key
-      const int r = col0 + mine, rr = row0 + r;  // row of the part, of the block
-      const bool on = r < args.part_rows && rr < block_rows;
+      if (!(ok = exchange(xch + kSums, l, true))) break;
       const int32_t* num_splits = sched + kSchedHeader + kUnitInts * args.num_units;
       const int ns = num_splits[a.wb * args.group];
       const bool split = ns > 1;
-      int64_t row = (int64_t)a.wb * block_rows + rr;
-      if (split) {
+      const int64_t off = split ? num_splits[args.num_qb + a.wb * args.group] : 0;
+      auto row_of = [&](int r) -> int64_t {  // of the warpgroup's row r in out or in the partials, -1 for none
+        const int rr = row0 + col0 + r;      // row of the block
+        if (col0 + r >= args.part_rows || rr >= block_rows) return -1;
+        if (!split) return (int64_t)a.wb * block_rows + rr;
         const int g = rr / args.H;
-        row = ((int64_t)num_splits[args.num_qb + a.wb * args.group] + g * ns + a.split) * args.H + (rr - g * args.H);
-      }
-      if (lane % kSpread == 0) {
-        sts32f(fac + 4 * mine, none ? 0.f : 1.f / sum);
-        if (on && w == 0) {
-          const float lse = none ? -INFINITY : (m_run + log2f(sum)) * 0.69314718055994530942f;
-          if (split) args.lse_acc[row] = lse; else args.lse[row] = lse;
+        return (off + g * ns + a.split) * args.H + (rr - g * args.H);
+      };
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const uint32_t c = 4 * (j * B + b);
+        const bool none = l[b] == 0.f;  // the row saw no key
+        if (u == 0) sts32f(fac + c, none ? 0.f : 1.f / l[b]);
+        if (u == 0 && w == 0) {
+          const int64_t row = row_of(4 * b + j);
+          const float lse = none ? -INFINITY : (lds32f(mx + c) + log2f(l[b])) * 0.69314718055994530942f;
+          if (row >= 0) {
+            if (split) args.lse_acc[row] = lse; else args.lse[row] = lse;
+          }
         }
       }
-      if (!on) row = -1;
+      const int64_t row = row_of(4 * (lane % B) + (lane % NC) / B);  // of column lane % NC
       __syncwarp();
       if (!(ok = i4_wait_warp(bar(IB_PV), piece++ & 1, wc, kSiteI4Pv))) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
-        const int dim = 128 * m + 32 * w + lane;
+      for (int mc = 0; mc < 4 * (NC / 16); ++mc) {
+        const int m = mc / (NC / 16), c = 16 * (mc % (NC / 16)), dim = 128 * m + 32 * w + lane;
+        uint32_t o[16];
+        tmem_ld16(tmem + lanes + TO + N * m + col0 + c, o);
+        tmem_wait_ld();
+        float f[16];
 #pragma unroll
-        for (int c = 0; c < NC; c += kC) {
-          uint32_t o[kC];
-          tmem_ld_cols(tmem + lanes + TO + N * m + col0 + c, o);
-          tmem_wait_ld();
-          float f[kC];
+        for (int q = 0; q < 4; ++q) lds128f(fac + 4 * c + 16 * q, f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
 #pragma unroll
-          for (int q = 0; q < kC / 4; ++q) lds128f(fac + 4 * c + 16 * q, f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-#pragma unroll
-          for (int k = 0; k < kC; k += 2) {
-            const float x0 = f[k] == 0.f ? 0.f : __uint_as_float(o[k]) * f[k], x1 = f[k + 1] == 0.f ? 0.f : __uint_as_float(o[k + 1]) * f[k + 1];
-            const int64_t r0 = __shfl_sync(0xffffffffu, row, (c + k) * kSpread), r1 = __shfl_sync(0xffffffffu, row, (c + k + 1) * kSpread);
-            if (split || args.out_f32) {
-              float* dst = split ? args.o_acc : static_cast<float*>(args.out);
-              if (r0 >= 0) dst[r0 * 512 + dim] = x0;
-              if (r1 >= 0) dst[r1 * 512 + dim] = x1;
-            } else {  // even lanes write two dims of the first row, odd lanes of the second
-              const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
-              const int64_t to = (lane & 1) ? r1 : r0;
-              const uint32_t two = (lane & 1) ? pack_bf16(got, x1) : pack_bf16(x0, got);
-              if (to >= 0) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(args.out) + to * 512 + (dim & ~1)) = two;
-            }
+        for (int k = 0; k < 16; k += 2) {
+          const float x0 = f[k] == 0.f ? 0.f : __uint_as_float(o[k]) * f[k], x1 = f[k + 1] == 0.f ? 0.f : __uint_as_float(o[k + 1]) * f[k + 1];
+          const int64_t r0 = __shfl_sync(0xffffffffu, row, c + k), r1 = __shfl_sync(0xffffffffu, row, c + k + 1);
+          if (split || args.out_f32) {
+            float* dst = split ? args.o_acc : static_cast<float*>(args.out);
+            if (r0 >= 0) dst[r0 * 512 + dim] = x0;
+            if (r1 >= 0) dst[r1 * 512 + dim] = x1;
+          } else {  // even lanes write two dims of the first row, odd lanes of the second
+            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
+            const int64_t to = (lane & 1) ? r1 : r0;
+            const uint32_t two = (lane & 1) ? pack_bf16(got, x1) : pack_bf16(x0, got);
+            if (to >= 0) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(args.out) + to * 512 + (dim & ~1)) = two;
           }
         }
       }
@@ -741,19 +810,19 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   __syncwarp();
   __syncthreads();
   if (*abort_flag) drain_delay(200000);  // in-flight copies and MMAs land before release
-  if (warp == 17) {
+  if (warp == kIssue + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-__global__ void __launch_bounds__(kI4Threads, 1) mla_decode_int4_n16_kernel(const __grid_constant__ Int4Args args) {
+__global__ void __launch_bounds__(I4Smem<16>::kThreads, 1) mla_decode_int4_n16_kernel(const __grid_constant__ Int4Args args) {
   decode_int4_body<16>(args);
 }
-__global__ void __launch_bounds__(kI4Threads, 1) mla_decode_int4_n32_kernel(const __grid_constant__ Int4Args args) {
+__global__ void __launch_bounds__(I4Smem<32>::kThreads, 1) mla_decode_int4_n32_kernel(const __grid_constant__ Int4Args args) {
   decode_int4_body<32>(args);
 }
-__global__ void __launch_bounds__(kI4Threads, 1) mla_decode_int4_n64_kernel(const __grid_constant__ Int4Args args) {
+__global__ void __launch_bounds__(I4Smem<64>::kThreads, 1) mla_decode_int4_n64_kernel(const __grid_constant__ Int4Args args) {
   decode_int4_body<64>(args);
 }
 

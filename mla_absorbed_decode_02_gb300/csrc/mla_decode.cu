@@ -439,13 +439,8 @@ int32_t launch_int4(const mla_decode_params* p, int32_t U, const void* q_nope, c
   a.parts = parts;
   a.part_rows = parts > 1 ? (H + 1) / 2 : G * H;
   const int N = a.part_rows <= 16 ? 16 : a.part_rows <= 32 ? 32 : 64;
-  const uint64_t rows = (uint64_t)NQB * H;
-  const uint64_t dq[3] = {64, rows, 8}, sq[2] = {1024, 128}, dr[2] = {64, rows}, sr[1] = {128};
-  const uint32_t bq[3] = {64, (uint32_t)N, 8}, br[2] = {64, (uint32_t)N};
-  int32_t st;
-  if ((st = encode_map(&a.map_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_nope, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B)) ||
-      (st = encode_map(&a.map_qr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_rope, dr, sr, br, CU_TENSOR_MAP_SWIZZLE_128B)))
-    return st;
+  a.q_nope = static_cast<const __nv_bfloat16*>(q_nope);
+  a.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
   a.kv = static_cast<const uint8_t*>(kv_pages);
   a.block_table = block_table;
   a.seqlens = cache_seqlens;
@@ -468,7 +463,7 @@ int32_t launch_int4(const mla_decode_params* p, int32_t U, const void* q_nope, c
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(parts * U, 1, 1);
-  cfg.blockDim = dim3(kI4Threads, 1, 1);
+  cfg.blockDim = dim3(N == 16 ? I4Smem<16>::kThreads : N == 32 ? I4Smem<32>::kThreads : I4Smem<64>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = N == 16 ? I4Smem<16>::kBytes : N == 32 ? I4Smem<32>::kBytes : I4Smem<64>::kBytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
