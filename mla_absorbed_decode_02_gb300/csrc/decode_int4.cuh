@@ -18,9 +18,8 @@
 // runs out first.  Of the scores' 128 rows 64 are keys, lanes 0..15 of each of tensor memory's four quadrants (the 16-lane
 // loads and stores then keep every lane of a warp busy, four on a key); the others hold whatever was there.
 //
-// Pages come by bulk copies into a ring in shared memory, as they are: loads into registers (64 bytes of a row at a time) kept
-// the load units busy for ~3000 cycles per 128 keys, which was more than everything else.  The four quarters of a tile (128 dims each)
-// are expanded by four warps each, into a ring of slots (16 KB each) in shared memory and of 64 columns each in tensor memory.
+// Pages come by bulk copies into shared memory, as they are, two in flight.  The four quarters of a tile (128 dims each) are
+// expanded by four warps each, into 16 KB of shared memory and 64 columns of tensor memory; up to 32 rows two tiles fit.
 //
 // Order of the values.  A lane expands 32 dims of a key, a quad of lanes a quarter, and the 16-lane stores deal a quad's words
 // out in turn: column 4 b + j of a quarter is word b of lane j.  So the scores run over the dims in that order, and the queries are
@@ -29,8 +28,11 @@
 //
 // Roles (warps): softmax (one warpgroup, two for N = 64, half of the columns each; a row's maximum lies across lanes and
 // warps, so scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the new maxima found and O
-// rescaled); 16 warps expand; one copies the pages and writes the tiles' records, one issues the MMAs, two load the queries.
+// rescaled); 16 warps expand; one copies the pages and writes the tiles' records, two issue the MMAs, one loads the
+// queries.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "decode_kernel.cuh"  // packed float pairs, bf16 packing, mma_bf16_ts
 #include "int4_rows.cuh"
@@ -50,12 +52,12 @@ struct I4Smem {
   static constexpr int kWg = N == 64 ? 2 : 1;                    // softmax warpgroups
   static constexpr int kNc = N / kWg;                            // columns of each
   static constexpr int kThreads = 128 * (kWg + 5);
-  static constexpr int kRaw = N == 64 ? 2 : 3;                   // pages as they came
-  static constexpr int kSlots = N == 64 ? 5 : N == 32 ? 6 : 7;   // quarters in shared memory
+  static constexpr int kRaw = 2;                                 // pages as they came
+  static constexpr int kTiles = N == 64 ? 1 : 2;                 // tiles in shared memory
   static constexpr int kA = N == 64 ? 2 : 4;                     // quarters in tensor memory
   static constexpr int kS = N == 64 ? 1 : 2;                     // score buffers
   static constexpr uint32_t V = 0;
-  static constexpr uint32_t Q = V + kSlots * kI4Slot;            // 9 blocks [N rows][64 dims]
+  static constexpr uint32_t Q = V + 4 * kTiles * kI4Slot;           // 9 blocks [N rows][64 dims]
   static constexpr uint32_t P = Q + 9 * N * 128;                 // [64 keys][N]
   static constexpr uint32_t RAW = P + N * 128;
   static constexpr uint32_t FLAG = RAW + kRaw * kI4Page;         // [tile parity][warp]: some score is far above the maximum
@@ -70,22 +72,23 @@ struct I4Smem {
 };
 
 enum : uint32_t {
-  IB_FULL = 0,               // + slot: one arrival per expanding warp
-  IB_EMPTY = IB_FULL + 7,    // + slot: the output product has read it
-  IB_A_EMPTY = IB_EMPTY + 7, // + quarter of a tile: the scores' product has read it in tensor memory
+  IB_FULL = 0,               // + quarter: one arrival per expanding warp
+  IB_EMPTY = IB_FULL + 4,    // + 4 (tile parity) + quarter: the output product has read it (one tile in shared memory: + quarter)
+  IB_A_EMPTY = IB_EMPTY + 8, // + quarter: the scores' product has read it in tensor memory
   IB_RAW = IB_A_EMPTY + 4,   // + page: landed
-  IB_RAW_EMPTY = IB_RAW + 3, // + page: one arrival per expanding warp
-  IB_Q_FULL = IB_RAW_EMPTY + 3,  // one arrival per loading warp
+  IB_RAW_EMPTY = IB_RAW + 2, // + page: one arrival per expanding warp
+  IB_Q_RAW = IB_RAW_EMPTY + 2, // landed
+  IB_Q_FULL,                 // in the keys' order; one arrival per expanding warp
   IB_Q_EMPTY,
   IB_S_FULL,                 // + tile parity
   IB_P_FULL = IB_S_FULL + 2, // one arrival per softmax warp
-  IB_PV,                     // a piece's last output product is done
+  IB_PV,                     // the tile's output product is done
   IB_FLAG,                   // + 2 warpgroup + tile parity: one arrival per warp
   IB_XCH = IB_FLAG + 4,      // + warpgroup
   IB_TILE = IB_XCH + 2,      // + record: written
   IB_TILE_READ = IB_TILE + kI4Ahead,  // + record: one arrival per softmax warp, the last readers
-  IB_DRAIN = IB_TILE_READ + kI4Ahead,
-  kI4Bars
+  IB_DRAIN = IB_TILE_READ + kI4Ahead,  // + issuing warp
+  kI4Bars = IB_DRAIN + 2
 };
 constexpr uint32_t kI4TmemSlot = 8 * kI4Bars, kI4Abort = kI4TmemSlot + 4;
 static_assert(kI4Abort + 4 <= 512, "barrier area");
@@ -93,7 +96,8 @@ static_assert(kI4Abort + 4 <= 512, "barrier area");
 enum I4Site : int { kSiteI4Ring = 44, kSiteI4Q, kSiteI4Scores, kSiteI4P, kSiteI4Pv, kSiteI4Flag, kSiteI4Drain, kSiteI4Tile, kSiteI4Raw };
 
 struct Int4Args {
-  const __nv_bfloat16 *q_nope, *q_rope;
+  CUtensorMap map_q;     // q~ rows: bf16 {64, rows, 8 blocks 128 bytes apart}, box {64, N, 8}, 128-byte swizzle
+  CUtensorMap map_qr;    // q^R rows: bf16 {64, rows}, box {64, N}
   const uint8_t* kv;
   const int32_t* block_table;
   const int32_t* seqlens;
@@ -204,6 +208,30 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&r)[4], int lane) {
   r[3] = high ? b3 : v;
 }
 
+// MMAs and commits of one lane (el != 0) of a converged warp: the predicate is on the instruction, not on a branch around it, so
+// that operands which are the same in all lanes can stay in uniform registers.
+__device__ __forceinline__ void mma_ts_if(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(el)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss_if(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(el)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t el, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(el)
+      : "memory");
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {  // multiples of 16
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
@@ -255,7 +283,7 @@ __device__ __forceinline__ bool i4_wait_warp(uint32_t bar, uint32_t parity, cons
 template <int N>
 __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   using S = I4Smem<N>;
-  constexpr int NC = S::kNc, B = NC / 4, kSlots = S::kSlots;  // B: columns of a lane
+  constexpr int NC = S::kNc, B = NC / 4, kTiles = S::kTiles;  // B: columns of a lane
   // tensor memory: O^T, score buffers, two buffers of the RoPE keys, the quarters of the latent keys
   constexpr uint32_t TO = 0, TS = 4 * N, TR = TS + N * S::kS, TA = TR + 64;
   static_assert(TA + 64 * S::kA <= 512, "tensor memory");
@@ -273,8 +301,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     for (uint32_t i = 0; i < kI4Bars; ++i) {
       uint32_t count = 1;
       if (i < IB_EMPTY) count = 4;
-      if (i >= IB_RAW_EMPTY && i < IB_Q_FULL) count = 16;
-      if (i == IB_Q_FULL) count = 2;
+      if ((i >= IB_RAW_EMPTY && i < IB_Q_RAW) || i == IB_Q_FULL) count = 16;
       if (i == IB_P_FULL || (i >= IB_TILE_READ && i < IB_DRAIN)) count = 4 * S::kWg;
       if (i >= IB_FLAG && i < IB_TILE) count = 4;
       mbar_init(bar(i), count);
@@ -292,6 +319,10 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (tid == 0) {
+    prefetch_tensormap(&args.map_q);
+    prefetch_tensormap(&args.map_qr);
+  }
   pdl_wait_prerequisites();
   const int32_t* sched = args.sched;
   const bool bad_meta = sched[0] != kSchedMagic || sched[1] != args.num_units || sched[2] != args.num_qb || sched[5] != args.group;
@@ -331,13 +362,34 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       chunk[q] = base + S::V + (j >> 1) * kI4Blk + p0 * 128 + (((uint32_t)(4 * (j & 1)) ^ (uint32_t)(p0 & 7) ^ (uint32_t)q ^ turn) << 4);
-    // The quarter that had this one's columns of tensor memory before: quarter a_prev of the tile a_tiles ago.  A wait looks at a
-    // phase's parity alone, so it must come neither two phases early -- the tile before that is done, since the slot that is waited
-    // for first is free only after its output product -- nor two late: that quarter's next product comes after this one's.
-    static_assert(S::kA == 2 || S::kA == 4, "an earlier quarter of an earlier tile could be a phase further");
+    // Its columns of tensor memory were quarter m - kA's before, of this tile or the one before.
+    static_assert(S::kA == 2 || S::kA == 4, "the quarters' places");
     const int a_prev = (m + 4 - S::kA) & 3;
-    const uint32_t a_tiles = m >= S::kA ? 0 : 1;
-    uint32_t slot = m, phase = 1, as = m % S::kA, raw = 0, raw_phase = 0;
+    const uint32_t a_tiles = m >= S::kA ? 0 : 1, as = m % S::kA;
+    uint32_t raw = 0, raw_phase = 0, piece = 0;
+    // A new block's queries: chunk b of a quarter gets word b of each of a quad's four lanes.  Half a warp takes a row's quarter
+    // (16 chunks, a quad four of them), or two rows' RoPE values.
+    auto order_queries = [&]() -> bool {
+      if (!i4_wait_warp(bar(IB_Q_RAW), piece++ & 1, wc, kSiteI4Q)) return false;
+      const int q = u & 3, half = lane >> 4;
+#pragma unroll 2
+      for (int it = warp - kExpand; it < 9 * N / 4; it += 16) {
+        const int task = 2 * it + half;
+        const bool lat = task < 4 * N;
+        const int row = lat ? task >> 2 : 2 * (task - 4 * N) + (q >> 1), from = lat ? 4 * j + (q ^ (j & 2)) : 4 * (q & 1) + j;
+        const int to = lat ? 4 * q + j : from, blk = lat ? 2 * (task & 3) : 8;
+        const uint32_t at = base + S::Q + row * 128, r7 = row & 7;
+        uint32_t v[4];
+        lds128(at + (blk + (from >> 3)) * (N * 128) + (((uint32_t)from & 7) ^ r7) * 16, v);
+        quad_transpose(v, lane);
+        __syncwarp();
+        sts128(at + (blk + (to >> 3)) * (N * 128) + (((uint32_t)to & 7) ^ r7) * 16, v[0], v[1], v[2], v[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(IB_Q_FULL));
+      return true;
+    };
     I4Tile a;
     for (uint32_t t = 0; read_tile(t, a) && a.valid(); ++t) {
       if (!i4_wait_warp(bar(IB_RAW + raw), raw_phase, wc, kSiteI4Raw)) break;
@@ -369,7 +421,10 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         raw = 0;
         raw_phase ^= 1;
       }
-      if (!i4_wait_warp(bar(IB_EMPTY + slot), phase, wc, kSiteI4Ring)) break;
+      // (the quarters that wait for this tile's scores in tensor memory do it first, the others once their keys are there)
+      if (a.first() && m >= S::kA && !order_queries()) break;
+      const uint32_t slot = 4 * (t % kTiles) + m;
+      if (!i4_wait_warp(bar(IB_EMPTY + slot), (t / kTiles & 1) ^ 1, wc, kSiteI4Ring)) break;
       if (t >= a_tiles && !i4_wait_warp(bar(IB_A_EMPTY + a_prev), (t - a_tiles) & 1, wc, kSiteI4Ring)) break;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -384,7 +439,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         tmem_st_16x16(tm + TA + 64 * as + 16 * q, r);
       }
       if (m < 2) {
-        // (this buffer's scores, of two tiles ago, are done: the slot that was waited for was read after them)
+        // (this buffer's scores, of two tiles ago, are done: those of the tile before are, or the output product of two tiles ago)
         uint32_t r[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -397,12 +452,8 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(IB_FULL + slot));
-      if ((slot += 4) >= kSlots) {
-        slot -= kSlots;
-        phase ^= 1;
-      }
-      as = (as + 4) % S::kA;
+      if (lane == 0) mbar_arrive(bar(IB_FULL + m));
+      if (a.first() && m < S::kA && !order_queries()) break;
     }
   } else if (warp == kIssue) {
     // ================================================================ pages and tile records
@@ -442,39 +493,27 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         raw_phase ^= 1;
       }
     }
-  } else if (warp > kIssue + 1) {
+  } else if (warp == kIssue + 3) {
     // ================================================================ queries
-    // Blocks of 64 values [N rows][128 bytes], 128-byte swizzle, the values in the order of the keys' tensor memory: chunk b of
-    // a quarter has word b of each of a quad's four lanes.  A quad takes four chunks.
-    const int loader = warp - kIssue - 2, j = lane & 3;
+    // Blocks of 64 values [N rows][128 bytes], 128-byte swizzle; the expanding warps turn them into the keys' order.
     I4Cursor cur;
     cur.init(args, rec);
     I4Tile r;
     uint32_t piece = 0;
+    const uint64_t keep = l2_policy_evict_last();
     while (cur.next(r)) {
       if (piece > 0 && !i4_wait_warp(bar(IB_Q_EMPTY), (piece - 1) & 1, wc, kSiteI4Q)) break;
-      const int64_t first = (int64_t)r.wb * block_rows + row0;
-      const int rows = min(args.part_rows, block_rows - row0);
-#pragma unroll 6
-      for (int it = 8 * loader + (lane >> 2); it < 18 * N; it += 16) {  // (N is a multiple of 16: whole warps)
-        const int row = it / 18, u = it - 18 * row, m = u >> 2, q = u & 3;
-        const __nv_bfloat16* src = u < 16 ? args.q_nope + (first + row) * 512 + 128 * m + 32 * j + 8 * (q ^ (j & 2))
-                                          : args.q_rope + (first + row) * 64 + 32 * (u - 16) + 8 * j;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < rows) v = *reinterpret_cast<const uint4*>(src);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        quad_transpose(w, lane);
-        const int chunk = u < 16 ? 4 * q + j : 4 * (u - 16) + j;  // of the quarter's 16, of the RoPE block's 8
-        const int blk = u < 16 ? 2 * m + (chunk >> 3) : 8;
-        sts128(base + S::Q + blk * (N * 128) + row * 128 + (((uint32_t)chunk ^ (uint32_t)row) & 7) * 16, w[0], w[1], w[2], w[3]);
+      if (lane == 0) {
+        const int row = r.wb * block_rows + row0;
+        mbar_arrive_expect_tx(bar(IB_Q_RAW), 9 * N * 128);
+        tma_load_3d(base + S::Q, &args.map_q, bar(IB_Q_RAW), 0, row, 0, keep);
+        tma_load_2d(base + S::Q + 8 * N * 128, &args.map_qr, bar(IB_Q_RAW), 0, row, keep);
       }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(IB_Q_FULL));
       ++piece;
       cur.skip_block();
     }
-  } else if (warp == kIssue + 1) {
+  } else if (warp == kIssue + 1 || warp == kIssue + 2) {
     // ================================================================ MMAs
     constexpr uint32_t id_qk = idesc_bf16_f32(128, N, 0, 0), id_pv = idesc_bf16_f32(128, N, 1, 1);
     // descriptors: an address 16 n bytes further is n more in the low word, the high words are constants
@@ -482,100 +521,79 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     const uint64_t desc_p = smem_desc(0, 16, N * 16, N == 64 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
     const uint32_t at_q = (base + S::Q) >> 4, at_c = (base + S::V) >> 4, at_p = (base + S::P) >> 4;
     auto at = [](uint64_t desc, uint32_t lo) { return desc | lo; };
-    uint32_t el_;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el_));
-    const bool el = el_ != 0;
-    uint32_t slot = 0, phase = 0, as = 0, pv_slot = 0, piece = 0;
-    auto wait = [&](uint32_t b, uint32_t parity, int site) -> bool { return i4_wait_warp(b, parity, wc, site); };
-    auto qk_quarter = [&](bool first, uint32_t t, int m) -> bool {
-      if (m == 0 && first) {
-        if (!wait(bar(IB_Q_FULL), piece & 1, kSiteI4Q)) return false;
-        ++piece;
-      }
-      if (!wait(bar(IB_FULL + slot), phase, kSiteI4Ring)) return false;
-      tc_fence_after();
-      const uint32_t d = tmem + TS + N * (t % S::kS), a = tmem + TA + 64 * as;
-      const uint32_t lo = at_q + m * (2 * N * 128 >> 4);
-      if (el) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_bf16_ts(d, a + 8 * k, at(desc_q, lo + (k >> 2) * (N * 128 >> 4) + 2 * (k & 3)), id_qk, m + k ? 1u : 0u);
-        mma_commit(bar(IB_A_EMPTY + m));
-      }
-      if (++slot == kSlots) {
-        slot = 0;
-        phase ^= 1;
-      }
-      if (++as == S::kA) as = 0;
-      return true;
-    };
-    auto qk_rope = [&](bool last, uint32_t t) {  // (the RoPE keys came with the first two quarters)
-      if (el) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16_ts(tmem + TS + N * (t % S::kS), tmem + TR + 32 * (t & 1) + 8 * k, at(desc_q, at_q + (8 * N * 128 >> 4) + 2 * k), id_qk, 1u);
-        mma_commit(bar(IB_S_FULL + (t & 1)));
-        if (last) mma_commit(bar(IB_Q_EMPTY));
-      }
-    };
-    auto pv = [&](bool first, bool last) {
-      tc_fence_after();
-#pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
-        const uint32_t lo = at_c + pv_slot * (kI4Slot >> 4);
-        if (el) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16_ss(tmem + TO + N * m, at(desc_c, lo + 128 * k), at(desc_p, at_p + (N * 32 >> 4) * k), id_pv, first && k == 0 ? 0u : 1u);
-          mma_commit(bar(IB_EMPTY + pv_slot));
-        }
-        if (++pv_slot == kSlots) pv_slot = 0;
-      }
-      if (el && last) mma_commit(bar(IB_PV));
-    };
+    uint32_t el;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el));
+    // One warp issues the scores' MMAs, the other the output's, each as soon as its tile is there.  What an MMA takes is known at
+    // compile time up to these bases (two tiles are unrolled): with slots counted and operands moved to uniform registers, eight
+    // MMAs took a warp 600 cycles.
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const bool scores = warp == kIssue + 1;
+    constexpr std::integral_constant<uint32_t, 0> even{};
+    constexpr std::integral_constant<uint32_t, 1> odd{};
     // (votes: what a record says is the same in all lanes, and known to be)
     auto flag = [&](const I4Tile& r, int f) -> bool { return __any_sync(0xffffffffu, r.flags & f); };
-    I4Tile b;
-    bool ok = read_tile(0, b), first = true, last = false;
-    if (ok) last = flag(b, I4Tile::kLast);
-    for (int m = 0; ok && m < 4; ++m) ok = qk_quarter(true, 0, m);
-    if (ok) qk_rope(last, 0);
-    for (uint32_t t = 0; ok; ++t) {
-      if (!(ok = read_tile(t + 1, b))) break;
-      const bool more = flag(b, I4Tile::kValid), b_first = flag(b, I4Tile::kFirst), b_last = flag(b, I4Tile::kLast);
-      // Beside the softmax run the next tile's quarters that the spare slots hold, as long as they are there first (not before a
-      // new query is, nor with one score buffer; and never all of a tile, so that a tile's scores come after the output product
-      // of the one before).
-      int m = 0;
-      const int early = S::kS > 1 && more && !b_first ? kSlots - 4 : 0;
-      while (m < early) {
-        if (__any_sync(0xffffffffu, mbar_test_wait(bar(IB_P_FULL), t & 1))) break;
-        if (__any_sync(0xffffffffu, mbar_test_wait(bar(IB_FULL + slot), phase))) {
-          if (!(ok = qk_quarter(false, t + 1, m))) break;
-          ++m;
-        } else if (__any_sync(0xffffffffu, *abort_flag)) {  // (some other role's wait has run out)
-          ok = false;
-          break;
-        }
+    I4Tile r;
+    bool ok = true, more = true;
+    uint32_t piece = 0;
+    auto qk = [&](auto parity, uint32_t t) {  // (parity: t & 1)
+      constexpr uint32_t o = decltype(parity)::value, d = TS + N * (o % S::kS);
+      if (!(ok = read_tile(t, r)) || !(more = flag(r, I4Tile::kValid))) return;
+      if (flag(r, I4Tile::kFirst) && !(ok = i4_wait_warp(bar(IB_Q_FULL), piece++ & 1, wc, kSiteI4Q))) return;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (!(ok = i4_wait_warp(bar(IB_FULL + m), t & 1, wc, kSiteI4Ring))) return;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts_if(el, tm + d, tm + TA + 64 * (m % S::kA) + 8 * k, at(desc_q, at_q + ((2 * m + (k >> 2)) * (N * 128) >> 4) + 2 * (k & 3)), id_qk,
+                    m + k ? 1u : 0u);
+        commit_if(el, bar(IB_A_EMPTY + m));
       }
-      if (!ok || !(ok = wait(bar(IB_P_FULL), t & 1, kSiteI4P))) break;
-      pv(first, last);
-      if (!more) break;
-      for (; ok && m < 4; ++m) ok = qk_quarter(b_first, t + 1, m);
-      if (!ok) break;
-      qk_rope(b_last, t + 1);
-      first = b_first;
-      last = b_last;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // (the RoPE keys came with the first two quarters)
+        mma_ts_if(el, tm + d, tm + TR + 32 * o + 8 * k, at(desc_q, at_q + (8 * N * 128 >> 4) + 2 * k), id_qk, 1u);
+      commit_if(el, bar(IB_S_FULL + o));
+      if (flag(r, I4Tile::kLast)) commit_if(el, bar(IB_Q_EMPTY));
+    };
+    auto pv = [&](auto parity, uint32_t t) {
+      constexpr uint32_t slots = 4 * (decltype(parity)::value % kTiles);
+      if (!(ok = read_tile(t, r)) || !(more = flag(r, I4Tile::kValid))) return;
+      const uint32_t add = flag(r, I4Tile::kFirst) ? 0u : 1u;
+      if (!(ok = i4_wait_warp(bar(IB_P_FULL), t & 1, wc, kSiteI4P))) return;
+      tc_fence_after();
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss_if(el, tm + TO + N * m, at(desc_c, at_c + (slots + m) * (kI4Slot >> 4) + 128 * k), at(desc_p, at_p + (N * 32 >> 4) * k), id_pv,
+                    k ? 1u : add);
+        commit_if(el, bar(IB_EMPTY + slots + m));
+      }
+      commit_if(el, bar(IB_PV));
+    };
+    // (Tile t + 2's scores go over tile t's, which have been read: its keys wait for the output product of tile t, and that for
+    // the softmax.)
+    if (scores) {
+      for (uint32_t t = 0; ok && more; t += 2) {
+        qk(even, t);
+        if (ok && more) qk(odd, t + 1);
+      }
+    } else {
+      for (uint32_t t = 0; ok && more; t += 2) {
+        pv(even, t);
+        if (ok && more) pv(odd, t + 1);
+      }
     }
     __syncwarp();
     // no MMA may still run when the CTA leaves
-    if (el) mma_commit(bar(IB_DRAIN));
+    const uint32_t drain = bar(IB_DRAIN + (scores ? 0 : 1));
+    commit_if(el, drain);
     __syncwarp();
     WaitCtx wd = wc;
     wd.timeout_ns = 100000000ull;
     volatile int no_abort = 0;
     wd.abort_local = &no_abort;
-    i4_wait_warp(bar(IB_DRAIN), 0, wd, kSiteI4Drain);
+    i4_wait_warp(drain, 0, wd, kSiteI4Drain);
   } else {
     // ================================================================ softmax
     // A lane: rows (of the warpgroup's NC) 4 b + j, b < B, for the keys in places p0 and p0 + 8.  Arrays over rows are kept in the
@@ -586,7 +604,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     const uint32_t mx = base + S::MAX + warp * NC * 4, fac = base + S::FAC + warp * NC * 4, xch = base + S::XCH + wg * 4 * NC * 4;
     constexpr uint32_t kSums = 4 * S::kWg * NC * 4;  // from the place of the maxima to that of the sums
     const float sl2 = args.scale_log2;
-    uint32_t exchanges = 0, piece = 0;
+    uint32_t exchanges = 0;
     float l[B];
     bool ok = true;
     I4Tile a;
@@ -681,7 +699,10 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       if (!(ok = i4_wait_warp(bar(IB_FLAG + 2 * wg + (t & 1)), (t >> 1) & 1, wc, kSiteI4Flag))) break;
       uint32_t f4[4];
       lds128(base + S::FLAG + 32 * (t & 1) + 16 * wg, f4);
+      // P is free, and the output so far complete, when the output product of the tile before is done
+      if (t > 0 && !(ok = i4_wait_warp(bar(IB_PV), (t - 1) & 1, wc, kSiteI4Pv))) break;
       if ((f4[0] | f4[1] | f4[2] | f4[3]) != 0) {
+        tc_fence_after();
         load_scores();
         mask_scores();
         float v[B];
@@ -701,7 +722,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         }
         __syncwarp();
         against_max();
-        if (!a.first()) {  // the output so far (the tile before has been added to it before this one's scores were done)
+        if (!a.first()) {
 #pragma unroll
           for (int b = 0; b < B; ++b) l[b] *= lds32f(fac + 4 * (j * B + b));
 #pragma unroll 1
@@ -722,7 +743,6 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
           tmem_wait_st();
         }
       }
-      // (P is free: the output product of the tile before came before this tile's scores)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t pp[B / 2];
@@ -776,7 +796,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       }
       const int64_t row = row_of(4 * (lane % B) + (lane % NC) / B);  // of column lane % NC
       __syncwarp();
-      if (!(ok = i4_wait_warp(bar(IB_PV), piece++ & 1, wc, kSiteI4Pv))) break;
+      if (!(ok = i4_wait_warp(bar(IB_PV), t & 1, wc, kSiteI4Pv))) break;
       tc_fence_after();
 #pragma unroll 1
       for (int mc = 0; mc < 4 * (NC / 16); ++mc) {

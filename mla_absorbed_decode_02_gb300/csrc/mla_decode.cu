@@ -439,8 +439,13 @@ int32_t launch_int4(const mla_decode_params* p, int32_t U, const void* q_nope, c
   a.parts = parts;
   a.part_rows = parts > 1 ? (H + 1) / 2 : G * H;
   const int N = a.part_rows <= 16 ? 16 : a.part_rows <= 32 ? 32 : 64;
-  a.q_nope = static_cast<const __nv_bfloat16*>(q_nope);
-  a.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
+  const uint64_t rows = (uint64_t)NQB * H;
+  const uint64_t dq[3] = {64, rows, 8}, sq[2] = {1024, 128}, dr[2] = {64, rows}, sr[1] = {128};
+  const uint32_t bq[3] = {64, (uint32_t)N, 8}, br[2] = {64, (uint32_t)N};
+  int32_t st;
+  if ((st = encode_map(&a.map_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_nope, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      (st = encode_map(&a.map_qr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_rope, dr, sr, br, CU_TENSOR_MAP_SWIZZLE_128B)))
+    return st;
   a.kv = static_cast<const uint8_t*>(kv_pages);
   a.block_table = block_table;
   a.seqlens = cache_seqlens;
