@@ -56,6 +56,7 @@ struct I4Smem {
   static constexpr int kTiles = N == 64 ? 1 : 2;                 // tiles in shared memory
   static constexpr int kA = N == 64 ? 2 : 4;                     // quarters in tensor memory
   static constexpr int kS = N == 64 ? 1 : 2;                     // score buffers
+  static constexpr int kSteps = kTiles == 2 ? 1 : 4;             // a tile leaves shared memory in one step, or quarter by quarter
   static constexpr uint32_t V = 0;
   static constexpr uint32_t Q = V + 4 * kTiles * kI4Slot;           // 9 blocks [N rows][64 dims]
   static constexpr uint32_t P = Q + 9 * N * 128;                 // [64 keys][N]
@@ -72,17 +73,16 @@ struct I4Smem {
 };
 
 enum : uint32_t {
-  IB_FULL = 0,               // + quarter: one arrival per expanding warp
-  IB_EMPTY = IB_FULL + 4,    // + 4 (tile parity) + quarter: the output product has read it (one tile in shared memory: + quarter)
-  IB_A_EMPTY = IB_EMPTY + 8, // + quarter: the scores' product has read it in tensor memory
-  IB_RAW = IB_A_EMPTY + 4,   // + page: landed
+  IB_FULL = 0,               // + part (kA quarters) of a tile: one arrival per expanding warp
+  IB_EMPTY = IB_FULL + 2,    // the output product has read it: + tile parity, or (one tile in shared memory) + quarter
+  IB_A_EMPTY = IB_EMPTY + 4, // + part: the scores' product has read it in tensor memory
+  IB_RAW = IB_A_EMPTY + 2,   // + page: landed
   IB_RAW_EMPTY = IB_RAW + 2, // + page: one arrival per expanding warp
   IB_Q_RAW = IB_RAW_EMPTY + 2, // landed
   IB_Q_FULL,                 // in the keys' order; one arrival per expanding warp
   IB_Q_EMPTY,
   IB_S_FULL,                 // + tile parity
   IB_P_FULL = IB_S_FULL + 2, // one arrival per softmax warp
-  IB_PV,                     // the tile's output product is done
   IB_FLAG,                   // + 2 warpgroup + tile parity: one arrival per warp
   IB_XCH = IB_FLAG + 4,      // + warpgroup
   IB_TILE = IB_XCH + 2,      // + record: written
@@ -208,30 +208,6 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&r)[4], int lane) {
   r[3] = high ? b3 : v;
 }
 
-// MMAs and commits of one lane (el != 0) of a converged warp: the predicate is on the instruction, not on a branch around it, so
-// that operands which are the same in all lanes can stay in uniform registers.
-__device__ __forceinline__ void mma_ts_if(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(el)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ss_if(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(el)
-      : "memory");
-}
-__device__ __forceinline__ void commit_if(uint32_t el, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"(el)
-      : "memory");
-}
-
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {  // multiples of 16
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
@@ -300,7 +276,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   if (tid == 0) {
     for (uint32_t i = 0; i < kI4Bars; ++i) {
       uint32_t count = 1;
-      if (i < IB_EMPTY) count = 4;
+      if (i < IB_EMPTY) count = 4 * S::kA;
       if ((i >= IB_RAW_EMPTY && i < IB_Q_RAW) || i == IB_Q_FULL) count = 16;
       if (i == IB_P_FULL || (i >= IB_TILE_READ && i < IB_DRAIN)) count = 4 * S::kWg;
       if (i >= IB_FLAG && i < IB_TILE) count = 4;
@@ -342,6 +318,10 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r.split) : "r"(at + 16) : "memory");
     return true;
   };
+  // the output product of tile t is done
+  auto wait_pv = [&](uint32_t t) -> bool {
+    return S::kSteps == 1 ? i4_wait_warp(bar(IB_EMPTY + (t & 1)), (t >> 1) & 1, wc, kSiteI4Pv) : i4_wait_warp(bar(IB_EMPTY + 3), t & 1, wc, kSiteI4Pv);
+  };
   const int block_rows = args.group * args.H, row0 = part * args.part_rows;
 
   if (idle) {
@@ -362,10 +342,8 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       chunk[q] = base + S::V + (j >> 1) * kI4Blk + p0 * 128 + (((uint32_t)(4 * (j & 1)) ^ (uint32_t)(p0 & 7) ^ (uint32_t)q ^ turn) << 4);
-    // Its columns of tensor memory were quarter m - kA's before, of this tile or the one before.
-    static_assert(S::kA == 2 || S::kA == 4, "the quarters' places");
-    const int a_prev = (m + 4 - S::kA) & 3;
-    const uint32_t a_tiles = m >= S::kA ? 0 : 1, as = m % S::kA;
+    static_assert(S::kA == 2 || S::kA == 4, "parts of a tile");
+    const uint32_t as = m % S::kA, part_of = m / S::kA;  // its place in tensor memory; the part was there before it: of this tile or the last
     uint32_t raw = 0, raw_phase = 0, piece = 0;
     // A new block's queries: chunk b of a quarter gets word b of each of a quad's four lanes.  Half a warp takes a row's quarter
     // (16 chunks, a quad four of them), or two rows' RoPE values.
@@ -424,8 +402,12 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       // (the quarters that wait for this tile's scores in tensor memory do it first, the others once their keys are there)
       if (a.first() && m >= S::kA && !order_queries()) break;
       const uint32_t slot = 4 * (t % kTiles) + m;
-      if (!i4_wait_warp(bar(IB_EMPTY + slot), (t / kTiles & 1) ^ 1, wc, kSiteI4Ring)) break;
-      if (t >= a_tiles && !i4_wait_warp(bar(IB_A_EMPTY + a_prev), (t - a_tiles) & 1, wc, kSiteI4Ring)) break;
+      if (t >= (uint32_t)kTiles && !(S::kSteps == 1 ? wait_pv(t - 2) : i4_wait_warp(bar(IB_EMPTY + m), (t & 1) ^ 1, wc, kSiteI4Ring))) break;
+      if (S::kA == 4 || part_of == 0) {  // after the last part of the tile before
+        if (t > 0 && !i4_wait_warp(bar(IB_A_EMPTY + 4 / S::kA - 1), (t & 1) ^ 1, wc, kSiteI4Ring)) break;
+      } else if (!i4_wait_warp(bar(IB_A_EMPTY), t & 1, wc, kSiteI4Ring)) {
+        break;
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t o[2][4], r[8];
@@ -452,7 +434,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(IB_FULL + m));
+      if (lane == 0) mbar_arrive(bar(IB_FULL + part_of));
       if (a.first() && m < S::kA && !order_queries()) break;
     }
   } else if (warp == kIssue) {
@@ -521,11 +503,12 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     const uint64_t desc_p = smem_desc(0, 16, N * 16, N == 64 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
     const uint32_t at_q = (base + S::Q) >> 4, at_c = (base + S::V) >> 4, at_p = (base + S::P) >> 4;
     auto at = [](uint64_t desc, uint32_t lo) { return desc | lo; };
-    uint32_t el;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el));
+    uint32_t el_;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el_));
+    const bool el = el_ != 0;
     // One warp issues the scores' MMAs, the other the output's, each as soon as its tile is there.  What an MMA takes is known at
-    // compile time up to these bases (two tiles are unrolled): with slots counted and operands moved to uniform registers, eight
-    // MMAs took a warp 600 cycles.
+    // compile time up to these bases (two tiles are unrolled), and a tile's MMAs are one run: with slots counted, operands moved to
+    // uniform registers and a wait for every quarter, eight MMAs took a warp 400 to 600 cycles.
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const bool scores = warp == kIssue + 1;
     constexpr std::integral_constant<uint32_t, 0> even{};
@@ -539,21 +522,29 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       constexpr uint32_t o = decltype(parity)::value, d = TS + N * (o % S::kS);
       if (!(ok = read_tile(t, r)) || !(more = flag(r, I4Tile::kValid))) return;
       if (flag(r, I4Tile::kFirst) && !(ok = i4_wait_warp(bar(IB_Q_FULL), piece++ & 1, wc, kSiteI4Q))) return;
+      const bool last = flag(r, I4Tile::kLast);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (!(ok = i4_wait_warp(bar(IB_FULL + m), t & 1, wc, kSiteI4Ring))) return;
+      for (int g = 0; g < 4 / S::kA; ++g) {
+        if (!(ok = i4_wait_warp(bar(IB_FULL + g), t & 1, wc, kSiteI4Ring))) return;
         tc_fence_after();
+        if (el) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts_if(el, tm + d, tm + TA + 64 * (m % S::kA) + 8 * k, at(desc_q, at_q + ((2 * m + (k >> 2)) * (N * 128) >> 4) + 2 * (k & 3)), id_qk,
-                    m + k ? 1u : 0u);
-        commit_if(el, bar(IB_A_EMPTY + m));
+          for (int m = g * S::kA; m < (g + 1) * S::kA; ++m)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16_ts(tm + d, tm + TA + 64 * (m % S::kA) + 8 * k, at(desc_q, at_q + ((2 * m + (k >> 2)) * (N * 128) >> 4) + 2 * (k & 3)), id_qk,
+                          m + k ? 1u : 0u);
+          mma_commit(bar(IB_A_EMPTY + g));
+          if (g == 4 / S::kA - 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ts(tm + d, tm + TR + 32 * o + 8 * k, at(desc_q, at_q + (8 * N * 128 >> 4) + 2 * k), id_qk, 1u);
+            mma_commit(bar(IB_S_FULL + o));
+            if (last) mma_commit(bar(IB_Q_EMPTY));
+          }
+        }
+        __syncwarp();
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)  // (the RoPE keys came with the first two quarters)
-        mma_ts_if(el, tm + d, tm + TR + 32 * o + 8 * k, at(desc_q, at_q + (8 * N * 128 >> 4) + 2 * k), id_qk, 1u);
-      commit_if(el, bar(IB_S_FULL + o));
-      if (flag(r, I4Tile::kLast)) commit_if(el, bar(IB_Q_EMPTY));
     };
     auto pv = [&](auto parity, uint32_t t) {
       constexpr uint32_t slots = 4 * (decltype(parity)::value % kTiles);
@@ -561,15 +552,18 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       const uint32_t add = flag(r, I4Tile::kFirst) ? 0u : 1u;
       if (!(ok = i4_wait_warp(bar(IB_P_FULL), t & 1, wc, kSiteI4P))) return;
       tc_fence_after();
+      if (el) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < 4; ++m) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss_if(el, tm + TO + N * m, at(desc_c, at_c + (slots + m) * (kI4Slot >> 4) + 128 * k), at(desc_p, at_p + (N * 32 >> 4) * k), id_pv,
-                    k ? 1u : add);
-        commit_if(el, bar(IB_EMPTY + slots + m));
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ss(tm + TO + N * m, at(desc_c, at_c + (slots + m) * (kI4Slot >> 4) + 128 * k), at(desc_p, at_p + (N * 32 >> 4) * k), id_pv,
+                        k ? 1u : add);
+          if (S::kSteps == 4) mma_commit(bar(IB_EMPTY + m));
+        }
+        if (S::kSteps == 1) mma_commit(bar(IB_EMPTY + decltype(parity)::value));
       }
-      commit_if(el, bar(IB_PV));
+      __syncwarp();
     };
     // (Tile t + 2's scores go over tile t's, which have been read: its keys wait for the output product of tile t, and that for
     // the softmax.)
@@ -587,7 +581,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     __syncwarp();
     // no MMA may still run when the CTA leaves
     const uint32_t drain = bar(IB_DRAIN + (scores ? 0 : 1));
-    commit_if(el, drain);
+    if (el) mma_commit(drain);
     __syncwarp();
     WaitCtx wd = wc;
     wd.timeout_ns = 100000000ull;
@@ -700,7 +694,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       uint32_t f4[4];
       lds128(base + S::FLAG + 32 * (t & 1) + 16 * wg, f4);
       // P is free, and the output so far complete, when the output product of the tile before is done
-      if (t > 0 && !(ok = i4_wait_warp(bar(IB_PV), (t - 1) & 1, wc, kSiteI4Pv))) break;
+      if (t > 0 && !(ok = wait_pv(t - 1))) break;
       if ((f4[0] | f4[1] | f4[2] | f4[3]) != 0) {
         tc_fence_after();
         load_scores();
@@ -796,7 +790,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       }
       const int64_t row = row_of(4 * (lane % B) + (lane % NC) / B);  // of column lane % NC
       __syncwarp();
-      if (!(ok = i4_wait_warp(bar(IB_PV), t & 1, wc, kSiteI4Pv))) break;
+      if (!(ok = wait_pv(t))) break;
       tc_fence_after();
 #pragma unroll 1
       for (int mc = 0; mc < 4 * (NC / 16); ++mc) {
