@@ -498,11 +498,9 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   } else if (warp == kIssue + 1 || warp == kIssue + 2) {
     // ================================================================ MMAs
     constexpr uint32_t id_qk = idesc_bf16_f32(128, N, 0, 0), id_pv = idesc_bf16_f32(128, N, 1, 1);
-    // descriptors: an address 16 n bytes further is n more in the low word, the high words are constants
-    const uint64_t desc_q = smem_desc(0, 16, 1024, kSwizzle128B), desc_c = smem_desc(0, kI4Blk, 1024, kSwizzle128B);
-    const uint64_t desc_p = smem_desc(0, 16, N * 16, N == 64 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
-    const uint32_t at_q = (base + S::Q) >> 4, at_c = (base + S::V) >> 4, at_p = (base + S::P) >> 4;
-    auto at = [](uint64_t desc, uint32_t lo) { return desc | lo; };
+    // descriptors: an address 16 n bytes further is n more in the low word
+    const uint64_t desc_q = smem_desc(base + S::Q, 16, 1024, kSwizzle128B), desc_c = smem_desc(base + S::V, kI4Blk, 1024, kSwizzle128B);
+    const uint64_t desc_p = smem_desc(base + S::P, 16, N * 16, N == 64 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
     uint32_t el_;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el_));
     const bool el = el_ != 0;
@@ -528,17 +526,17 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         if (!(ok = i4_wait_warp(bar(IB_FULL + g), t & 1, wc, kSiteI4Ring))) return;
         tc_fence_after();
         if (el) {
-#pragma unroll
+#pragma unroll 1
           for (int m = g * S::kA; m < (g + 1) * S::kA; ++m)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_bf16_ts(tm + d, tm + TA + 64 * (m % S::kA) + 8 * k, at(desc_q, at_q + ((2 * m + (k >> 2)) * (N * 128) >> 4) + 2 * (k & 3)), id_qk,
+              mma_bf16_ts(tm + d, tm + TA + 64 * (m % S::kA) + 8 * k, desc_q + ((2 * m + (k >> 2)) * (N * 128) >> 4) + 2 * (k & 3), id_qk,
                           m + k ? 1u : 0u);
           mma_commit(bar(IB_A_EMPTY + g));
           if (g == 4 / S::kA - 1) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_bf16_ts(tm + d, tm + TR + 32 * o + 8 * k, at(desc_q, at_q + (8 * N * 128 >> 4) + 2 * k), id_qk, 1u);
+              mma_bf16_ts(tm + d, tm + TR + 32 * o + 8 * k, desc_q + (8 * N * 128 >> 4) + 2 * k, id_qk, 1u);
             mma_commit(bar(IB_S_FULL + o));
             if (last) mma_commit(bar(IB_Q_EMPTY));
           }
@@ -557,7 +555,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16_ss(tm + TO + N * m, at(desc_c, at_c + (slots + m) * (kI4Slot >> 4) + 128 * k), at(desc_p, at_p + (N * 32 >> 4) * k), id_pv,
+            mma_bf16_ss(tm + TO + N * m, desc_c + (slots + m) * (kI4Slot >> 4) + 128 * k, desc_p + (N * 32 >> 4) * k, id_pv,
                         k ? 1u : add);
           if (S::kSteps == 4) mma_commit(bar(IB_EMPTY + m));
         }
