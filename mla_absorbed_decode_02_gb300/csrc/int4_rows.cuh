@@ -31,7 +31,7 @@ __device__ __forceinline__ void expand_int4_word(uint32_t x, uint32_t s2, uint32
 
 // 16 latent values of a lane (bf16 numbers; lanes 2 k and 2 k + 1 share 32 values) -> two words of codes and the scale's
 // bits: scale = amax / 7 rounded up to four significant bits, at least 2^-126 (1 for zeros); code = 8 + rint(x / scale), 1 .. 15.
-// NaN in the place of the scale where a value is not finite, or the scale above 2^119 (136 scale would overflow).
+// NaN in the place of the scale, codes of 8, where a value is not finite, or the scale above 2^119 (136 scale would overflow).
 // The quotient is x r, r = 1 / scale, corrected once by its remainder (Markstein, "Computation of elementary functions on the
 // IBM RISC System/6000 processor", 1990): correctly rounded for all 128 x 8 pairs of significands (tests/test_int4_rows.py), so
 // that ties stay ties.  Outside (2^-60, 2^100) it is divided.
@@ -66,6 +66,7 @@ __device__ __forceinline__ void quantize_int4_16(const float (&x)[16], uint32_t 
       const uint32_t n = __float_as_uint(z[8 * w + i] + 12582920.f) & 15u;
       code[w] |= n << (4 * (i >> 1) + 16 * (i & 1));
     }
+    if (bad) code[w] = 0x88888888u;
   }
 }
 
