@@ -56,7 +56,6 @@ struct I4Smem {
   static constexpr int kTiles = N == 64 ? 1 : 2;                 // tiles in shared memory
   static constexpr int kA = N == 64 ? 2 : 4;                     // quarters in tensor memory
   static constexpr int kS = N == 64 ? 1 : 2;                     // score buffers
-  static constexpr int kSteps = kTiles == 2 ? 1 : 4;             // a tile leaves shared memory in one step, or quarter by quarter
   static constexpr uint32_t V = 0;
   static constexpr uint32_t Q = V + 4 * kTiles * kI4Slot;           // 9 blocks [N rows][64 dims]
   static constexpr uint32_t P = Q + 9 * N * 128;                 // [64 keys][N]
@@ -74,9 +73,9 @@ struct I4Smem {
 
 enum : uint32_t {
   IB_FULL = 0,               // + part (kA quarters) of a tile: one arrival per expanding warp
-  IB_EMPTY = IB_FULL + 2,    // the output product has read it: + tile parity, or (one tile in shared memory) + quarter
-  IB_A_EMPTY = IB_EMPTY + 4, // + part: the scores' product has read it in tensor memory
-  IB_RAW = IB_A_EMPTY + 2,   // + page: landed
+  IB_EMPTY = IB_FULL + 2,    // + 4 (tile parity, where two tiles fit) + quarter: the output product has read it
+  IB_A_EMPTY = IB_EMPTY + 8, // + quarter: the scores' product has read it in tensor memory
+  IB_RAW = IB_A_EMPTY + 4,   // + page: landed
   IB_RAW_EMPTY = IB_RAW + 2, // + page: one arrival per expanding warp
   IB_Q_RAW = IB_RAW_EMPTY + 2, // landed
   IB_Q_FULL,                 // in the keys' order; one arrival per expanding warp
@@ -320,7 +319,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   };
   // the output product of tile t is done
   auto wait_pv = [&](uint32_t t) -> bool {
-    return S::kSteps == 1 ? i4_wait_warp(bar(IB_EMPTY + (t & 1)), (t >> 1) & 1, wc, kSiteI4Pv) : i4_wait_warp(bar(IB_EMPTY + 3), t & 1, wc, kSiteI4Pv);
+    return i4_wait_warp(bar(IB_EMPTY + 4 * (t % kTiles) + 3), t / kTiles & 1, wc, kSiteI4Pv);
   };
   const int block_rows = args.group * args.H, row0 = part * args.part_rows;
 
@@ -343,7 +342,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     for (int q = 0; q < 4; ++q)
       chunk[q] = base + S::V + (j >> 1) * kI4Blk + p0 * 128 + (((uint32_t)(4 * (j & 1)) ^ (uint32_t)(p0 & 7) ^ (uint32_t)q ^ turn) << 4);
     static_assert(S::kA == 2 || S::kA == 4, "parts of a tile");
-    const uint32_t as = m % S::kA, part_of = m / S::kA;  // its place in tensor memory; the part was there before it: of this tile or the last
+    const uint32_t as = m % S::kA, part_of = m / S::kA;  // its place in tensor memory, and its part of the tile
     uint32_t raw = 0, raw_phase = 0, piece = 0;
     // A new block's queries: chunk b of a quarter gets word b of each of a quad's four lanes.  Half a warp takes a row's quarter
     // (16 chunks, a quad four of them), or two rows' RoPE values.
@@ -402,10 +401,10 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       // (the quarters that wait for this tile's scores in tensor memory do it first, the others once their keys are there)
       if (a.first() && m >= S::kA && !order_queries()) break;
       const uint32_t slot = 4 * (t % kTiles) + m;
-      if (t >= (uint32_t)kTiles && !(S::kSteps == 1 ? wait_pv(t - 2) : i4_wait_warp(bar(IB_EMPTY + m), (t & 1) ^ 1, wc, kSiteI4Ring))) break;
-      if (S::kA == 4 || part_of == 0) {  // after the last part of the tile before
-        if (t > 0 && !i4_wait_warp(bar(IB_A_EMPTY + 4 / S::kA - 1), (t & 1) ^ 1, wc, kSiteI4Ring)) break;
-      } else if (!i4_wait_warp(bar(IB_A_EMPTY), t & 1, wc, kSiteI4Ring)) {
+      if (!i4_wait_warp(bar(IB_EMPTY + slot), (t / kTiles & 1) ^ 1, wc, kSiteI4Ring)) break;
+      if (part_of == 0) {  // quarter m - kA, which had its columns before, is one of the tile before
+        if (t > 0 && !i4_wait_warp(bar(IB_A_EMPTY + (m + 4 - S::kA)), (t & 1) ^ 1, wc, kSiteI4Ring)) break;
+      } else if (!i4_wait_warp(bar(IB_A_EMPTY + m - S::kA), t & 1, wc, kSiteI4Ring)) {
         break;
       }
 #pragma unroll
@@ -521,21 +520,20 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       if (!(ok = read_tile(t, r)) || !(more = flag(r, I4Tile::kValid))) return;
       if (flag(r, I4Tile::kFirst) && !(ok = i4_wait_warp(bar(IB_Q_FULL), piece++ & 1, wc, kSiteI4Q))) return;
       const bool last = flag(r, I4Tile::kLast);
-#pragma unroll
-      for (int g = 0; g < 4 / S::kA; ++g) {
-        if (!(ok = i4_wait_warp(bar(IB_FULL + g), t & 1, wc, kSiteI4Ring))) return;
-        tc_fence_after();
-        if (el) {
 #pragma unroll 1
-          for (int m = g * S::kA; m < (g + 1) * S::kA; ++m)
+      for (int m = 0; m < 4; ++m) {
+        if (m % S::kA == 0) {
+          if (!(ok = i4_wait_warp(bar(IB_FULL + m / S::kA), t & 1, wc, kSiteI4Ring))) return;
+          tc_fence_after();
+        }
+        if (el) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16_ts(tm + d, tm + TA + 64 * (m % S::kA) + 8 * k, desc_q + ((2 * m + (k >> 2)) * (N * 128) >> 4) + 2 * (k & 3), id_qk,
-                          m + k ? 1u : 0u);
-          mma_commit(bar(IB_A_EMPTY + g));
-          if (g == 4 / S::kA - 1) {
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ts(tm + d, tm + TA + 64 * (m % S::kA) + 8 * k, desc_q + ((2 * m + (k >> 2)) * (N * 128) >> 4) + 2 * (k & 3), id_qk, m + k ? 1u : 0u);
+          mma_commit(bar(IB_A_EMPTY + m));
+          if (m == 3) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k)  // (the RoPE keys came with the first two quarters)
               mma_bf16_ts(tm + d, tm + TR + 32 * o + 8 * k, desc_q + (8 * N * 128 >> 4) + 2 * k, id_qk, 1u);
             mma_commit(bar(IB_S_FULL + o));
             if (last) mma_commit(bar(IB_Q_EMPTY));
@@ -557,9 +555,8 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
           for (int k = 0; k < 4; ++k)
             mma_bf16_ss(tm + TO + N * m, desc_c + (slots + m) * (kI4Slot >> 4) + 128 * k, desc_p + (N * 32 >> 4) * k, id_pv,
                         k ? 1u : add);
-          if (S::kSteps == 4) mma_commit(bar(IB_EMPTY + m));
+          mma_commit(bar(IB_EMPTY + slots + m));
         }
-        if (S::kSteps == 1) mma_commit(bar(IB_EMPTY + decltype(parity)::value));
       }
       __syncwarp();
     };
