@@ -11,20 +11,18 @@
 // memory.  A unit of the plan is one CTA, or two for 65 to 128 heads, which read the same pages at the same time (the
 // second from L2).  With several new tokens a sequence, as many as fit into 64 rows share every key.
 //
-// The scores' A operand, K [keys x 576], lies in tensor memory, the output's, C^T, in shared memory (MN-major, [64 keys][64
-// dims] blocks with the 128-byte swizzle): the expanding warps write both from the same registers.  MMA rates, M = 128, K = 16,
-// cta_group::1: A from shared memory 39 / 40 / 48 cycles for N = 16 / 32 / 64 (4 KB of A and 32 N bytes of B at 128 bytes a cycle,
-// K- or MN-major alike), from tensor memory 12 / 17 / 32.  With both products' A in shared memory its data path is what
-// runs out first.  Of the scores' 128 rows 64 are keys, lanes 0..15 of each of tensor memory's four quadrants (the 16-lane
-// loads and stores then keep every lane of a warp busy, four on a key); the others hold whatever was there.
+// That one copy is both products' A operand: [64 keys][64 dims] blocks of shared memory with the 128-byte swizzle, K-major for the
+// scores (M = 64), MN-major for the output (M = 128 dims).  MMA rates beside other work, K = 16: scores 32 / 32 / 37 cycles for
+// N = 16 / 32 / 64, output 44 / 44 / 50.  (The scores' A in tensor memory takes 12 to 32 cycles by itself, but 53 while the
+// expanding warps store to tensor memory, and the output's 70 then: a tile took 2800 cycles so.)
 //
-// Pages come by bulk copies into shared memory, as they are, two in flight.  The four quarters of a tile (128 dims each) are
-// expanded by four warps each, into 16 KB of shared memory and 64 columns of tensor memory; up to 32 rows two tiles fit.
+// Pages come by bulk copies into shared memory, as they are.  (Loads into registers, 64 bytes of a row at a time, kept the load
+// units busy for ~1500 cycles a page.)  The four quarters of a tile (128 dims each) are expanded by four warps each, into
+// 16 KB of shared memory each; up to 32 rows two tiles fit.
 //
-// Order of the values.  A lane expands 32 dims of a key, a quad of lanes a quarter, and the 16-lane stores deal a quad's words
-// out in turn: column 4 b + j of a quarter is word b of lane j.  So the scores run over the dims in that order, and the queries are
-// laid out in it when they are loaded.  The 16-lane loads deal the scores' columns out the same way: lane j of a quad has
-// rows 4 b + j, and its weights are neighbours in P, so that row 4 b + j of a warpgroup is column j NC / 4 + b of P and O^T.
+// The scores' 64 rows are lanes 0..15 of each of tensor memory's four quadrants; the 16-lane loads deal a row of columns out to
+// four lanes in turn: lane j of a quad has rows 4 b + j of the block, and its weights are neighbours in P, so that row 4 b + j of a
+// warpgroup is column j NC / 4 + b of P and O^T.
 //
 // Roles (warps): softmax (one warpgroup, two for N = 64, half of the columns each; a row's maximum lies across lanes and
 // warps, so scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the new maxima found and O
@@ -51,13 +49,12 @@ template <int N>
 struct I4Smem {
   static constexpr int kWg = N == 64 ? 2 : 1;                    // softmax warpgroups
   static constexpr int kNc = N / kWg;                            // columns of each
-  static constexpr int kThreads = 128 * (kWg + 5);
-  static constexpr int kRaw = 2;                                 // pages as they came
+  static constexpr int kThreads = 128 * kWg + 576;
+  static constexpr int kRaw = N == 32 ? 1 : 2;                   // pages as they came
   static constexpr int kTiles = N == 64 ? 1 : 2;                 // tiles in shared memory
-  static constexpr int kA = N == 64 ? 2 : 4;                     // quarters in tensor memory
-  static constexpr int kS = N == 64 ? 1 : 2;                     // score buffers
   static constexpr uint32_t V = 0;
-  static constexpr uint32_t Q = V + 4 * kTiles * kI4Slot;           // 9 blocks [N rows][64 dims]
+  static constexpr uint32_t R = V + 4 * kTiles * kI4Slot;        // a tile's RoPE keys: a block
+  static constexpr uint32_t Q = R + kTiles * kI4Blk;             // 9 blocks [N rows][64 dims]
   static constexpr uint32_t P = Q + 9 * N * 128;                 // [64 keys][N]
   static constexpr uint32_t RAW = P + N * 128;
   static constexpr uint32_t FLAG = RAW + kRaw * kI4Page;         // [tile parity][warp]: some score is far above the maximum
@@ -72,13 +69,11 @@ struct I4Smem {
 };
 
 enum : uint32_t {
-  IB_FULL = 0,               // + part (kA quarters) of a tile: one arrival per expanding warp
-  IB_EMPTY = IB_FULL + 2,    // + 4 (tile parity, where two tiles fit) + quarter: the output product has read it
-  IB_A_EMPTY = IB_EMPTY + 8, // + quarter: the scores' product has read it in tensor memory
-  IB_RAW = IB_A_EMPTY + 4,   // + page: landed
+  IB_FULL = 0,               // + 4 (tile parity, where two tiles fit) + quarter: one arrival per expanding warp
+  IB_EMPTY = IB_FULL + 8,    // the same: the output product has read it
+  IB_RAW = IB_EMPTY + 8,     // + page: landed
   IB_RAW_EMPTY = IB_RAW + 2, // + page: one arrival per expanding warp
-  IB_Q_RAW = IB_RAW_EMPTY + 2, // landed
-  IB_Q_FULL,                 // in the keys' order; one arrival per expanding warp
+  IB_Q_FULL = IB_RAW_EMPTY + 2,
   IB_Q_EMPTY,
   IB_S_FULL,                 // + tile parity
   IB_P_FULL = IB_S_FULL + 2, // one arrival per softmax warp
@@ -86,8 +81,8 @@ enum : uint32_t {
   IB_XCH = IB_FLAG + 4,      // + warpgroup
   IB_TILE = IB_XCH + 2,      // + record: written
   IB_TILE_READ = IB_TILE + kI4Ahead,  // + record: one arrival per softmax warp, the last readers
-  IB_DRAIN = IB_TILE_READ + kI4Ahead,  // + issuing warp
-  kI4Bars = IB_DRAIN + 2
+  IB_DRAIN = IB_TILE_READ + kI4Ahead,
+  kI4Bars = IB_DRAIN + 1
 };
 constexpr uint32_t kI4TmemSlot = 8 * kI4Bars, kI4Abort = kI4TmemSlot + 4;
 static_assert(kI4Abort + 4 <= 512, "barrier area");
@@ -162,13 +157,8 @@ struct I4Cursor {
   __device__ void skip_block() { t = end; }
 };
 
-// 16 lanes x 16 columns of tensor memory and a warp: lane l has, in r[2 b + h], column 4 b + l % 4 of lane l / 4 + 8 h.
-__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-// The same for 2 K columns, K = 8 or 16 values a lane.
+// 16 lanes x 2 K columns of tensor memory and a warp, K = 8 or 16 values a lane: lane l gets, in r[2 b + h], column 4 b + l % 4 of
+// lane l / 4 + 8 h.
 template <int K>
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[K]) {
   if constexpr (K == 8) {
@@ -195,18 +185,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Lane j of a quad has words r[0..3]; afterwards it has word j of the quad's lanes 0..3.
-__device__ __forceinline__ void quad_transpose(uint32_t (&r)[4], int lane) {
-  const bool odd = lane & 1, high = lane & 2;
-  const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? r[0] : r[1], 1), y = __shfl_xor_sync(0xffffffffu, odd ? r[2] : r[3], 1);
-  const uint32_t b0 = odd ? x : r[0], b1 = odd ? r[1] : x, b2 = odd ? y : r[2], b3 = odd ? r[3] : y;
-  const uint32_t u = __shfl_xor_sync(0xffffffffu, high ? b0 : b2, 2), v = __shfl_xor_sync(0xffffffffu, high ? b1 : b3, 2);
-  r[0] = high ? u : b0;
-  r[1] = high ? v : b1;
-  r[2] = high ? b2 : u;
-  r[3] = high ? b3 : v;
-}
-
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {  // multiples of 16
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
@@ -259,9 +237,8 @@ template <int N>
 __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   using S = I4Smem<N>;
   constexpr int NC = S::kNc, B = NC / 4, kTiles = S::kTiles;  // B: columns of a lane
-  // tensor memory: O^T, score buffers, two buffers of the RoPE keys, the quarters of the latent keys
-  constexpr uint32_t TO = 0, TS = 4 * N, TR = TS + N * S::kS, TA = TR + 64;
-  static_assert(TA + 64 * S::kA <= 512, "tensor memory");
+  constexpr uint32_t TO = 0, TS = 4 * N;  // tensor memory: O^T, two score buffers
+  static_assert(TS + 2 * N <= 512, "tensor memory");
   constexpr int kExpand = 4 * S::kWg, kIssue = kExpand + 16;  // first warps of the roles
   extern __shared__ uint8_t i4_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(i4_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -275,8 +252,8 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   if (tid == 0) {
     for (uint32_t i = 0; i < kI4Bars; ++i) {
       uint32_t count = 1;
-      if (i < IB_EMPTY) count = 4 * S::kA;
-      if ((i >= IB_RAW_EMPTY && i < IB_Q_RAW) || i == IB_Q_FULL) count = 16;
+      if (i < IB_EMPTY) count = 4;
+      if (i >= IB_RAW_EMPTY && i < IB_Q_FULL) count = 16;
       if (i == IB_P_FULL || (i >= IB_TILE_READ && i < IB_DRAIN)) count = 4 * S::kWg;
       if (i >= IB_FLAG && i < IB_TILE) count = 4;
       mbar_init(bar(i), count);
@@ -328,10 +305,9 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     // ================================================================ pages -> bf16
     // Four warps a quarter, 16 keys each: a quad has a key and, in the registers' other half, the key eight further; a lane 32 dims
     // (16 bytes of codes).  Neighbouring quads take keys two apart: 416 bytes are 26 chunks of 16, so that the quads of an
-    // eight-lane phase read all eight bank groups.  (Row p of tensor memory's quadrant and of the slot is key perm(p).)
+    // eight-lane phase read all eight bank groups.  (So row p of the slot is not key p.)
     const int w = warp & 3, m = (warp - kExpand) >> 2, j = lane & 3, u = lane >> 2;
     const int p0 = 16 * w + u, key0 = 16 * w + ((u & 4) | (u & 1) << 1 | (u & 2) >> 1);
-    const uint32_t tm = tmem + ((uint32_t)(32 * w) << 16);
     constexpr uint32_t kNext = 8 * kI4Row;  // the second key
     const uint32_t src_lane = base + S::RAW + key0 * kI4Row + 16 * j;
     // chunk q of a lane's 32 dims in its slot; lanes of the slot's second block take their words in another order, so that no two
@@ -341,43 +317,21 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       chunk[q] = base + S::V + (j >> 1) * kI4Blk + p0 * 128 + (((uint32_t)(4 * (j & 1)) ^ (uint32_t)(p0 & 7) ^ (uint32_t)q ^ turn) << 4);
-    static_assert(S::kA == 2 || S::kA == 4, "parts of a tile");
-    const uint32_t as = m % S::kA, part_of = m / S::kA;  // its place in tensor memory, and its part of the tile
-    uint32_t raw = 0, raw_phase = 0, piece = 0;
-    // A new block's queries: chunk b of a quarter gets word b of each of a quad's four lanes.  Half a warp takes a row's quarter
-    // (16 chunks, a quad four of them), or two rows' RoPE values.
-    auto order_queries = [&]() -> bool {
-      if (!i4_wait_warp(bar(IB_Q_RAW), piece++ & 1, wc, kSiteI4Q)) return false;
-      const int q = u & 3, half = lane >> 4;
-#pragma unroll 2
-      for (int it = warp - kExpand; it < 9 * N / 4; it += 16) {
-        const int task = 2 * it + half;
-        const bool lat = task < 4 * N;
-        const int row = lat ? task >> 2 : 2 * (task - 4 * N) + (q >> 1), from = lat ? 4 * j + (q ^ (j & 2)) : 4 * (q & 1) + j;
-        const int to = lat ? 4 * q + j : from, blk = lat ? 2 * (task & 3) : 8;
-        const uint32_t at = base + S::Q + row * 128, r7 = row & 7;
-        uint32_t v[4];
-        lds128(at + (blk + (from >> 3)) * (N * 128) + (((uint32_t)from & 7) ^ r7) * 16, v);
-        quad_transpose(v, lane);
-        __syncwarp();
-        sts128(at + (blk + (to >> 3)) * (N * 128) + (((uint32_t)to & 7) ^ r7) * 16, v[0], v[1], v[2], v[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(IB_Q_FULL));
-      return true;
-    };
+    // RoPE keys: quarter m's warps take values 16 m .. 16 m + 15, two lanes of a quad a chunk of the row each
+    const uint32_t rope_dst = base + S::R + p0 * 128 + ((uint32_t)(2 * m + (j & 1)) ^ (uint32_t)(p0 & 7)) * 16;
+    uint32_t raw = 0, raw_phase = 0;
     I4Tile a;
     for (uint32_t t = 0; read_tile(t, a) && a.valid(); ++t) {
       if (!i4_wait_warp(bar(IB_RAW + raw), raw_phase, wc, kSiteI4Raw)) break;
-      uint32_t code[2][4], s2[2], a2[2], rope[2][4];
+      uint32_t code[2][4], s2[2], a2[2], rope[4];
       const uint32_t src = src_lane + raw * kI4Page;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         lds128(src + i * kNext + 64 * m, code[i]);
         s2[i] = lds16(src + i * kNext + kI4Codes + 8 * m - 14 * j);
-        if (m < 2) lds128(src + i * kNext + kI4Rope + 64 * m, rope[i]);
       }
+      lds128(src + (j >> 1) * kNext + kI4Rope + 32 * m + 16 * ((j & 1) - j), rope);  // (lanes 2 and 3: of the second key)
+      uint32_t poison = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         s2[i] |= s2[i] << 16;
@@ -388,7 +342,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
           // a key that only some of the tokens see: its values must not reach the others (0 x NaN); the softmax
           // gives NaN to those that see it
           s2[i] = 0;
-          smem[S::POISON + 128 * (t & 1) + p0 + 8 * i] = smem[S::POISON + 128 * (t & 1) + 64 + p0 + 8 * i] = 1;
+          poison |= 1u << i;
         }
         a2[i] = int4_offset(s2[i]);
       }
@@ -398,51 +352,33 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         raw = 0;
         raw_phase ^= 1;
       }
-      // (the quarters that wait for this tile's scores in tensor memory do it first, the others once their keys are there)
-      if (a.first() && m >= S::kA && !order_queries()) break;
       const uint32_t slot = 4 * (t % kTiles) + m;
       if (!i4_wait_warp(bar(IB_EMPTY + slot), (t / kTiles & 1) ^ 1, wc, kSiteI4Ring)) break;
-      if (part_of == 0) {  // quarter m - kA, which had its columns before, is one of the tile before
-        if (t > 0 && !i4_wait_warp(bar(IB_A_EMPTY + (m + 4 - S::kA)), (t & 1) ^ 1, wc, kSiteI4Ring)) break;
-      } else if (!i4_wait_warp(bar(IB_A_EMPTY + m - S::kA), t & 1, wc, kSiteI4Ring)) {
-        break;
-      }
+      // (only now: the softmax has read and reset the bytes of the tile two before)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t o[2][4], r[8];
+      for (int i = 0; i < 2; ++i)
+        if (poison >> i & 1) smem[S::POISON + 128 * (t & 1) + p0 + 8 * i] = smem[S::POISON + 128 * (t & 1) + 64 + p0 + 8 * i] = 1;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          expand_int4_word(turn ? code[i][q ^ 2] : code[i][q], s2[i], a2[i], o[i]);
-          sts128(chunk[q] + slot * kI4Slot + i * 1024, o[i][0], o[i][1], o[i][2], o[i][3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) r[2 * k + i] = o[i][k];
+          uint32_t o[4];
+          expand_int4_word(turn ? code[i][q ^ 2] : code[i][q], s2[i], a2[i], o);
+          sts128(chunk[q] + slot * kI4Slot + i * 1024, o[0], o[1], o[2], o[3]);
         }
-        tmem_st_16x16(tm + TA + 64 * as + 16 * q, r);
-      }
-      if (m < 2) {
-        // (this buffer's scores, of two tiles ago, are done: those of the tile before are, or the output product of two tiles ago)
-        uint32_t r[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          r[2 * k] = rope[0][k];
-          r[2 * k + 1] = rope[1][k];
-        }
-        tmem_st_16x16(tm + TR + 32 * (t & 1) + 16 * m, r);
-      }
-      tmem_wait_st();
+      sts128(rope_dst + (t % kTiles) * kI4Blk + (j >> 1) * 1024, rope[0], rope[1], rope[2], rope[3]);
       fence_proxy_async_smem();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(IB_FULL + part_of));
-      if (a.first() && m < S::kA && !order_queries()) break;
+      if (lane == 0) mbar_arrive(bar(IB_FULL + slot));
     }
   } else if (warp == kIssue) {
-    // ================================================================ pages and tile records
+    // ================================================================ pages, queries and tile records
     I4Cursor cur;
     cur.init(args, rec);
     I4Tile r;
     bool more = true;
-    uint32_t raw = 0, raw_phase = 1;
+    uint32_t raw = 0, raw_phase = 1, piece = 0;
+    const uint64_t keep = l2_policy_evict_last();
     for (uint32_t t = 0; more; ++t) {
       more = cur.next(r);
       int page = 0;
@@ -469,120 +405,105 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         bulk_load(base + S::RAW + raw * kI4Page, args.kv + (int64_t)page * kI4Page, kI4Page, bar(IB_RAW + raw));
       }
       __syncwarp();
+      if (r.first()) {  // blocks of 64 values [N rows][128 bytes], 128-byte swizzle
+        if (piece > 0 && !i4_wait_warp(bar(IB_Q_EMPTY), (piece - 1) & 1, wc, kSiteI4Q)) break;
+        if (lane == 0) {
+          const int row = r.wb * block_rows + row0;
+          mbar_arrive_expect_tx(bar(IB_Q_FULL), 9 * N * 128);
+          tma_load_3d(base + S::Q, &args.map_q, bar(IB_Q_FULL), 0, row, 0, keep);
+          tma_load_2d(base + S::Q + 8 * N * 128, &args.map_qr, bar(IB_Q_FULL), 0, row, keep);
+        }
+        __syncwarp();
+        ++piece;
+      }
       if (++raw == S::kRaw) {
         raw = 0;
         raw_phase ^= 1;
       }
     }
-  } else if (warp == kIssue + 3) {
-    // ================================================================ queries
-    // Blocks of 64 values [N rows][128 bytes], 128-byte swizzle; the expanding warps turn them into the keys' order.
-    I4Cursor cur;
-    cur.init(args, rec);
-    I4Tile r;
-    uint32_t piece = 0;
-    const uint64_t keep = l2_policy_evict_last();
-    while (cur.next(r)) {
-      if (piece > 0 && !i4_wait_warp(bar(IB_Q_EMPTY), (piece - 1) & 1, wc, kSiteI4Q)) break;
-      if (lane == 0) {
-        const int row = r.wb * block_rows + row0;
-        mbar_arrive_expect_tx(bar(IB_Q_RAW), 9 * N * 128);
-        tma_load_3d(base + S::Q, &args.map_q, bar(IB_Q_RAW), 0, row, 0, keep);
-        tma_load_2d(base + S::Q + 8 * N * 128, &args.map_qr, bar(IB_Q_RAW), 0, row, keep);
-      }
-      __syncwarp();
-      ++piece;
-      cur.skip_block();
-    }
-  } else if (warp == kIssue + 1 || warp == kIssue + 2) {
+  } else if (warp > kIssue) {
     // ================================================================ MMAs
-    constexpr uint32_t id_qk = idesc_bf16_f32(128, N, 0, 0), id_pv = idesc_bf16_f32(128, N, 1, 1);
+    constexpr uint32_t id_qk = idesc_bf16_f32(64, N, 0, 0), id_pv = idesc_bf16_f32(128, N, 1, 1);
     // descriptors: an address 16 n bytes further is n more in the low word
+    const uint64_t desc_k = smem_desc(base + S::V, 16, 1024, kSwizzle128B), desc_r = smem_desc(base + S::R, 16, 1024, kSwizzle128B);
     const uint64_t desc_q = smem_desc(base + S::Q, 16, 1024, kSwizzle128B), desc_c = smem_desc(base + S::V, kI4Blk, 1024, kSwizzle128B);
     const uint64_t desc_p = smem_desc(base + S::P, 16, N * 16, N == 64 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
-    uint32_t el_;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el_));
-    const bool el = el_ != 0;
-    // One warp issues the scores' MMAs, the other the output's, each as soon as its tile is there.  What an MMA takes is known at
-    // compile time up to these bases (two tiles are unrolled), and a tile's MMAs are one run: with slots counted, operands moved to
-    // uniform registers and a wait for every quarter, eight MMAs took a warp 400 to 600 cycles.
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const bool scores = warp == kIssue + 1;
-    constexpr std::integral_constant<uint32_t, 0> even{};
-    constexpr std::integral_constant<uint32_t, 1> odd{};
-    // (votes: what a record says is the same in all lanes, and known to be)
-    auto flag = [&](const I4Tile& r, int f) -> bool { return __any_sync(0xffffffffu, r.flags & f); };
-    I4Tile r;
-    bool ok = true, more = true;
-    uint32_t piece = 0;
-    auto qk = [&](auto parity, uint32_t t) {  // (parity: t & 1)
-      constexpr uint32_t o = decltype(parity)::value, d = TS + N * (o % S::kS);
-      if (!(ok = read_tile(t, r)) || !(more = flag(r, I4Tile::kValid))) return;
-      if (flag(r, I4Tile::kFirst) && !(ok = i4_wait_warp(bar(IB_Q_FULL), piece++ & 1, wc, kSiteI4Q))) return;
-      const bool last = flag(r, I4Tile::kLast);
-#pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
-        if (m % S::kA == 0) {
-          if (!(ok = i4_wait_warp(bar(IB_FULL + m / S::kA), t & 1, wc, kSiteI4Ring))) return;
-          tc_fence_after();
-        }
-        if (el) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_bf16_ts(tm + d, tm + TA + 64 * (m % S::kA) + 8 * k, desc_q + ((2 * m + (k >> 2)) * (N * 128) >> 4) + 2 * (k & 3), id_qk, m + k ? 1u : 0u);
-          mma_commit(bar(IB_A_EMPTY + m));
-          if (m == 3) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // (the RoPE keys came with the first two quarters)
-              mma_bf16_ts(tm + d, tm + TR + 32 * o + 8 * k, desc_q + (8 * N * 128 >> 4) + 2 * k, id_qk, 1u);
-            mma_commit(bar(IB_S_FULL + o));
-            if (last) mma_commit(bar(IB_Q_EMPTY));
-          }
-        }
-        __syncwarp();
-      }
-    };
-    auto pv = [&](auto parity, uint32_t t) {
-      constexpr uint32_t slots = 4 * (decltype(parity)::value % kTiles);
-      if (!(ok = read_tile(t, r)) || !(more = flag(r, I4Tile::kValid))) return;
-      const uint32_t add = flag(r, I4Tile::kFirst) ? 0u : 1u;
-      if (!(ok = i4_wait_warp(bar(IB_P_FULL), t & 1, wc, kSiteI4P))) return;
-      tc_fence_after();
-      if (el) {
+    uint32_t el;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el));
+    if (el) {
+      // One thread issues all of them, whatever is ready first: a quarter's scores, or the output of the tile before.  (MMAs of
+      // two warps take turns one by one, and each turn costs: 59 cycles an MMA.  Votes and warp-wide waits between the quarters
+      // cost as much as a quarter's MMAs.)
+      bool ok = true;
+      uint32_t piece = 0, t = 0, tp = 0, starts = 0;  // tile t's scores, tile tp's output; bit i: tile t - 1 - i starts a piece
+      auto pv = [&]() {
+        const uint32_t slots = 4 * (tp % kTiles), add = starts >> (t - 1 - tp) & 1 ? 0u : 1u;
+        const uint64_t c = desc_c + slots * (kI4Slot >> 4);
+        tc_fence_after();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16_ss(tm + TO + N * m, desc_c + (slots + m) * (kI4Slot >> 4) + 128 * k, desc_p + (N * 32 >> 4) * k, id_pv,
-                        k ? 1u : add);
+            mma_bf16_ss(tmem + TO + N * m, c + m * (kI4Slot >> 4) + 128 * k, desc_p + (N * 32 >> 4) * k, id_pv, k ? 1u : add);
           mma_commit(bar(IB_EMPTY + slots + m));
         }
+        ++tp;
+      };
+      // until the barrier's phase is over; the output meanwhile, when its weights are there
+      auto wait = [&](uint32_t b, uint32_t phase, int site) -> bool {
+        uint64_t t0 = 0;
+        for (uint32_t i = 1;; ++i) {
+          if (tp < t && mbar_test_wait(bar(IB_P_FULL), tp & 1)) pv();
+          if (mbar_test_wait(b, phase)) return true;
+          if ((i & 1023) == 0) {
+            if (*wc.abort_local) return false;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > wc.timeout_ns) {
+              raise_abort(wc, site);
+              return false;
+            }
+          }
+        }
+      };
+      for (;;) {
+        const uint32_t rec_at = t % kI4Ahead, o = t & 1, slots = 4 * (t % kTiles);
+        if (!(ok = wait(bar(IB_TILE + rec_at), (t / kI4Ahead) & 1, kSiteI4Tile))) break;
+        uint32_t f;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(f) : "r"(base + S::RING + 32 * rec_at) : "memory");
+        if (!(f & I4Tile::kValid)) break;
+        if ((f & I4Tile::kFirst) && !(ok = wait(bar(IB_Q_FULL), piece++ & 1, kSiteI4Q))) break;
+        const uint32_t d = tmem + TS + N * o;
+        uint64_t ak = desc_k + slots * (kI4Slot >> 4), bq = desc_q;
+#pragma unroll 1
+        for (int m = 0; m < 4 && ok; ++m) {
+          if (!(ok = wait(bar(IB_FULL + slots + m), t / kTiles & 1, kSiteI4Ring))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ss(d, ak + (k >> 2) * (kI4Blk >> 4) + 2 * (k & 3), bq + (k >> 2) * (N * 128 >> 4) + 2 * (k & 3), id_qk, m + k ? 1u : 0u);
+          ak += kI4Slot >> 4;
+          bq += 2 * N * 128 >> 4;
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // (every quarter's warps bring a part of the RoPE keys)
+          mma_bf16_ss(d, desc_r + (t % kTiles) * (kI4Blk >> 4) + 2 * k, bq + 2 * k, id_qk, 1u);
+        mma_commit(bar(IB_S_FULL + o));
+        if (f & I4Tile::kLast) mma_commit(bar(IB_Q_EMPTY));
+        starts = starts << 1 | (f & I4Tile::kFirst ? 1u : 0u);
+        ++t;  // (the scores of tile t + 2 go over those of tile t, which have been read: its keys wait for tile t's output)
       }
-      __syncwarp();
-    };
-    // (Tile t + 2's scores go over tile t's, which have been read: its keys wait for the output product of tile t, and that for
-    // the softmax.)
-    if (scores) {
-      for (uint32_t t = 0; ok && more; t += 2) {
-        qk(even, t);
-        if (ok && more) qk(odd, t + 1);
-      }
-    } else {
-      for (uint32_t t = 0; ok && more; t += 2) {
-        pv(even, t);
-        if (ok && more) pv(odd, t + 1);
-      }
+      if (ok && t > 0) wait(bar(IB_EMPTY + 4 * ((t - 1) % kTiles) + 3), (t - 1) / kTiles & 1, kSiteI4Pv);
+      mma_commit(bar(IB_DRAIN));
     }
     __syncwarp();
     // no MMA may still run when the CTA leaves
-    const uint32_t drain = bar(IB_DRAIN + (scores ? 0 : 1));
-    if (el) mma_commit(drain);
-    __syncwarp();
     WaitCtx wd = wc;
     wd.timeout_ns = 100000000ull;
     volatile int no_abort = 0;
     wd.abort_local = &no_abort;
-    i4_wait_warp(drain, 0, wd, kSiteI4Drain);
+    i4_wait_warp(bar(IB_DRAIN), 0, wd, kSiteI4Drain);
   } else {
     // ================================================================ softmax
     // A lane: rows (of the warpgroup's NC) 4 b + j, b < B, for the keys in places p0 and p0 + 8.  Arrays over rows are kept in the
@@ -631,7 +552,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       float d[2][B];
       auto load_scores = [&]() {
         uint32_t v[2 * B];
-        tmem_ld_16(tmem + lanes + TS + N * (t % S::kS) + col0, v);
+        tmem_ld_16(tmem + lanes + TS + N * (t & 1) + col0, v);
         tmem_wait_ld();
 #pragma unroll
         for (int b = 0; b < B; ++b)
