@@ -39,7 +39,7 @@ namespace mla {
 
 constexpr int kI4MaxRows = 64;           // rows of a CTA
 constexpr int kI4Tile = 64;              // keys of a tile
-constexpr int kI4Ahead = 8;              // tile records in shared memory
+constexpr int kI4Ahead = 4;              // tile records in shared memory
 constexpr uint32_t kI4Page = 64 * kI4Row;
 constexpr uint32_t kI4Blk = 8192;        // [64 keys][64 dims] bf16, 128-byte swizzle
 constexpr uint32_t kI4Slot = 2 * kI4Blk;
@@ -50,34 +50,34 @@ struct I4Smem {
   static constexpr int kWg = N == 64 ? 2 : 1;                    // softmax warpgroups
   static constexpr int kNc = N / kWg;                            // columns of each
   static constexpr int kThreads = 128 * kWg + 576;
-  static constexpr int kRaw = N == 32 ? 1 : 2;                   // pages as they came
-  static constexpr int kTiles = N == 64 ? 1 : 2;                 // tiles in shared memory
+  static constexpr int kSlots = N == 64 ? 6 : 8;           // a ring of quarter tiles
+  static constexpr int kR = N == 64 ? 1 : 2;                     // tiles' RoPE keys, a block each
   static constexpr uint32_t V = 0;
-  static constexpr uint32_t R = V + 4 * kTiles * kI4Slot;        // a tile's RoPE keys: a block
-  static constexpr uint32_t Q = R + kTiles * kI4Blk;             // 9 blocks [N rows][64 dims]
-  static constexpr uint32_t P = Q + 9 * N * 128;                 // [64 keys][N]
-  static constexpr uint32_t RAW = P + N * 128;
-  static constexpr uint32_t FLAG = RAW + kRaw * kI4Page;         // [tile parity][warp]: some score is far above the maximum
-  static constexpr uint32_t MAX = FLAG + 64;                     // [warp][kNc]: the running maxima, log2 units
+  static constexpr uint32_t R = V + kSlots * kI4Slot;
+  static constexpr uint32_t Q = R + kR * kI4Blk;                 // 9 blocks [N rows][64 dims]
+  static constexpr uint32_t P = Q + 9 * N * 128;                 // [tile parity][64 keys][N]
+  static constexpr uint32_t RAW = P + 2 * N * 128;               // a page as it came
+  static constexpr uint32_t FLAG = RAW + kI4Page;                // [tile parity][warp]: some score is far above the maximum
+  static constexpr uint32_t MAX = FLAG + 32 * kWg;                     // [warp][kNc]: the running maxima, log2 units
   static constexpr uint32_t FAC = MAX + 4 * kWg * kNc * 4;       // [warp][kNc]: factors of a rescale or of the output
   static constexpr uint32_t XCH = FAC + 4 * kWg * kNc * 4;       // [maxima, sums][warpgroup][warp][kNc]
-  static constexpr uint32_t POISON = XCH + 8 * kWg * kNc * 4;    // [tile parity][warpgroup][64 keys]
-  static constexpr uint32_t RING = POISON + 256;                 // kI4Ahead tile records of 32 bytes
+  static constexpr uint32_t POISON = XCH + 8 * kWg * kNc * 4;    // [tile % 4][warpgroup][64 keys]
+  static constexpr uint32_t RING = POISON + 256 * kWg;               // kI4Ahead tile records of 32 bytes
   static constexpr uint32_t BAR = RING + 32 * kI4Ahead;
   static constexpr uint32_t kBytes = BAR + 512 + 1024;           // + alignment slack
   static_assert(kBytes <= 232448, "shared memory");
 };
 
 enum : uint32_t {
-  IB_FULL = 0,               // + 4 (tile parity, where two tiles fit) + quarter: one arrival per expanding warp
-  IB_EMPTY = IB_FULL + 8,    // the same: the output product has read it
-  IB_RAW = IB_EMPTY + 8,     // + page: landed
-  IB_RAW_EMPTY = IB_RAW + 2, // + page: one arrival per expanding warp
-  IB_Q_FULL = IB_RAW_EMPTY + 2,
+  IB_FULL = 0,               // N = 64: + slot, else + tile parity: one arrival per expanding warp
+  IB_EMPTY = IB_FULL + 6,    // + slot: the output product has read it
+  IB_RAW = IB_EMPTY + 8,     // landed
+  IB_RAW_EMPTY,              // one arrival per expanding warp
+  IB_Q_FULL,
   IB_Q_EMPTY,
   IB_S_FULL,                 // + tile parity
-  IB_P_FULL = IB_S_FULL + 2, // one arrival per softmax warp
-  IB_FLAG,                   // + 2 warpgroup + tile parity: one arrival per warp
+  IB_P_FULL = IB_S_FULL + 2, // + tile parity: one arrival per softmax warp
+  IB_FLAG = IB_P_FULL + 2,   // + 2 warpgroup + tile parity: one arrival per warp
   IB_XCH = IB_FLAG + 4,      // + warpgroup
   IB_TILE = IB_XCH + 2,      // + record: written
   IB_TILE_READ = IB_TILE + kI4Ahead,  // + record: one arrival per softmax warp, the last readers
@@ -236,7 +236,8 @@ __device__ __forceinline__ bool i4_wait_warp(uint32_t bar, uint32_t parity, cons
 template <int N>
 __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   using S = I4Smem<N>;
-  constexpr int NC = S::kNc, B = NC / 4, kTiles = S::kTiles;  // B: columns of a lane
+  constexpr int NC = S::kNc, B = NC / 4, kSlots = S::kSlots;  // B: columns of a lane
+  constexpr bool kWhole = kSlots >= 8;  // two tiles fit: their scores wait for whole ones
   constexpr uint32_t TO = 0, TS = 4 * N;  // tensor memory: O^T, two score buffers
   static_assert(TS + 2 * N <= 512, "tensor memory");
   constexpr int kExpand = 4 * S::kWg, kIssue = kExpand + 16;  // first warps of the roles
@@ -252,16 +253,16 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   if (tid == 0) {
     for (uint32_t i = 0; i < kI4Bars; ++i) {
       uint32_t count = 1;
-      if (i < IB_EMPTY) count = 4;
-      if (i >= IB_RAW_EMPTY && i < IB_Q_FULL) count = 16;
-      if (i == IB_P_FULL || (i >= IB_TILE_READ && i < IB_DRAIN)) count = 4 * S::kWg;
+      if (i < IB_EMPTY) count = kWhole ? 16 : 4;
+      if (i == IB_RAW_EMPTY) count = 16;
+      if (i == IB_P_FULL || i == IB_P_FULL + 1 || (i >= IB_TILE_READ && i < IB_DRAIN)) count = 4 * S::kWg;
       if (i >= IB_FLAG && i < IB_TILE) count = 4;
       mbar_init(bar(i), count);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (tid < 64) asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + S::POISON + 4 * tid), "r"(0u) : "memory");
+  if (tid < 64 * S::kWg) asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + S::POISON + 4 * tid), "r"(0u) : "memory");
   if (warp == kIssue + 1) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
@@ -296,7 +297,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   };
   // the output product of tile t is done
   auto wait_pv = [&](uint32_t t) -> bool {
-    return i4_wait_warp(bar(IB_EMPTY + 4 * (t % kTiles) + 3), t / kTiles & 1, wc, kSiteI4Pv);
+    return i4_wait_warp(bar(IB_EMPTY + (4 * t + 3) % kSlots), (4 * t + 3) / kSlots & 1, wc, kSiteI4Pv);
   };
   const int block_rows = args.group * args.H, row0 = part * args.part_rows;
 
@@ -317,20 +318,25 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       chunk[q] = base + S::V + (j >> 1) * kI4Blk + p0 * 128 + (((uint32_t)(4 * (j & 1)) ^ (uint32_t)(p0 & 7) ^ (uint32_t)q ^ turn) << 4);
-    // RoPE keys: quarter m's warps take values 16 m .. 16 m + 15, two lanes of a quad a chunk of the row each
-    const uint32_t rope_dst = base + S::R + p0 * 128 + ((uint32_t)(2 * m + (j & 1)) ^ (uint32_t)(p0 & 7)) * 16;
-    uint32_t raw = 0, raw_phase = 0;
+    // RoPE keys: the last two quarters' warps (their slots are free later than the block that they write) take 32 values each, a
+    // lane a chunk of the row
+    const uint32_t rope_dst = base + S::R + p0 * 128 + ((uint32_t)(4 * (m & 1) + j) ^ (uint32_t)(p0 & 7)) * 16;
     I4Tile a;
-    for (uint32_t t = 0; read_tile(t, a) && a.valid(); ++t) {
-      if (!i4_wait_warp(bar(IB_RAW + raw), raw_phase, wc, kSiteI4Raw)) break;
-      uint32_t code[2][4], s2[2], a2[2], rope[4];
-      const uint32_t src = src_lane + raw * kI4Page;
+    for (uint32_t t = 0; read_tile(t, a); ++t) {
+      const uint32_t slot = (4 * t + m) % kSlots, phase = (4 * t + m) / kSlots & 1, full = bar(IB_FULL + (kWhole ? t & 1 : slot));
+      if (!a.valid()) {
+        // (where it asks for whole tiles, the issuing thread learns of the end as of one)
+        if (kWhole && i4_wait_warp(bar(IB_EMPTY + slot), phase ^ 1, wc, kSiteI4Ring) && lane == 0) mbar_arrive(full);
+        break;
+      }
+      if (!i4_wait_warp(bar(IB_RAW), t & 1, wc, kSiteI4Raw)) break;
+      uint32_t code[2][4], s2[2], a2[2], rope[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        lds128(src + i * kNext + 64 * m, code[i]);
-        s2[i] = lds16(src + i * kNext + kI4Codes + 8 * m - 14 * j);
+        lds128(src_lane + i * kNext + 64 * m, code[i]);
+        s2[i] = lds16(src_lane + i * kNext + kI4Codes + 8 * m - 14 * j);
+        if (m >= 2) lds128(src_lane + i * kNext + kI4Rope + 64 * (m & 1), rope[i]);
       }
-      lds128(src + (j >> 1) * kNext + kI4Rope + 32 * m + 16 * ((j & 1) - j), rope);  // (lanes 2 and 3: of the second key)
       uint32_t poison = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -347,17 +353,12 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         a2[i] = int4_offset(s2[i]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(IB_RAW_EMPTY + raw));
-      if (++raw == S::kRaw) {
-        raw = 0;
-        raw_phase ^= 1;
-      }
-      const uint32_t slot = 4 * (t % kTiles) + m;
-      if (!i4_wait_warp(bar(IB_EMPTY + slot), (t / kTiles & 1) ^ 1, wc, kSiteI4Ring)) break;
-      // (only now: the softmax has read and reset the bytes of the tile two before)
+      if (lane == 0) mbar_arrive(bar(IB_RAW_EMPTY));
+      if (!i4_wait_warp(bar(IB_EMPTY + slot), phase ^ 1, wc, kSiteI4Ring)) break;
+      // (only now: the softmax has read and reset the bytes of the tile four before)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (poison >> i & 1) smem[S::POISON + 128 * (t & 1) + p0 + 8 * i] = smem[S::POISON + 128 * (t & 1) + 64 + p0 + 8 * i] = 1;
+        if (poison >> i & 1) for (int g = 0; g < S::kWg; ++g) smem[S::POISON + 64 * (S::kWg * (t & 3) + g) + p0 + 8 * i] = 1;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -366,10 +367,12 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
           expand_int4_word(turn ? code[i][q ^ 2] : code[i][q], s2[i], a2[i], o);
           sts128(chunk[q] + slot * kI4Slot + i * 1024, o[0], o[1], o[2], o[3]);
         }
-      sts128(rope_dst + (t % kTiles) * kI4Blk + (j >> 1) * 1024, rope[0], rope[1], rope[2], rope[3]);
+      if (m >= 2)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sts128(rope_dst + (t % S::kR) * kI4Blk + i * 1024, rope[i][0], rope[i][1], rope[i][2], rope[i][3]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(IB_FULL + slot));
+      if (lane == 0) mbar_arrive(full);
     }
   } else if (warp == kIssue) {
     // ================================================================ pages, queries and tile records
@@ -377,7 +380,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     cur.init(args, rec);
     I4Tile r;
     bool more = true;
-    uint32_t raw = 0, raw_phase = 1, piece = 0;
+    uint32_t piece = 0;
     const uint64_t keep = l2_policy_evict_last();
     for (uint32_t t = 0; more; ++t) {
       more = cur.next(r);
@@ -399,10 +402,10 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         if (lane == 0) atomicCAS(&g_mla_error, 0, 1);
         page = 0;
       }
-      if (!i4_wait_warp(bar(IB_RAW_EMPTY + raw), raw_phase, wc, kSiteI4Raw)) break;
+      if (!i4_wait_warp(bar(IB_RAW_EMPTY), t & 1 ^ 1, wc, kSiteI4Raw)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar(IB_RAW + raw), kI4Page);
-        bulk_load(base + S::RAW + raw * kI4Page, args.kv + (int64_t)page * kI4Page, kI4Page, bar(IB_RAW + raw));
+        mbar_arrive_expect_tx(bar(IB_RAW), kI4Page);
+        bulk_load(base + S::RAW, args.kv + (int64_t)page * kI4Page, kI4Page, bar(IB_RAW));
       }
       __syncwarp();
       if (r.first()) {  // blocks of 64 values [N rows][128 bytes], 128-byte swizzle
@@ -415,10 +418,6 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         }
         __syncwarp();
         ++piece;
-      }
-      if (++raw == S::kRaw) {
-        raw = 0;
-        raw_phase ^= 1;
       }
     }
   } else if (warp > kIssue) {
@@ -437,15 +436,17 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       bool ok = true;
       uint32_t piece = 0, t = 0, tp = 0, starts = 0;  // tile t's scores, tile tp's output; bit i: tile t - 1 - i starts a piece
       auto pv = [&]() {
-        const uint32_t slots = 4 * (tp % kTiles), add = starts >> (t - 1 - tp) & 1 ? 0u : 1u;
-        const uint64_t c = desc_c + slots * (kI4Slot >> 4);
+        const uint32_t add = starts >> (t - 1 - tp) & 1 ? 0u : 1u;
+        const uint64_t w = desc_p + (tp & 1) * (N * 128 >> 4);
+        uint32_t slot = 4 * tp % kSlots;
         tc_fence_after();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
+          const uint64_t c = desc_c + slot * (kI4Slot >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16_ss(tmem + TO + N * m, c + m * (kI4Slot >> 4) + 128 * k, desc_p + (N * 32 >> 4) * k, id_pv, k ? 1u : add);
-          mma_commit(bar(IB_EMPTY + slots + m));
+          for (int k = 0; k < 4; ++k) mma_bf16_ss(tmem + TO + N * m, c + 128 * k, w + (N * 32 >> 4) * k, id_pv, k ? 1u : add);
+          mma_commit(bar(IB_EMPTY + slot));
+          slot = slot + 1 == kSlots ? 0 : slot + 1;
         }
         ++tp;
       };
@@ -453,7 +454,10 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       auto wait = [&](uint32_t b, uint32_t phase, int site) -> bool {
         uint64_t t0 = 0;
         for (uint32_t i = 1;; ++i) {
-          if (tp < t && mbar_test_wait(bar(IB_P_FULL), tp & 1)) pv();
+          if (tp < t && mbar_test_wait(bar(IB_P_FULL + (tp & 1)), tp >> 1 & 1)) {
+            pv();
+            continue;
+          }
           if (mbar_test_wait(b, phase)) return true;
           if ((i & 1023) == 0) {
             if (*wc.abort_local) return false;
@@ -467,34 +471,44 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         }
       };
       for (;;) {
-        const uint32_t rec_at = t % kI4Ahead, o = t & 1, slots = 4 * (t % kTiles);
-        if (!(ok = wait(bar(IB_TILE + rec_at), (t / kI4Ahead) & 1, kSiteI4Tile))) break;
+        const uint32_t rec_at = t % kI4Ahead, o = t & 1;
+        const uint32_t d = tmem + TS + N * o;
+        uint64_t bq = desc_q;
+        uint32_t slot = 4 * t % kSlots, phase = 4 * t / kSlots & 1;
+        // Where two tiles fit, a tile's quarters are mostly ready together: one question (~120 cycles) for all, and its record
+        // has been seen then.  (All quarters' one by one: 64 streams x 16 heads 99 us instead of 86.)  Where one fits, they become
+        // ready one by one.
+        if constexpr (kWhole) ok = wait(bar(IB_FULL + o), t >> 1 & 1, kSiteI4Ring);
+        else ok = wait(bar(IB_TILE + rec_at), (t / kI4Ahead) & 1, kSiteI4Tile);
+        if (!ok) break;
         uint32_t f;
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(f) : "r"(base + S::RING + 32 * rec_at) : "memory");
         if (!(f & I4Tile::kValid)) break;
         if ((f & I4Tile::kFirst) && !(ok = wait(bar(IB_Q_FULL), piece++ & 1, kSiteI4Q))) break;
-        const uint32_t d = tmem + TS + N * o;
-        uint64_t ak = desc_k + slots * (kI4Slot >> 4), bq = desc_q;
 #pragma unroll 1
-        for (int m = 0; m < 4 && ok; ++m) {
-          if (!(ok = wait(bar(IB_FULL + slots + m), t / kTiles & 1, kSiteI4Ring))) break;
+        for (int m = 0; m < 4; ++m) {
+          if (!kWhole && !(ok = wait(bar(IB_FULL + slot), phase, kSiteI4Ring))) break;
           tc_fence_after();
+          const uint64_t ak = desc_k + slot * (kI4Slot >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_bf16_ss(d, ak + (k >> 2) * (kI4Blk >> 4) + 2 * (k & 3), bq + (k >> 2) * (N * 128 >> 4) + 2 * (k & 3), id_qk, m + k ? 1u : 0u);
-          ak += kI4Slot >> 4;
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
           bq += 2 * N * 128 >> 4;
         }
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // (every quarter's warps bring a part of the RoPE keys)
-          mma_bf16_ss(d, desc_r + (t % kTiles) * (kI4Blk >> 4) + 2 * k, bq + 2 * k, id_qk, 1u);
+          mma_bf16_ss(d, desc_r + (t % S::kR) * (kI4Blk >> 4) + 2 * k, bq + 2 * k, id_qk, 1u);
         mma_commit(bar(IB_S_FULL + o));
         if (f & I4Tile::kLast) mma_commit(bar(IB_Q_EMPTY));
         starts = starts << 1 | (f & I4Tile::kFirst ? 1u : 0u);
         ++t;  // (the scores of tile t + 2 go over those of tile t, which have been read: its keys wait for tile t's output)
       }
-      if (ok && t > 0) wait(bar(IB_EMPTY + 4 * ((t - 1) % kTiles) + 3), (t - 1) / kTiles & 1, kSiteI4Pv);
+      if (ok && t > 0) wait(bar(IB_EMPTY + (4 * t - 1) % kSlots), (4 * t - 1) / kSlots & 1, kSiteI4Pv);
       mma_commit(bar(IB_DRAIN));
     }
     __syncwarp();
@@ -567,7 +581,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         for (int i = 0; i < 2; ++i) {
           const int key = key0 + 8 * i;
           hidden[i] = (key >= a.nkeys ? 1 << 20 : args.causal ? max(key - a.some + 1, 0) * args.H : 0) - row0 - col0;
-          uint8_t* poison = smem + S::POISON + 128 * (t & 1) + 64 * wg + p0 + 8 * i;
+          uint8_t* poison = smem + S::POISON + 64 * (S::kWg * (t & 3) + wg) + p0 + 8 * i;
           bad[i] = *poison != 0;
           __syncwarp();
           if (bad[i] && j == 0) *poison = 0;
@@ -602,16 +616,16 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       for (int b = 0; b < B; ++b) top = fmax3(top, d[0][b], d[1][b]);
       const bool over = __any_sync(0xffffffffu, top > 8.f);
       if (lane == 0) {
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + S::FLAG + 32 * (t & 1) + 4 * warp), "r"(over ? 1u : 0u) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + S::FLAG + 16 * S::kWg * (t & 1) + 4 * warp), "r"(over ? 1u : 0u) : "memory");
         mbar_arrive(bar(IB_FLAG + 2 * wg + (t & 1)));
       }
       __syncwarp();
       if (!(ok = i4_wait_warp(bar(IB_FLAG + 2 * wg + (t & 1)), (t >> 1) & 1, wc, kSiteI4Flag))) break;
       uint32_t f4[4];
-      lds128(base + S::FLAG + 32 * (t & 1) + 16 * wg, f4);
-      // P is free, and the output so far complete, when the output product of the tile before is done
-      if (t > 0 && !(ok = wait_pv(t - 1))) break;
+      lds128(base + S::FLAG + 16 * S::kWg * (t & 1) + 16 * wg, f4);
+      // (P is free: the tile's keys took the place of those whose output product read it)
       if ((f4[0] | f4[1] | f4[2] | f4[3]) != 0) {
+        if (t > 0 && !(ok = wait_pv(t - 1))) break;  // the output so far is complete
         tc_fence_after();
         load_scores();
         mask_scores();
@@ -666,7 +680,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
           l[b + 1] += x1;
         }
         const int p = p0 + 8 * i;
-        const uint32_t swz = N == 64 ? p & 7 : N == 32 ? (p >> 1) & 3 : (p >> 2) & 1, at = base + S::P + p * (2 * N);
+        const uint32_t swz = N == 64 ? p & 7 : N == 32 ? (p >> 1) & 3 : (p >> 2) & 1, at = base + S::P + (t & 1) * (N * 128) + p * (2 * N);
         if constexpr (B == 8)
           sts128(at + (((uint32_t)(col0 / 8 + j) ^ swz) << 4), pp[0], pp[1], pp[2], pp[3]);
         else
@@ -675,7 +689,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(IB_P_FULL));
+      if (lane == 0) mbar_arrive(bar(IB_P_FULL + (t & 1)));
       if (!a.last()) continue;
 
       // O / l of the finished piece -> its rows of out, or a split partial
