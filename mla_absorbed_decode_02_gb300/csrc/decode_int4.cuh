@@ -11,14 +11,17 @@
 // memory.  A unit of the plan is one CTA, or two for 65 to 128 heads, which read the same pages at the same time (the
 // second from L2).  With several new tokens a sequence, as many as fit into 64 rows share every key.
 //
-// That one copy is both products' A operand: [64 keys][64 dims] blocks of shared memory with the 128-byte swizzle, K-major for the
-// scores (M = 64), MN-major for the output (M = 128 dims).  MMA rates beside other work, K = 16: scores 32 / 32 / 37 cycles for
-// N = 16 / 32 / 64, output 44 / 44 / 50.  (The scores' A in tensor memory takes 12 to 32 cycles by itself, but 53 while the
-// expanding warps store to tensor memory, and the output's 70 then: a tile took 2800 cycles so.)
+// That one copy is both products' A operand: blocks [64 keys][64 dims] of shared memory with the 128-byte swizzle, K-major for the
+// scores (M = 64), MN-major for the output (M = 128 dims).  MMAs of K = 16 take 32 / 32 / 37 cycles for the scores, 44 / 44 / 50
+// for the output (N = 16 / 32 / 64).  What bounds them is the shared memory: both operands of every MMA, the pages and the expanded
+// keys are ~2000 cycles of its bandwidth a tile for N = 16, ~2850 for N = 64; a tile takes 2500 and 4000.  (The scores' A in tensor
+// memory is read without it, at 12 to 32 cycles an MMA, but beside the expanding warps' stores there they took 53, and the output's
+// MMAs 70: 64 streams x 16 heads 87 us instead of 83, 128 heads ragged 218 instead of 157.)
 //
 // Pages come by bulk copies into shared memory, as they are.  (Loads into registers, 64 bytes of a row at a time, kept the load
-// units busy for ~1500 cycles a page.)  The four quarters of a tile (128 dims each) are expanded by four warps each, into
-// 16 KB of shared memory each; up to 32 rows two tiles fit.
+// units busy for ~1500 cycles a page.  A second page ahead changed nothing.)  The four quarters of a tile (128 dims each) are
+// expanded by four warps each into a ring of quarters of 16 KB, eight up to 32 rows, six for 64: there the next tile's first two are
+// expanded and multiplied with the queries while the softmax works (with four: 178 us instead of 157).
 //
 // The scores' 64 rows are lanes 0..15 of each of tensor memory's four quadrants; the 16-lane loads deal a row of columns out to
 // four lanes in turn: lane j of a quad has rows 4 b + j of the block, and its weights are neighbours in P, so that row 4 b + j of a
@@ -26,13 +29,13 @@
 //
 // Roles (warps): softmax (one warpgroup, two for N = 64, half of the columns each; a row's maximum lies across lanes and
 // warps, so scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the new maxima found and O
-// rescaled); 16 warps expand; one copies the pages and writes the tiles' records, two issue the MMAs, one loads the
-// queries.
+// rescaled); 16 warps expand; one copies pages and queries and writes the tiles' records; a thread of the last issues the MMAs.
+//
+// Measured: 64 streams x 16 heads, 190 MB of cache, 83 us; 128 heads, 64 ragged sequences up to 32,768 keys (142 MB) 157 us, 4 up to
+// 131,072 (94 MB) 119 us; 24 sequences of 4 tokens x 20 heads (36 MB) 60 us.
 #pragma once
-#include <type_traits>
-
 #include "common.cuh"
-#include "decode_kernel.cuh"  // packed float pairs, bf16 packing, mma_bf16_ts
+#include "decode_kernel.cuh"  // packed float pairs, bf16 packing
 #include "int4_rows.cuh"
 
 namespace mla {
@@ -57,12 +60,12 @@ struct I4Smem {
   static constexpr uint32_t Q = R + kR * kI4Blk;                 // 9 blocks [N rows][64 dims]
   static constexpr uint32_t P = Q + 9 * N * 128;                 // [tile parity][64 keys][N]
   static constexpr uint32_t RAW = P + 2 * N * 128;               // a page as it came
-  static constexpr uint32_t FLAG = RAW + kI4Page;                // [tile parity][warp]: some score is far above the maximum
-  static constexpr uint32_t MAX = FLAG + 32 * kWg;                     // [warp][kNc]: the running maxima, log2 units
+  static constexpr uint32_t FLAG = RAW + kI4Page;          // [tile parity][warp]: some score is far above the maximum
+  static constexpr uint32_t MAX = FLAG + 32 * kWg;         // [warp][kNc]: the running maxima, log2 units
   static constexpr uint32_t FAC = MAX + 4 * kWg * kNc * 4;       // [warp][kNc]: factors of a rescale or of the output
   static constexpr uint32_t XCH = FAC + 4 * kWg * kNc * 4;       // [maxima, sums][warpgroup][warp][kNc]
   static constexpr uint32_t POISON = XCH + 8 * kWg * kNc * 4;    // [tile % 4][warpgroup][64 keys]
-  static constexpr uint32_t RING = POISON + 256 * kWg;               // kI4Ahead tile records of 32 bytes
+  static constexpr uint32_t RING = POISON + 256 * kWg;     // kI4Ahead tile records of 32 bytes
   static constexpr uint32_t BAR = RING + 32 * kI4Ahead;
   static constexpr uint32_t kBytes = BAR + 512 + 1024;           // + alignment slack
   static_assert(kBytes <= 232448, "shared memory");
@@ -325,8 +328,8 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     for (uint32_t t = 0; read_tile(t, a); ++t) {
       const uint32_t slot = (4 * t + m) % kSlots, phase = (4 * t + m) / kSlots & 1, full = bar(IB_FULL + (kWhole ? t & 1 : slot));
       if (!a.valid()) {
-        // (where it asks for whole tiles, the issuing thread learns of the end as of one)
-        if (kWhole && i4_wait_warp(bar(IB_EMPTY + slot), phase ^ 1, wc, kSiteI4Ring) && lane == 0) mbar_arrive(full);
+        // (the issuing thread learns of the end as of a tile)
+        if (i4_wait_warp(bar(IB_EMPTY + slot), phase ^ 1, wc, kSiteI4Ring) && lane == 0) mbar_arrive(full);
         break;
       }
       if (!i4_wait_warp(bar(IB_RAW), t & 1, wc, kSiteI4Raw)) break;
@@ -430,9 +433,9 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     uint32_t el;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el));
     if (el) {
-      // One thread issues all of them, whatever is ready first: a quarter's scores, or the output of the tile before.  (MMAs of
-      // two warps take turns one by one, and each turn costs: 59 cycles an MMA.  Votes and warp-wide waits between the quarters
-      // cost as much as a quarter's MMAs.)
+      // One thread issues all of them, whatever is ready first: scores of the next tile, or the output of one before.  (MMAs of two
+      // warps take turns one by one, and each turn costs: 59 cycles an MMA.  A warp that votes after every question is slower too,
+      // one that asks with all its lanes at once is not faster.)
       bool ok = true;
       uint32_t piece = 0, t = 0, tp = 0, starts = 0;  // tile t's scores, tile tp's output; bit i: tile t - 1 - i starts a piece
       auto pv = [&]() {
@@ -471,23 +474,20 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         }
       };
       for (;;) {
-        const uint32_t rec_at = t % kI4Ahead, o = t & 1;
-        const uint32_t d = tmem + TS + N * o;
+        const uint32_t o = t & 1, d = tmem + TS + N * o;
         uint64_t bq = desc_q;
         uint32_t slot = 4 * t % kSlots, phase = 4 * t / kSlots & 1;
-        // Where two tiles fit, a tile's quarters are mostly ready together: one question (~120 cycles) for all, and its record
-        // has been seen then.  (All quarters' one by one: 64 streams x 16 heads 99 us instead of 86.)  Where one fits, they become
-        // ready one by one.
-        if constexpr (kWhole) ok = wait(bar(IB_FULL + o), t >> 1 & 1, kSiteI4Ring);
-        else ok = wait(bar(IB_TILE + rec_at), (t / kI4Ahead) & 1, kSiteI4Tile);
-        if (!ok) break;
+        // Where two tiles fit, a tile's quarters are mostly ready together, and one question (~120 cycles) is asked for all (one
+        // for each: 64 streams x 16 heads 93 us instead of 86).  Where one and a half fit, they become ready one by one.
+        if (!(ok = wait(bar(IB_FULL + (kWhole ? o : slot)), kWhole ? t >> 1 & 1 : phase, kSiteI4Ring))) break;
         uint32_t f;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(f) : "r"(base + S::RING + 32 * rec_at) : "memory");
+        // (the expanding warps have seen the tile's record)
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(f) : "r"(base + S::RING + 32 * (t % kI4Ahead)) : "memory");
         if (!(f & I4Tile::kValid)) break;
         if ((f & I4Tile::kFirst) && !(ok = wait(bar(IB_Q_FULL), piece++ & 1, kSiteI4Q))) break;
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
-          if (!kWhole && !(ok = wait(bar(IB_FULL + slot), phase, kSiteI4Ring))) break;
+          if (!kWhole && m > 0 && !(ok = wait(bar(IB_FULL + slot), phase, kSiteI4Ring))) break;
           tc_fence_after();
           const uint64_t ak = desc_k + slot * (kI4Slot >> 4);
 #pragma unroll
@@ -501,7 +501,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         }
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // (every quarter's warps bring a part of the RoPE keys)
+        for (int k = 0; k < 4; ++k)  // (the last two quarters' warps bring the RoPE keys)
           mma_bf16_ss(d, desc_r + (t % S::kR) * (kI4Blk >> 4) + 2 * k, bq + 2 * k, id_qk, 1u);
         mma_commit(bar(IB_S_FULL + o));
         if (f & I4Tile::kLast) mma_commit(bar(IB_Q_EMPTY));
