@@ -65,7 +65,8 @@ typedef enum {
                                (one per 128-code tile, value = code * scale), then k^R as 64 bf16 */
   MLA_KV_INT4 = 2,          /* page = [64][416 bytes]: 512 four-bit codes of c (256 bytes), then 16 bf16 scales (one per
                                32 values), then k^R as 64 bf16.  value = (code - 8) * scale, exact in bf16: a scale has
-                               four significant bits (its low four mantissa bits are zero).  The 32-bit word (little
+                               four significant bits (its low four mantissa bits are zero) and is below 2^121 (larger
+                               ones, infinities and NaN stand for values that are not finite).  The 32-bit word (little
                                endian) of dims 8 w .. 8 w + 7 has the code of dim 8 w + 2 i in bits 4 i .. 4 i + 3 and of dim
                                8 w + 2 i + 1 in bits 16 + 4 i .. 19 + 4 i, i = 0 .. 3 */
 } mla_kv_dtype;
@@ -151,7 +152,8 @@ int32_t mla_get_scheduler_metadata(const mla_decode_params* p, const int32_t* ca
  *   workspace        device, workspace_bytes from mla_get_workspace_size
  * Cache rows of the last page past L_b are not used (they may hold any bits).  INT4 cache: a block-table entry
  * outside [0, num_pages) sets MLA_ERR_INVALID_ARG in the device error word and leaves that sequence's result
- * undefined; a key whose row holds NaN makes NaN of the tokens that see it, and of no others.
+ * undefined; a key whose row holds NaN, or a scale from 2^121 on, makes NaN of
+ * the tokens that see it, and of no others.
  */
 int32_t mla_decode(const mla_decode_params* p, const void* q_nope_absorbed, const void* q_rope, const void* kv_pages,
                    const int32_t* block_table, const int32_t* cache_seqlens, float scale, void* out, float* lse,

@@ -347,7 +347,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         const int key = key0 + 8 * i;
         if (key >= a.nkeys) {
           s2[i] = 0;  // no key: the products must see zeros
-        } else if (key >= a.some && (s2[i] & 0x7F80u) == 0x7F80u) {
+        } else if (key >= a.some && (s2[i] & 0x7FFFu) >= 0x7C00u) {  // from 2^121 on 136 scales overflow
           // a key that only some of the tokens see: its values must not reach the others (0 x NaN); the softmax
           // gives NaN to those that see it
           s2[i] = 0;

@@ -223,10 +223,14 @@ __global__ void __launch_bounds__(256) mla_append_rotated_kernel(const __grid_co
   pdl_launch_dependents();
   if (t >= g.max_tokens) return;
   uint4 a = make_uint4(0, 0, 0, 0), b = a, ra = a, rb = a;
+  uint2 four[4];  // values 128 k + 4 lane ..
   if (share == 0) {
     const uint4* src = reinterpret_cast<const uint4*>(g.latent + t * g.latent_stride);
     a = src[2 * lane];
     b = src[2 * lane + 1];
+    if (g.weight)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) four[k] = reinterpret_cast<const uint2*>(src)[32 * k + lane];
     const uint4* r = reinterpret_cast<const uint4*>(g.rope + t * g.rope_stride);
     ra = r[c];
     rb = r[c + 4];
@@ -256,15 +260,23 @@ __global__ void __launch_bounds__(256) mla_append_rotated_kernel(const __grid_co
   if (share == 0) {
     rotate16(ra, rb, cs, sn, kInterleaved);
     if (g.weight) {
-      // float32 throughout, rounded to bf16 once: what a norm of its own would hand to the append
-      float x[16], w[16], sum = 0.f;
+      // float32 throughout, rounded to bf16 once: what a norm of its own would hand to the append.  Squares are summed four
+      // neighbours at a time across the warp, then over the four, then over neighbouring lanes: as a norm in elementary operations
+      // sums float32 rows, so that its last bit is the same too (a bf16 value that it turns can turn a whole 4-bit code).
+      float x[16], w[16], part[4] = {0.f, 0.f, 0.f, 0.f};
       widen16(a, b, x);
       const uint4* ws = reinterpret_cast<const uint4*>(g.weight);
       widen16(ws[2 * lane], ws[2 * lane + 1], w);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) sum = fmaf(x[k], x[k], sum);
+      for (int k = 0; k < 4; ++k) {
+        const float v[4] = {__uint_as_float(four[k].x << 16), __uint_as_float(four[k].x & 0xFFFF0000u), __uint_as_float(four[k].y << 16),
+                            __uint_as_float(four[k].y & 0xFFFF0000u)};
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int i = 0; i < 4; ++i) part[i] = fmaf(v[i], v[i], part[i]);
+      }
+      float sum = part[0] + part[1] + part[2] + part[3];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       const float inv = rsqrtf(sum * (1.f / 512.f) + g.eps);
       uint32_t y[8];
 #pragma unroll

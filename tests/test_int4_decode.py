@@ -167,6 +167,26 @@ def test_a_key_that_holds_nan(H, s_q, where, row):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,s_q", [(16, 4), (128, 3)])
+@pytest.mark.parametrize("bits", [0x7C00, 0x7F00, 0x7F80])
+@pytest.mark.parametrize("row", [297, 299])
+def test_a_scale_that_overflows(H, s_q, bits, row):
+    """2^121, the largest binade and infinity: tokens that do not see the key keep their bits."""
+    import torch
+    L = [300, 70]
+    q = Problem(L, H, s_q=s_q, seed=10)
+    before, lse0 = q.run()
+    q.pool[int(q.bt[0, row // 64]), row % 64][256:288].view(torch.int16)[3] = bits
+    out, lse = q.run()
+    for t in range(s_q):
+        if row < L[0] - (s_q - 1 - t):
+            assert torch.isnan(out[0, t]).all() and torch.isnan(lse[0, t]).all()
+        else:
+            assert torch.equal(out[0, t], before[0, t]) and torch.equal(lse[0, t], lse0[0, t])
+    assert torch.equal(out[1], before[1]) and torch.equal(lse[1], lse0[1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("H,units", [(16, 0), (40, 5), (128, 0)])
 def test_the_same_bits_every_time(H, units):
     import torch
