@@ -14,14 +14,14 @@
 // That one copy is both products' A operand: blocks [64 keys][64 dims] of shared memory with the 128-byte swizzle, K-major for the
 // scores (M = 64), MN-major for the output (M = 128 dims).  MMAs of K = 16 take 32 / 32 / 37 cycles for the scores, 44 / 44 / 50
 // for the output (N = 16 / 32 / 64).  What bounds them is the shared memory: both operands of every MMA, the pages and the expanded
-// keys are ~2000 cycles of its bandwidth a tile for N = 16, ~2850 for N = 64; a tile takes 2500 and 4000.  (The scores' A in tensor
+// keys are ~2000 cycles of its bandwidth a tile for N = 16, ~2850 for N = 64; a tile takes 2500 and 3800.  (The scores' A in tensor
 // memory is read without it, at 12 to 32 cycles an MMA, but beside the expanding warps' stores there they took 53, and the output's
-// MMAs 70: 64 streams x 16 heads 87 us instead of 83, 128 heads ragged 218 instead of 157.)
+// MMAs 70: 64 streams x 16 heads 87 us instead of 83, 128 heads ragged 218 instead of 153.)
 //
 // Pages come by bulk copies into shared memory, as they are.  (Loads into registers, 64 bytes of a row at a time, kept the load
 // units busy for ~1500 cycles a page.  A second page ahead changed nothing.)  The four quarters of a tile (128 dims each) are
 // expanded by four warps each into a ring of quarters of 16 KB, eight up to 32 rows, six for 64: there the next tile's first two are
-// expanded and multiplied with the queries while the softmax works (with four: 178 us instead of 157).
+// expanded and multiplied with the queries while the softmax works (with four: 178 us instead of 153).
 //
 // The scores' 64 rows are lanes 0..15 of each of tensor memory's four quadrants; the 16-lane loads deal a row of columns out to
 // four lanes in turn: lane j of a quad has rows 4 b + j of the block, and its weights are neighbours in P, so that row 4 b + j of a
@@ -31,8 +31,8 @@
 // warps, so scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the new maxima found and O
 // rescaled); 16 warps expand; one copies pages and queries and writes the tiles' records; a thread of the last issues the MMAs.
 //
-// Measured: 64 streams x 16 heads, 190 MB of cache, 83 us; 128 heads, 64 ragged sequences up to 32,768 keys (142 MB) 157 us, 4 up to
-// 131,072 (94 MB) 119 us; 24 sequences of 4 tokens x 20 heads (36 MB) 60 us.
+// Measured: 64 streams x 16 heads, 190 MB of cache, 83 us; 128 heads, 64 ragged sequences up to 32,768 keys (142 MB) 153 us, 4 up to
+// 131,072 (94 MB) 115 us; 24 sequences of 4 tokens x 20 heads (36 MB) 59 us.
 #pragma once
 #include "common.cuh"
 #include "decode_kernel.cuh"  // packed float pairs, bf16 packing
@@ -54,12 +54,12 @@ struct I4Smem {
   static constexpr int kNc = N / kWg;                            // columns of each
   static constexpr int kThreads = 128 * kWg + 576;
   static constexpr int kSlots = N == 64 ? 6 : 8;           // a ring of quarter tiles
-  static constexpr int kR = N == 64 ? 1 : 2;                     // tiles' RoPE keys, a block each
+  static constexpr int kP = N == 64 ? 1 : 2;                     // tiles' weights
   static constexpr uint32_t V = 0;
-  static constexpr uint32_t R = V + kSlots * kI4Slot;
-  static constexpr uint32_t Q = R + kR * kI4Blk;                 // 9 blocks [N rows][64 dims]
-  static constexpr uint32_t P = Q + 9 * N * 128;                 // [tile parity][64 keys][N]
-  static constexpr uint32_t RAW = P + 2 * N * 128;               // a page as it came
+  static constexpr uint32_t R = V + kSlots * kI4Slot;            // RoPE keys: [tile parity] a block
+  static constexpr uint32_t Q = R + 2 * kI4Blk;                  // 9 blocks [N rows][64 dims]
+  static constexpr uint32_t P = Q + 9 * N * 128;                 // [kP][64 keys][N]
+  static constexpr uint32_t RAW = P + kP * N * 128;              // a page as it came
   static constexpr uint32_t FLAG = RAW + kI4Page;          // [tile parity][warp]: some score is far above the maximum
   static constexpr uint32_t MAX = FLAG + 32 * kWg;         // [warp][kNc]: the running maxima, log2 units
   static constexpr uint32_t FAC = MAX + 4 * kWg * kNc * 4;       // [warp][kNc]: factors of a rescale or of the output
@@ -321,8 +321,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       chunk[q] = base + S::V + (j >> 1) * kI4Blk + p0 * 128 + (((uint32_t)(4 * (j & 1)) ^ (uint32_t)(p0 & 7) ^ (uint32_t)q ^ turn) << 4);
-    // RoPE keys: the last two quarters' warps (their slots are free later than the block that they write) take 32 values each, a
-    // lane a chunk of the row
+    // RoPE keys: the first two quarters' warps take 32 values each, a lane a chunk of the row
     const uint32_t rope_dst = base + S::R + p0 * 128 + ((uint32_t)(4 * (m & 1) + j) ^ (uint32_t)(p0 & 7)) * 16;
     I4Tile a;
     for (uint32_t t = 0; read_tile(t, a); ++t) {
@@ -338,7 +337,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       for (int i = 0; i < 2; ++i) {
         lds128(src_lane + i * kNext + 64 * m, code[i]);
         s2[i] = lds16(src_lane + i * kNext + kI4Codes + 8 * m - 14 * j);
-        if (m >= 2) lds128(src_lane + i * kNext + kI4Rope + 64 * (m & 1), rope[i]);
+        if (m < 2) lds128(src_lane + i * kNext + kI4Rope + 64 * (m & 1), rope[i]);
       }
       uint32_t poison = 0;
 #pragma unroll
@@ -357,22 +356,29 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(IB_RAW_EMPTY));
+      uint32_t o[4][2][4];
+      auto expand = [&]() {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) expand_int4_word(turn ? code[i][q ^ 2] : code[i][q], s2[i], a2[i], o[q][i]);
+      };
+      // At 64 rows the next scores wait for the slots: the values are there before (ragged 128 heads 153 us instead of 155).  Below, the
+      // expanding warps would only be in the others' way (64 streams x 16 heads 85 us instead of 83).
+      if (!kWhole) expand();
       if (!i4_wait_warp(bar(IB_EMPTY + slot), phase ^ 1, wc, kSiteI4Ring)) break;
       // (only now: the softmax has read and reset the bytes of the tile four before)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (poison >> i & 1) for (int g = 0; g < S::kWg; ++g) smem[S::POISON + 64 * (S::kWg * (t & 3) + g) + p0 + 8 * i] = 1;
+      if (kWhole) expand();
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t o[4];
-          expand_int4_word(turn ? code[i][q ^ 2] : code[i][q], s2[i], a2[i], o);
-          sts128(chunk[q] + slot * kI4Slot + i * 1024, o[0], o[1], o[2], o[3]);
-        }
-      if (m >= 2)
+        for (int i = 0; i < 2; ++i) sts128(chunk[q] + slot * kI4Slot + i * 1024, o[q][i][0], o[q][i][1], o[q][i][2], o[q][i][3]);
+      if (m < 2)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) sts128(rope_dst + (t % S::kR) * kI4Blk + i * 1024, rope[i][0], rope[i][1], rope[i][2], rope[i][3]);
+        for (int i = 0; i < 2; ++i) sts128(rope_dst + (t & 1) * kI4Blk + i * 1024, rope[i][0], rope[i][1], rope[i][2], rope[i][3]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
@@ -440,7 +446,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       uint32_t piece = 0, t = 0, tp = 0, starts = 0;  // tile t's scores, tile tp's output; bit i: tile t - 1 - i starts a piece
       auto pv = [&]() {
         const uint32_t add = starts >> (t - 1 - tp) & 1 ? 0u : 1u;
-        const uint64_t w = desc_p + (tp & 1) * (N * 128 >> 4);
+        const uint64_t w = desc_p + (tp % S::kP) * (N * 128 >> 4);
         uint32_t slot = 4 * tp % kSlots;
         tc_fence_after();
 #pragma unroll
@@ -485,24 +491,29 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(f) : "r"(base + S::RING + 32 * (t % kI4Ahead)) : "memory");
         if (!(f & I4Tile::kValid)) break;
         if ((f & I4Tile::kFirst) && !(ok = wait(bar(IB_Q_FULL), piece++ & 1, kSiteI4Q))) break;
+        auto quarters = [&](int m, int end) {
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          if (!kWhole && m > 0 && !(ok = wait(bar(IB_FULL + slot), phase, kSiteI4Ring))) break;
-          tc_fence_after();
-          const uint64_t ak = desc_k + slot * (kI4Slot >> 4);
+          for (; m < end; ++m) {
+            if (!kWhole && m > 0 && !(ok = wait(bar(IB_FULL + slot), phase, kSiteI4Ring))) break;
+            tc_fence_after();
+            const uint64_t ak = desc_k + slot * (kI4Slot >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_bf16_ss(d, ak + (k >> 2) * (kI4Blk >> 4) + 2 * (k & 3), bq + (k >> 2) * (N * 128 >> 4) + 2 * (k & 3), id_qk, m + k ? 1u : 0u);
-          if (++slot == kSlots) {
-            slot = 0;
-            phase ^= 1;
+            for (int k = 0; k < 8; ++k)
+              mma_bf16_ss(d, ak + (k >> 2) * (kI4Blk >> 4) + 2 * (k & 3), bq + (k >> 2) * (N * 128 >> 4) + 2 * (k & 3), id_qk, m + k ? 1u : 0u);
+            if (++slot == kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
+            bq += 2 * N * 128 >> 4;
           }
-          bq += 2 * N * 128 >> 4;
-        }
+        };
+        quarters(0, 2);
         if (!ok) break;
+        // (the first two quarters' warps have brought the RoPE keys)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // (the last two quarters' warps bring the RoPE keys)
-          mma_bf16_ss(d, desc_r + (t % S::kR) * (kI4Blk >> 4) + 2 * k, bq + 2 * k, id_qk, 1u);
+        for (int k = 0; k < 4; ++k) mma_bf16_ss(d, desc_r + o * (kI4Blk >> 4) + 2 * k, desc_q + (8 * N * 128 >> 4) + 2 * k, id_qk, 1u);
+        quarters(2, 4);
+        if (!ok) break;
         mma_commit(bar(IB_S_FULL + o));
         if (f & I4Tile::kLast) mma_commit(bar(IB_Q_EMPTY));
         starts = starts << 1 | (f & I4Tile::kFirst ? 1u : 0u);
@@ -623,7 +634,8 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       if (!(ok = i4_wait_warp(bar(IB_FLAG + 2 * wg + (t & 1)), (t >> 1) & 1, wc, kSiteI4Flag))) break;
       uint32_t f4[4];
       lds128(base + S::FLAG + 16 * S::kWg * (t & 1) + 16 * wg, f4);
-      // (P is free: the tile's keys took the place of those whose output product read it)
+      // (P is free: the scores' commit waited for all MMAs issued before them, the last output product that read it among them: for
+      // two P that of tile t - 2, for one that of tile t - 1, which gave the place for this tile's last quarters)
       if ((f4[0] | f4[1] | f4[2] | f4[3]) != 0) {
         if (t > 0 && !(ok = wait_pv(t - 1))) break;  // the output so far is complete
         tc_fence_after();
@@ -680,7 +692,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
           l[b + 1] += x1;
         }
         const int p = p0 + 8 * i;
-        const uint32_t swz = N == 64 ? p & 7 : N == 32 ? (p >> 1) & 3 : (p >> 2) & 1, at = base + S::P + (t & 1) * (N * 128) + p * (2 * N);
+        const uint32_t swz = N == 64 ? p & 7 : N == 32 ? (p >> 1) & 3 : (p >> 2) & 1, at = base + S::P + (t % S::kP) * (N * 128) + p * (2 * N);
         if constexpr (B == 8)
           sts128(at + (((uint32_t)(col0 / 8 + j) ^ swz) << 4), pp[0], pp[1], pp[2], pp[3]);
         else
