@@ -497,13 +497,21 @@ def mla_append_rotated_kv(p: MlaPoolParams, latent, k_rope, cos_sin, cu_seqlens,
     token's position is its row in its sequence, or positions[t] (int32 [T]).  Returns q_out."""
     i32, f32, bf16 = _dtypes()
     B, call = p.batch, "mla_append_rotated_kv: "
-    for name, t, n in (("latent", latent, 512), ("k_rope", k_rope, 64)):
-        if t is None or t.dtype != bf16 or t.dim() != 2 or t.shape[1] != n or t.stride(1) != 1:
-            _refuse(call + name)
-    T = int(latent.shape[0])
-    if k_rope.shape[0] != T:
+    # (shapes and strides are asked for once each: a step's call is bound by the host)
+    if latent is None or latent.dtype is not bf16 or latent.dim() != 2:
+        _refuse(call + "latent")
+    (T, n), (latent_stride, one) = latent.shape, latent.stride()
+    if n != 512 or one != 1:
+        _refuse(call + "latent")
+    if k_rope is None or k_rope.dtype is not bf16 or k_rope.dim() != 2:
         _refuse(call + "k_rope")
-    if cos_sin is None or cos_sin.dim() != 2 or _bad(cos_sin, f32, (cos_sin.shape[0], 64)) or cos_sin.shape[0] == 0:
+    (n, width), (rope_stride, one) = k_rope.shape, k_rope.stride()
+    if n != T or width != 64 or one != 1:
+        _refuse(call + "k_rope")
+    if cos_sin is None or cos_sin.dtype is not f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        _refuse(call + "cos_sin")
+    num_positions, width = cos_sin.shape
+    if width != 64 or num_positions == 0:
         _refuse(call + "cos_sin")
     if _bad(cu_seqlens, i32, (B + 1,)):
         _refuse(call + "cu_seqlens")
@@ -517,20 +525,23 @@ def mla_append_rotated_kv(p: MlaPoolParams, latent, k_rope, cos_sin, cu_seqlens,
         _refuse(call + "norm_weight")
     if served is not None and _bad(served, i32, (B,)):
         _refuse(call + "served")
-    H = 0
+    H = token_stride = head_stride = q_at = out_at = 0
     if q_rope is not None:
-        if q_rope.dtype != bf16 or q_rope.dim() != 3 or q_rope.shape[0] != T or q_rope.shape[2] != 64 or q_rope.stride(2) != 1:
+        if q_rope.dtype is not bf16 or q_rope.dim() != 3:
             _refuse(call + "q_rope")
-        H = int(q_rope.shape[1])
+        (n, H, width), (token_stride, head_stride, one) = q_rope.shape, q_rope.stride()
+        if n != T or width != 64 or one != 1:
+            _refuse(call + "q_rope")
         if q_out is None:
             q_out = _new(q_rope, stream, (T, H, 64), bf16)
         elif _bad(q_out, bf16, (T, H, 64)):
             _refuse(call + "q_out")
         # (read and written by the same threads where the two are one, by others where they merely overlap)
-        if T and H and not (q_out.data_ptr() == q_rope.data_ptr() and q_rope.is_contiguous()):
-            lo, out = q_rope.data_ptr(), q_out.data_ptr()
-            hi = lo + 2 * ((T - 1) * q_rope.stride(0) + (H - 1) * q_rope.stride(1) + 64)
-            if lo < out + q_out.numel() * 2 and out < hi:
+        if T and H:
+            q_at, out_at = q_rope.data_ptr(), q_out.data_ptr()
+            last = (T - 1) * token_stride + (H - 1) * head_stride + 64
+            if (q_at < out_at + T * H * 128 and out_at < q_at + 2 * last
+                    and not (out_at == q_at and q_rope.is_contiguous())):
                 _refuse(call + "q_out overlaps q_rope")
     elif q_out is not None:
         _refuse(call + "q_out without q_rope")
@@ -538,13 +549,12 @@ def mla_append_rotated_kv(p: MlaPoolParams, latent, k_rope, cos_sin, cu_seqlens,
     if T == 0:
         return q_out
     _expect_device("mla_append_rotated_kv", latent, k_rope, cos_sin, cu_seqlens, cache_seqlens, block_table, kv_pages,
-                   *(t for t in (positions, norm_weight, served, q_rope, q_out) if t is not None))
+                   *[t for t in (positions, norm_weight, served, q_rope, q_out) if t is not None])
     # (one row, or one head: its stride says nothing)
-    r = MlaRotateParams(T, int(latent.stride(0)) if T > 1 else 512, int(k_rope.stride(0)) if T > 1 else 64,
-                        int(q_rope.stride(0)) if H and T > 1 else 0, int(q_rope.stride(1)) if H > 1 else 0, H, int(bool(interleaved)),
-                        int(cos_sin.shape[0]), float(norm_eps))
+    r = MlaRotateParams(T, latent_stride if T > 1 else 512, rope_stride if T > 1 else 64, token_stride if H and T > 1 else 0,
+                        head_stride if H > 1 else 0, H, 1 if interleaved else 0, num_positions, norm_eps)
     _check(load_library().mla_append_rotated_kv(ctypes.byref(p), ctypes.byref(r), latent.data_ptr(), k_rope.data_ptr(), _ptr(norm_weight),
-                                                cos_sin.data_ptr(), _ptr(positions), _ptr(q_rope) if H else 0, _ptr(q_out) if H else 0,
+                                                cos_sin.data_ptr(), _ptr(positions), q_at, out_at,
                                                 cu_seqlens.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(), _ptr(served),
                                                 kv_pages.data_ptr(), _stream(stream)), "mla_append_rotated_kv")
     return q_out
