@@ -90,7 +90,7 @@ enum : uint32_t {
 constexpr uint32_t kI4TmemSlot = 8 * kI4Bars, kI4Abort = kI4TmemSlot + 4;
 static_assert(kI4Abort + 4 <= 512, "barrier area");
 
-enum I4Site : int { kSiteI4Ring = 44, kSiteI4Q, kSiteI4Scores, kSiteI4P, kSiteI4Pv, kSiteI4Flag, kSiteI4Drain, kSiteI4Tile, kSiteI4Raw };
+enum I4Site : int { kSiteI4Ring = 44, kSiteI4Q, kSiteI4Scores, kSiteI4Pv, kSiteI4Flag, kSiteI4Drain, kSiteI4Tile, kSiteI4Raw };
 
 struct Int4Args {
   CUtensorMap map_q;     // q~ rows: bf16 {64, rows, 8 blocks 128 bytes apart}, box {64, N, 8}, 128-byte swizzle
