@@ -7,7 +7,7 @@
 // HBM, beyond that the tensor cores; and a key's 512 values have to become bf16 in every SM that reads it.
 //
 // Work split.  The keys are the M dimension: S^T = K Q^T and O^T = C^T P^T.  A tile is a page, 64 keys, expanded once
-// by a CTA that needs no other's help: up to 64 rows are its N = 16, 32 or 64 columns, O^T is 4 x [128 dims x N] in tensor
+// by a CTA that needs no other's help: up to 64 rows are its N = 16, 32, 48 or 64 columns, O^T is 4 x [128 dims x N] in tensor
 // memory.  A unit of the plan is one CTA, or two for 65 to 128 heads, which read the same pages at the same time (the
 // second from L2).  With several new tokens a sequence, as many as fit into 64 rows share every key.
 //
@@ -50,16 +50,17 @@ static_assert(kI4Tile == kTile, "a tile of the plan is a page");
 
 template <int N>
 struct I4Smem {
-  static constexpr int kWg = N == 64 ? 2 : 1;                    // softmax warpgroups
+  static constexpr int kWg = N == 64 ? 2 : N == 48 ? 3 : 1;      // softmax warpgroups
   static constexpr int kNc = N / kWg;                            // columns of each
   static constexpr int kThreads = 128 * kWg + 576;
-  static constexpr int kSlots = N == 64 ? 6 : 8;           // a ring of quarter tiles
-  static constexpr int kP = N == 64 ? 1 : 2;                     // tiles' weights
+  static constexpr int kSlots = N == 64 ? 6 : N == 48 ? 7 : 8;  // a ring of quarter tiles
+  static constexpr int kP = N > 32 ? 1 : 2;                      // tiles' weights
   static constexpr uint32_t V = 0;
+  static constexpr uint32_t kPRow = N > 32 ? 128 : 2 * N;        // bytes of a key's weights
   static constexpr uint32_t R = V + kSlots * kI4Slot;            // RoPE keys: [tile parity] a block
   static constexpr uint32_t Q = R + 2 * kI4Blk;                  // 9 blocks [N rows][64 dims]
-  static constexpr uint32_t P = Q + 9 * N * 128;                 // [kP][64 keys][N]
-  static constexpr uint32_t RAW = P + kP * N * 128;              // a page as it came
+  static constexpr uint32_t P = Q + 9 * N * 128;                 // [kP][64 keys][kPRow]
+  static constexpr uint32_t RAW = P + kP * 64 * kPRow;              // a page as it came
   static constexpr uint32_t FLAG = RAW + kI4Page;          // [tile parity][warp]: some score is far above the maximum
   static constexpr uint32_t MAX = FLAG + 32 * kWg;         // [warp][kNc]: the running maxima, log2 units
   static constexpr uint32_t FAC = MAX + 4 * kWg * kNc * 4;       // [warp][kNc]: factors of a rescale or of the output
@@ -72,8 +73,8 @@ struct I4Smem {
 };
 
 enum : uint32_t {
-  IB_FULL = 0,               // N = 64: + slot, else + tile parity: one arrival per expanding warp
-  IB_EMPTY = IB_FULL + 6,    // + slot: the output product has read it
+  IB_FULL = 0,               // six or seven slots: + slot, else + tile parity: one arrival per expanding warp
+  IB_EMPTY = IB_FULL + 7,    // + slot: the output product has read it
   IB_RAW = IB_EMPTY + 8,     // landed
   IB_RAW_EMPTY,              // one arrival per expanding warp
   IB_Q_FULL,
@@ -81,8 +82,8 @@ enum : uint32_t {
   IB_S_FULL,                 // + tile parity
   IB_P_FULL = IB_S_FULL + 2, // + tile parity: one arrival per softmax warp
   IB_FLAG = IB_P_FULL + 2,   // + 2 warpgroup + tile parity: one arrival per warp
-  IB_XCH = IB_FLAG + 4,      // + warpgroup
-  IB_TILE = IB_XCH + 2,      // + record: written
+  IB_XCH = IB_FLAG + 6,      // + warpgroup
+  IB_TILE = IB_XCH + 3,      // + record: written
   IB_TILE_READ = IB_TILE + kI4Ahead,  // + record: one arrival per softmax warp, the last readers
   IB_DRAIN = IB_TILE_READ + kI4Ahead,
   kI4Bars = IB_DRAIN + 1
@@ -435,7 +436,7 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
     // descriptors: an address 16 n bytes further is n more in the low word
     const uint64_t desc_k = smem_desc(base + S::V, 16, 1024, kSwizzle128B), desc_r = smem_desc(base + S::R, 16, 1024, kSwizzle128B);
     const uint64_t desc_q = smem_desc(base + S::Q, 16, 1024, kSwizzle128B), desc_c = smem_desc(base + S::V, kI4Blk, 1024, kSwizzle128B);
-    const uint64_t desc_p = smem_desc(base + S::P, 16, N * 16, N == 64 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
+    const uint64_t desc_p = smem_desc(base + S::P, 16, 8 * S::kPRow, N > 32 ? kSwizzle128B : N == 32 ? kSwizzle64B : kSwizzle32B);
     uint32_t el;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el));
     if (el) {
@@ -446,14 +447,14 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       uint32_t piece = 0, t = 0, tp = 0, starts = 0;  // tile t's scores, tile tp's output; bit i: tile t - 1 - i starts a piece
       auto pv = [&]() {
         const uint32_t add = starts >> (t - 1 - tp) & 1 ? 0u : 1u;
-        const uint64_t w = desc_p + (tp % S::kP) * (N * 128 >> 4);
+        const uint64_t w = desc_p + (tp % S::kP) * (64 * S::kPRow >> 4);
         uint32_t slot = 4 * tp % kSlots;
         tc_fence_after();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint64_t c = desc_c + slot * (kI4Slot >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16_ss(tmem + TO + N * m, c + 128 * k, w + (N * 32 >> 4) * k, id_pv, k ? 1u : add);
+          for (int k = 0; k < 4; ++k) mma_bf16_ss(tmem + TO + N * m, c + 128 * k, w + S::kPRow * k, id_pv, k ? 1u : add);
           mma_commit(bar(IB_EMPTY + slot));
           slot = slot + 1 == kSlots ? 0 : slot + 1;
         }
@@ -692,11 +693,11 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
           l[b + 1] += x1;
         }
         const int p = p0 + 8 * i;
-        const uint32_t swz = N == 64 ? p & 7 : N == 32 ? (p >> 1) & 3 : (p >> 2) & 1, at = base + S::P + (t % S::kP) * (N * 128) + p * (2 * N);
+        const uint32_t swz = N > 32 ? p & 7 : N == 32 ? (p >> 1) & 3 : (p >> 2) & 1, at = base + S::P + (t % S::kP) * (64 * S::kPRow) + p * S::kPRow;
         if constexpr (B == 8)
           sts128(at + (((uint32_t)(col0 / 8 + j) ^ swz) << 4), pp[0], pp[1], pp[2], pp[3]);
         else
-          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(at + (((uint32_t)(j >> 1) ^ swz) << 4) + 8 * (j & 1)), "r"(pp[0]), "r"(pp[1]) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(at + (((uint32_t)(col0 / 8 + (j >> 1)) ^ swz) << 4) + 8 * (j & 1)), "r"(pp[0]), "r"(pp[1]) : "memory");
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -777,6 +778,9 @@ __global__ void __launch_bounds__(I4Smem<16>::kThreads, 1) mla_decode_int4_n16_k
 }
 __global__ void __launch_bounds__(I4Smem<32>::kThreads, 1) mla_decode_int4_n32_kernel(const __grid_constant__ Int4Args args) {
   decode_int4_body<32>(args);
+}
+__global__ void __launch_bounds__(I4Smem<48>::kThreads, 1) mla_decode_int4_n48_kernel(const __grid_constant__ Int4Args args) {
+  decode_int4_body<48>(args);
 }
 __global__ void __launch_bounds__(I4Smem<64>::kThreads, 1) mla_decode_int4_n64_kernel(const __grid_constant__ Int4Args args) {
   decode_int4_body<64>(args);

@@ -233,6 +233,7 @@ int32_t device_info(DeviceInfo** out) {
         return MLA_ERR_CUDA;
     if (cudaFuncSetAttribute(mla_decode_int4_n16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I4Smem<16>::kBytes) != cudaSuccess ||
         cudaFuncSetAttribute(mla_decode_int4_n32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I4Smem<32>::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(mla_decode_int4_n48_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I4Smem<48>::kBytes) != cudaSuccess ||
         cudaFuncSetAttribute(mla_decode_int4_n64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I4Smem<64>::kBytes) != cudaSuccess)
       return MLA_ERR_CUDA;
     for (int G = 1; G <= 4; ++G) {  // GPCs hold whole clusters: bigger ones leave SMs idle
@@ -438,7 +439,7 @@ int32_t launch_int4(const mla_decode_params* p, int32_t U, const void* q_nope, c
   std::memset(&a, 0, sizeof a);
   a.parts = parts;
   a.part_rows = parts > 1 ? (H + 1) / 2 : G * H;
-  const int N = a.part_rows <= 16 ? 16 : a.part_rows <= 32 ? 32 : 64;
+  const int N = a.part_rows <= 16 ? 16 : a.part_rows <= 32 ? 32 : a.part_rows <= 48 ? 48 : 64;
   const uint64_t rows = (uint64_t)NQB * H;
   const uint64_t dq[3] = {64, rows, 8}, sq[2] = {1024, 128}, dr[2] = {64, rows}, sr[1] = {128};
   const uint32_t bq[3] = {64, (uint32_t)N, 8}, br[2] = {64, (uint32_t)N};
@@ -468,8 +469,8 @@ int32_t launch_int4(const mla_decode_params* p, int32_t U, const void* q_nope, c
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(parts * U, 1, 1);
-  cfg.blockDim = dim3(N == 16 ? I4Smem<16>::kThreads : N == 32 ? I4Smem<32>::kThreads : I4Smem<64>::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = N == 16 ? I4Smem<16>::kBytes : N == 32 ? I4Smem<32>::kBytes : I4Smem<64>::kBytes;
+  cfg.blockDim = dim3(N == 16 ? I4Smem<16>::kThreads : N == 32 ? I4Smem<32>::kThreads : N == 48 ? I4Smem<48>::kThreads : I4Smem<64>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = N == 16 ? I4Smem<16>::kBytes : N == 32 ? I4Smem<32>::kBytes : N == 48 ? I4Smem<48>::kBytes : I4Smem<64>::kBytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -477,6 +478,7 @@ int32_t launch_int4(const mla_decode_params* p, int32_t U, const void* q_nope, c
   cfg.numAttrs = 1;
   const cudaError_t e = N == 16   ? cudaLaunchKernelEx(&cfg, mla_decode_int4_n16_kernel, a)
                         : N == 32 ? cudaLaunchKernelEx(&cfg, mla_decode_int4_n32_kernel, a)
+                        : N == 48 ? cudaLaunchKernelEx(&cfg, mla_decode_int4_n48_kernel, a)
                                   : cudaLaunchKernelEx(&cfg, mla_decode_int4_n64_kernel, a);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
