@@ -20,19 +20,20 @@
 //
 // Pages come by bulk copies into shared memory, as they are.  (Loads into registers, 64 bytes of a row at a time, kept the load
 // units busy for ~1500 cycles a page.  A second page ahead changed nothing.)  The four quarters of a tile (128 dims each) are
-// expanded by four warps each into a ring of quarters of 16 KB, eight up to 32 rows, six for 64: there the next tile's first two are
+// expanded by four warps each into a ring of quarters of 16 KB, eight up to 32 rows, seven for 48, six for 64: there the next tile's first ones are
 // expanded and multiplied with the queries while the softmax works (with four: 178 us instead of 153).
 //
 // The scores' 64 rows are lanes 0..15 of each of tensor memory's four quadrants; the 16-lane loads deal a row of columns out to
 // four lanes in turn: lane j of a quad has rows 4 b + j of the block, and its weights are neighbours in P, so that row 4 b + j of a
 // warpgroup is column j NC / 4 + b of P and O^T.
 //
-// Roles (warps): softmax (one warpgroup, two for N = 64, half of the columns each; a row's maximum lies across lanes and
+// Roles (warps): softmax (a warpgroup for 16 columns, for N = 64 for 32; a row's maximum lies across lanes and
 // warps, so scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the new maxima found and O
 // rescaled); 16 warps expand; one copies pages and queries and writes the tiles' records; a thread of the last issues the MMAs.
 //
 // Measured: 64 streams x 16 heads, 190 MB of cache, 83 us; 128 heads, 64 ragged sequences up to 32,768 keys (142 MB) 153 us, 4 up to
-// 131,072 (94 MB) 115 us; 24 sequences of 4 tokens x 20 heads (36 MB) 59 us.
+// 131,072 (94 MB) 115 us; 24 sequences of 4 tokens x 20 heads (36 MB) 54 us (with
+// 64 columns 59).  64 x 8192 keys, 218 MB: 32 heads 100 us, 40 128, 64 134.
 #pragma once
 #include "common.cuh"
 #include "decode_kernel.cuh"  // packed float pairs, bf16 packing
@@ -50,7 +51,7 @@ static_assert(kI4Tile == kTile, "a tile of the plan is a page");
 
 template <int N>
 struct I4Smem {
-  static constexpr int kWg = N == 64 ? 2 : N == 48 ? 3 : 1;      // softmax warpgroups
+  static constexpr int kWg = N == 64 ? 2 : N / 16;               // softmax warpgroups (64: four would be 34 warps)
   static constexpr int kNc = N / kWg;                            // columns of each
   static constexpr int kThreads = 128 * kWg + 576;
   static constexpr int kSlots = N == 64 ? 6 : N == 48 ? 7 : 8;  // a ring of quarter tiles
