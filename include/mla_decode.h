@@ -167,7 +167,8 @@ int32_t mla_decode(const mla_decode_params* p, const void* q_nope_absorbed, cons
  *                         partials (in workspace) of the others;
  *   mla_combine        -- merges the split partials through their LSE into
  *                         out/lse and writes out = 0, lse = -inf for tokens that
- *                         see no key.  Must follow mla_decode_splitkv on the
+ *                         see no key.  A partial with lse = NaN makes NaN of the
+ *                         row, in out and lse.  Must follow mla_decode_splitkv on the
  *                         same stream with the same p, sched and workspace.
  * mla_decode == mla_decode_splitkv followed by mla_combine.
  */

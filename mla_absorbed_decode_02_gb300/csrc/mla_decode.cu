@@ -55,7 +55,9 @@ __global__ void __launch_bounds__(1024) mla_sched_kernel(const int32_t* seqlens,
 // out = sum_i exp(lse_i - lse) * out_i, lse = M + ln sum_i exp(lse_i - M), M = max_i lse_i
 // (the merge of split-KV partial results, "MLA inference: two computation paths and
 // FlashMLA", section "Decode attention becomes a compute problem").  Query blocks that see
-// no key get out = 0, lse = -inf.  One CTA of 256 threads per (query block, 16 heads, one
+// no key get out = 0, lse = -inf; a split with lse = NaN makes NaN of both (a maximum would
+// drop it, and a row of NaN alone would look like one that saw no key).
+// One CTA of 256 threads per (query block, 16 heads, one
 // of Z column slices): the 16 combined LSEs first (two heads per warp, the splits spread
 // over 16 lanes), then 16 threads per head stream the slice's float4 columns of every
 // split, kNf columns each, the splits dealt round-robin over kG adjacent lanes (summed by
@@ -83,7 +85,13 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(const int32_t* sched, 
   {
     const int hh = 2 * warp + (lane >> 4), h = h0 + hh, sub = lane & 15;
     float M = -INFINITY;
-    for (int i = sub; i < ns && h < H; i += 16) M = fmaxf(M, lse_acc[(int64_t)(off + i) * H + h]);
+    bool nan = false;
+    for (int i = sub; i < ns && h < H; i += 16) {
+      const float x = lse_acc[(int64_t)(off + i) * H + h];
+      nan |= isnan(x);
+      M = fmaxf(M, x);
+    }
+    nan = (__ballot_sync(0xffffffffu, nan) >> (lane & 16) & 0xFFFFu) != 0;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float S = 0.f;
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(const int32_t* sched, 
       for (int i = sub; i < ns && h < H; i += 16) S += expf(lse_acc[(int64_t)(off + i) * H + h] - M);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-    if (sub == 0) s_lse[hh] = M > -INFINITY ? M + logf(S) : -INFINITY;
+    if (sub == 0) s_lse[hh] = nan ? NAN : M > -INFINITY ? M + logf(S) : -INFINITY;
   }
   __syncthreads();
   const int hh = tid >> 4, h = h0 + hh, sub = tid & 15, g = sub % kG, ci = sub / kG;
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(const int32_t* sched, 
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float wk = L > -INFINITY ? expf(wgt[k] - L) : 0.f;  // every split empty: out = 0
+        const float wk = L == -INFINITY ? 0.f : expf(wgt[k] - L);  // every split empty: out = 0
 #pragma unroll
         for (int f = 0; f < kNf; ++f) {
           acc[f].x += wk * v[k][f].x;

@@ -296,3 +296,35 @@ def test_what_the_device_reports():
     dec.decode(q.d_q, q.d_qr, q.pool, q.d_bt, q.d_L, SCALE, out=out, lse=lse)
     assert _lib.mla_device_error(clear=True) == _lib.MLA_ERR_WORKSPACE
     assert (out == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,s_q", [(16, 1), (16, 3), (40, 1), (128, 1)])
+@pytest.mark.parametrize("units", [5, 0])
+def test_nan_in_every_split(H, s_q, units):
+    """One key of every tile holds NaN: the merged row is NaN too, and does not look like one that saw no key."""
+    import torch
+    L = [2000, 1900, 130]
+    q = Problem(L, H, s_q=s_q, seed=15, units=units)
+    before, lse0 = q.run()
+    for j in range(-(-L[0] // 64)):
+        q.pool[int(q.bt[0, j]), 3][256:288].view(torch.bfloat16)[j % 16] = math.nan
+    out, lse = q.run()
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.equal(out[1:], before[1:]) and torch.equal(lse[1:], lse0[1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,s_q", [(16, 1), (20, 2), (128, 1)])
+@pytest.mark.parametrize("units", [1, 5, 0])
+def test_a_query_that_holds_nan(H, s_q, units):
+    """One head of one token: NaN for it, split or not, and the bits of the others as without it."""
+    import torch
+    q = Problem([2000, 1900, 130], H, s_q=s_q, seed=16, units=units)
+    before, lse0 = q.run()
+    b, t, h = 1, s_q - 1, H // 2
+    q.d_q[b, t, h, 100] = math.nan
+    out, lse = q.run()
+    assert torch.isnan(out[b, t, h]).all() and torch.isnan(lse[b, t, h])
+    out[b, t, h], lse[b, t, h] = before[b, t, h], lse0[b, t, h]
+    assert torch.equal(out, before) and torch.equal(lse, lse0)
