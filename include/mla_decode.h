@@ -66,7 +66,7 @@ typedef enum {
   MLA_KV_INT4 = 2,          /* page = [64][416 bytes]: 512 four-bit codes of c (256 bytes), then 16 bf16 scales (one per
                                32 values), then k^R as 64 bf16.  value = (code - 8) * scale, exact in bf16: a scale has
                                four significant bits (its low four mantissa bits are zero) and is below 2^121 (larger
-                               ones, infinities and NaN stand for values that are not finite).  The 32-bit word (little
+                               ones, infinities and NaN make NaN of their 32 values).  The 32-bit word (little
                                endian) of dims 8 w .. 8 w + 7 has the code of dim 8 w + 2 i in bits 4 i .. 4 i + 3 and of dim
                                8 w + 2 i + 1 in bits 16 + 4 i .. 19 + 4 i, i = 0 .. 3 */
 } mla_kv_dtype;

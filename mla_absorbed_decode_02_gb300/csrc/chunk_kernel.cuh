@@ -980,7 +980,8 @@ __device__ __forceinline__ void expand_row(const uint8_t* src, __nv_bfloat16* ds
   } else {
     static_assert(kFmt == kKvInt4, "format");
     const uint2 c = *reinterpret_cast<const uint2*>(src + 8 * lane);
-    const uint32_t s = *reinterpret_cast<const uint16_t*>(src + kI4Codes + (lane & ~1)), s2 = s | s << 16, a2 = int4_offset(s2);
+    const uint32_t s = *reinterpret_cast<const uint16_t*>(src + kI4Codes + (lane & ~1));
+    const uint32_t s2 = int4_scale_overflows(s) ? kI4Nan : s | s << 16, a2 = int4_offset(s2);
     expand_int4_word(c.x, s2, a2, reinterpret_cast<uint32_t(&)[4]>(o[0]));
     expand_int4_word(c.y, s2, a2, reinterpret_cast<uint32_t(&)[4]>(o[4]));
   }

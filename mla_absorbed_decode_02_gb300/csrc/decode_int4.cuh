@@ -344,16 +344,14 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       uint32_t poison = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s2[i] |= s2[i] << 16;
         const int key = key0 + 8 * i;
-        if (key >= a.nkeys) {
-          s2[i] = 0;  // no key: the products must see zeros
-        } else if (key >= a.some && (s2[i] & 0x7FFFu) >= 0x7C00u) {  // from 2^121 on 136 scales overflow
-          // a key that only some of the tokens see: its values must not reach the others (0 x NaN); the softmax
-          // gives NaN to those that see it
-          s2[i] = 0;
-          poison |= 1u << i;
-        }
+        const bool over = int4_scale_overflows(s2[i]), late = key >= a.some;
+        s2[i] |= s2[i] << 16;
+        if (over) s2[i] = kI4Nan;
+        // Zeros for what is no key, and for a key that only some of the tokens see and whose values must not reach the others (0 x NaN):
+        // the softmax gives NaN to those that see it.
+        if (over && late && key < a.nkeys) poison |= 1u << i;
+        if (key >= a.nkeys || (over && late)) s2[i] = 0;
         a2[i] = int4_offset(s2[i]);
       }
       __syncwarp();

@@ -15,6 +15,10 @@ namespace mla {
 constexpr int kI4Row = 416;
 constexpr int kI4Codes = 256, kI4Rope = kI4Codes + 32;  // offsets of the scales and of the RoPE values
 
+// From 2^121 on 136 s is an infinity, which would make infinities of one sign of all codes: a product with a weight of 0, or a
+// maximum, can lose those.  kI4Nan takes the place of such a scale, and every value is NaN.
+__device__ __forceinline__ bool int4_scale_overflows(uint32_t s) { return (s & 0x7FFFu) >= 0x7C00u; }
+constexpr uint32_t kI4Nan = 0x7FC07FC0u;
 __device__ __forceinline__ uint32_t int4_offset(uint32_t s2) {  // -136 s of both halves
   uint32_t a2;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(a2) : "r"(s2), "r"(0xC308C308u));

@@ -328,3 +328,24 @@ def test_a_query_that_holds_nan(H, s_q, units):
     assert torch.isnan(out[b, t, h]).all() and torch.isnan(lse[b, t, h])
     out[b, t, h], lse[b, t, h] = before[b, t, h], lse0[b, t, h]
     assert torch.equal(out, before) and torch.equal(lse, lse0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,s_q", [(16, 1), (16, 3), (40, 1), (64, 1), (128, 2)])
+@pytest.mark.parametrize("bits", [0x7C00, 0x7F00, 0x7F80, 0xFC00, 0xFF80])
+@pytest.mark.parametrize("row", [5, 130, 299])
+def test_a_scale_that_overflows_where_no_score_would_be_nan(H, s_q, bits, row):
+    """Queries that are all positive, so that products with values of one infinity do not cancel to NaN by themselves."""
+    import torch
+    L = [300, 70]
+    q = Problem(L, H, s_q=s_q, seed=17)
+    q.d_q.abs_()
+    before, lse0 = q.run()
+    q.pool[int(q.bt[0, row // 64]), row % 64][256:288].view(torch.int16)[3] = bits - (1 << 16 if bits >> 15 else 0)
+    out, lse = q.run()
+    for t in range(s_q):
+        if row < L[0] - (s_q - 1 - t):
+            assert torch.isnan(lse[0, t]).all() and torch.isnan(out[0, t]).all()
+        else:
+            assert torch.equal(out[0, t], before[0, t]) and torch.equal(lse[0, t], lse0[0, t])
+    assert torch.equal(out[1], before[1]) and torch.equal(lse[1], lse0[1])

@@ -311,3 +311,48 @@ def test_chunk_attention_in_other_ways():
     _chunk([3, 1], [2600, 130], 128, seed=1, units=2)
     _chunk([4, 9], [130, 600], 16, seed=2, causal=False)
     _chunk([0, 0], [70, 5], 16, seed=3, pad=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [0x7C00, 0x7F00, 0x7F80, 0x7FC0, 0xFC00, 0xFF80])
+def test_scales_that_overflow_read_back_as_nan(bits):
+    """All 32 values of the group, whatever their codes; the largest scale below them is still exact."""
+    import torch
+    rng = np.random.default_rng(22)
+    raw = random_rows(rng, 9)
+    raw[4, 256:288].view(np.uint16)[5] = bits
+    raw[6, 256:288].view(np.uint16)[2] = 0x7BF0
+    raw[6, :256].view(np.uint32)[8:12] = 0x08080808 | 0x10111111    # (codes whose values a float32 holds: -8 .. 1 times 1.875 2^120)
+    out = torch.empty(9, 576, dtype=torch.bfloat16, device="cuda")
+    _lib.mla_dequantize_kv(MLA_KV_INT4, torch.from_numpy(raw).cuda(), out, 9)
+    got = out.double().cpu().numpy()
+    assert np.isnan(got[4, 160:192]).all()
+    raw[4, 256:288].view(np.uint16)[5] = 0x3F80
+    want = dequantize_rows(raw)
+    got[4, 160:192] = want[4, 160:192]
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.gpu
+def test_chunks_over_a_scale_that_overflows():
+    """The tokens that see the key get NaN, the others keep their bits; all queries positive."""
+    import torch
+    rng = np.random.default_rng(23)
+    P, bt = place(rng, np.array([300, 70]))
+    raw = random_rows(rng, P * 64).reshape(P, 64, 416)
+    g = torch.Generator("cuda").manual_seed(23)
+    q, qr = (torch.randn(9, 16, d, device="cuda", generator=g).abs().to(torch.bfloat16) for d in (512, 64))
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    attn = _lib.ChunkAttention(MlaChunkParams.make(2, 9, 16, P, bt.shape[1], kv_dtype=MLA_KV_INT4, max_kv_tokens=(5 + 2) * 64))
+    attn.plan(i32(0, 6, 9), i32(300, 70))
+    table = torch.from_numpy(bt).cuda()
+    before, lse0 = attn.attend(q, qr, torch.from_numpy(raw).cuda(), table, SCALE)
+    for row in (40, 296):
+        bad = raw.copy()
+        bad[bt[0, row // 64], row % 64, 256:288].view(np.uint16)[9] = 0x7C00
+        out, lse = attn.attend(q, qr, torch.from_numpy(bad).cuda(), table, SCALE)
+        sees = [t for t in range(6) if row <= 294 + t]
+        keep = [t for t in range(9) if t not in sees]
+        assert torch.isnan(out[sees]).all() and torch.isnan(lse[sees]).all()
+        assert torch.equal(out[keep], before[keep]) and torch.equal(lse[keep], lse0[keep])
+    assert _lib.mla_device_error(clear=True) == 0
