@@ -266,16 +266,18 @@ def mla_quantize_kv_fp8(kv_bf16, kv_fp8, num_tokens: int, stream=None):
            "mla_quantize_kv_fp8")
 
 
-def _rows_of(call, t, name, num_tokens, row_bytes):
+def _rows_of(call, t, name, num_tokens, row_bytes, dtypes):
     """Checks a buffer of rows one after another, on the current device."""
-    if t is None or not t.is_contiguous() or num_tokens < 0 or t.numel() * t.element_size() < num_tokens * row_bytes:
+    if (t is None or t.dtype not in dtypes or not t.is_contiguous() or num_tokens < 0
+            or t.numel() * t.element_size() < num_tokens * row_bytes):
         _refuse(f"{call}: {name}")
 
 
 def mla_quantize_kv_int4(kv_bf16, kv_int4, num_tokens: int, stream=None):
-    """bf16 cache rows [n, 576] -> 416-byte INT4 rows [n, 416] (codes, scales, RoPE)."""
-    _rows_of("mla_quantize_kv_int4", kv_bf16, "kv_bf16", num_tokens, 1152)
-    _rows_of("mla_quantize_kv_int4", kv_int4, "kv_int4", num_tokens, 416)
+    """bf16 cache rows [n, 576] -> 416-byte INT4 rows, uint8 [n, 416] (codes, scales, RoPE)."""
+    import torch
+    _rows_of("mla_quantize_kv_int4", kv_bf16, "kv_bf16", num_tokens, 1152, (torch.bfloat16,))
+    _rows_of("mla_quantize_kv_int4", kv_int4, "kv_int4", num_tokens, 416, (torch.uint8, torch.int8))
     if num_tokens == 0:
         return
     _expect_device("mla_quantize_kv_int4", kv_bf16, kv_int4)
@@ -284,11 +286,14 @@ def mla_quantize_kv_int4(kv_bf16, kv_int4, num_tokens: int, stream=None):
 
 
 def mla_dequantize_kv(kv_dtype: int, kv_rows, kv_bf16, num_tokens: int, stream=None):
-    """Rows of a cache of any format (MLA_KV_*, a pool's pages hold them one after another) -> bf16 rows [n, 576]."""
+    """Rows of a cache of any format (MLA_KV_*, a pool's pages hold them one after another; uint8, or bf16 rows as such)
+    -> bf16 rows [n, 576]."""
+    import torch
     if not 0 <= kv_dtype < 3:
         _refuse("mla_dequantize_kv: kv_dtype")
-    _rows_of("mla_dequantize_kv", kv_rows, "kv_rows", num_tokens, _ROW_BYTES[kv_dtype])
-    _rows_of("mla_dequantize_kv", kv_bf16, "kv_bf16", num_tokens, 1152)
+    rows = (torch.uint8, torch.int8) + ((torch.bfloat16,) if kv_dtype == MLA_KV_BF16 else ())
+    _rows_of("mla_dequantize_kv", kv_rows, "kv_rows", num_tokens, _ROW_BYTES[kv_dtype], rows)
+    _rows_of("mla_dequantize_kv", kv_bf16, "kv_bf16", num_tokens, 1152, (torch.bfloat16,))
     if num_tokens == 0:
         return
     _expect_device("mla_dequantize_kv", kv_rows, kv_bf16)

@@ -356,3 +356,21 @@ def test_chunks_over_a_scale_that_overflows():
         assert torch.isnan(out[sees]).all() and torch.isnan(lse[sees]).all()
         assert torch.equal(out[keep], before[keep]) and torch.equal(lse[keep], lse0[keep])
     assert _lib.mla_device_error(clear=True) == 0
+
+
+def test_calls_refuse_other_types():
+    """bf16 rows that are no bf16, packed rows that are no bytes."""
+    import torch
+    x, rows = torch.zeros(4, 576, dtype=torch.bfloat16), torch.zeros(4, 416, dtype=torch.uint8)
+    q, d = _lib.mla_quantize_kv_int4, _lib.mla_dequantize_kv
+    for call, args, name in ((q, (x.float(), rows, 4), "kv_bf16"), (q, (x.half(), rows, 4), "kv_bf16"), (q, (x.view(torch.uint8), rows, 4), "kv_bf16"),
+                             (q, (x, torch.zeros(4, 208, dtype=torch.int16), 4), "kv_int4"), (q, (x, torch.zeros(4, 416, dtype=torch.bfloat16), 4), "kv_int4"),
+                             (d, (MLA_KV_INT4, rows, x.float(), 4), "kv_bf16"), (d, (MLA_KV_FP8_E4M3, torch.zeros(4, 656, dtype=torch.uint8), x.half(), 4), "kv_bf16"),
+                             (d, (MLA_KV_INT4, torch.zeros(4, 416), x, 4), "kv_rows"), (d, (MLA_KV_FP8_E4M3, torch.zeros(4, 328, dtype=torch.int16), x, 4), "kv_rows"),
+                             (d, (MLA_KV_BF16, x.half(), x, 4), "kv_rows"), (d, (MLA_KV_BF16, x.float(), x, 4), "kv_rows")):
+        with pytest.raises(MlaError, match=name) as e:
+            call(*args, stream=0)
+        assert e.value.status == _lib.MLA_ERR_INVALID_ARG
+    for kv, t in ((MLA_KV_BF16, x.clone()), (MLA_KV_BF16, torch.zeros(4, 1152, dtype=torch.uint8)), (MLA_KV_INT4, rows)):
+        with pytest.raises(MlaError, match="device"):      # (taken, but for lying on the host)
+            d(kv, t, x, 4, stream=0)
