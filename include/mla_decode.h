@@ -221,7 +221,7 @@ int32_t mla_quantize_kv_fp8(const void* kv_bf16, void* kv_fp8, int64_t num_token
  *   kv_int4   device [num_tokens][416 bytes]: 256 bytes of codes, 16 bf16 scales, the 64 RoPE values unchanged
  * Per 32 latent values: scale = amax / 7 rounded up to four significant bits and at least 2^-126 (1 where all are
  * zero); code = 8 + x / scale rounded to nearest even, 1 .. 15.  Values of which one is not finite, or above 7 * 2^119, read
- * back as NaN, all 32.  num_tokens = 0 launches nothing.  Both buffers 16-byte aligned; asynchronous on stream.
+ * back as NaN, all 32.  num_tokens = 0 launches nothing.  Both buffers 16-byte aligned and apart; asynchronous on stream.
  */
 int32_t mla_quantize_kv_int4(const void* kv_bf16, void* kv_int4, int64_t num_tokens, void* stream);
 

@@ -273,6 +273,13 @@ def _rows_of(call, t, name, num_tokens, row_bytes, dtypes):
         _refuse(f"{call}: {name}")
 
 
+def _rows_apart(call, a, b, num_tokens, a_bytes, b_bytes):
+    """The rows of two buffers do not meet: other warps read one while a row of the other is written."""
+    at, to = a.data_ptr(), b.data_ptr()
+    if at < to + num_tokens * b_bytes and to < at + num_tokens * a_bytes:
+        _refuse(f"{call}: rows overlap")
+
+
 def mla_quantize_kv_int4(kv_bf16, kv_int4, num_tokens: int, stream=None):
     """bf16 cache rows [n, 576] -> 416-byte INT4 rows, uint8 [n, 416] (codes, scales, RoPE)."""
     import torch
@@ -280,6 +287,7 @@ def mla_quantize_kv_int4(kv_bf16, kv_int4, num_tokens: int, stream=None):
     _rows_of("mla_quantize_kv_int4", kv_int4, "kv_int4", num_tokens, 416, (torch.uint8, torch.int8))
     if num_tokens == 0:
         return
+    _rows_apart("mla_quantize_kv_int4", kv_bf16, kv_int4, num_tokens, 1152, 416)
     _expect_device("mla_quantize_kv_int4", kv_bf16, kv_int4)
     _check(load_library().mla_quantize_kv_int4(_ptr(kv_bf16), _ptr(kv_int4), int(num_tokens), _stream(stream)),
            "mla_quantize_kv_int4")
@@ -296,6 +304,7 @@ def mla_dequantize_kv(kv_dtype: int, kv_rows, kv_bf16, num_tokens: int, stream=N
     _rows_of("mla_dequantize_kv", kv_bf16, "kv_bf16", num_tokens, 1152, (torch.bfloat16,))
     if num_tokens == 0:
         return
+    _rows_apart("mla_dequantize_kv", kv_rows, kv_bf16, num_tokens, _ROW_BYTES[kv_dtype], 1152)
     _expect_device("mla_dequantize_kv", kv_rows, kv_bf16)
     _check(load_library().mla_dequantize_kv(kv_dtype, _ptr(kv_rows), _ptr(kv_bf16), int(num_tokens), _stream(stream)),
            "mla_dequantize_kv")

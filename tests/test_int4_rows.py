@@ -374,3 +374,20 @@ def test_calls_refuse_other_types():
     for kv, t in ((MLA_KV_BF16, x.clone()), (MLA_KV_BF16, torch.zeros(4, 1152, dtype=torch.uint8)), (MLA_KV_INT4, rows)):
         with pytest.raises(MlaError, match="device"):      # (taken, but for lying on the host)
             d(kv, t, x, 4, stream=0)
+
+
+def test_calls_refuse_rows_written_over_others():
+    import torch
+    buf = torch.zeros(4 * 1152 + 4 * 656, dtype=torch.uint8)
+    wide_rows = buf[:4 * 1152].view(torch.bfloat16).view(4, 576)
+    for at in (0, 416, 4 * 1152 - 16):
+        with pytest.raises(MlaError, match="overlap"):
+            _lib.mla_quantize_kv_int4(wide_rows, buf[at:at + 4 * 416], 4, stream=0)
+        with pytest.raises(MlaError, match="overlap"):
+            _lib.mla_dequantize_kv(MLA_KV_INT4, buf[at:at + 4 * 416], wide_rows, 4, stream=0)
+    with pytest.raises(MlaError, match="overlap"):
+        _lib.mla_dequantize_kv(MLA_KV_BF16, wide_rows, wide_rows, 4, stream=0)
+    with pytest.raises(MlaError, match="device"):          # side by side
+        _lib.mla_quantize_kv_int4(wide_rows, buf[4 * 1152:], 4, stream=0)
+    with pytest.raises(MlaError, match="device"):          # (rows past num_tokens are not touched)
+        _lib.mla_dequantize_kv(MLA_KV_INT4, buf[2 * 1152:], wide_rows, 2, stream=0)
