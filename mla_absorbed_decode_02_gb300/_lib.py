@@ -502,6 +502,16 @@ def mla_rope_table(max_positions: int, theta: float = 10000.0, device="cuda"):
     return torch.cat([angle.cos(), angle.sin()], -1).float()
 
 
+def _meets(at: int, size: int, first: int, rows: int, stride: int, row_bytes: int) -> bool:
+    """Whether [at, at + size) touches one of the rows that start at first, first + stride, ..."""
+    if at >= first + (rows - 1) * stride + row_bytes or at + size <= first:
+        return False
+    if rows == 1 or at <= first or stride < row_bytes:
+        return True
+    into = (at - first) % stride  # from the last row that starts at or before it
+    return into < row_bytes or into + size > stride
+
+
 def mla_append_rotated_kv(p: MlaPoolParams, latent, k_rope, cos_sin, cu_seqlens, cache_seqlens, block_table, kv_pages,
                           q_rope=None, q_out=None, positions=None, norm_weight=None, norm_eps: float = 1e-6,
                           interleaved: bool = False, served=None, stream=None):
@@ -546,17 +556,22 @@ def mla_append_rotated_kv(p: MlaPoolParams, latent, k_rope, cos_sin, cu_seqlens,
         (n, H, width), (token_stride, head_stride, one) = q_rope.shape, q_rope.stride()
         if n != T or width != 64 or one != 1:
             _refuse(call + "q_rope")
-        if q_out is None:
+        made = q_out is None
+        if made:
             q_out = _new(q_rope, stream, (T, H, 64), bf16)
         elif _bad(q_out, bf16, (T, H, 64)):
             _refuse(call + "q_out")
-        # (read and written by the same threads where the two are one, by others where they merely overlap)
         if T and H:
             q_at, out_at = q_rope.data_ptr(), q_out.data_ptr()
-            last = (T - 1) * token_stride + (H - 1) * head_stride + 64
-            if (q_at < out_at + T * H * 128 and out_at < q_at + 2 * last
-                    and not (out_at == q_at and q_rope.is_contiguous())):
-                _refuse(call + "q_out overlaps q_rope")
+            if not made:
+                # (read and written by the same threads where the two are one, by others where they merely overlap)
+                size, last = T * H * 128, (T - 1) * token_stride + (H - 1) * head_stride + 64
+                if (q_at < out_at + size and out_at < q_at + 2 * last
+                        and not (out_at == q_at and q_rope.is_contiguous())):
+                    _refuse(call + "q_out overlaps q_rope")
+                if (_meets(out_at, size, latent.data_ptr(), T, 2 * latent_stride, 1024)
+                        or _meets(out_at, size, k_rope.data_ptr(), T, 2 * rope_stride, 128)):
+                    _refuse(call + "q_out overlaps latent or k_rope")
     elif q_out is not None:
         _refuse(call + "q_out without q_rope")
     _expect_pool("mla_append_rotated_kv", kv_pages, p)

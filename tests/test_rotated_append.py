@@ -338,3 +338,31 @@ def test_a_step_of_a_layer(kv):
     assert _lib.mla_device_error(clear=True) == 0
     for t, v in zip((out, lse, q, *state), want):
         assert torch.equal(t, v)
+
+
+def test_queries_are_not_written_over_the_rows():
+    """q_out over latent or k_rope, which other warps read in the same launch; a place between strided rows is nobody's."""
+    import torch
+    args, kw = _good()
+    x = torch.zeros(4, 2048, dtype=torch.bfloat16)
+    args[1], args[2] = x[:, :512], x[:, 512:576]
+    flat = x.view(-1)
+    one = lambda at, T=4: flat[at:at + T * 192].view(T, 3, 64)  # noqa: E731
+    for at in (0, 64, 504, 512, 568, 1984, 2048 * 3 + 512 - 8):
+        with pytest.raises(MlaError, match="overlaps"):
+            _lib.mla_append_rotated_kv(*args, **dict(kw, q_out=one(at)), stream=0)
+    for at in (576, 2048 - 768, 2048 * 3 + 576):
+        with pytest.raises(MlaError, match="device"):
+            _lib.mla_append_rotated_kv(*args, **dict(kw, q_out=one(at)), stream=0)
+
+
+def test_where_a_buffer_meets_strided_rows():
+    rng = np.random.default_rng(4)
+    hits = 0
+    for _ in range(4000):
+        rows, width, gap, first, size = (int(v) for v in rng.integers([1, 1, 0, 0, 1], [6, 9, 12, 40, 20]))
+        at = int(rng.integers(0, 110))
+        want = any(at < first + i * (width + gap) + width and first + i * (width + gap) < at + size for i in range(rows))
+        assert _lib._meets(at, size, first, rows, width + gap, width) == want, (at, size, first, rows, width, gap)
+        hits += want
+    assert 500 < hits < 3500
