@@ -159,7 +159,6 @@ struct I4Cursor {
     return true;
   }
   __device__ int page() const { return t - 1; }  // of the tile that next() gave
-  __device__ void skip_block() { t = end; }
 };
 
 // 16 lanes x 2 K columns of tensor memory and a warp, K = 8 or 16 values a lane: lane l gets, in r[2 b + h], column 4 b + l % 4 of
