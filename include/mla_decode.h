@@ -603,9 +603,10 @@ int32_t mla_compact_pages(const mla_pool_params* p, void* kv_pages, int32_t* blo
 int32_t mla_device_error(int32_t* word, int32_t clear);
 
 /*
- * Failure-path self test: launches one CTA whose bounded wait on a barrier that
- * nothing completes runs out after timeout_us, sets the device error word and
- * returns normally.  The GPU context stays usable.  Read the result with
+ * Failure-path self test: launches one CTA that waits on a barrier that nothing completes, in
+ * each way that the library's kernels wait.  Each wait runs out after timeout_us; the first
+ * sets the device error word to MLA_ERR_TIMEOUT, and the kernel returns normally (a wait that did
+ * not run out leaves MLA_ERR_CUDA).  The GPU context stays usable.  Read the result with
  * mla_device_error().
  */
 int32_t mla_wait_selftest(int32_t timeout_us, void* stream);

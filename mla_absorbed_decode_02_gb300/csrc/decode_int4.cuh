@@ -237,6 +237,25 @@ __device__ __forceinline__ bool i4_wait_warp(uint32_t bar, uint32_t parity, cons
   return __all_sync(0xffffffffu, ok);
 }
 
+// By one thread, which asks without being suspended and does other work meanwhile: busy() does a piece of it, or gives false.
+template <class Busy>
+__device__ __forceinline__ bool i4_wait_busy(uint32_t bar, uint32_t parity, const WaitCtx& w, int site, Busy busy) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (busy()) continue;
+    if (mbar_test_wait(bar, parity)) return true;
+    if ((i & 1023) == 0) {
+      if (*w.abort_local) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > w.timeout_ns) {
+        raise_abort(w, site);
+        return false;
+      }
+    }
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
   using S = I4Smem<N>;
@@ -460,23 +479,11 @@ __device__ __forceinline__ void decode_int4_body(const Int4Args& args) {
       };
       // until the barrier's phase is over; the output meanwhile, when its weights are there
       auto wait = [&](uint32_t b, uint32_t phase, int site) -> bool {
-        uint64_t t0 = 0;
-        for (uint32_t i = 1;; ++i) {
-          if (tp < t && mbar_test_wait(bar(IB_P_FULL + (tp & 1)), tp >> 1 & 1)) {
-            pv();
-            continue;
-          }
-          if (mbar_test_wait(b, phase)) return true;
-          if ((i & 1023) == 0) {
-            if (*wc.abort_local) return false;
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > wc.timeout_ns) {
-              raise_abort(wc, site);
-              return false;
-            }
-          }
-        }
+        return i4_wait_busy(b, phase, wc, site, [&]() -> bool {
+          if (!(tp < t && mbar_test_wait(bar(IB_P_FULL + (tp & 1)), tp >> 1 & 1))) return false;
+          pv();
+          return true;
+        });
       };
       for (;;) {
         const uint32_t o = t & 1, d = tmem + TS + N * o;

@@ -192,23 +192,31 @@ __global__ void __launch_bounds__(256) mla_quantize_fp8_kernel(const __nv_bfloat
 }
 
 // ----------------------------------------------------------------- bounded-wait self test
-// One CTA waits on a barrier that nothing ever completes; the bounded wait runs
-// out, records MLA_ERR_TIMEOUT in the device error word and the kernel returns.
+// One warp waits on a barrier that nothing ever completes, in each way that the kernels wait, one after another.  Each
+// wait runs out and raises its abort flag, the first records MLA_ERR_TIMEOUT in the device error word, and the kernel
+// returns.  A wait that did not give up by itself leaves MLA_ERR_CUDA there instead.
 __global__ void mla_wait_selftest_kernel(uint64_t timeout_ns) {
   __shared__ uint64_t barrier_word;
-  __shared__ int abort_word;
+  __shared__ int abort_word[3];
   const uint32_t b = smem_addr(&barrier_word);
   if (threadIdx.x == 0) {
     mbar_init(b, 1);
-    abort_word = 0;
+    for (int i = 0; i < 3; ++i) abort_word[i] = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  WaitCtx w;
-  w.abort_local = &abort_word;
-  w.abort_peer = 0;
-  w.timeout_ns = timeout_ns;
-  wait_warp(b, 0, w, kSiteSelftest);
+  auto ctx = [&](int i) {
+    WaitCtx w;
+    w.abort_local = &abort_word[i];
+    w.abort_peer = 0;
+    w.timeout_ns = timeout_ns;
+    return w;
+  };
+  bool came = wait_warp(b, 0, ctx(0), kSiteSelftest);
+  came |= i4_wait_warp(b, 0, ctx(1), kSiteSelftest);
+  if (threadIdx.x == 0) came |= i4_wait_busy(b, 0, ctx(2), kSiteSelftest, []() { return false; });
+  __syncwarp();
+  if (threadIdx.x == 0 && (came || !abort_word[0] || !abort_word[1] || !abort_word[2])) atomicExch(&g_mla_error, MLA_ERR_CUDA);
 }
 
 }  // namespace mla

@@ -468,3 +468,22 @@ def test_unaligned_pointer_rejected():
     buf = torch.empty(100000, dtype=torch.uint8, device="cuda")
     with pytest.raises(MlaError):
         mla_decode(p, q_nope, q_rope, kv, bt, seq, w.scale, buf[1:], buf, buf, buf)
+
+
+def test_bounded_waits_of_every_kind_run_out():
+    """The self test lets each of the library's waits run out, one after another: the plain one, the INT4 decode's, and that of its issuing
+    thread.  The word is a timeout's only if all of them gave up; each takes the limit."""
+    import torch
+    from mla_absorbed_decode_02_gb300 import mla_wait_selftest, mla_device_error
+    mla_device_error(clear=True)
+    mla_wait_selftest(1000)
+    torch.cuda.synchronize()
+    assert mla_device_error(clear=True) % 16 == 4
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    mla_wait_selftest(20000)
+    end.record()
+    torch.cuda.synchronize()
+    word = mla_device_error(clear=True)
+    assert word % 16 == 4 and word // 16 > 0
+    assert 3 * 20.0 <= start.elapsed_time(end) + 1.0 and start.elapsed_time(end) < 1000.0
