@@ -9,7 +9,8 @@
 // Work split.  The keys are the M dimension: S^T = K Q^T and O^T = C^T P^T.  A tile is a page, 64 keys, expanded once
 // by a CTA that needs no other's help: up to 64 rows are its N = 16, 32, 48 or 64 columns, O^T is 4 x [128 dims x N] in tensor
 // memory.  A unit of the plan is one CTA, or two for 65 to 128 heads, which read the same pages at the same time (the
-// second from L2).  With several new tokens a sequence, as many as fit into 64 rows share every key.
+// second from L2).  With several new tokens a sequence, groups of them of up to 64 rows share every
+// key; a group's number of tokens divides s_q.
 //
 // That one copy is both products' A operand: blocks [64 keys][64 dims] of shared memory with the 128-byte swizzle, K-major for the
 // scores (M = 64), MN-major for the output (M = 128 dims).  MMAs of K = 16 take 32 / 32 / 37 cycles for the scores, 44 / 44 / 50

@@ -349,3 +349,18 @@ def test_a_scale_that_overflows_where_no_score_would_be_nan(H, s_q, bits, row):
         else:
             assert torch.equal(out[0, t], before[0, t]) and torch.equal(lse[0, t], lse0[0, t])
     assert torch.equal(out[1], before[1]) and torch.equal(lse[1], lse0[1])
+
+
+# ------------------------------------------------------------------ numbers of tokens, heads and rows beyond the ones above
+@pytest.mark.parametrize("H,s_q,want", [(16, 5, 1), (16, 7, 1), (10, 7, 1), (32, 3, 1), (12, 5, 5), (9, 7, 7), (16, 6, 3), (20, 6, 3), (40, 2, 1)])
+def test_a_group_divides_the_new_tokens(H, s_q, want):
+    """Fewer tokens than fit where their number does not divide s_q."""
+    assert _lib.mla_plan_host(_params(num_heads=H, s_q=s_q, batch=2), 7, [100, 300])[5] == want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("s_q", [5, 6, 7])
+@pytest.mark.parametrize("H", [3, 9, 12, 16, 20, 33, 96])
+@pytest.mark.parametrize("causal", [True, False])
+def test_odd_numbers_of_new_tokens(s_q, H, causal):
+    Problem([8, 3, 64 + s_q - 1, 129, 131, 260, 0], H, s_q=s_q, causal=causal, seed=s_q).check()
