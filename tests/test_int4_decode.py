@@ -364,3 +364,46 @@ def test_a_group_divides_the_new_tokens(H, s_q, want):
 @pytest.mark.parametrize("causal", [True, False])
 def test_odd_numbers_of_new_tokens(s_q, H, causal):
     Problem([8, 3, 64 + s_q - 1, 129, 131, 260, 0], H, s_q=s_q, causal=causal, seed=s_q).check()
+
+
+def _isolated(L, H, s_q, seed, put, row, units=0):
+    """`put` spoils row `row` of the first sequence: NaN for the tokens that see it, and the bits of the others as without it."""
+    import torch
+    q = Problem(L, H, s_q=s_q, seed=seed, units=units)
+    before, lse0 = q.run()
+    put(q.pool[int(q.bt[0, row // 64]), row % 64])
+    out, lse = q.run()
+    for t in range(s_q):
+        if row < L[0] - (s_q - 1 - t):
+            assert torch.isnan(out[0, t]).all() and torch.isnan(lse[0, t]).all()
+        else:
+            assert torch.equal(out[0, t], before[0, t]) and torch.equal(lse[0, t], lse0[0, t])
+    assert torch.equal(out[1:], before[1:]) and torch.equal(lse[1:], lse0[1:])
+
+
+# rows of a CTA: 20, 30, 32 (two softmax warpgroups), 40, 48 (three), 64; two CTAs of 33 and of 48
+SHARED = [(20, 1), (10, 3), (16, 2), (20, 2), (16, 3), (40, 1), (12, 5), (66, 2), (96, 3)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,s_q", SHARED)
+@pytest.mark.parametrize("where", ["scale", "rope"])
+@pytest.mark.parametrize("row", [5, 297, 298, 299])
+def test_a_key_that_holds_nan_at_every_number_of_rows(H, s_q, where, row):
+    import torch
+
+    def put(at):
+        (at[256:288] if where == "scale" else at[288:]).view(torch.bfloat16)[7] = math.nan
+    _isolated([300, 70], H, s_q, 13, put, row)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,s_q", SHARED)
+@pytest.mark.parametrize("bits", [0x7C00, 0x7F80])
+@pytest.mark.parametrize("row", [297, 299])
+def test_a_scale_that_overflows_at_every_number_of_rows(H, s_q, bits, row):
+    import torch
+
+    def put(at):
+        at[256:288].view(torch.int16)[11] = bits
+    _isolated([300, 70], H, s_q, 14, put, row)
