@@ -391,3 +391,25 @@ def test_calls_refuse_rows_written_over_others():
         _lib.mla_quantize_kv_int4(wide_rows, buf[4 * 1152:], 4, stream=0)
     with pytest.raises(MlaError, match="device"):          # (rows past num_tokens are not touched)
         _lib.mla_dequantize_kv(MLA_KV_INT4, buf[2 * 1152:], wide_rows, 2, stream=0)
+
+
+# ------------------------------------------------------------------ bounds of every group, scales past the largest, types
+@pytest.mark.gpu
+def test_quantised_again():
+    """Rows of very different sizes, read back and written again: the bytes are those of the definition on the values read, and each
+    group of 32 moves by half a step of its own new scale at most."""
+    import torch
+    rng = np.random.default_rng(21)
+    n = 999
+    x = rng.standard_normal((n, 576), dtype=np.float32) * np.exp(5 * rng.standard_normal((n, 1))).astype(np.float32)
+    rows = _write(mw.to_bf16_bits(x))
+    back = torch.empty(n, 576, dtype=torch.bfloat16, device="cuda")
+    _lib.mla_dequantize_kv(MLA_KV_INT4, rows, back, n)
+    again, twice = torch.empty_like(rows), torch.empty_like(back)
+    _lib.mla_quantize_kv_int4(back, again, n)
+    _lib.mla_dequantize_kv(MLA_KV_INT4, again, twice, n)
+    bits = back.view(torch.int16).cpu().numpy().view(np.uint16)
+    assert np.array_equal(again.cpu().numpy(), quantize_rows(wide(bits[:, :512]), bits[:, 512:]))
+    step = wide(again[:, 256:288].contiguous().cpu().numpy().view(np.uint16)).astype(np.float64).repeat(32, 1)
+    assert (np.abs((twice[:, :512].double() - back[:, :512].double()).cpu().numpy()) <= step / 2).all()
+    assert torch.equal(twice[:, 512:], back[:, 512:])
