@@ -366,3 +366,28 @@ def test_where_a_buffer_meets_strided_rows():
         assert _lib._meets(at, size, first, rows, width + gap, width) == want, (at, size, first, rows, width, gap)
         hits += want
     assert 500 < hits < 3500
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 5, 64, 1000, 10000])
+@pytest.mark.parametrize("sigma", [1e-3, 1.0, 300.0])
+def test_the_norms_last_bit(T, sigma):
+    """The squares are summed in a fixed order, four neighbours at a time: over the rows' quarters, over the four, then over the lanes.
+    A norm in elementary float32 operations in that order has the same bits, and so has one over torch's mean of a row."""
+    import torch
+    s = Case([T], [T], 0, MLA_KV_BF16, seed=T, sigma=sigma)
+    s.call(norm_weight=s.weight, norm_eps=1e-6)
+    assert _lib.mla_device_error(clear=True) == 0
+    pg, r = (torch.from_numpy(np.asarray(v, np.int64)).cuda() for v in s.at)
+    got = s.pool[pg, r].contiguous().view(torch.bfloat16)[:, :512]
+    x = s.lat.float()
+    sq = x.square().view(T, 4, 32, 4)                       # quarter, lane, neighbour (a bf16's square is exact in float32)
+    part = sq[:, 0]
+    for k in (1, 2, 3):
+        part = part + sq[:, k]
+    lane = ((part[..., 0] + part[..., 1]) + part[..., 2]) + part[..., 3]
+    while lane.shape[1] > 1:
+        lane = lane[:, 0::2] + lane[:, 1::2]
+    for mean in (lane / 512, x.square().mean(1, keepdim=True)):
+        want = (x * torch.rsqrt(mean + 1e-6) * s.weight.float()).to(torch.bfloat16)
+        assert torch.equal(got, want), int((got != want).any(1).sum())
