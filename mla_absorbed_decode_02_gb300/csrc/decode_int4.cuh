@@ -14,10 +14,14 @@
 //
 // That one copy is both products' A operand: blocks [64 keys][64 dims] of shared memory with the 128-byte swizzle, K-major for the
 // scores (M = 64), MN-major for the output (M = 128 dims).  MMAs of K = 16 take 32 / 32 / 37 cycles for the scores, 44 / 44 / 50
-// for the output (N = 16 / 32 / 64).  What bounds them is the shared memory: both operands of every MMA, the pages and the expanded
-// keys are ~2000 cycles of its bandwidth a tile for N = 16, ~2850 for N = 64; a tile takes 2500 and 3800.  (The scores' A in tensor
+// for the output (N = 16 / 32 / 64).  What bounds a tile is the way to shared memory: for N = 16 / 48 / 64 the tensor cores read their
+// operands in 1306 / 1725 / 1928 passes of 128 bytes (A's are ~1095 of them), the warps load and store in 1279 / 1549 / 1649, together 2585 / 3274 /
+// 3577 of the 2690 / 3870 / 3790 cycles that a tile takes (counters of a launch; the tile's time from its growth with the length, at
+// 2070 MHz).  (The scores' A in tensor
 // memory is read without it, at 12 to 32 cycles an MMA, but beside the expanding warps' stores there they took 53, and the output's
 // MMAs 70: 64 streams x 16 heads 87 us instead of 83, 128 heads ragged 218 instead of 153.)
+// Beyond its tiles a call takes 11 / 14 / 18 us (launch, the first page and queries, the last tile's way out, the merge's launch), and a
+// unit's every further piece 5.6 / 8.0 / 12.6 us, four to seven tiles: the plan's price of a piece is six.
 //
 // Pages come by bulk copies into shared memory, as they are.  (Loads into registers, 64 bytes of a row at a time, kept the load
 // units busy for ~1500 cycles a page.  A second page ahead changed nothing.)  The four quarters of a tile (128 dims each) are
@@ -32,9 +36,12 @@
 // warps, so scores are taken against the maximum so far, and only where one exceeds it by 2^8 are the new maxima found and O
 // rescaled); 16 warps expand; one copies pages and queries and writes the tiles' records; a thread of the last issues the MMAs.
 //
-// Measured: 64 streams x 16 heads, 190 MB of cache, 83 us; 128 heads, 64 ragged sequences up to 32,768 keys (142 MB) 153 us, 4 up to
-// 131,072 (94 MB) 115 us; 24 sequences of 4 tokens x 20 heads (36 MB) 54 us (with
-// 64 columns 59).  64 x 8192 keys, 218 MB: 32 heads 100 us, 40 128, 64 134.
+// Measured: 64 streams x 16 heads, 190 MB of cache, 82 us; 128 heads, 64 ragged sequences up to 32,768 keys (142 MB) 151 us, 4 up to
+// 131,072 (94 MB) 114 us; 24 sequences of 4 tokens x 20 heads (36 MB) 55 us (with
+// 64 columns 59).  64 x 8192 keys, 218 MB: 16 heads 90 us, 32 99, 40 127, 64 130, 128 235.  At 65 to 128 heads the decode of the same
+// lengths over bf16 pages is the faster one (148 us), and so is that over FP8 pages (193 us): each of the two CTAs here expands all
+// 512 dims of a page, each of a pair's there has its own half of them.  Up to 64 heads this one is (16 heads: 138 and 184 us).
+// Registers: n48 spills 20 bytes (44 loaded back), n64 8 (44); n16 and n32 none.
 #pragma once
 #include "common.cuh"
 #include "decode_kernel.cuh"  // packed float pairs, bf16 packing

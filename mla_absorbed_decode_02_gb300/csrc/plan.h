@@ -31,6 +31,9 @@ constexpr int kTile = 64;                     // tokens per work tile (one page)
 // 128 x 288 query half, the epilogue writing the 128 x 256 output half, and the
 // pipeline refill between pieces -- measured at about six tiles' time per piece
 // boundary on GB300 (the plan balances positions, so this is what evens the units).
+// The kernels over INT4 pages are planned with the same six: there a boundary took 5.6 us
+// = 4.3 tiles at 16 rows, 8.0 = 4.1 at 40, 12.6 = 6.9 at 128 heads (96 tiles a unit as one
+// block, as two, as three).
 #ifndef MLA_PIECE_COST
 #define MLA_PIECE_COST 6
 #endif
