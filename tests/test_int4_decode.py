@@ -407,3 +407,20 @@ def test_a_scale_that_overflows_at_every_number_of_rows(H, s_q, bits, row):
     def put(at):
         at[256:288].view(torch.int16)[11] = bits
     _isolated([300, 70], H, s_q, 14, put, row)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,s_q,units", [(16, 1, 0), (16, 3, 5), (40, 1, 0), (128, 2, 0)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, 3e38])
+def test_a_query_that_is_not_finite_leaves_the_others(H, s_q, units, value):
+    """A head whose scores are infinite or overflow: the other heads of the tile keep their bits, though maxima are exchanged at every tile."""
+    import torch
+    q = Problem([2000, 700, 130], H, s_q=s_q, seed=18, units=units)
+    before, lse0 = q.run()
+    b, t, h = 0, s_q // 2, H - 1
+    q.d_q[b, t, h, 8:12] = value
+    q.d_qr[b, t, h, 5] = -value
+    out, lse = q.run()
+    assert not torch.isfinite(lse[b, t, h])
+    out[b, t, h], lse[b, t, h] = before[b, t, h], lse0[b, t, h]
+    assert torch.equal(out, before) and torch.equal(lse, lse0)
