@@ -522,7 +522,8 @@ typedef struct mla_rotate_params {
  *   cos_sin          device float32 [max_positions][64]: 32 cosines, then 32 sines, of each position
  *   positions        device int32 [max_tokens], or NULL: a token's position is its row in its sequence, L_b - n_b + i
  *   q_rope           device bf16 (strides above); q_out device bf16 [max_tokens][num_heads][64], contiguous: the q_rope input
- *                    of mla_decode and mla_chunk_attend; may be q_rope itself where that is contiguous, not overlap it otherwise
+ *                    of mla_decode and mla_chunk_attend; may be q_rope itself where that is contiguous, not overlap it otherwise,
+ *                    nor latent or k_rope
  *   cu_seqlens, cache_seqlens, block_table, kv_pages   as for mla_append_kv
  *   served           device int32 [batch], or NULL: as for mla_append_served_kv; left-out tokens' queries are left as they are
  * A token whose row lies outside the block table, whose page is not in [0, num_pages), or whose position is not in
